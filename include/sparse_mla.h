@@ -16,6 +16,8 @@
  * decode-context-parallel ranks, into the result of the whole lists,
  * sparse_mla_v_up applies the per-head value up-projection to O, and
  * sparse_mla_topk builds the index lists from per-position scores.
+ * sparse_mla_append writes new tokens' rows into the cache, and
+ * sparse_mla_q_up brings their queries into its space.
  *
  * Sources (page title, section):
  *   vLLM PR #60220 "FlashMLA sparse: stage fp8 mixed-batch q/out in the
@@ -77,7 +79,8 @@ typedef enum smla_status {
     SMLA_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed */
     SMLA_ERR_TIMEOUT = 4,      /* a bounded wait inside a kernel gave up */
     SMLA_ERR_INDEX_RANGE = 5   /* checked mode: a list entry other than -1 was outside
-                                  [0, num_slots) (it was masked) */
+                                  [0, num_slots) (it was masked); or sparse_mla_append or
+                                  sparse_mla_q_up met a slot or position out of range */
 } smla_status;
 
 typedef enum smla_kv_format {
@@ -291,6 +294,70 @@ smla_status sparse_mla_masked_mha(const void* q, const void* k, const void* v, c
                                   void* stream);
 
 /*
+ * sparse_mla_append -- write new tokens' rows into the cache that the forward
+ * reads: the latent through its RMS norm (if weights are given), the 64 rope
+ * dims rotated by the token's position, packed as a bf16 or fp8 row.  Per token
+ * t with input row [c (512) | k (64)]:
+ *     n  = c * rsqrt(mean(c^2) + eps) * norm_weight     (c without weights)
+ *     k' = the 32 pairs (a, b) of k as (a cos - b sin, b cos + a sin)
+ *     row slots[t] = [n | k'] as bf16; or, as 656 bytes, per 128 values of n
+ *     scale = max|n| / 448 (1 if all are zero) and e4m3(n / scale), k' as bf16
+ * in fp32, each value rounded once (nearest even; e4m3 saturates at 448).
+ *   kv          device, T rows of 576 bf16, kv_stride ELEMENTS apart (a multiple
+ *               of 8, >= 576: a slice of a fused projection's output will do);
+ *               16-byte aligned
+ *   positions   device, [T] int32;  slots  device, [T] int32
+ *   cos_sin     device, [max_pos, 64] fp32: row p holds the 32 cosines, then the
+ *               32 sines of position p
+ *   interleaved nonzero: the pairs are dims (2i, 2i + 1); zero: (i, i + 32)
+ *   norm_weight device, [512] bf16, 16-byte aligned, or NULL (no norm; eps is
+ *               then ignored)
+ *   kv_cache    device, num_slots rows as in sparse_mla_fwd, written in place
+ * slots[t] = -1 writes nothing for token t (an unused place of a padded batch),
+ * and rows that no slot names keep their bytes.  Any other slot outside
+ * [0, num_slots), or a position outside [0, max_pos) with a slot that is not
+ * -1, also writes nothing, and the next sparse_mla_sync_status() returns
+ * SMLA_ERR_INDEX_RANGE.  The slots of a call other than -1 must be distinct: a
+ * cache row belongs to one token, and two tokens that name it would write it in
+ * no set order.  kv must not overlap kv_cache.
+ * T = 0 is a no-op.  Allocates nothing; asynchronous on `stream`.  Errors:
+ * SMLA_ERR_INVALID_ARG for bad sizes, stride, format or eps, a null pointer or
+ * misalignment; SMLA_ERR_CUDA if the launch fails.
+ */
+smla_status sparse_mla_append(const void* kv, int64_t kv_stride, const int32_t* positions, const int32_t* slots,
+                              int32_t T, const float* cos_sin, int32_t max_pos, int32_t interleaved,
+                              const void* norm_weight, float eps, void* kv_cache, int64_t num_slots,
+                              int32_t kv_format, void* stream);
+
+/*
+ * sparse_mla_q_up -- the queries in the cache's space, the counterpart of
+ * sparse_mla_v_up in front of the attention: per token t and head h
+ *     out[t, h, n]  = sum_{d < dn} q[t, h, d] * w[h, d, n]       n < 512
+ *     out[t, h, 512 + .] = the 32 pairs of q[t, h, dn : dn + 64] rotated by the
+ *                     token's position, as sparse_mla_append rotates a row's
+ * (kv_lora_rank 512, qk_nope 128, 192 or 256: PR #55738 report, the
+ * `_is_masked_mha_available` geometry table).  fp32 accumulation on the tcgen05
+ * tensor cores, out rounded to bf16: the q of sparse_mla_fwd.
+ *   q           device, [T, h, dn + 64] bf16, 16-byte aligned
+ *   w           device, [h, dn, 512] bf16: row d of head h holds what nope dim d
+ *               adds to the 512 latent dims (the key rows of the up-projection
+ *               as they are stored); 16-byte aligned
+ *   positions   device, [T] int32; -1 marks an unused token (rope dims zero)
+ *   dn          128, 192 or 256 (others: SMLA_ERR_UNSUPPORTED)
+ *   cos_sin, max_pos, interleaved   as in sparse_mla_append
+ *   out         device, [T, h, 576] bf16, caller-owned, 16-byte aligned; must not
+ *               overlap q
+ * A position other than -1 outside [0, max_pos) gives zero rope dims, and the
+ * next sparse_mla_sync_status() returns SMLA_ERR_INDEX_RANGE.  T = 0 is a no-op.
+ * Allocates nothing; asynchronous on `stream`.  Errors: SMLA_ERR_INVALID_ARG for
+ * bad sizes, a null pointer or misalignment; SMLA_ERR_CUDA if a tensor map or the
+ * launch fails; a bounded wait that ran out is reported by
+ * sparse_mla_sync_status().
+ */
+smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positions, int32_t T, int32_t h, int32_t dn,
+                            const float* cos_sin, int32_t max_pos, int32_t interleaved, void* out, void* stream);
+
+/*
  * sparse_mla_fwd_host -- the same forward pass taking HOST buffers for the
  * per-step inputs and outputs, for callers whose q/indices live in host memory.
  * It queues on `stream`: copies of q_host and indices_host into `workspace`,
@@ -337,7 +404,8 @@ smla_status sparse_mla_fwd_host_packed(const void* in_host, const void* kv_cache
  * kernel gave up on a bounded wait since the last call (the device is then
  * synchronised and the barrier words of every merge scratch on it cleared),
  * else SMLA_ERR_INDEX_RANGE if a sparse_mla_fwd_checked launch met a list
- * entry other than -1 outside [0, num_slots), SMLA_ERR_CUDA if the
+ * entry other than -1 outside [0, num_slots) or a sparse_mla_append or
+ * sparse_mla_q_up launch a slot or position out of range, SMLA_ERR_CUDA if the
  * synchronisation failed, SMLA_OK otherwise.  The word is per device, so a
  * report covers every launch on the device since the last read.  Not for the
  * hot path.

@@ -22,6 +22,7 @@ EXPORTED = ("sparse_mla_fwd", "sparse_mla_fwd_ex", "sparse_mla_fwd_checked", "sp
             "sparse_mla_fwd_host", "sparse_mla_fwd_host_packed", "sparse_mla_host_io_layout",
             "sparse_mla_host_workspace_bytes", "sparse_mla_merge",
             "sparse_mla_v_up", "sparse_mla_topk", "sparse_mla_scatter_mask", "sparse_mla_masked_mha",
+            "sparse_mla_append", "sparse_mla_q_up",
             "sparse_mla_sync_status",
             "sparse_mla_launch_info", "sparse_mla_last_error", "sparse_mla_version")
 
@@ -69,6 +70,10 @@ def library() -> ctypes.CDLL:
     lib.sparse_mla_scatter_mask.argtypes = [vp, i32, i32, i64, vp, vp]
     lib.sparse_mla_masked_mha.restype = ctypes.c_int
     lib.sparse_mla_masked_mha.argtypes = [vp, vp, vp, vp, i32, i64, i32, i32, i32, f32, vp, vp, vp]
+    lib.sparse_mla_append.restype = ctypes.c_int
+    lib.sparse_mla_append.argtypes = [vp, i64, vp, vp, i32, vp, i32, i32, vp, f32, vp, i64, i32, vp]
+    lib.sparse_mla_q_up.restype = ctypes.c_int
+    lib.sparse_mla_q_up.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, vp]
     lib.sparse_mla_host_io_layout.restype = ctypes.c_int
     lib.sparse_mla_host_io_layout.argtypes = [i32, i32, i32, vp, vp, vp, vp]
     lib.sparse_mla_fwd_host_packed.restype = ctypes.c_int
@@ -365,6 +370,91 @@ def sparse_mla_masked_mha(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mas
                                              _stream_handle(stream, dev))
     _check(st)
     return out, lse
+
+
+def _positions_and_table(T: int, positions: torch.Tensor, cos_sin: torch.Tensor) -> int:
+    if positions.shape != (T,) or positions.dtype != torch.int32 or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous [{T}] int32 tensor")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != D_QK - D_V or cos_sin.dtype != torch.float32 \
+            or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous [max_pos, 64] fp32 tensor")
+    return int(cos_sin.shape[0])
+
+
+def sparse_mla_append(kv: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor, kv_cache: torch.Tensor,
+                      cos_sin: torch.Tensor, *, norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      interleaved: bool = True, kv_format: str = "bf16", stream=None) -> torch.Tensor:
+    """Write new tokens' rows into the paged latent cache (include/sparse_mla.h): the latent (through
+    its RMS norm when norm_weight is given), the rope dims rotated by their position, as bf16 or fp8
+    rows.  Returns kv_cache, written in place.
+
+    kv [T, 576] bf16, 512 latent then 64 rope dims; rows may lie apart (a slice of a fused
+    projection's output) as long as each is contiguous.  positions and slots [T] int32, slot -1 =
+    write nothing.  cos_sin [max_pos, 64] fp32, 32 cosines then 32 sines a row.  The slots other than
+    -1 must be distinct.  A slot or position out of range writes nothing and makes the next
+    sync_status() raise SMLA_ERR_INDEX_RANGE.
+    """
+    if kv.dim() != 2 or kv.shape[1] != D_QK or kv.dtype != torch.bfloat16:
+        raise ValueError(f"kv must be [T, 576] bf16, got {tuple(kv.shape)} {kv.dtype}")
+    T = int(kv.shape[0])
+    row_stride = int(kv.stride(0)) if T > 1 else D_QK
+    if kv.stride(1) != 1 or row_stride < D_QK or row_stride % 8:
+        raise ValueError(f"kv rows must be contiguous and a multiple of 8 elements (>= 576) apart, "
+                         f"got strides {tuple(kv.stride())}")
+    if slots.shape != (T,) or slots.dtype != torch.int32 or not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous [{T}] int32 tensor")
+    max_pos = _positions_and_table(T, positions, cos_sin)
+    if kv_format not in KV_FORMATS:
+        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
+    row, dtype = (D_QK, torch.bfloat16) if kv_format == "bf16" else (FP8_ROW_BYTES, torch.uint8)
+    if kv_cache.dim() != 2 or kv_cache.shape[1] != row or kv_cache.dtype != dtype or not kv_cache.is_contiguous():
+        raise ValueError(f"{kv_format} kv_cache must be a contiguous [num_slots, {row}] {dtype} tensor, got "
+                         f"{tuple(kv_cache.shape)} {kv_cache.dtype}")
+    tensors = [("kv", kv), ("positions", positions), ("slots", slots), ("kv_cache", kv_cache), ("cos_sin", cos_sin)]
+    if norm_weight is not None:
+        if norm_weight.shape != (D_V,) or norm_weight.dtype != torch.bfloat16 or not norm_weight.is_contiguous():
+            raise ValueError("norm_weight must be a contiguous [512] bf16 tensor")
+        tensors.append(("norm_weight", norm_weight))
+    dev = _device_of(tensors)
+    with _on(dev):
+        st = library().sparse_mla_append(
+            kv.data_ptr(), row_stride, positions.data_ptr(), slots.data_ptr(), T, cos_sin.data_ptr(), max_pos,
+            int(bool(interleaved)), None if norm_weight is None else norm_weight.data_ptr(), float(eps),
+            kv_cache.data_ptr(), int(kv_cache.shape[0]), KV_FORMATS[kv_format], _stream_handle(stream, dev))
+    _check(st)
+    return kv_cache
+
+
+def sparse_mla_q_up(q: torch.Tensor, w: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, *,
+                    interleaved: bool = True, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The queries in the latent space (include/sparse_mla.h): per head the nope dims through w on the
+    tensor cores, the rope dims rotated by the token's position; what sparse_mla_fwd takes as q.
+
+    q [T, h, dn + 64] bf16 (dn = 128, 192 or 256 nope dims, then 64 rope dims), w [h, dn, 512] bf16,
+    positions [T] int32 (-1 = unused token: zero rope dims), cos_sin [max_pos, 64] fp32 as in
+    sparse_mla_append; returns out [T, h, 576] bf16.  Any other position out of range gives zero rope
+    dims and makes the next sync_status() raise SMLA_ERR_INDEX_RANGE.
+    """
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [T, h, dn + 64] bf16 tensor")
+    T, h, d = (int(x) for x in q.shape)
+    dn = d - (D_QK - D_V)
+    if w.shape != (h, dn, D_V) or w.dtype != torch.bfloat16 or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous [{h}, {dn}, 512] bf16 tensor")
+    max_pos = _positions_and_table(T, positions, cos_sin)
+    dev = _device_of((("q", q), ("w", w), ("positions", positions), ("cos_sin", cos_sin)))
+    if out is None:
+        out = torch.empty((T, h, D_QK), dtype=torch.bfloat16, device=dev)
+    else:
+        if out.shape != (T, h, D_QK) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+            raise ValueError("out must be a contiguous [T, h, 576] bf16 tensor")
+        _device_of((("q", q), ("out", out)))
+    with _on(dev):
+        st = library().sparse_mla_q_up(
+            q.data_ptr(), w.data_ptr(), positions.data_ptr(), T, h, dn, cos_sin.data_ptr(), max_pos,
+            int(bool(interleaved)), out.data_ptr(), _stream_handle(stream, dev))
+    _check(st)
+    return out
 
 
 def host_workspace_bytes(T: int, h: int, topk: int) -> int:

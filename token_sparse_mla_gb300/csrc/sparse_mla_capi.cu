@@ -19,6 +19,8 @@
 #include "sparse_mla_v_up.cuh"
 #include "sparse_mla_topk.cuh"
 #include "sparse_mla_masked.cuh"
+#include "sparse_mla_append.cuh"
+#include "sparse_mla_q_up.cuh"
 
 namespace {
 
@@ -81,6 +83,9 @@ cudaError_t set_kernel_attrs() {
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_masked_mha_kernel<192, 256>, smla::MmLayout<192, 256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_masked_mha_kernel<256, 128>, smla::MmLayout<256, 128>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_masked_mha_kernel<256, 256>, smla::MmLayout<256, 256>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<128>, smla::QupLayout<128>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<192>, smla::QupLayout<192>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256>, smla::QupLayout<256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_scatter_mask_kernel, smla::kScatterMaxS / 32 * 4);
     return e;
 }
@@ -586,8 +591,14 @@ smla_status sparse_mla_sync_status(void* stream) {
         }
         if (word & smla::kErrLayout)
             return fail(SMLA_ERR_CUDA, "kernel reported an error (error word 0x%x)", word);
+        if (!(word & smla::kErrIndexRange))
+            return fail(SMLA_ERR_INDEX_RANGE,
+                        "an append or q_up launch met a slot outside [0, num_slots) or a position outside "
+                        "[0, max_pos); those rows were not written (q_up: their rotated part is zero)");
         return fail(SMLA_ERR_INDEX_RANGE,
-                    "a checked launch met list entries other than -1 outside [0, num_slots); they were masked");
+                    "a checked launch met list entries other than -1 outside [0, num_slots); they were masked%s",
+                    (word & smla::kErrRowRange) ? "; an append or q_up launch also met an out-of-range slot or position"
+                                                : "");
     }
     return SMLA_OK;
 }
@@ -893,6 +904,143 @@ smla_status sparse_mla_masked_mha(const void* q, const void* k, const void* v, c
         e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_masked_mha_kernel<256, 256>, tm_q, tm_k, tm_v, tm_o, mp);
     }
     if (e != cudaSuccess) return cuda_fail(e, "masked MHA kernel launch");
+    return SMLA_OK;
+}
+
+
+smla_status sparse_mla_append(const void* kv, int64_t kv_stride, const int32_t* positions, const int32_t* slots,
+                              int32_t T, const float* cos_sin, int32_t max_pos, int32_t interleaved,
+                              const void* norm_weight, float eps, void* kv_cache, int64_t num_slots,
+                              int32_t kv_format, void* stream) {
+    if (T < 0) return fail(SMLA_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+    if (kv_format != SMLA_KV_BF16 && kv_format != SMLA_KV_FP8)
+        return fail(SMLA_ERR_INVALID_ARG, "unknown kv_format %d", kv_format);
+    if (num_slots < 1 || num_slots > 0x7fffffffLL)
+        return fail(SMLA_ERR_INVALID_ARG, "num_slots must be in [1, 2^31-1] (got %lld)", static_cast<long long>(num_slots));
+    if (max_pos < 1) return fail(SMLA_ERR_INVALID_ARG, "max_pos must be >= 1 (got %d)", max_pos);
+    if (T == 0) return SMLA_OK;
+    // kv_stride in elements; a negative or overlapping stride has no use here
+    if (kv_stride < smla::kDQK || kv_stride % 8 != 0)
+        return fail(SMLA_ERR_INVALID_ARG, "kv_stride must be a multiple of 8 and at least 576 (got %lld)",
+                    static_cast<long long>(kv_stride));
+    if (norm_weight != nullptr && !(std::isfinite(eps) && eps >= 0.f))
+        return fail(SMLA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!kv || !positions || !slots || !cos_sin || !kv_cache) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(kv, 16) || !aligned(kv_cache, 16) || !aligned(norm_weight, 16))
+        return fail(SMLA_ERR_INVALID_ARG, "kv, kv_cache and norm_weight must be 16-byte aligned");
+    if (!aligned(positions, 4) || !aligned(slots, 4) || !aligned(cos_sin, 4))
+        return fail(SMLA_ERR_INVALID_ARG, "positions, slots and cos_sin must be 4-byte aligned");
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    smla_status st = device_state(&dev, &ds);
+    if (st != SMLA_OK) return st;
+    smla::AppendParams ap;
+    ap.kv = static_cast<const __nv_bfloat16*>(kv);
+    ap.positions = positions;
+    ap.slots = slots;
+    ap.cos_sin = cos_sin;
+    ap.norm_w = static_cast<const __nv_bfloat16*>(norm_weight);
+    ap.cache = kv_cache;
+    ap.kv_stride = kv_stride;
+    ap.num_slots = num_slots;
+    ap.T = T;
+    ap.max_pos = max_pos;
+    ap.eps = eps;
+    ap.interleaved = interleaved != 0;
+    constexpr int kRows = smla::kAppendThreads / 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(T) + kRows - 1) / kRows), 1, 1);
+    cfg.blockDim = dim3(smla::kAppendThreads, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = kv_format == SMLA_KV_FP8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_append_kernel<1>, ap)
+                                                   : cudaLaunchKernelEx(&cfg, smla::sparse_mla_append_kernel<0>, ap);
+    if (e != cudaSuccess) return cuda_fail(e, "append kernel launch");
+    return SMLA_OK;
+}
+
+
+smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positions, int32_t T, int32_t h, int32_t dn,
+                            const float* cos_sin, int32_t max_pos, int32_t interleaved, void* out, void* stream) {
+    if (T < 0 || h < 1) return fail(SMLA_ERR_INVALID_ARG, "T must be >= 0 and h >= 1 (got %d, %d)", T, h);
+    if (!(dn == 128 || dn == 192 || dn == 256))
+        return fail(SMLA_ERR_UNSUPPORTED, "nope dims must be 128, 192 or 256 (got %d)", dn);
+    if (max_pos < 1) return fail(SMLA_ERR_INVALID_ARG, "max_pos must be >= 1 (got %d)", max_pos);
+    if (T == 0) return SMLA_OK;
+    if (!q || !w || !positions || !cos_sin || !out) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(q, 16) || !aligned(w, 16) || !aligned(out, 16))
+        return fail(SMLA_ERR_INVALID_ARG, "q, w and out must be 16-byte aligned");
+    if (!aligned(positions, 4) || !aligned(cos_sin, 4))
+        return fail(SMLA_ERR_INVALID_ARG, "positions and cos_sin must be 4-byte aligned");
+    if (static_cast<int64_t>(T) * h > 0x7fffffffLL || static_cast<int64_t>(h) * smla::kQupSlices > 0x7fffffffLL)
+        return fail(SMLA_ERR_INVALID_ARG, "T * h too large (%d, %d)", T, h);
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    smla_status st = device_state(&dev, &ds);
+    if (st != SMLA_OK) return st;
+    EncodeTiledFn enc = nullptr;
+    if ((st = encode_fn(&enc)) != SMLA_OK) return st;
+    // q [T, h, dn + 64] and out [T, h, 576]: boxes of 128 tokens x 64 dims of one head;
+    // w [h, dn, 512]: a 64-dim column panel of all dn rows
+    alignas(64) CUtensorMap tm_q;
+    alignas(64) CUtensorMap tm_w;
+    alignas(64) CUtensorMap tm_o;
+    auto make = [&](CUtensorMap* tm, const void* base, int64_t d0, int64_t d1, int64_t d2, uint32_t b1, uint32_t b2) -> CUresult {
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d0) * 2, static_cast<cuuint64_t>(d0) * 2 * static_cast<cuuint64_t>(d1)};
+        const cuuint32_t box[3] = {64, b1, b2};
+        const cuuint32_t es[3] = {1, 1, 1};
+        return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = make(&tm_q, q, dn + 64, h, T, 1, smla::kQupRows);
+    if (r == CUDA_SUCCESS) r = make(&tm_w, w, smla::kDV, dn, h, static_cast<uint32_t>(dn), 1);
+    if (r == CUDA_SUCCESS) r = make(&tm_o, out, smla::kDQK, h, T, 1, smla::kQupRows);
+    if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/w/out failed (%d)", (int)r);
+    smla::QupParams qp;
+    qp.q = static_cast<const __nv_bfloat16*>(q);
+    qp.out = static_cast<__nv_bfloat16*>(out);
+    qp.positions = positions;
+    qp.cos_sin = cos_sin;
+    qp.T = T;
+    qp.h = h;
+    qp.max_pos = max_pos;
+    qp.interleaved = interleaved != 0;
+    qp.mtiles = static_cast<int32_t>((static_cast<int64_t>(T) + smla::kQupRows - 1) / smla::kQupRows);
+    // one CTA per SM: the (head, slice) groups share the SMs, each group's token tiles split
+    // evenly over its CTAs (at least one tile each)
+    const int64_t groups = static_cast<int64_t>(h) * smla::kQupSlices;
+    int64_t cpg = groups >= ds->num_sms ? 1 : ds->num_sms / groups;
+    if (cpg > qp.mtiles) cpg = qp.mtiles;
+    qp.cpg = static_cast<int32_t>(cpg);
+    const int64_t grid = groups * cpg;
+    if (grid > 0x7fffffffLL) return fail(SMLA_ERR_INVALID_ARG, "grid too large");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(smla::kQupThreads, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e;
+    if (dn == 128) {
+        cfg.dynamicSmemBytes = smla::QupLayout<128>::kBytes;
+        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_q_up_kernel<128>, tm_q, tm_w, tm_o, qp);
+    } else if (dn == 192) {
+        cfg.dynamicSmemBytes = smla::QupLayout<192>::kBytes;
+        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_q_up_kernel<192>, tm_q, tm_w, tm_o, qp);
+    } else {
+        cfg.dynamicSmemBytes = smla::QupLayout<256>::kBytes;
+        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_q_up_kernel<256>, tm_q, tm_w, tm_o, qp);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "q_up kernel launch");
     return SMLA_OK;
 }
 

@@ -27,6 +27,7 @@ constexpr uint64_t kDrainLimitNs = 200000000ull;    // draining in-flight work a
 constexpr unsigned int kErrTimeout = 1u;
 constexpr unsigned int kErrLayout = 2u;
 constexpr unsigned int kErrIndexRange = 4u;         // checked mode: an entry other than -1 was invalid
+constexpr unsigned int kErrRowRange = 8u;           // append / q_up: a slot or position was out of range
 
 struct FwdParams {
     const __nv_bfloat16* q;   // [T, h, 576]
