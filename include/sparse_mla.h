@@ -308,7 +308,7 @@ smla_status sparse_mla_masked_mha(const void* q, const void* k, const void* v, c
  *               16-byte aligned
  *   positions   device, [T] int32;  slots  device, [T] int32
  *   cos_sin     device, [max_pos, 64] fp32: row p holds the 32 cosines, then the
- *               32 sines of position p
+ *               32 sines of position p; 16-byte aligned
  *   interleaved nonzero: the pairs are dims (2i, 2i + 1); zero: (i, i + 32)
  *   norm_weight device, [512] bf16, 16-byte aligned, or NULL (no norm; eps is
  *               then ignored)

@@ -121,13 +121,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
 }
 
 // Shared -> global tensor store of one box (bulk-group completion: commit, then wait).
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(m)),
-                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
-
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2, int c3) {
     asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
                      reinterpret_cast<uint64_t>(m)),
@@ -141,11 +134,6 @@ __device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bul
 // global writes finish on their own).
 __device__ __forceinline__ void bulk_wait_group_read_0() {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
-// The same, but the latest committed group may still be reading.
-__device__ __forceinline__ void bulk_wait_group_read_1() {
-    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 
 // 1-D bulk copy global -> shared, completion counted on an mbarrier.

@@ -14,8 +14,8 @@
 // carried into its scale, so the tile reads back as NaN rather than as a finite value.
 //
 // A stream over HBM: 1152 bytes in and 1152 (656) out per token, nothing reused, so one warp per
-// token keeps a row in registers and needs no shared memory.  Lane l holds pair l of the rotated
-// part (its cos and sin are then words l and 32 + l of the table row) and 16 latent values: for
+// token keeps a row in registers and needs no shared memory.  Lane l holds word l of the rotated
+// part (and words l and 32 + l of the table row) and 16 latent values: for
 // bf16 rows dims [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8), so that each 16-byte instruction covers
 // 512 contiguous bytes of the row; for fp8 rows dims [16l, 16l + 16), so that a scale tile is 8
 // neighbouring lanes and the codes leave as one 512-byte store.
@@ -70,25 +70,24 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* x) {
                       pack_bf16x2(x[6], x[7]));
 }
 
-// Pair `lane` of a 64-wide rotated part at src, turned by (cos, sin) and stored at dst.  Rounding:
-// each product and the sum are fp32, the result bf16.
-__device__ __forceinline__ uint32_t load_pair(const __nv_bfloat16* src, int lane, bool interleaved) {
-    if (interleaved) return __ldg(reinterpret_cast<const uint32_t*>(src) + lane);
-    const uint16_t* s = reinterpret_cast<const uint16_t*>(src);
-    return static_cast<uint32_t>(__ldg(s + lane)) | (static_cast<uint32_t>(__ldg(s + 32 + lane)) << 16);
-}
-
-__device__ __forceinline__ void store_turned(__nv_bfloat16* dst, uint32_t pair, float cs, float sn, int lane,
-                                             bool interleaved) {
+// A 64-wide rotated part is held by a warp as word `lane` (two neighbouring values) of it and word
+// `lane` of the cosines and of the sines.  Interleaved, a lane's two values are its pair.  Otherwise
+// the partner of values 2l and 2l + 1 sits 16 lanes away and the angles of both lanes' values are
+// words 2 (l % 16) and 2 (l % 16) + 1, fetched by shuffles: two-byte loads and stores of the halves
+// would cost four times the memory instructions.  The whole warp calls it.  Products and sum are
+// fp32, the result is rounded to bf16 once.
+__device__ __forceinline__ uint32_t turn_pair(uint32_t pair, float cs, float sn, int lane, bool interleaved) {
     const float a = __uint_as_float(pair << 16), b = __uint_as_float(pair & 0xFFFF0000u);
-    const uint32_t r = pack_bf16x2(a * cs - b * sn, b * cs + a * sn);
-    if (interleaved) {
-        reinterpret_cast<uint32_t*>(dst)[lane] = r;
-    } else {
-        uint16_t* d = reinterpret_cast<uint16_t*>(dst);
-        d[lane] = static_cast<uint16_t>(r & 0xFFFFu);
-        d[32 + lane] = static_cast<uint16_t>(r >> 16);
+    if (interleaved) return pack_bf16x2(a * cs - b * sn, b * cs + a * sn);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, pair, 16);
+    const int l = 2 * (lane & 15);
+    const float c0 = __shfl_sync(0xffffffffu, cs, l), c1 = __shfl_sync(0xffffffffu, cs, l + 1);
+    float s0 = __shfl_sync(0xffffffffu, sn, l), s1 = __shfl_sync(0xffffffffu, sn, l + 1);
+    if (lane < 16) {
+        s0 = -s0;
+        s1 = -s1;
     }
+    return pack_bf16x2(a * c0 + __uint_as_float(other << 16) * s0, b * c1 + __uint_as_float(other & 0xFFFF0000u) * s1);
 }
 
 // KVF: 0 = bf16 rows, 1 = fp8 rows
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(kAppendThreads) sparse_mla_append_kernel(const
     const int c1 = KVF == 0 ? 32 + lane : 2 * lane + 1;
     const uint4 v0 = ptx::ld_nc_v4(src16 + c0);
     const uint4 v1 = ptx::ld_nc_v4(src16 + c1);
-    const uint32_t pair = load_pair(src + kDV, lane, p.interleaved != 0);
+    const uint32_t pair = __ldg(reinterpret_cast<const uint32_t*>(src + kDV) + lane);
     const float* cs = p.cos_sin + static_cast<int64_t>(pos) * 64;
     const float cosv = __ldg(cs + lane), sinv = __ldg(cs + 32 + lane);
 
@@ -135,12 +134,13 @@ __global__ void __launch_bounds__(kAppendThreads) sparse_mla_append_kernel(const
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
     }
+    const uint32_t turned = turn_pair(pair, cosv, sinv, lane, p.interleaved != 0);
     if constexpr (KVF == 0) {
         __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.cache) + static_cast<int64_t>(slot) * kDQK;
         uint4* row16 = reinterpret_cast<uint4*>(row);
         row16[c0] = pack_bf16x8(x);
         row16[c1] = pack_bf16x8(x + 8);
-        store_turned(row + kDV, pair, cosv, sinv, lane, p.interleaved != 0);
+        reinterpret_cast<uint32_t*>(row + kDV)[lane] = turned;
     } else {
         float amax = fabsf(x[0]);
 #pragma unroll
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kAppendThreads) sparse_mla_append_kernel(const
         uint8_t* row = static_cast<uint8_t*>(p.cache) + static_cast<int64_t>(slot) * kFp8RowBytes;
         reinterpret_cast<uint4*>(row)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
         if ((lane & 7) == 0) reinterpret_cast<float*>(row + kDV)[lane >> 3] = scale;
-        store_turned(reinterpret_cast<__nv_bfloat16*>(row + kDV + 16), pair, cosv, sinv, lane, p.interleaved != 0);
+        reinterpret_cast<uint32_t*>(row + kDV + 16)[lane] = turned;
     }
 }
 

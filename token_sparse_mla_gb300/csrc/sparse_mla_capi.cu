@@ -83,9 +83,12 @@ cudaError_t set_kernel_attrs() {
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_masked_mha_kernel<192, 256>, smla::MmLayout<192, 256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_masked_mha_kernel<256, 128>, smla::MmLayout<256, 128>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_masked_mha_kernel<256, 256>, smla::MmLayout<256, 256>::kBytes);
-    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<128>, smla::QupLayout<128>::kBytes);
-    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<192>, smla::QupLayout<192>::kBytes);
-    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256>, smla::QupLayout<256>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<128, 128>, smla::QupLayout<128, 128>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<128, 512>, smla::QupLayout<128, 512>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<192, 128>, smla::QupLayout<192, 128>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<192, 256>, smla::QupLayout<192, 256>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256, 128>, smla::QupLayout<256, 128>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256, 256>, smla::QupLayout<256, 256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_scatter_mask_kernel, smla::kScatterMaxS / 32 * 4);
     return e;
 }
@@ -928,8 +931,8 @@ smla_status sparse_mla_append(const void* kv, int64_t kv_stride, const int32_t* 
     if (!kv || !positions || !slots || !cos_sin || !kv_cache) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned(kv, 16) || !aligned(kv_cache, 16) || !aligned(norm_weight, 16))
         return fail(SMLA_ERR_INVALID_ARG, "kv, kv_cache and norm_weight must be 16-byte aligned");
-    if (!aligned(positions, 4) || !aligned(slots, 4) || !aligned(cos_sin, 4))
-        return fail(SMLA_ERR_INVALID_ARG, "positions, slots and cos_sin must be 4-byte aligned");
+    if (!aligned(positions, 4) || !aligned(slots, 4) || !aligned(cos_sin, 16))
+        return fail(SMLA_ERR_INVALID_ARG, "positions and slots must be 4-byte and cos_sin 16-byte aligned");
     int dev = 0;
     DeviceState* ds = nullptr;
     smla_status st = device_state(&dev, &ds);
@@ -974,21 +977,19 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
     if (!q || !w || !positions || !cos_sin || !out) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned(q, 16) || !aligned(w, 16) || !aligned(out, 16))
         return fail(SMLA_ERR_INVALID_ARG, "q, w and out must be 16-byte aligned");
-    if (!aligned(positions, 4) || !aligned(cos_sin, 4))
-        return fail(SMLA_ERR_INVALID_ARG, "positions and cos_sin must be 4-byte aligned");
-    if (static_cast<int64_t>(T) * h > 0x7fffffffLL || static_cast<int64_t>(h) * smla::kQupSlices > 0x7fffffffLL)
-        return fail(SMLA_ERR_INVALID_ARG, "T * h too large (%d, %d)", T, h);
+    if (!aligned(positions, 4) || !aligned(cos_sin, 16))
+        return fail(SMLA_ERR_INVALID_ARG, "positions must be 4-byte and cos_sin 16-byte aligned");
+    if (static_cast<int64_t>(T) * h > 0x7fffffffLL) return fail(SMLA_ERR_INVALID_ARG, "T * h too large (%d, %d)", T, h);
     int dev = 0;
     DeviceState* ds = nullptr;
     smla_status st = device_state(&dev, &ds);
     if (st != SMLA_OK) return st;
     EncodeTiledFn enc = nullptr;
     if ((st = encode_fn(&enc)) != SMLA_OK) return st;
-    // q [T, h, dn + 64] and out [T, h, 576]: boxes of 128 tokens x 64 dims of one head;
-    // w [h, dn, 512]: a 64-dim column panel of all dn rows
+    // q [T, h, dn + 64]: boxes of 128 tokens x 64 dims of one head; w [h, dn, 512]: a 64-dim
+    // column panel of all dn rows
     alignas(64) CUtensorMap tm_q;
     alignas(64) CUtensorMap tm_w;
-    alignas(64) CUtensorMap tm_o;
     auto make = [&](CUtensorMap* tm, const void* base, int64_t d0, int64_t d1, int64_t d2, uint32_t b1, uint32_t b2) -> CUresult {
         const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
         const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d0) * 2, static_cast<cuuint64_t>(d0) * 2 * static_cast<cuuint64_t>(d1)};
@@ -1000,8 +1001,7 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
     };
     CUresult r = make(&tm_q, q, dn + 64, h, T, 1, smla::kQupRows);
     if (r == CUDA_SUCCESS) r = make(&tm_w, w, smla::kDV, dn, h, static_cast<uint32_t>(dn), 1);
-    if (r == CUDA_SUCCESS) r = make(&tm_o, out, smla::kDQK, h, T, 1, smla::kQupRows);
-    if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/w/out failed (%d)", (int)r);
+    if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/w failed (%d)", (int)r);
     smla::QupParams qp;
     qp.q = static_cast<const __nv_bfloat16*>(q);
     qp.out = static_cast<__nv_bfloat16*>(out);
@@ -1012,16 +1012,14 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
     qp.max_pos = max_pos;
     qp.interleaved = interleaved != 0;
     qp.mtiles = static_cast<int32_t>((static_cast<int64_t>(T) + smla::kQupRows - 1) / smla::kQupRows);
-    // one CTA per SM: the (head, slice) groups share the SMs, each group's token tiles split
-    // evenly over its CTAs (at least one tile each)
-    const int64_t groups = static_cast<int64_t>(h) * smla::kQupSlices;
-    int64_t cpg = groups >= ds->num_sms ? 1 : ds->num_sms / groups;
-    if (cpg > qp.mtiles) cpg = qp.mtiles;
-    qp.cpg = static_cast<int32_t>(cpg);
-    const int64_t grid = groups * cpg;
-    if (grid > 0x7fffffffLL) return fail(SMLA_ERR_INVALID_ARG, "grid too large");
+    // wide slices (q read once or twice) once a head's tiles fill the SMs, 128-dim slices below that
+    const int wide = dn == 128 ? 512 : 256;
+    qp.items = static_cast<int64_t>(h) * qp.mtiles;
+    const int ns = qp.items * (smla::kDV / wide) >= ds->num_sms ? wide : 128;
+    const int slices = smla::kDV / ns;
+    const int64_t runs = qp.items < ds->num_sms / slices ? qp.items : ds->num_sms / slices;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(runs * slices), 1, 1);
     cfg.blockDim = dim3(smla::kQupThreads, 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
@@ -1030,16 +1028,16 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e;
-    if (dn == 128) {
-        cfg.dynamicSmemBytes = smla::QupLayout<128>::kBytes;
-        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_q_up_kernel<128>, tm_q, tm_w, tm_o, qp);
-    } else if (dn == 192) {
-        cfg.dynamicSmemBytes = smla::QupLayout<192>::kBytes;
-        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_q_up_kernel<192>, tm_q, tm_w, tm_o, qp);
-    } else {
-        cfg.dynamicSmemBytes = smla::QupLayout<256>::kBytes;
-        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_q_up_kernel<256>, tm_q, tm_w, tm_o, qp);
-    }
+    auto go = [&](auto kernel, int bytes) {
+        cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
+        e = cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_w, qp);
+    };
+    if (dn == 128 && ns == 128) go(smla::sparse_mla_q_up_kernel<128, 128>, smla::QupLayout<128, 128>::kBytes);
+    else if (dn == 128) go(smla::sparse_mla_q_up_kernel<128, 512>, smla::QupLayout<128, 512>::kBytes);
+    else if (dn == 192 && ns == 128) go(smla::sparse_mla_q_up_kernel<192, 128>, smla::QupLayout<192, 128>::kBytes);
+    else if (dn == 192) go(smla::sparse_mla_q_up_kernel<192, 256>, smla::QupLayout<192, 256>::kBytes);
+    else if (ns == 128) go(smla::sparse_mla_q_up_kernel<256, 128>, smla::QupLayout<256, 128>::kBytes);
+    else go(smla::sparse_mla_q_up_kernel<256, 256>, smla::QupLayout<256, 256>::kBytes);
     if (e != cudaSuccess) return cuda_fail(e, "q_up kernel launch");
     return SMLA_OK;
 }

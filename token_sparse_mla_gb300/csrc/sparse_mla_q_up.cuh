@@ -10,18 +10,23 @@
 //
 // Writing the result is what it cannot avoid: 1152 bytes out and 2 (DN + 64) in per (token, head)
 // against 1024 DN flops, so at the measured rates the products take about a third of the stores'
-// time.  A GEMM per head: M = 128 tokens, N = 128 latent dims, K = DN.  Each CTA owns one (head,
-// 128-dim slice) and a contiguous run of 128-token tiles; its slice of W stays in shared memory as
-// the MN-major operand, token panels stream through a TMA ring, the fp32 accumulator is double
-// buffered in TMEM, and the rounded tile leaves through shared memory and a TMA store (rows are
-// 1152 * h bytes apart: direct stores touch a line per lane).  The rotated dims ride along: the four
-// slices of a head take 32 tokens of each tile each, on warps of their own.
+// time.  A GEMM per head: M = 128 tokens, K = DN, and a slice of NS latent dims per CTA whose part of
+// W stays in shared memory as the MN-major operand, while token panels stream through a TMA ring.
+// The wider the slice, the fewer times q is read (512 / NS) and the fewer CTAs share a head's tile:
+//   NS = 512 (DN 128) or 256 (DN 192, 256, where 512 dims of W do not fit)   once the tiles fill the SMs
+//   NS = 128                                                                 below that, for latency
+// The (head, token tile) items are dealt in equal contiguous runs, one CTA per SM; the CTAs of a
+// run's slices go through it side by side, so that q leaves HBM once, and a run that crosses into
+// another head reloads W.  The fp32 accumulators are four TMEM buffers of 128 dims, taken in turn.
+// A warp of the epilogue stages 64 dims of its 32 tokens in its own piece
+// of shared memory and stores them as whole 128-byte lines (a row per lane would touch 32 lines per
+// instruction), so no barrier joins the epilogue's warps.
 //
-// Roles (320 threads):
-//   warp 0      TMA producer (one thread): the W slice, then the token panels into the ring.
-//   warp 1      MMA issuer (one thread) and TMEM owner.
-//   warps 2-5   epilogue: TMEM lane quadrant -> bf16 -> shared memory -> TMA store.
-//   warps 6-9   the rotated dims of this slice's quarter of the tile, eight tokens a warp.
+// Roles (448 threads):
+//   warp 0       TMA producer (one thread): slices of W, token panels into the ring.
+//   warp 1       MMA issuer (one thread) and TMEM owner.
+//   warps 2-9    epilogue: two warps per TMEM lane quadrant, every other accumulator each.
+//   warps 10-13  the rotated dims of this slice's share of the tile, up to 16 tokens at a time.
 // Every wait is bounded; a CTA that gives up drains its copies and MMAs before it leaves.
 #pragma once
 
@@ -30,36 +35,46 @@
 namespace smla {
 
 constexpr int kQupRows = 128;                    // tokens per tile (MMA M)
-constexpr int kQupN = 128;                       // latent dims per CTA (MMA N)
-constexpr int kQupSlices = kDV / kQupN;          // CTA slices per head
-constexpr int kQupStages = 5;                    // 80 KB of q in flight
+constexpr int kQupN = 128;                       // latent dims per accumulator (MMA N)
+constexpr int kQupAcc = 4;                       // accumulators in TMEM
 constexpr int kQupPanelBytes = kQupRows * 128;   // 128 tokens x 64 bf16, SW128
-constexpr int kQupThreads = 320;
-constexpr int kQupTmemCols = 2 * kQupN;
+constexpr int kQupEpiWarps = 8;
+constexpr int kQupRopeWarps = 4;
+constexpr int kQupThreads = 64 + 32 * (kQupEpiWarps + kQupRopeWarps);
+constexpr int kQupMaxStages = 6;
 
-template <int DN>
+template <int DN, int NS>
 struct QupLayout {
     static_assert(DN == 128 || DN == 192 || DN == 256, "nope dims");
+    static_assert(NS == 128 || NS == 256 || NS == 512, "slice width");
     static constexpr int kPanelsK = DN / 64;
+    static constexpr int kSlices = kDV / NS;
+    static constexpr int kChunks = NS / kQupN;
     static constexpr int kWPanel = DN * 128;                                   // [DN k][64 n], SW128
-    static constexpr int kOffW = 0;                                            // two panels
-    static constexpr int kOffA = kOffW + 2 * kWPanel;
-    static constexpr int kOffOut = kOffA + kQupStages * kQupPanelBytes;        // [2 buffers][2 panels][128 t][64 n]
-    static constexpr int kOffBar = kOffOut + 4 * kQupPanelBytes;
-    static constexpr int kNumBars = 1 + 2 * kQupStages + 4 + 1;
+    static constexpr int kWBytes = (NS / 64) * kWPanel;
+    static constexpr int kOutBytes = kQupEpiWarps * 32 * 128;                  // 32 tokens x 64 dims per warp
+    static constexpr int kFit = (232448 - 256 - kWBytes - kOutBytes) / kQupPanelBytes;
+    static constexpr int kStages = kFit < kQupMaxStages ? kFit : kQupMaxStages;
+    static constexpr int kOffW = 0;
+    static constexpr int kOffA = kOffW + kWBytes;
+    static constexpr int kOffOut = kOffA + kStages * kQupPanelBytes;
+    static constexpr int kOffBar = kOffOut + kOutBytes;
+    static constexpr int kNumBars = 2 + 2 * kQupMaxStages + 2 * kQupAcc + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;                    // tmem base, abort flag
     static constexpr int kBytes = kOffMisc + 16;
+    static_assert(kStages >= kPanelsK, "a tile's panels are all in the ring while its accumulators are formed");
     static_assert(kOffA % 1024 == 0 && kOffOut % 1024 == 0, "swizzled operands need 1 KB alignment");
     static_assert(kBytes <= 232448, "shared memory budget (227 KB)");
 };
 
 enum : int {
-    kQbW = 0,
-    kQbFull = 1,                            // +stage
-    kQbEmpty = 1 + kQupStages,              // +stage
-    kQbAccFull = 1 + 2 * kQupStages,        // +buffer
-    kQbAccEmpty = 3 + 2 * kQupStages,       // +buffer
-    kQbDrain = 5 + 2 * kQupStages
+    kQbWFull = 0,
+    kQbWEmpty = 1,                             // the MMAs of a slice are done with its W
+    kQbFull = 2,                               // +stage
+    kQbEmpty = 2 + kQupMaxStages,              // +stage
+    kQbAccFull = 2 + 2 * kQupMaxStages,        // +buffer
+    kQbAccEmpty = kQbAccFull + kQupAcc,        // +buffer
+    kQbDrain = kQbAccEmpty + kQupAcc
 };
 
 struct QupParams {
@@ -67,17 +82,102 @@ struct QupParams {
     __nv_bfloat16* out;          // [T, h, 576]
     const int32_t* positions;    // [T]
     const float* cos_sin;        // [max_pos][64]
+    int64_t items;               // h * mtiles
     int32_t T, h;
     int32_t max_pos, interleaved;
-    int32_t cpg;                 // CTAs per (head, slice)
     int32_t mtiles;              // ceil(T / 128)
 };
 
-template <int DN>
+// Eight of a token's 64 rotated values (lane l of eight: values 8l .. 8l + 7) turned.  cs and sn are
+// words 4l .. 4l + 3 of the table's cosines and sines.  Interleaved, those are the angles of the
+// lane's four pairs.  Otherwise the partner values sit four lanes away and the lane's eight angles
+// are its own four and that lane's, the lower ones with the lower of the two.  The whole warp calls.
+template <bool INTER>
+__device__ __forceinline__ uint4 turn_eight(const uint4 x, const float4 cs, const float4 sn, int lane) {
+    float a[8];
+    unpack_bf16x8(x, a);
+    float y[8];
+    const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};
+    if constexpr (INTER) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[2 * i] = a[2 * i] * c[i] - a[2 * i + 1] * s[i];
+            y[2 * i + 1] = a[2 * i + 1] * c[i] + a[2 * i] * s[i];
+        }
+    } else {
+        const uint4 xo = make_uint4(__shfl_xor_sync(0xffffffffu, x.x, 4), __shfl_xor_sync(0xffffffffu, x.y, 4),
+                                    __shfl_xor_sync(0xffffffffu, x.z, 4), __shfl_xor_sync(0xffffffffu, x.w, 4));
+        float o[8];
+        unpack_bf16x8(xo, o);
+        // angles 8 (l % 4) .. + 7 lie in words 4 l' .. of lanes l' = 2 (l % 4) and l' + 1
+        const int src = (lane & 24) + 2 * (lane & 3);
+        const float sign = (lane & 4) ? 1.f : -1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float ci = __shfl_sync(0xffffffffu, c[i & 3], src + (i >> 2));
+            const float si = __shfl_sync(0xffffffffu, s[i & 3], src + (i >> 2));
+            y[i] = a[i] * ci + sign * (o[i] * si);
+        }
+    }
+    return pack_bf16x8(y);
+}
+
+// The rotated dims of this CTA's items, on warp rw of kQupRopeWarps.  Eight lanes per token, 16 bytes
+// each (a pair per lane spent 4 us on a pass of 16 tokens, in the latency of its instructions), and
+// up to 16 tokens' loads in flight; their positions are loaded an item ahead, one per lane.  Loads
+// have no branch -- an unused token reads row 0 of the table, a token past the last reads the last
+// one's -- because a conditional load made each token wait for its own.
+template <int DN, int SLICES, bool INTER>
+__device__ __forceinline__ void turn_items(const QupParams& p, int nh, int hh, int j, int nt, int rw, int lane) {
+    constexpr int kOwn = kQupRows / SLICES / kQupRopeWarps;  // tokens of an item per warp: 8, 16 or 32
+    constexpr int kPer = kOwn < 16 ? kOwn : 16;
+    const int tok = lane >> 3, l8 = lane & 7;
+    auto first = [&](int jj) -> int64_t { return static_cast<int64_t>(jj) * kQupRows + (nh * kQupRopeWarps + rw) * kOwn; };
+    auto load_pos = [&](int jj) -> int {
+        const int64_t t = first(jj) + lane;
+        return lane < kOwn && t < p.T ? __ldg(p.positions + t) : -1;
+    };
+    int next = nt > 0 ? load_pos(j) : -1;
+    for (int i = 0; i < nt; ++i, hh += j == 0) {
+        const int64_t t0 = first(j);
+        const int mine = next;
+        if (++j == p.mtiles) j = 0;
+        if (i + 1 < nt) next = load_pos(j);
+        const bool bad = mine != -1 && (mine < 0 || mine >= p.max_pos);
+        if (bad) atomicOr(&g_smla_error, kErrRowRange);
+        const int good = bad ? -1 : mine;
+#pragma unroll 1
+        for (int u = 0; u < kOwn; u += kPer) {
+            uint4 x[kPer / 4], cs[kPer / 4], sn[kPer / 4];
+#pragma unroll
+            for (int e = 0; e < kPer / 4; ++e) {
+                const int pos = max(__shfl_sync(0xffffffffu, good, u + 4 * e + tok), 0);
+                const int64_t t = min(t0 + u + 4 * e + tok, static_cast<int64_t>(p.T) - 1);
+                x[e] = ptx::ld_nc_v4(p.q + (t * p.h + hh) * (DN + 64) + DN + 8 * l8);
+                cs[e] = ptx::ld_nc_v4(p.cos_sin + static_cast<int64_t>(pos) * 64 + 4 * l8);
+                sn[e] = ptx::ld_nc_v4(p.cos_sin + static_cast<int64_t>(pos) * 64 + 32 + 4 * l8);
+            }
+#pragma unroll
+            for (int e = 0; e < kPer / 4; ++e) {
+                const bool used = __shfl_sync(0xffffffffu, good, u + 4 * e + tok) >= 0;
+                const float4 c4 = make_float4(__uint_as_float(cs[e].x), __uint_as_float(cs[e].y), __uint_as_float(cs[e].z),
+                                              __uint_as_float(cs[e].w));
+                const float4 s4 = make_float4(__uint_as_float(sn[e].x), __uint_as_float(sn[e].y), __uint_as_float(sn[e].z),
+                                              __uint_as_float(sn[e].w));
+                uint4 r = turn_eight<INTER>(x[e], c4, s4, lane);
+                if (!used) r = make_uint4(0u, 0u, 0u, 0u);
+                const int64_t t = t0 + u + 4 * e + tok;
+                if (t < p.T) __stcs(reinterpret_cast<uint4*>(p.out + (t * p.h + hh) * kDQK + kDV) + l8, r);
+            }
+        }
+    }
+}
+
+template <int DN, int NS>
 __global__ void __launch_bounds__(kQupThreads, 1)
     sparse_mla_q_up_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_w,
-                           const __grid_constant__ CUtensorMap tm_o, const QupParams p) {
-    using L = QupLayout<DN>;
+                           const QupParams p) {
+    using L = QupLayout<DN, NS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = ptx::smem_u32(smem);
     if (sbase & 1023u) {  // uniform across the grid: every CTA leaves before any barrier
@@ -92,22 +192,24 @@ __global__ void __launch_bounds__(kQupThreads, 1)
         return ptx::mbar_wait(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
     };
 
-    // this CTA: group g = (head hh, slice nh) and token tiles [j0, j1)
-    const int g = static_cast<int>(blockIdx.x) / p.cpg;
-    const int kc = static_cast<int>(blockIdx.x) % p.cpg;
-    const int hh = g / kQupSlices, nh = g % kQupSlices;
-    const int j0 = static_cast<int>(static_cast<int64_t>(kc) * p.mtiles / p.cpg);
-    const int j1 = static_cast<int>(static_cast<int64_t>(kc + 1) * p.mtiles / p.cpg);
-    const int nt = j1 - j0;
+    // this CTA's slice nh and its run of items (head, tile) = head * mtiles + tile; the CTAs of the
+    // other slices have the same run
+    const int nh = static_cast<int>(blockIdx.x) % L::kSlices;
+    const int64_t run = blockIdx.x / L::kSlices, runs = gridDim.x / L::kSlices;
+    const int64_t i0 = p.items * run / runs;
+    const int nt = static_cast<int>(p.items * (run + 1) / runs - i0);
+    const int h0 = static_cast<int>(i0 / p.mtiles);
+    const int j0 = static_cast<int>(i0 % p.mtiles);
 
     if (threadIdx.x == 0) {
         *sAbort = 0;
-        ptx::mbar_init(bar(kQbW), 1);
-        for (int s = 0; s < kQupStages; ++s) {
+        ptx::mbar_init(bar(kQbWFull), 1);
+        ptx::mbar_init(bar(kQbWEmpty), 1);
+        for (int s = 0; s < L::kStages; ++s) {
             ptx::mbar_init(bar(kQbFull + s), 1);
             ptx::mbar_init(bar(kQbEmpty + s), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kQupAcc; ++b) {
             ptx::mbar_init(bar(kQbAccFull + b), 1);
             ptx::mbar_init(bar(kQbAccEmpty + b), 4);
         }
@@ -115,7 +217,7 @@ __global__ void __launch_bounds__(kQupThreads, 1)
         ptx::fence_mbarrier_init();
     }
     if (warp == 1) {
-        ptx::tmem_alloc(sbase + L::kOffMisc, kQupTmemCols);
+        ptx::tmem_alloc(sbase + L::kOffMisc, kQupAcc * kQupN);
         ptx::tmem_relinquish();
     }
     // launched as a programmatic dependent: q may be the previous launch's output
@@ -131,140 +233,152 @@ __global__ void __launch_bounds__(kQupThreads, 1)
         if (lane == 0 && nt > 0) {
             ptx::prefetch_tmap(&tm_q);
             ptx::prefetch_tmap(&tm_w);
-            ptx::mbar_arrive_expect_tx(bar(kQbW), static_cast<uint32_t>(2 * L::kWPanel));
-            for (int i = 0; i < 2; ++i)
-                ptx::tma_load_3d(sbase + L::kOffW + i * L::kWPanel, &tm_w, kQupN * nh + 64 * i, 0, hh, bar(kQbW));
-            int it = 0;
+            int it = 0, nw = 0;
             bool ok = true;
-            for (int j = j0; j < j1 && ok; ++j) {
+            int hh = h0, j = j0;
+            for (int i = 0; i < nt && ok; ++i) {
+                if (i == 0 || j == 0) {  // a head begins: its W, once the last one's MMAs are done
+                    if (nw > 0 && !(ok = wait(kQbWEmpty, (nw - 1) & 1))) break;
+                    ptx::mbar_arrive_expect_tx(bar(kQbWFull), static_cast<uint32_t>(L::kWBytes));
+                    for (int n = 0; n < NS / 64; ++n)
+                        ptx::tma_load_3d(sbase + L::kOffW + n * L::kWPanel, &tm_w, NS * nh + 64 * n, 0, hh, bar(kQbWFull));
+                    ++nw;
+                }
                 for (int pn = 0; pn < L::kPanelsK; ++pn) {
-                    const int s = it % kQupStages;
-                    if (it >= kQupStages && !(ok = wait(kQbEmpty + s, ((it / kQupStages) - 1) & 1))) break;
+                    const int s = it % L::kStages;
+                    if (it >= L::kStages && !(ok = wait(kQbEmpty + s, ((it / L::kStages) - 1) & 1))) break;
                     ptx::mbar_arrive_expect_tx(bar(kQbFull + s), static_cast<uint32_t>(kQupPanelBytes));
                     ptx::tma_load_3d(sbase + L::kOffA + s * kQupPanelBytes, &tm_q, 64 * pn, hh, kQupRows * j,
                                      bar(kQbFull + s));
                     ++it;
                 }
+                if (++j == p.mtiles) {
+                    j = 0;
+                    ++hh;
+                }
             }
-            // no copy may still be landing when the CTA leaves: W and the ring's last loads
-            ptx::mbar_wait(bar(kQbW), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
-            for (int i = it - (it < kQupStages ? it : kQupStages); i < it; ++i)
-                ptx::mbar_wait(bar(kQbFull + i % kQupStages), (i / kQupStages) & 1, nullptr, &g_smla_error, 0u,
+            // no copy may still be landing when the CTA leaves: the last W and the ring's last loads
+            ptx::mbar_wait(bar(kQbWFull), (nw - 1) & 1, nullptr, &g_smla_error, 0u, kDrainLimitNs);
+            for (int i = it - (it < L::kStages ? it : L::kStages); i < it; ++i)
+                ptx::mbar_wait(bar(kQbFull + i % L::kStages), (i / L::kStages) & 1, nullptr, &g_smla_error, 0u,
                                kDrainLimitNs);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ================================================================ MMA issuer
-        // A: 16 tokens' worth of k is 32 bytes of a K-major panel; B: 16 k rows are 2048 bytes of
-        // the MN-major panels, whose 64-dim halves lie one panel apart (the descriptor's leading
-        // offset)
+        // A: 16 k are 32 bytes of a K-major panel; B: 16 k rows are 2048 bytes of the MN-major
+        // panels, whose 64-dim halves lie one panel apart (the descriptor's leading offset).  A
+        // tile's panels serve all of the slice's accumulators; the last one releases them.
         if (lane == 0 && nt > 0) {
             constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kQupRows, kQupN, 0, 1);
             const uint64_t dw = ptx::smem_desc_sw128(sbase + L::kOffW, L::kWPanel, 1024);
             const uint64_t da = ptx::smem_desc_sw128(sbase + L::kOffA, 16, 1024);
-            bool ok = wait(kQbW, 0);
-            int it = 0;
-            for (int jj = 0; jj < nt && ok; ++jj) {
-                const int buf = jj & 1;
-                if (jj >= 2 && !(ok = wait(kQbAccEmpty + buf, ((jj >> 1) - 1) & 1))) break;
-                ptx::tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(buf * kQupN);
-                for (int pn = 0; pn < L::kPanelsK; ++pn, ++it) {
-                    const int s = it % kQupStages;
-                    if (!(ok = wait(kQbFull + s, (it / kQupStages) & 1))) break;
-                    ptx::tc_fence_after();
-                    const uint64_t a0 = da + static_cast<uint64_t>((s * kQupPanelBytes) >> 4);
-                    const uint64_t b0 = dw + static_cast<uint64_t>((pn * 64 * 128) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_bf16_ss(d, a0 + ((kk * 32) >> 4), b0 + ((kk * 2048) >> 4), kIdesc, (pn | kk) != 0);
-                    ptx::mma_commit(bar(kQbEmpty + s));
+            bool ok = true;
+            int it = 0, nw = 0, ac = 0;
+            int j = j0;
+            for (int i = 0; i < nt && ok; ++i) {
+                if (i == 0 || j == 0) {
+                    if (nw > 0) ptx::mma_commit(bar(kQbWEmpty));
+                    if (!(ok = wait(kQbWFull, nw & 1))) break;
+                    ++nw;
                 }
-                if (!ok) break;
-                ptx::mma_commit(bar(kQbAccFull + buf));
+                for (int c = 0; c < L::kChunks && ok; ++c, ++ac) {
+                    const int buf = ac % kQupAcc;
+                    if (ac >= kQupAcc && !(ok = wait(kQbAccEmpty + buf, ((ac / kQupAcc) - 1) & 1))) break;
+                    ptx::tc_fence_after();
+                    const uint32_t d = tmem + static_cast<uint32_t>(buf * kQupN);
+                    for (int pn = 0; pn < L::kPanelsK; ++pn) {
+                        const int s = (it + pn) % L::kStages;
+                        if (c == 0) {
+                            if (!(ok = wait(kQbFull + s, ((it + pn) / L::kStages) & 1))) break;
+                            ptx::tc_fence_after();
+                        }
+                        const uint64_t a0 = da + static_cast<uint64_t>((s * kQupPanelBytes) >> 4);
+                        const uint64_t b0 = dw + static_cast<uint64_t>((2 * c * L::kWPanel + pn * 64 * 128) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_bf16_ss(d, a0 + ((kk * 32) >> 4), b0 + ((kk * 2048) >> 4), kIdesc, (pn | kk) != 0);
+                        if (c == L::kChunks - 1) ptx::mma_commit(bar(kQbEmpty + s));
+                    }
+                    if (ok) ptx::mma_commit(bar(kQbAccFull + buf));
+                }
+                it += L::kPanelsK;
+                if (++j == p.mtiles) j = 0;
             }
             ptx::mma_commit(bar(kQbDrain));
             ptx::mbar_wait(bar(kQbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
         }
         __syncwarp();
-    } else if (warp < 6) {
+    } else if (warp < 2 + kQupEpiWarps) {
         // ================================================================ epilogue
+        // Accumulator ac (counted over the CTA) belongs to the warps of part ac % 2.
         const int quad = warp & 3;  // the TMEM lane quadrant this warp may read
+        const int part = (warp - 2) >> 2;
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-        const int r = quad * 32 + lane;  // token row of the tile
-        const bool elected = warp == 2 && lane == 0;
+        const uint32_t stage = sbase + L::kOffOut + (warp - 2) * 32 * 128;
+        int hh = h0, j = j0;
+        int ac = 0;
         bool ok = true;
-        for (int jj = 0; jj < nt; ++jj) {
-            const int buf = jj & 1;
-            if (lane == 0) ok = wait(kQbAccFull + buf, (jj >> 1) & 1);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            __syncwarp();
-            // the store of tile jj - 2 has read its staging buffer; a warp that gave up takes all out
-            if (elected) ptx::bulk_wait_group_read_1();
-            if (ptx::named_bar_red_or(1, 128, !ok)) break;
-            ptx::tc_fence_after();
-            const uint32_t stage = sbase + L::kOffOut + buf * 2 * kQupPanelBytes + r * 128;
+        for (int i = 0; i < nt && ok; ++i) {
+            const int64_t t0 = static_cast<int64_t>(j) * kQupRows + quad * 32;
+#pragma unroll 1
+            for (int c = 0; c < L::kChunks; ++c, ++ac) {
+                if ((ac & 1) != part) continue;
+                const int buf = ac % kQupAcc;
+                if (lane == 0) ok = wait(kQbAccFull + buf, (ac / kQupAcc) & 1);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                __syncwarp();
+                if (!ok) break;
+                ptx::tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < kQupN / 32; ++c) {
-                uint32_t v[32];
-                SMLA_TMEM_LD16(tmem + lane_base + static_cast<uint32_t>(buf * kQupN + c * 32), v);
-                SMLA_TMEM_LD16(tmem + lane_base + static_cast<uint32_t>(buf * kQupN + c * 32 + 16), v + 16);
-                ptx::tmem_wait_ld();
+                for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t ch = static_cast<uint32_t>((c & 1) * 4 + e);
-                    ptx::st_shared_v4(stage + (c >> 1) * kQupPanelBytes + ((ch ^ static_cast<uint32_t>(r & 7)) << 4),
-                                      pack_bf16x8(reinterpret_cast<const float*>(v) + 8 * e));
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            SMLA_TMEM_LD16(tmem + lane_base + static_cast<uint32_t>(buf * kQupN + half * 64 + q * 32 + e * 16),
+                                           v + 16 * e);
+                        ptx::tmem_wait_ld();
+                        if (half == 1 && q == 1) {
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(bar(kQbAccEmpty + buf));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            ptx::st_shared_v4(stage + lane * 128 + ((static_cast<uint32_t>(4 * q + e) ^ static_cast<uint32_t>(lane & 7)) << 4),
+                                              pack_bf16x8(reinterpret_cast<const float*>(v) + 8 * e));
+                    }
+                    __syncwarp();
+                    // eight lanes store one token's 128 bytes, four tokens per instruction
+                    __nv_bfloat16* dst = p.out + (t0 * p.h + hh) * kDQK + NS * nh + c * kQupN + half * 64 + (lane & 7) * 8;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = 4 * e + (lane >> 3);
+                        const uint4 w = ptx::ld_shared_v4(stage + r * 128 + ((static_cast<uint32_t>(lane & 7) ^ static_cast<uint32_t>(r & 7)) << 4));
+                        if (t0 + r < p.T) __stcs(reinterpret_cast<uint4*>(dst + static_cast<int64_t>(r) * p.h * kDQK), w);
+                    }
+                    __syncwarp();
                 }
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(kQbAccEmpty + buf));
-            ptx::fence_proxy_async_smem();
-            ptx::named_bar_sync(2, 128);
-            if (elected) {  // tokens past the last fall outside the map and are not written
-                for (int i = 0; i < 2; ++i)
-                    ptx::tma_store_3d(&tm_o, sbase + L::kOffOut + (buf * 2 + i) * kQupPanelBytes, kQupN * nh + 64 * i, hh,
-                                      (j0 + jj) * kQupRows);
-                ptx::bulk_commit_group();
+            if (++j == p.mtiles) {
+                j = 0;
+                ++hh;
             }
         }
-        if (elected) ptx::bulk_wait_group_read_0();  // shared memory may not be released before it is read
     } else {
         // ================================================================ the rotated dims
-        constexpr int kPer = 8;  // tokens per warp: their loads are in flight together
-        const bool inter = p.interleaved != 0;
-        for (int j = j0; j < j1; ++j) {
-            const int64_t t0 = static_cast<int64_t>(j) * kQupRows + nh * 32 + (warp - 6) * kPer;
-            if (t0 >= p.T) break;
-            uint32_t pair[kPer];
-            float cs[kPer], sn[kPer];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int64_t t = t0 + i;
-                pair[i] = 0u;
-                cs[i] = sn[i] = 0.f;
-                if (t < p.T) {
-                    const int pos = __ldg(p.positions + t);
-                    if (pos >= 0 && pos < p.max_pos) {
-                        pair[i] = load_pair(p.q + (t * p.h + hh) * (DN + 64) + DN, lane, inter);
-                        cs[i] = __ldg(p.cos_sin + static_cast<int64_t>(pos) * 64 + lane);
-                        sn[i] = __ldg(p.cos_sin + static_cast<int64_t>(pos) * 64 + 32 + lane);
-                    } else if (pos != -1 && lane == 0) {
-                        atomicOr(&g_smla_error, kErrRowRange);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (t0 + i < p.T) store_turned(p.out + ((t0 + i) * p.h + hh) * kDQK + kDV, pair[i], cs[i], sn[i], lane, inter);
-        }
+        if (p.interleaved != 0)
+            turn_items<DN, L::kSlices, true>(p, nh, h0, j0, nt, warp - 2 - kQupEpiWarps, lane);
+        else
+            turn_items<DN, L::kSlices, false>(p, nh, h0, j0, nt, warp - 2 - kQupEpiWarps, lane);
     }
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, kQupTmemCols);
+        ptx::tmem_dealloc(tmem, kQupAcc * kQupN);
     }
 }
 
