@@ -17,7 +17,8 @@
  * sparse_mla_v_up applies the per-head value up-projection to O, and
  * sparse_mla_topk builds the index lists from per-position scores.
  * sparse_mla_append writes new tokens' rows into the cache, and
- * sparse_mla_q_up brings their queries into its space.
+ * sparse_mla_q_up brings their queries into its space, and sparse_mla_prefix is
+ * the attention over rows that a whole batch shares.
  *
  * Sources (page title, section):
  *   vLLM PR #60220 "FlashMLA sparse: stage fp8 mixed-batch q/out in the
@@ -356,6 +357,45 @@ smla_status sparse_mla_append(const void* kv, int64_t kv_stride, const int32_t* 
  */
 smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positions, int32_t T, int32_t h, int32_t dn,
                             const float* cos_sin, int32_t max_pos, int32_t interleaved, void* out, void* stream);
+
+/*
+ * sparse_mla_prefix -- attention over a prefix that the whole batch shares (a
+ * system prompt, a document): every token and head attends to the same
+ * prefix_len cache rows, so they are read once for many query rows instead of
+ * once per token's list.  Position i of the prefix is cache slot
+ * block_table[i / 64] * 64 + i % 64 (blocks as in sparse_mla_topk).  Per token
+ * and head
+ *     s_i = scale * <q, kv[slot i, :]>  (576 dims),  O = softmax(s) . kv[slot i, 0:512],
+ *     LSE = ln sum exp(s_i)
+ * in the form that sparse_mla_merge joins with the token's own part (its list
+ * without the prefix, through sparse_mla_fwd).  bf16 products, fp32 softmax and
+ * accumulation on the tcgen05 tensor cores, O rounded to bf16; fp8 rows are
+ * dequantised to bf16 as in sparse_mla_fwd.
+ *   q            device, [T, h, 576] bf16, 16-byte aligned; any h >= 1
+ *   kv_cache     device, num_slots rows as in sparse_mla_fwd, 16-byte aligned
+ *   block_table  device, [ceil(prefix_len / 64)] int32.  An entry outside the
+ *                cache masks its 64 positions, and positions that fall on slots
+ *                >= num_slots are masked
+ *   prefix_len   0 .. 2^31-1.  Rows past it in its last block are not used,
+ *                whatever they hold
+ *   out          device, [T, h, 512] bf16, caller-owned, 16-byte aligned
+ *   lse          device, [T, h] fp32, caller-owned
+ *   workspace    device, at least sparse_mla_prefix_workspace_bytes(T, h,
+ *                prefix_len) bytes, 256-byte aligned, caller-owned; partial
+ *                results of row tiles that several CTAs share.  Calls that may
+ *                overlap in time need workspaces of their own.  NULL when that
+ *                function returns 0 (it asks the current device)
+ * A row whose every position is masked, or prefix_len = 0, gives O = 0 and
+ * LSE = -inf.  Repeated calls with the same arguments give identical bytes.
+ * T = 0 is a no-op.  Allocates nothing; asynchronous on `stream`.  Errors:
+ * SMLA_ERR_INVALID_ARG for bad sizes, format, scale or workspace, a null pointer
+ * or misalignment; SMLA_ERR_CUDA if a tensor map or a launch fails; a bounded
+ * wait that ran out is reported by sparse_mla_sync_status().
+ */
+size_t sparse_mla_prefix_workspace_bytes(int32_t T, int32_t h, int64_t prefix_len);
+smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t* block_table, int32_t T, int32_t h,
+                              int64_t prefix_len, int64_t num_slots, int32_t kv_format, float scale, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * sparse_mla_fwd_host -- the same forward pass taking HOST buffers for the

@@ -13,7 +13,8 @@ returns out [T, h, 512] bf16 and lse [T, h] fp32.  sparse_mla_merge combines
 the (out, lse) of lists split into parts (the DCP merge); sparse_mla_v_up applies the
 per-head value up-projection to out on the tensor cores; sparse_mla_topk builds the
 index lists from per-position scores; sparse_mla_append writes new tokens' rows into the cache
-and sparse_mla_q_up brings their queries into its space; sparse_mla_scatter_mask and sparse_mla_masked_mha are
+and sparse_mla_q_up brings their queries into its space; sparse_mla_prefix is the attention over a
+prefix that the whole batch shares; sparse_mla_scatter_mask and sparse_mla_masked_mha are
 the masked dense route for short prefills (the lists as a bit mask, then dense MHA over per-head
 K and V under that mask).
 """
@@ -33,7 +34,9 @@ from ._binding import (  # noqa: F401
     sparse_mla_fwd_host_packed,
     sparse_mla_fwd_noalloc,
     sparse_mla_masked_mha,
+    prefix_workspace_bytes,
     sparse_mla_merge,
+    sparse_mla_prefix,
     sparse_mla_q_up,
     sparse_mla_scatter_mask,
     sparse_mla_topk,
@@ -57,7 +60,9 @@ __all__ = [
     "sparse_mla_fwd_host_packed",
     "sparse_mla_fwd_noalloc",
     "sparse_mla_masked_mha",
+    "prefix_workspace_bytes",
     "sparse_mla_merge",
+    "sparse_mla_prefix",
     "sparse_mla_q_up",
     "sparse_mla_scatter_mask",
     "sparse_mla_topk",

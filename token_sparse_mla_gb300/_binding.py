@@ -22,7 +22,7 @@ EXPORTED = ("sparse_mla_fwd", "sparse_mla_fwd_ex", "sparse_mla_fwd_checked", "sp
             "sparse_mla_fwd_host", "sparse_mla_fwd_host_packed", "sparse_mla_host_io_layout",
             "sparse_mla_host_workspace_bytes", "sparse_mla_merge",
             "sparse_mla_v_up", "sparse_mla_topk", "sparse_mla_scatter_mask", "sparse_mla_masked_mha",
-            "sparse_mla_append", "sparse_mla_q_up",
+            "sparse_mla_append", "sparse_mla_q_up", "sparse_mla_prefix", "sparse_mla_prefix_workspace_bytes",
             "sparse_mla_sync_status",
             "sparse_mla_launch_info", "sparse_mla_last_error", "sparse_mla_version")
 
@@ -74,6 +74,10 @@ def library() -> ctypes.CDLL:
     lib.sparse_mla_append.argtypes = [vp, i64, vp, vp, i32, vp, i32, i32, vp, f32, vp, i64, i32, vp]
     lib.sparse_mla_q_up.restype = ctypes.c_int
     lib.sparse_mla_q_up.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, vp]
+    lib.sparse_mla_prefix_workspace_bytes.restype = sz
+    lib.sparse_mla_prefix_workspace_bytes.argtypes = [i32, i32, i64]
+    lib.sparse_mla_prefix.restype = ctypes.c_int
+    lib.sparse_mla_prefix.argtypes = [vp, vp, vp, i32, i32, i64, i64, i32, f32, vp, vp, vp, sz, vp]
     lib.sparse_mla_host_io_layout.restype = ctypes.c_int
     lib.sparse_mla_host_io_layout.argtypes = [i32, i32, i32, vp, vp, vp, vp]
     lib.sparse_mla_fwd_host_packed.restype = ctypes.c_int
@@ -455,6 +459,76 @@ def sparse_mla_q_up(q: torch.Tensor, w: torch.Tensor, positions: torch.Tensor, c
             int(bool(interleaved)), out.data_ptr(), _stream_handle(stream, dev))
     _check(st)
     return out
+
+
+def prefix_workspace_bytes(T: int, h: int, prefix_len: int) -> int:
+    """Bytes of workspace that sparse_mla_prefix needs on the current device (0: none)."""
+    return int(library().sparse_mla_prefix_workspace_bytes(T, h, prefix_len))
+
+
+def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, prefix_len: int,
+                      scale: Optional[float] = None, *, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, kv_format: str = "bf16",
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of every token and head over one shared prefix (include/sparse_mla.h), its rows read
+    once for the batch: q [T, h, 576] bf16, kv_cache as in sparse_mla_fwd, block_table
+    [ceil(prefix_len / 64)] int32 (position i is slot block_table[i / 64] * 64 + i % 64).
+
+    Returns out [T, h, 512] bf16 and lse [T, h] fp32, which sparse_mla_merge joins with each token's
+    own part.  scale defaults to 576 ** -0.5.  workspace: a uint8 tensor of prefix_workspace_bytes(T,
+    h, prefix_len) bytes for callers that keep one (calls that may overlap need their own); allocated
+    here otherwise, from torch's allocator on the stream of the call.
+    """
+    if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous [T, h, 576] bf16 tensor, got {tuple(q.shape)} {q.dtype}")
+    T, h = int(q.shape[0]), int(q.shape[1])
+    prefix_len = int(prefix_len)
+    if kv_format not in KV_FORMATS:
+        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
+    row, dtype = (D_QK, torch.bfloat16) if kv_format == "bf16" else (FP8_ROW_BYTES, torch.uint8)
+    if kv_cache.dim() != 2 or kv_cache.shape[1] != row or kv_cache.dtype != dtype or not kv_cache.is_contiguous():
+        raise ValueError(f"{kv_format} kv_cache must be a contiguous [num_slots, {row}] {dtype} tensor, got "
+                         f"{tuple(kv_cache.shape)} {kv_cache.dtype}")
+    if prefix_len < 0 or block_table.dim() != 1 or block_table.dtype != torch.int32 \
+            or block_table.numel() * 64 < prefix_len or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous [ceil(prefix_len / 64)] int32 tensor, prefix_len >= 0")
+    dev = _device_of((("q", q), ("kv_cache", kv_cache), ("block_table", block_table)))
+    if scale is None:
+        scale = D_QK ** -0.5
+    if out is None:
+        out = torch.empty((T, h, D_V), dtype=torch.bfloat16, device=dev)
+    elif out.shape != (T, h, D_V) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [T, h, 512] bf16 tensor")
+    if lse is None:
+        lse = torch.empty((T, h), dtype=torch.float32, device=dev)
+    elif lse.shape != (T, h) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous [T, h] fp32 tensor")
+    _device_of((("q", q), ("out", out), ("lse", lse)))
+    with _on(dev):
+        lib = library()
+        handle = _stream_handle(stream, dev)
+        if workspace is None:
+            need = int(lib.sparse_mla_prefix_workspace_bytes(T, h, prefix_len))
+            if need:
+                workspace = _workspace_on(need, dev, handle)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+        st = lib.sparse_mla_prefix(
+            q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), T, h, prefix_len, int(kv_cache.shape[0]),
+            KV_FORMATS[kv_format], float(scale), out.data_ptr(), lse.data_ptr(),
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+            handle)
+    _check(st)
+    return out, lse
+
+
+def _workspace_on(nbytes: int, dev: torch.device, handle) -> torch.Tensor:
+    """nbytes of scratch for one call on the stream `handle`.  The allocator may hand a freed block to
+    the next request on the stream it was allocated for, so it is allocated for the call's stream."""
+    if handle == torch.cuda.current_stream(dev).cuda_stream:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle or 0, device=dev)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
 def host_workspace_bytes(T: int, h: int, topk: int) -> int:

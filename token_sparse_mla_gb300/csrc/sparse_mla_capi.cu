@@ -21,6 +21,7 @@
 #include "sparse_mla_masked.cuh"
 #include "sparse_mla_append.cuh"
 #include "sparse_mla_q_up.cuh"
+#include "sparse_mla_prefix.cuh"
 
 namespace {
 
@@ -89,6 +90,8 @@ cudaError_t set_kernel_attrs() {
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<192, 256>, smla::QupLayout<192, 256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256, 128>, smla::QupLayout<256, 128>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256, 256>, smla::QupLayout<256, 256>::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_prefix_kernel<0>, smla::PfLayout::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_prefix_kernel<1>, smla::PfLayout::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_scatter_mask_kernel, smla::kScatterMaxS / 32 * 4);
     return e;
 }
@@ -437,6 +440,34 @@ smla_status launch(const void* q, const void* kv, const int32_t* idx, int32_t T,
                 : cudaLaunchKernelEx(&cfg, smla::sparse_mla_fwd_tc_kernel<64, 0>, tm_q, prm);
     if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
     return SMLA_OK;
+}
+
+// How sparse_mla_prefix cuts its work: `work` (row tile, page) blocks in `runs` equal runs, one per
+// CTA pair, and the workspace of the partials of cut tiles (0 if no tile is cut).
+struct PrefixPlan {
+    int64_t rows = 0, tiles = 0, nblk = 0, work = 0;
+    int runs = 0, slot_rows = 0;
+    size_t part_bytes = 0, ml_bytes = 0;
+};
+
+PrefixPlan prefix_plan(int64_t rows, int64_t prefix, int num_sms) {
+    PrefixPlan pl;
+    pl.rows = rows;
+    pl.tiles = (rows + smla::kPfRows - 1) / smla::kPfRows;
+    pl.nblk = (prefix + smla::kPfKeys - 1) / smla::kPfKeys;
+    pl.work = pl.tiles * pl.nblk;
+    if (pl.work == 0) return pl;
+    const int64_t pairs = num_sms / 2;
+    pl.runs = static_cast<int>(pl.work < pairs ? pl.work : pairs);
+    pl.slot_rows = static_cast<int>(rows < smla::kPfRows ? rows : smla::kPfRows);
+    bool cut = false;
+    for (int k = 1; k < pl.runs && !cut; ++k) cut = (pl.work * k / pl.runs) % pl.nblk != 0;
+    if (cut) {
+        const size_t slots = static_cast<size_t>(pl.runs) * 2 * pl.slot_rows;
+        pl.part_bytes = slots * smla::kDV * 4;
+        pl.ml_bytes = slots * 2 * 4;
+    }
+    return pl;
 }
 
 }  // namespace
@@ -1039,6 +1070,127 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
     else if (ns == 128) go(smla::sparse_mla_q_up_kernel<256, 128>, smla::QupLayout<256, 128>::kBytes);
     else go(smla::sparse_mla_q_up_kernel<256, 256>, smla::QupLayout<256, 256>::kBytes);
     if (e != cudaSuccess) return cuda_fail(e, "q_up kernel launch");
+    return SMLA_OK;
+}
+
+
+size_t sparse_mla_prefix_workspace_bytes(int32_t T, int32_t h, int64_t prefix_len) {
+    if (T <= 0 || h <= 0 || prefix_len <= 0) return 0;
+    int num_sms = 152;
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    if (device_state(&dev, &ds) == SMLA_OK) num_sms = ds->num_sms;
+    const PrefixPlan pl = prefix_plan(static_cast<int64_t>(T) * h, prefix_len, num_sms);
+    return pl.part_bytes + pl.ml_bytes;
+}
+
+smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t* block_table, int32_t T, int32_t h,
+                              int64_t prefix_len, int64_t num_slots, int32_t kv_format, float scale, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (T < 0 || h < 1) return fail(SMLA_ERR_INVALID_ARG, "T must be >= 0 and h >= 1 (got %d, %d)", T, h);
+    if (prefix_len < 0 || prefix_len > 0x7fffffffLL)
+        return fail(SMLA_ERR_INVALID_ARG, "prefix_len must be in [0, 2^31-1] (got %lld)", static_cast<long long>(prefix_len));
+    if (num_slots < 1 || num_slots > 0x7fffffffLL)
+        return fail(SMLA_ERR_INVALID_ARG, "num_slots must be in [1, 2^31-1] (got %lld)", static_cast<long long>(num_slots));
+    if (kv_format != SMLA_KV_BF16 && kv_format != SMLA_KV_FP8)
+        return fail(SMLA_ERR_INVALID_ARG, "unknown kv_format %d", kv_format);
+    if (!std::isfinite(scale)) return fail(SMLA_ERR_INVALID_ARG, "scale must be finite");
+    if (T == 0) return SMLA_OK;
+    if (!q || !out || !lse || (prefix_len > 0 && (!kv_cache || !block_table)))
+        return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16))
+        return fail(SMLA_ERR_INVALID_ARG, "q, kv_cache and out must be 16-byte aligned");
+    if (!aligned(block_table, 4) || !aligned(lse, 4))
+        return fail(SMLA_ERR_INVALID_ARG, "block_table and lse must be 4-byte aligned");
+    const int64_t rows = static_cast<int64_t>(T) * h;
+    if (rows > 0x7fffff00LL) return fail(SMLA_ERR_INVALID_ARG, "T * h too large (%d, %d)", T, h);
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    smla_status st = device_state(&dev, &ds);
+    if (st != SMLA_OK) return st;
+    const PrefixPlan pl = prefix_plan(rows, prefix_len, ds->num_sms);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    smla::PfParams pp = {};
+    pp.out = static_cast<__nv_bfloat16*>(out);
+    pp.lse = lse;
+    pp.rows = rows;
+    cudaError_t e;
+    if (prefix_len == 0) {
+        const int64_t want = (rows * (smla::kDV / 8) + 255) / 256, cap = static_cast<int64_t>(ds->num_sms) * 8;
+        cfg.gridDim = dim3(static_cast<unsigned>(want < cap ? want : cap), 1, 1);
+        cfg.blockDim = dim3(256, 1, 1);
+        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_empty_kernel, pp);
+        return e == cudaSuccess ? SMLA_OK : cuda_fail(e, "empty prefix kernel launch");
+    }
+    if (pl.work / pl.runs >= 0x7fffffffLL) return fail(SMLA_ERR_INVALID_ARG, "T * h * prefix_len too large");
+    const size_t need = pl.part_bytes + pl.ml_bytes;
+    if (need > 0) {
+        if (!workspace || !aligned(workspace, 256))
+            return fail(SMLA_ERR_INVALID_ARG, "workspace must be given, 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(SMLA_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, need);
+    }
+    EncodeTiledFn enc = nullptr;
+    if ((st = encode_fn(&enc)) != SMLA_OK) return st;
+    // [n, 576] rows viewed as (64 dims, n, 9 panels): one box lands as SW128 panels one after another
+    alignas(64) CUtensorMap tm_q;
+    alignas(64) CUtensorMap tm_k;
+    alignas(64) CUtensorMap tm_v;
+    auto make = [&](CUtensorMap* tm, const void* base, int64_t n, uint32_t box_rows, uint32_t box_panels) -> CUresult {
+        const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(n), smla::kPanels};
+        const cuuint64_t strides[2] = {smla::kDQK * 2, 128};
+        const cuuint32_t box[3] = {64, box_rows, box_panels};
+        const cuuint32_t es[3] = {1, 1, 1};
+        return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    const bool fp8 = kv_format == SMLA_KV_FP8;
+    CUresult r = make(&tm_q, q, rows, smla::kPfHalf, smla::kPanels);
+    if (fp8) {  // the producers read the rows themselves; the kernel does not touch these maps
+        tm_k = tm_q;
+        tm_v = tm_q;
+    } else {
+        if (r == CUDA_SUCCESS) r = make(&tm_k, kv_cache, num_slots, 32, smla::kPanels);
+        if (r == CUDA_SUCCESS) r = make(&tm_v, kv_cache, num_slots, smla::kPfKeys, 4);
+    }
+    if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/kv_cache failed (%d)", (int)r);
+    pp.kv = kv_cache;
+    pp.pages = block_table;
+    pp.part_o = static_cast<float*>(workspace);
+    pp.part_ml = need > 0 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.part_bytes) : nullptr;
+    pp.prefix = prefix_len;
+    pp.num_slots = num_slots;
+    pp.work = pl.work;
+    pp.nblk = static_cast<int32_t>(pl.nblk);
+    pp.runs = pl.runs;
+    pp.slot_rows = pl.slot_rows;
+    pp.sm_scale_log2 = scale * 1.4426950408889634f;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pl.runs), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(fp8 ? smla::PfRoles<1>::kThreads : smla::PfRoles<0>::kThreads), 1, 1);
+    cfg.dynamicSmemBytes = smla::PfLayout::kBytes;
+    e = fp8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_kernel<1>, tm_q, tm_k, tm_v, pp)
+            : cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_kernel<0>, tm_q, tm_k, tm_v, pp);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
+    if (need > 0) {
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(rows), 1, 1);
+        cfg.blockDim = dim3(smla::kPfMergeThreads, 1, 1);
+        cfg.dynamicSmemBytes = 0;
+        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel, pp);
+        if (e != cudaSuccess) return cuda_fail(e, "prefix merge kernel launch");
+    }
     return SMLA_OK;
 }
 
