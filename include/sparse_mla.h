@@ -381,10 +381,11 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
  *   out          device, [T, h, 512] bf16, caller-owned, 16-byte aligned
  *   lse          device, [T, h] fp32, caller-owned
  *   workspace    device, at least sparse_mla_prefix_workspace_bytes(T, h,
- *                prefix_len) bytes, 256-byte aligned, caller-owned; partial
- *                results of row tiles that several CTAs share.  Calls that may
- *                overlap in time need workspaces of their own.  NULL when that
- *                function returns 0 (it asks the current device)
+ *                prefix_len, kv_format) bytes, 256-byte aligned, caller-owned;
+ *                partial results of row tiles that several CTAs share, and the
+ *                prefix as bf16 rows if the cache is fp8.  Calls that may overlap
+ *                in time need workspaces of their own.  NULL when that function
+ *                returns 0 (it asks the current device)
  * A row whose every position is masked, or prefix_len = 0, gives O = 0 and
  * LSE = -inf.  Repeated calls with the same arguments give identical bytes.
  * T = 0 is a no-op.  Allocates nothing; asynchronous on `stream`.  Errors:
@@ -392,7 +393,7 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
  * or misalignment; SMLA_ERR_CUDA if a tensor map or a launch fails; a bounded
  * wait that ran out is reported by sparse_mla_sync_status().
  */
-size_t sparse_mla_prefix_workspace_bytes(int32_t T, int32_t h, int64_t prefix_len);
+size_t sparse_mla_prefix_workspace_bytes(int32_t T, int32_t h, int64_t prefix_len, int32_t kv_format);
 smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t* block_table, int32_t T, int32_t h,
                               int64_t prefix_len, int64_t num_slots, int32_t kv_format, float scale, void* out,
                               float* lse, void* workspace, size_t workspace_bytes, void* stream);

@@ -74,7 +74,7 @@ def _run(q, cache, pages, P, fmt, scale=SCALE, **kw):
     T, h, _ = q.shape
     guard_o = torch.full((T + 2, h, 512), 2.5, dtype=torch.bfloat16, device=DEV)
     guard_l = torch.full((T + 2, h), 2.5, dtype=torch.float32, device=DEV)
-    need = smla.prefix_workspace_bytes(T, h, P)
+    need = smla.prefix_workspace_bytes(T, h, P, fmt)
     ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN where nothing is written
     out, lse = smla.sparse_mla_prefix(q.to(DEV), cache.to(DEV), pages.to(DEV), P, scale, out=guard_o[1:T + 1],
                                       lse=guard_l[1:T + 1], kv_format=fmt, workspace=ws, **kw)
@@ -85,7 +85,7 @@ def _run(q, cache, pages, P, fmt, scale=SCALE, **kw):
     return out.cpu(), lse.cpu()
 
 
-SHAPES = [(1, 16, 64), (1, 1, 1), (1, 16, 63), (2, 8, 65), (1, 16, 1000), (5, 13, 129), (16, 8, 500), (17, 8, 4096),
+SHAPES = [(1, 16, 64), (1, 1, 1), (1, 16, 63), (2, 8, 65), (1, 16, 1000), (5, 13, 129), (16, 8, 500), (17, 8, 4096), (8, 16, 128), (130, 1, 257),
           (40, 16, 777), (64, 64, 70), (100, 64, 200), (3, 128, 640), (333, 8, 320)]
 
 
@@ -301,12 +301,19 @@ def test_no_tokens_is_a_noop(lib):
 
 def test_workspace_bytes(lib):
     """None where no tile is cut, else two slots of a tile's rows per CTA pair (152 SMs assumed without
-    a device)."""
+    a device), rounded up to 256 bytes."""
+
+    def partials(runs, rows):
+        return -(-2 * runs * rows * 514 * 4 // 256) * 256
+
     assert smla.prefix_workspace_bytes(0, 8, 100) == 0 and smla.prefix_workspace_bytes(1, 8, 0) == 0
-    assert smla.prefix_workspace_bytes(1, 8, 64) == 0
-    assert smla.prefix_workspace_bytes(16 * 76, 8, 64 * 5) == 0
-    assert smla.prefix_workspace_bytes(1, 16, 128) == 2 * 2 * 16 * 514 * 4
-    assert smla.prefix_workspace_bytes(128, 64, 32768) == 76 * 2 * 128 * 514 * 4
+    assert smla.prefix_workspace_bytes(1, 8, 128) == 0
+    assert smla.prefix_workspace_bytes(16 * 76, 8, 128 * 5) == 0
+    assert smla.prefix_workspace_bytes(1, 16, 129) == partials(2, 16)
+    assert smla.prefix_workspace_bytes(128, 64, 32768) == partials(76, 128)
+    # an fp8 prefix also has its whole pages as bf16 rows
+    assert smla.prefix_workspace_bytes(1, 8, 100, "fp8") == 128 * 1152
+    assert smla.prefix_workspace_bytes(1, 16, 129, "fp8") == partials(2, 16) + 192 * 1152
 
 
 def _args(T=3, h=8, P=130):

@@ -75,7 +75,7 @@ def library() -> ctypes.CDLL:
     lib.sparse_mla_q_up.restype = ctypes.c_int
     lib.sparse_mla_q_up.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, i32, vp, vp]
     lib.sparse_mla_prefix_workspace_bytes.restype = sz
-    lib.sparse_mla_prefix_workspace_bytes.argtypes = [i32, i32, i64]
+    lib.sparse_mla_prefix_workspace_bytes.argtypes = [i32, i32, i64, i32]
     lib.sparse_mla_prefix.restype = ctypes.c_int
     lib.sparse_mla_prefix.argtypes = [vp, vp, vp, i32, i32, i64, i64, i32, f32, vp, vp, vp, sz, vp]
     lib.sparse_mla_host_io_layout.restype = ctypes.c_int
@@ -461,9 +461,9 @@ def sparse_mla_q_up(q: torch.Tensor, w: torch.Tensor, positions: torch.Tensor, c
     return out
 
 
-def prefix_workspace_bytes(T: int, h: int, prefix_len: int) -> int:
+def prefix_workspace_bytes(T: int, h: int, prefix_len: int, kv_format: str = "bf16") -> int:
     """Bytes of workspace that sparse_mla_prefix needs on the current device (0: none)."""
-    return int(library().sparse_mla_prefix_workspace_bytes(T, h, prefix_len))
+    return int(library().sparse_mla_prefix_workspace_bytes(T, h, prefix_len, KV_FORMATS[kv_format]))
 
 
 def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, prefix_len: int,
@@ -476,7 +476,7 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
 
     Returns out [T, h, 512] bf16 and lse [T, h] fp32, which sparse_mla_merge joins with each token's
     own part.  scale defaults to 576 ** -0.5.  workspace: a uint8 tensor of prefix_workspace_bytes(T,
-    h, prefix_len) bytes for callers that keep one (calls that may overlap need their own); allocated
+    h, prefix_len, kv_format) bytes for callers that keep one (calls that may overlap need their own); allocated
     here otherwise, from torch's allocator on the stream of the call.
     """
     if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != torch.bfloat16 or not q.is_contiguous():
@@ -508,7 +508,7 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
         lib = library()
         handle = _stream_handle(stream, dev)
         if workspace is None:
-            need = int(lib.sparse_mla_prefix_workspace_bytes(T, h, prefix_len))
+            need = int(lib.sparse_mla_prefix_workspace_bytes(T, h, prefix_len, KV_FORMATS[kv_format]))
             if need:
                 workspace = _workspace_on(need, dev, handle)
         elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:

@@ -90,8 +90,7 @@ cudaError_t set_kernel_attrs() {
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<192, 256>, smla::QupLayout<192, 256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256, 128>, smla::QupLayout<256, 128>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256, 256>, smla::QupLayout<256, 256>::kBytes);
-    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_prefix_kernel<0>, smla::PfLayout::kBytes);
-    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_prefix_kernel<1>, smla::PfLayout::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_prefix_kernel, smla::PfLayout::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_scatter_mask_kernel, smla::kScatterMaxS / 32 * 4);
     return e;
 }
@@ -442,31 +441,31 @@ smla_status launch(const void* q, const void* kv, const int32_t* idx, int32_t T,
     return SMLA_OK;
 }
 
-// How sparse_mla_prefix cuts its work: `work` (row tile, page) blocks in `runs` equal runs, one per
-// CTA pair, and the workspace of the partials of cut tiles (0 if no tile is cut).
+// How sparse_mla_prefix cuts its work: `work` (row tile, block) items in `runs` equal runs, one per
+// CTA pair; and its workspace: the partials of cut tiles, if any, and the expanded rows of an fp8 cache.
 struct PrefixPlan {
-    int64_t rows = 0, tiles = 0, nblk = 0, work = 0;
+    int64_t rows = 0, tiles = 0, npages = 0, nblk = 0, work = 0;
     int runs = 0, slot_rows = 0;
-    size_t part_bytes = 0, ml_bytes = 0;
+    bool cut = false;
+    size_t off_ml = 0, off_expanded = 0, bytes = 0;
 };
 
-PrefixPlan prefix_plan(int64_t rows, int64_t prefix, int num_sms) {
+PrefixPlan prefix_plan(int64_t rows, int64_t prefix, bool fp8, int num_sms) {
     PrefixPlan pl;
     pl.rows = rows;
     pl.tiles = (rows + smla::kPfRows - 1) / smla::kPfRows;
+    pl.npages = (prefix + smla::kPfPage - 1) / smla::kPfPage;
     pl.nblk = (prefix + smla::kPfKeys - 1) / smla::kPfKeys;
     pl.work = pl.tiles * pl.nblk;
     if (pl.work == 0) return pl;
     const int64_t pairs = num_sms / 2;
     pl.runs = static_cast<int>(pl.work < pairs ? pl.work : pairs);
     pl.slot_rows = static_cast<int>(rows < smla::kPfRows ? rows : smla::kPfRows);
-    bool cut = false;
-    for (int k = 1; k < pl.runs && !cut; ++k) cut = (pl.work * k / pl.runs) % pl.nblk != 0;
-    if (cut) {
-        const size_t slots = static_cast<size_t>(pl.runs) * 2 * pl.slot_rows;
-        pl.part_bytes = slots * smla::kDV * 4;
-        pl.ml_bytes = slots * 2 * 4;
-    }
+    for (int k = 1; k < pl.runs && !pl.cut; ++k) pl.cut = (pl.work * k / pl.runs) % pl.nblk != 0;
+    const size_t slots = pl.cut ? static_cast<size_t>(pl.runs) * 2 * pl.slot_rows : 0;
+    pl.off_ml = slots * smla::kDV * 4;
+    pl.off_expanded = align256(pl.off_ml + slots * 2 * 4);
+    pl.bytes = pl.off_expanded + (fp8 ? static_cast<size_t>(pl.npages) * smla::kPfPage * smla::kDQK * 2 : 0);
     return pl;
 }
 
@@ -1074,14 +1073,13 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
 }
 
 
-size_t sparse_mla_prefix_workspace_bytes(int32_t T, int32_t h, int64_t prefix_len) {
-    if (T <= 0 || h <= 0 || prefix_len <= 0) return 0;
+size_t sparse_mla_prefix_workspace_bytes(int32_t T, int32_t h, int64_t prefix_len, int32_t kv_format) {
+    if (T <= 0 || h <= 0 || prefix_len <= 0 || prefix_len > 0x7fffffffLL) return 0;
     int num_sms = 152;
     int dev = 0;
     DeviceState* ds = nullptr;
     if (device_state(&dev, &ds) == SMLA_OK) num_sms = ds->num_sms;
-    const PrefixPlan pl = prefix_plan(static_cast<int64_t>(T) * h, prefix_len, num_sms);
-    return pl.part_bytes + pl.ml_bytes;
+    return prefix_plan(static_cast<int64_t>(T) * h, prefix_len, kv_format == SMLA_KV_FP8, num_sms).bytes;
 }
 
 smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t* block_table, int32_t T, int32_t h,
@@ -1108,7 +1106,8 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
     DeviceState* ds = nullptr;
     smla_status st = device_state(&dev, &ds);
     if (st != SMLA_OK) return st;
-    const PrefixPlan pl = prefix_plan(rows, prefix_len, ds->num_sms);
+    const bool fp8 = kv_format == SMLA_KV_FP8;
+    const PrefixPlan pl = prefix_plan(rows, prefix_len, fp8, ds->num_sms);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1129,12 +1128,11 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
         return e == cudaSuccess ? SMLA_OK : cuda_fail(e, "empty prefix kernel launch");
     }
     if (pl.work / pl.runs >= 0x7fffffffLL) return fail(SMLA_ERR_INVALID_ARG, "T * h * prefix_len too large");
-    const size_t need = pl.part_bytes + pl.ml_bytes;
-    if (need > 0) {
+    if (pl.bytes > 0) {
         if (!workspace || !aligned(workspace, 256))
             return fail(SMLA_ERR_INVALID_ARG, "workspace must be given, 256-byte aligned");
-        if (workspace_bytes < need)
-            return fail(SMLA_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, need);
+        if (workspace_bytes < pl.bytes)
+            return fail(SMLA_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, pl.bytes);
     }
     EncodeTiledFn enc = nullptr;
     if ((st = encode_fn(&enc)) != SMLA_OK) return st;
@@ -1151,39 +1149,43 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     };
-    const bool fp8 = kv_format == SMLA_KV_FP8;
+    char* ws = static_cast<char*>(workspace);
+    const void* rows_at = fp8 ? ws + pl.off_expanded : kv_cache;
+    const int64_t num_rows = fp8 ? pl.npages * smla::kPfPage : num_slots;
     CUresult r = make(&tm_q, q, rows, smla::kPfHalf, smla::kPanels);
-    if (fp8) {  // the producers read the rows themselves; the kernel does not touch these maps
-        tm_k = tm_q;
-        tm_v = tm_q;
-    } else {
-        if (r == CUDA_SUCCESS) r = make(&tm_k, kv_cache, num_slots, 32, smla::kPanels);
-        if (r == CUDA_SUCCESS) r = make(&tm_v, kv_cache, num_slots, smla::kPfKeys, 4);
-    }
+    if (r == CUDA_SUCCESS) r = make(&tm_k, rows_at, num_rows, smla::kPfPage, smla::kPanels / smla::kPfGroups);
+    if (r == CUDA_SUCCESS) r = make(&tm_v, rows_at, num_rows, smla::kPfPage, 4);
     if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/kv_cache failed (%d)", (int)r);
     pp.kv = kv_cache;
+    pp.expanded = fp8 ? reinterpret_cast<__nv_bfloat16*>(ws + pl.off_expanded) : nullptr;
     pp.pages = block_table;
-    pp.part_o = static_cast<float*>(workspace);
-    pp.part_ml = need > 0 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.part_bytes) : nullptr;
+    pp.part_o = pl.cut ? reinterpret_cast<float*>(ws) : nullptr;
+    pp.part_ml = pl.cut ? reinterpret_cast<float*>(ws + pl.off_ml) : nullptr;
     pp.prefix = prefix_len;
     pp.num_slots = num_slots;
     pp.work = pl.work;
+    pp.npages = static_cast<int32_t>(pl.npages);
     pp.nblk = static_cast<int32_t>(pl.nblk);
     pp.runs = pl.runs;
     pp.slot_rows = pl.slot_rows;
     pp.sm_scale_log2 = scale * 1.4426950408889634f;
+    if (fp8) {
+        cfg.gridDim = dim3(static_cast<unsigned>(pl.npages * smla::kPfPage / (smla::kPfExpandThreads / 32)), 1, 1);
+        cfg.blockDim = dim3(smla::kPfExpandThreads, 1, 1);
+        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_expand_kernel, pp);
+        if (e != cudaSuccess) return cuda_fail(e, "prefix expand kernel launch");
+    }
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pl.runs), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(fp8 ? smla::PfRoles<1>::kThreads : smla::PfRoles<0>::kThreads), 1, 1);
+    cfg.blockDim = dim3(smla::kPfThreads, 1, 1);
     cfg.dynamicSmemBytes = smla::PfLayout::kBytes;
-    e = fp8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_kernel<1>, tm_q, tm_k, tm_v, pp)
-            : cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_kernel<0>, tm_q, tm_k, tm_v, pp);
+    e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_kernel, tm_q, tm_k, tm_v, pp);
     if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
-    if (need > 0) {
+    if (pl.cut) {
         cfg.numAttrs = 1;
         cfg.gridDim = dim3(static_cast<unsigned>(rows), 1, 1);
         cfg.blockDim = dim3(smla::kPfMergeThreads, 1, 1);
