@@ -42,13 +42,6 @@ struct AppendParams {
     int32_t interleaved;
 };
 
-// max that keeps a NaN of either operand
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 // two fp32 values as an e4m3 pair (lo in the low byte), nearest even, saturated to +-448
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
     uint16_t r;
@@ -144,9 +137,9 @@ __global__ void __launch_bounds__(kAppendThreads) sparse_mla_append_kernel(const
     } else {
         float amax = fabsf(x[0]);
 #pragma unroll
-        for (int i = 1; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
+        for (int i = 1; i < 16; ++i) amax = ptx::max_nan(amax, fabsf(x[i]));
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int o = 1; o < 8; o <<= 1) amax = ptx::max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         float scale = __fdiv_rn(amax, 448.f);
         if (scale == 0.f) scale = 1.f;  // a tile of zeros (or of values too small for a scale): codes 0
         uint32_t code[4];

@@ -36,13 +36,15 @@
 // are multiplied: 0 times whatever the page holds there must stay 0.  A page number outside the
 // cache masks its page; rows of a page past the cache's end are masked.
 //
-// Roles (192 threads):
+// Roles (352 threads):
 //   warp 0      TMA producer (one thread).
-//   warp 1      MMA issuer (one thread of the even CTA) and TMEM owner.
-//   warps 2-5   softmax, rescaling and output: thread = TMEM lane, i.e. row r = lane % 64 and page
-//               lane / 64 of a block, dims 256 (lane / 64) .. + 255 of O.  The running max is moved
-//               only when it grows by more than 2^8; the two warps of a row vote per block and swap
-//               maxima only then.
+//   warp 1      S issuer (one thread of the even CTA) and TMEM owner.
+//   warps 2-9   softmax, rescaling and output, two warps per TMEM lane quadrant: row r = lane % 64,
+//               page lane / 64 of a block and 32 of its keys, dims 256 (lane / 64) .. + 255 of O and
+//               128 of those.  The running max is moved only when it grows by more than 2^8; the four
+//               warps of a row vote per block and swap maxima only then.  (One warp per quadrant took
+//               2.4 us a block, longer than the block's MMAs.)
+//   warp 10     PV issuer (one thread of the even CTA).
 // Every wait is bounded; a CTA that gives up meets the other at the final cluster barrier.
 #pragma once
 
@@ -54,7 +56,9 @@ constexpr int kPfRows = 128;                      // query rows per CTA pair (MM
 constexpr int kPfHalf = 64;                       // query rows per CTA
 constexpr int kPfPage = 64;                       // rows per page
 constexpr int kPfKeys = 2 * kPfPage;              // keys per block
-constexpr int kPfThreads = 192;
+constexpr int kPfSoftmaxWarps = 8;
+constexpr int kPfPvWarp = 2 + kPfSoftmaxWarps;
+constexpr int kPfThreads = 32 * (kPfPvWarp + 1);
 constexpr int kPfPanel = 64 * 128;                // 64 rows x 64 bf16, SW128
 constexpr int kPfQBytes = kPanels * kPfPanel;
 constexpr int kPfGroups = 3;                      // K is refilled in groups of panels
@@ -68,9 +72,9 @@ struct PfLayout {
     static constexpr int kOffK = kOffQ + kPfQBytes;
     static constexpr int kOffV = kOffK + kPfQBytes;
     static constexpr int kOffP = kOffV + 2 * kPfVPage;        // two panels; output staging between pieces
-    static constexpr int kOffX = kOffP + 2 * kPfPanel;        // [2][64] values swapped by a row's two threads
-    static constexpr int kOffBar = kOffX + 2 * kPfHalf * 4;
-    static constexpr int kNumBars = 19;
+    static constexpr int kOffX = kOffP + 2 * kPfPanel;        // [4][64] values swapped by a row's four threads
+    static constexpr int kOffBar = kOffX + 4 * kPfHalf * 4;
+    static constexpr int kNumBars = 20;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag
     static constexpr int kBytes = kOffMisc + 16;
     // TMEM columns: O [0, 256) | S x2 [256, 384)
@@ -91,7 +95,8 @@ enum : int {
     kPbSEmpty = 14,  // +buffer, even CTA
     kPbPFull = 16,   // even CTA
     kPbPvDone = 17,  // both
-    kPbTail = 18     // own CTA: V of a page that the prefix ends in
+    kPbTail = 18,    // own CTA: V of a page that the prefix ends in
+    kPbDrain = 19    // even CTA: everything both issuers issued is done
 };
 
 struct PfParams {
@@ -134,19 +139,28 @@ __device__ __forceinline__ bool pf_tail(const PfParams& p, int i) {
 
 // The pieces of a run, the same for every role: blocks [b0, b1) of tile t.
 struct PfWalk {
-    int64_t at, end;
-    int32_t nblk;
+    int64_t left;    // blocks of the run still to come
     int64_t tile;
+    int32_t nblk;
     int b0, b1;
-    __device__ __forceinline__ PfWalk(const PfParams& p, int run)
-        : at(p.work * run / p.runs), end(p.work * (run + 1) / p.runs), nblk(p.nblk), tile(0), b0(0), b1(0) {}
-    __device__ __forceinline__ bool next() {
-        if (at >= end) return false;
+    bool first;      // the run's first piece
+    __device__ __forceinline__ PfWalk(const PfParams& p, int run) : nblk(p.nblk), b1(0), first(true) {
+        const int64_t at = p.work * run / p.runs;
+        left = p.work * (run + 1) / p.runs - at;
         tile = at / nblk;
         b0 = static_cast<int>(at - tile * nblk);
-        const int64_t n = end - at < nblk - b0 ? end - at : nblk - b0;
+    }
+    // first call: the first piece; later calls: the next tile's
+    __device__ __forceinline__ bool next() {
+        if (b1 != 0) {
+            b0 = 0;
+            ++tile;
+            first = false;
+        }
+        if (left <= 0) return false;
+        const int64_t n = left < nblk - b0 ? left : nblk - b0;
         b1 = b0 + static_cast<int>(n);
-        at += n;
+        left -= n;
         return true;
     }
 };
@@ -169,14 +183,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     auto bar = [&](int i) -> uint32_t { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
     auto even_bar = [&](int i) -> uint32_t { return ptx::map_shared_rank(bar(i), 0); };
     auto wait = [&](int i, uint32_t parity) -> bool {
-        return ptx::mbar_wait_cluster(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
+        return ptx::mbar_wait(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
     };
 
     if (threadIdx.x == 0) {
         *sAbort = 0;
         for (int i = 0; i < L::kNumBars; ++i) {
             const bool by_warps = i == kPbSEmpty || i == kPbSEmpty + 1 || i == kPbPFull;  // both CTAs' softmax warps
-            ptx::mbar_init(bar(i), by_warps ? 8 : 1);
+            ptx::mbar_init(bar(i), by_warps ? 2 * kPfSoftmaxWarps : i == kPbDrain ? 2 : 1);
         }
         ptx::fence_mbarrier_init();
     }
@@ -184,10 +198,28 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         ptx::tmem_alloc_pair(sbase + L::kOffMisc, L::kTmemCols);
         ptx::tmem_relinquish_pair();
     }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+        ptx::prefetch_tmap(&tm_v);
+    }
+    PfWalk w(p, run);
+    const bool any = w.next();
     // launched as a programmatic dependent: nothing above touched global memory
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
+    auto page_row = [&](int i) -> int {  // first row of page i; one that is not there loads as zeros, from rows below 0
+        if (p.expanded != nullptr) return i < p.npages ? i * kPfPage : -kPfPage;
+        const int page = pf_page(p, i);
+        return pf_in_cache(p, page) ? page * kPfPage : -kPfPage;
+    };
+    int row[2] = {0, 0};
+    if (warp == 0 && lane == 0) {
+        row[0] = page_row(2 * w.b0);
+        row[1] = page_row(2 * w.b0 + 1);
+    }
     ptx::tc_fence_before();
+    __syncwarp();         // the cluster barrier wants its warps whole
     ptx::cluster_sync();  // both CTAs' barriers are initialised before anyone signals them
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
@@ -198,38 +230,33 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // own copies.  K runs a block ahead of V, the order in which the tensor cores release them:
         // K(x) waits for S(x - 1), V(x - 1) for PV(x - 2).
         if (lane == 0) {
-            ptx::prefetch_tmap(&tm_q);
-            ptx::prefetch_tmap(&tm_k);
-            ptx::prefetch_tmap(&tm_v);
-            auto page_row = [&](int i) -> int {  // a page that is not there loads as zeros, from rows below 0
-                if (p.expanded != nullptr) return i < p.npages ? i * kPfPage : -kPfPage;
-                const int page = pf_page(p, i);
-                return pf_in_cache(p, page) ? page * kPfPage : -kPfPage;
-            };
-            auto load_v = [&](int x, int b, const int (&row)[2]) -> bool {
+            auto load_v = [&](int x, int b, int row0, int row1) -> bool {
+#pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (x > 0 && !wait(kPbVEmpty + i, (x - 1) & 1)) return false;
                     const uint32_t dst = sbase + L::kOffV + i * kPfVPage;
                     if (pf_tail(p, 2 * b + i)) {  // the softmax warps wait for this one themselves and zero its end
                         ptx::mbar_arrive_expect_tx(bar(kPbTail), static_cast<uint32_t>(kPfVPage));
-                        ptx::tma_load_3d(dst, &tm_v, 0, row[i], 4 * rank, bar(kPbTail));
+                        ptx::tma_load_3d(dst, &tm_v, 0, i ? row1 : row0, 4 * rank, bar(kPbTail));
                     } else {
                         if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbVFull + i), 2u * kPfVPage);
-                        ptx::tma_load_3d_pair(dst, &tm_v, 0, row[i], 4 * rank, even_bar(kPbVFull + i));
+                        ptx::tma_load_3d_pair(dst, &tm_v, 0, i ? row1 : row0, 4 * rank, even_bar(kPbVFull + i));
                     }
                 }
                 return true;
             };
             bool ok = true;
             int x = 0, piece = 0, b_v = 0;
-            int row[2] = {0, 0}, row_v[2] = {0, 0};
-            for (PfWalk w(p, run); ok && w.next(); ++piece) {
+            int row_v0 = 0, row_v1 = 0;
+            for (bool more = any; ok && more; more = w.next(), ++piece) {
                 if (piece > 0 && !(ok = wait(kPbQEmpty, (piece - 1) & 1))) break;
                 if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbQFull), 2u * kPfQBytes);
                 ptx::tma_load_3d_pair(sbase + L::kOffQ, &tm_q, 0, static_cast<int>(w.tile * kPfRows + rank * kPfHalf), 0,
                                       even_bar(kPbQFull));
-                row[0] = page_row(2 * w.b0);
-                row[1] = page_row(2 * w.b0 + 1);
+                if (piece > 0) {
+                    row[0] = page_row(2 * w.b0);
+                    row[1] = page_row(2 * w.b0 + 1);
+                }
                 for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
                     const int mine = rank == 0 ? row[0] : row[1];
                     for (int g = 0; ok && g < kPfGroups; ++g) {
@@ -239,86 +266,102 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                                               even_bar(kPbKFull + g));
                     }
                     const int next0 = page_row(2 * b + 2), next1 = page_row(2 * b + 3);  // loaded under the waits
-                    if (ok && x > 0) ok = load_v(x - 1, b_v, row_v);
-                    row_v[0] = row[0];
-                    row_v[1] = row[1];
+                    if (ok && x > 0) ok = load_v(x - 1, b_v, row_v0, row_v1);
+                    row_v0 = row[0];
+                    row_v1 = row[1];
                     b_v = b;
                     row[0] = next0;
                     row[1] = next1;
                 }
             }
-            if (ok && x > 0) load_v(x - 1, b_v, row_v);
+            if (ok && x > 0) ok = load_v(x - 1, b_v, row_v0, row_v1);
+            // every copy has landed and been used, and no release of a stage is still on its way to
+            // this CTA's barriers, before it leaves
+            for (int g = 0; ok && g < kPfGroups; ++g) ok = wait(kPbKEmpty + g, (x - 1) & 1);
+            for (int i = 0; ok && i < 2; ++i) ok = wait(kPbVEmpty + i, (x - 1) & 1);
+            if (ok) ok = wait(kPbQEmpty, (piece - 1) & 1);
+            if (!ok) {  // gave up: copies in flight complete on the other CTA's barriers; leave them time to land
+                const uint64_t t0 = ptx::globaltimer_ns();
+                while (ptx::globaltimer_ns() - t0 < 2000000ull) {
+                }
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ================================================================ MMA issuer
-        // Order: S(0), S(1), PV(0), S(2), PV(1), ...: the softmax of block x runs under S(x + 1).
+        // ================================================================ S issuer (TMEM owner)
         if (rank == 0 && lane == 0) {
             constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kPfRows, kPfKeys, 0, 0);
-            constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kPfRows, 256, 0, 1);
             const uint64_t dq = ptx::smem_desc_sw128(sbase + L::kOffQ, 16, 1024);
             const uint64_t dk = ptx::smem_desc_sw128(sbase + L::kOffK, 16, 1024);
-            const uint64_t dv = ptx::smem_desc_sw128(sbase + L::kOffV, kPfPanel, 1024);
-            const uint64_t dp = ptx::smem_desc_sw128(sbase + L::kOffP, 16, 1024);
-            auto issue_s = [&](int x, bool first, bool last, int piece) -> bool {
-                const int s = x & 1;
-                if (first && !wait(kPbQFull, piece & 1)) return false;
-                if (x >= 2 && !wait(kPbSEmpty + s, ((x >> 1) - 1) & 1)) return false;
-                const uint32_t d = tmem + L::kColS + s * kPfPage;
-#pragma unroll
-                for (int g = 0; g < kPfGroups; ++g) {
-                    if (!wait(kPbKFull + g, x & 1)) return false;
-                    ptx::tc_fence_after();
-#pragma unroll
-                    for (int j = 0; j < kPanels / kPfGroups; ++j)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int pn = g * (kPanels / kPfGroups) + j;
-                            ptx::mma_bf16_ss_pair(d, dq + ((pn * kPfPanel + k * 32) >> 4), dk + ((pn * kPfPanel + k * 32) >> 4),
-                                                  kIdescS, (pn | k) != 0);
-                        }
-                    ptx::mma_commit_pair(bar(kPbKEmpty + g));
-                }
-                ptx::mma_commit_pair(bar(kPbSFull + s));
-                if (last) ptx::mma_commit_pair(bar(kPbQEmpty));
-                return true;
-            };
-            uint32_t v_parity = 0u;  // bit i: parity of the loads that came to V page i (tails have their own barrier)
-            auto issue_pv = [&](int x, int b, bool first) -> bool {
-                if (!wait(kPbPFull, x & 1)) return false;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (!pf_tail(p, 2 * b + i)) {
-                        if (!wait(kPbVFull + i, (v_parity >> i) & 1u)) return false;
-                        v_parity ^= 1u << i;
-                    }
-                    ptx::tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
-                            ptx::mma_bf16_ss_pair(tmem + L::kColO + 128 * n, dp + ((i * kPfPanel + k * 32) >> 4),
-                                                  dv + ((i * kPfVPage + 2 * n * kPfPanel + k * 2048) >> 4), kIdescPV,
-                                                  (!first || i > 0 || k > 0) ? 1u : 0u);
-                    ptx::mma_commit_pair(bar(kPbVEmpty + i));
-                }
-                ptx::mma_commit_pair(bar(kPbPvDone));
-                return true;
-            };
             bool ok = true;
             int x = 0, piece = 0;
-            int pend_b = 0;
-            bool pend_first = false, pend = false;
-            for (PfWalk w(p, run); ok && w.next(); ++piece) {
+            for (bool more = any; ok && more; more = w.next(), ++piece) {
+                if (!(ok = wait(kPbQFull, piece & 1))) break;
                 for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
-                    ok = issue_s(x, b == w.b0, b + 1 == w.b1, piece);
-                    if (ok && pend) ok = issue_pv(x - 1, pend_b, pend_first);
-                    pend = true;
-                    pend_b = b;
-                    pend_first = b == w.b0;
+                    const int s = x & 1;
+                    if (x >= 2 && !(ok = wait(kPbSEmpty + s, ((x >> 1) - 1) & 1))) break;
+                    const uint32_t d = tmem + L::kColS + s * kPfPage;
+#pragma unroll
+                    for (int g = 0; g < kPfGroups; ++g) {
+                        if (!(ok = wait(kPbKFull + g, x & 1))) break;
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int j = 0; j < kPanels / kPfGroups; ++j)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int pn = g * (kPanels / kPfGroups) + j;
+                                ptx::mma_bf16_ss_pair(d, dq + ((pn * kPfPanel + k * 32) >> 4), dk + ((pn * kPfPanel + k * 32) >> 4),
+                                                      kIdescS, (pn | k) != 0);
+                            }
+                        ptx::mma_commit_pair(bar(kPbKEmpty + g));
+                    }
+                    if (!ok) break;
+                    ptx::mma_commit_pair(bar(kPbSFull + s));
+                    if (b + 1 == w.b1) ptx::mma_commit_pair(bar(kPbQEmpty));
                 }
             }
-            if (ok && pend) issue_pv(x - 1, pend_b, pend_first);
+            // nothing is in flight when TMEM is freed, also after giving up
+            ptx::mma_commit_pair_local(bar(kPbDrain));
+            ptx::mbar_wait(bar(kPbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == kPfPvWarp) {
+        // ================================================================ PV issuer
+        // A thread of its own: issuing an MMA costs its thread more time (76 cycles for S, 120 for PV,
+        // with their operands moved to uniform registers each time) than the tensor cores take for it
+        // (32 and 64), so two threads issue side by side.
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kPfRows, 256, 0, 1);
+            const uint64_t dv = ptx::smem_desc_sw128(sbase + L::kOffV, kPfPanel, 1024);
+            const uint64_t dp = ptx::smem_desc_sw128(sbase + L::kOffP, 16, 1024);
+            uint32_t v_parity = 0u;  // bit i: parity of the loads that came to V page i (tails have their own barrier)
+            bool ok = true;
+            int x = 0;
+            for (bool more = any; ok && more; more = w.next()) {
+                for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
+                    if (!(ok = wait(kPbPFull, x & 1))) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!pf_tail(p, 2 * b + i)) {
+                            if (!(ok = wait(kPbVFull + i, (v_parity >> i) & 1u))) break;
+                            v_parity ^= 1u << i;
+                        }
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int n = 0; n < 2; ++n)
+                                ptx::mma_bf16_ss_pair(tmem + L::kColO + 128 * n, dp + ((i * kPfPanel + k * 32) >> 4),
+                                                      dv + ((i * kPfVPage + 2 * n * kPfPanel + k * 2048) >> 4), kIdescPV,
+                                                      (b != w.b0 || i > 0 || k > 0) ? 1u : 0u);
+                        ptx::mma_commit_pair(bar(kPbVEmpty + i));
+                    }
+                    if (ok) ptx::mma_commit_pair(bar(kPbPvDone));
+                }
+            }
+            // nothing is in flight when TMEM is freed, also after giving up
+            ptx::mma_commit_pair_local(bar(kPbDrain));
+            ptx::mbar_wait(bar(kPbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
         }
         __syncwarp();
     } else {
@@ -326,9 +369,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int quad = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
         const int half = quad >> 1;                 // page of the block, dims 256 half .. + 255
+        const int sub = (warp - 2) >> 2;            // keys 32 sub .. + 31 of the page, 128 of the dims
+        const int part = 2 * half + sub;            // which of the row's four threads
         const int r = (quad & 1) * 32 + lane;       // row of this CTA's 64
         const uint32_t grp = 1u + static_cast<uint32_t>(quad & 1);
-        const float c = p.sm_scale_log2;
+        // logits as |c| times +-s, so that their max is that of +-s and one fma gives log2 of P
+        const float c = fabsf(p.sm_scale_log2);
+        const bool flip = p.sm_scale_log2 < 0.f;
         volatile float* sX = reinterpret_cast<volatile float*>(smem + L::kOffX);
         auto warp_wait = [&](int i, uint32_t parity) -> bool {
             bool okw = true;
@@ -339,58 +386,61 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         };
         const uint32_t s_empty0 = even_bar(kPbSEmpty), s_empty1 = even_bar(kPbSEmpty + 1), p_full = even_bar(kPbPFull);
         const uint32_t p_row = sbase + L::kOffP + half * kPfPanel + r * 128;
+        const int ocol0 = L::kColO + 128 * sub;
         bool failed = false;
         int x = 0, tails = 0;
-        for (PfWalk w(p, run); !failed && w.next();) {
+        for (bool more = any; !failed && more; more = w.next()) {
             float m = -CUDART_INF_F, l = 0.f;
             int page = pf_page(p, 2 * w.b0 + half);
             for (int b = w.b0; b < w.b1; ++b, ++x) {
-                const int n = pf_valid(p, 2 * b + half, page);  // keys of this thread's 64 that take part
+                const int n = pf_valid(p, 2 * b + half, page) - 32 * sub;  // keys of this thread's 32 that take part
                 page = pf_page(p, 2 * b + 2 + half);
                 const int s = x & 1;
-                uint32_t sv[64];
+                uint32_t sv[32];
                 float mx = -CUDART_INF_F;
                 if (!failed && !warp_wait(kPbSFull + s, (x >> 1) & 1)) failed = true;
                 if (!failed) {
                     ptx::tc_fence_after();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) SMLA_TMEM_LD16(tmem + lane_base + L::kColS + s * kPfPage + 16 * q, sv + 16 * q);
+                    for (int q = 0; q < 2; ++q)
+                        SMLA_TMEM_LD16(tmem + lane_base + L::kColS + s * kPfPage + 32 * sub + 16 * q, sv + 16 * q);
                     ptx::tmem_wait_ld();
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(s ? s_empty1 : s_empty0);
+                    if (flip) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float2 y = ptx::mul2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])),
-                                                   make_float2(c, c));
-                        sv[2 * i] = __float_as_uint(y.x);
-                        sv[2 * i + 1] = __float_as_uint(y.y);
+                        for (int i = 0; i < 32; ++i) sv[i] ^= 0x80000000u;
                     }
-                    if (n < kPfPage) {
+                    if (n < 32) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
+                        for (int i = 0; i < 32; ++i)
                             if (i >= n) sv[i] = __float_as_uint(-CUDART_INF_F);
                     }
-                    float mxa[8];
+                    float mxa[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) mxa[i] = __uint_as_float(sv[i]);
+                    for (int i = 0; i < 4; ++i) mxa[i] = fmaxf(__uint_as_float(sv[i]), __uint_as_float(sv[i + 4]));
 #pragma unroll
-                    for (int i = 8; i < 64; ++i) mxa[i & 7] = fmaxf(mxa[i & 7], __uint_as_float(sv[i]));
-                    mx = fmaxf(fmaxf(fmaxf(mxa[0], mxa[1]), fmaxf(mxa[2], mxa[3])),
-                               fmaxf(fmaxf(mxa[4], mxa[5]), fmaxf(mxa[6], mxa[7])));
-                    if (mx != mx) mx = -CUDART_INF_F;  // a row of NaN only: P and the sum carry it
+                    for (int i = 8; i < 32; i += 8)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mxa[j] = ptx::max3(mxa[j], __uint_as_float(sv[i + j]), __uint_as_float(sv[i + j + 4]));
+                    mx = fmaxf(fmaxf(mxa[0], mxa[1]), fmaxf(mxa[2], mxa[3]));
+                    // (scale 0: every logit is 0.  A row of NaN only: P and the sum carry it.)
+                    mx *= c;
+                    if (n <= 0 || mx != mx) mx = -CUDART_INF_F;
                 }
-                if (ptx::named_bar_red_or(grp, 64u, failed || mx > m + kRescaleLog2)) {
-                    // the row's max over both threads' keys (NaN: one of them gave up)
-                    sX[half * kPfHalf + r] = failed ? CUDART_NAN_F : mx;
-                    ptx::named_bar_sync(grp, 64u);
-                    const float o = sX[(half ^ 1) * kPfHalf + r];
-                    ptx::named_bar_sync(grp, 64u);
-                    if (__any_sync(0xffffffffu, failed || o != o)) {
+                if (ptx::named_bar_red_or(grp, 128u, failed || mx > m + kRescaleLog2)) {
+                    // the row's max over its four threads' keys (NaN: one of them gave up)
+                    sX[part * kPfHalf + r] = failed ? CUDART_NAN_F : mx;
+                    ptx::named_bar_sync(grp, 128u);
+                    const float o0 = sX[r], o1 = sX[kPfHalf + r], o2 = sX[2 * kPfHalf + r], o3 = sX[3 * kPfHalf + r];
+                    ptx::named_bar_sync(grp, 128u);
+                    const float mn = ptx::max_nan(ptx::max_nan(o0, o1), ptx::max_nan(o2, o3));
+                    if (__any_sync(0xffffffffu, mn != mn)) {
                         failed = true;
                         break;
                     }
-                    const float mn = fmaxf(mx, o);
                     const bool grow = mn > m + kRescaleLog2;
                     float alpha = 1.f;
                     if (grow) {
@@ -406,31 +456,37 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         }
                         ptx::tc_fence_after();
 #pragma unroll 1
-                        for (int cc = 0; cc < 16; ++cc) {
+                        for (int cc = 0; cc < 8; ++cc) {
                             uint32_t ov[16];
-                            SMLA_TMEM_LD16(tmem + lane_base + L::kColO + cc * 16, ov);
+                            SMLA_TMEM_LD16(tmem + lane_base + ocol0 + cc * 16, ov);
                             ptx::tmem_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                            SMLA_TMEM_ST16(tmem + lane_base + L::kColO + cc * 16, ov);
+                            SMLA_TMEM_ST16(tmem + lane_base + ocol0 + cc * 16, ov);
                         }
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before();
                     }
                 }
-                // P = 2^(x - m) as bf16, the operand of PV (its rounding averages out over the keys;
-                // the sum takes the unrounded values)
+                // P = 2^(c s - m) as bf16, the operand of PV (its rounding averages out over the keys;
+                // the sum takes the unrounded values).  A masked key holds -inf, which only a scale of 0
+                // would not keep out.
                 const float nm = m == -CUDART_INF_F ? 0.f : -m;
                 float2 la[4];
+                uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) la[i] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float2 d = ptx::add2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])),
-                                               make_float2(nm, nm));
-                    const float2 pp = make_float2(ptx::ex2_approx(d.x), ptx::ex2_approx(d.y));
+                for (int i = 0; i < 16; ++i) {
+                    const float2 d = ptx::fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])),
+                                               make_float2(c, c), make_float2(nm, nm));
+                    float2 pp = make_float2(ptx::ex2_approx(d.x), ptx::ex2_approx(d.y));
+                    if (n < 32) {
+                        if (2 * i >= n) pp.x = 0.f;
+                        if (2 * i + 1 >= n) pp.y = 0.f;
+                    }
                     la[i & 3] = ptx::add2(la[i & 3], pp);
-                    sv[i] = pack_bf16x2(pp.x, pp.y);
+                    pk[i] = ptx::cvt_bf16x2(pp.x, pp.y);
                 }
                 l += ((la[0].x + la[0].y) + (la[1].x + la[1].y)) + ((la[2].x + la[2].y) + (la[3].x + la[3].y));
                 // P is one buffer: PV(x - 1) has read it
@@ -439,9 +495,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     continue;  // the next reduction (or the one after the loop) takes the group out
                 }
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    ptx::st_shared_v4(p_row + ((static_cast<uint32_t>(q) ^ static_cast<uint32_t>(r & 7)) << 4),
-                                      make_uint4(sv[4 * q], sv[4 * q + 1], sv[4 * q + 2], sv[4 * q + 3]));
+                for (int q = 0; q < 4; ++q)
+                    ptx::st_shared_v4(p_row + ((static_cast<uint32_t>(4 * sub + q) ^ static_cast<uint32_t>(r & 7)) << 4),
+                                      make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
                 for (int i = 0; i < 2; ++i) {
                     if (!pf_tail(p, 2 * b + i)) continue;
                     // the page's rows past the prefix's end, zeroed in this CTA's V tile
@@ -453,12 +509,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     const int first = static_cast<int>(p.prefix % kPfPage);
                     const int tid = (warp - 2) * 32 + lane;
                     const uint32_t vt = sbase + L::kOffV + i * kPfVPage;
-                    for (int j = tid; j < (kPfPage - first) * 32; j += 128)
+                    for (int j = tid; j < (kPfPage - first) * 32; j += 32 * kPfSoftmaxWarps)
                         ptx::st_shared_v4(vt + (j & 3) * kPfPanel + (first + (j >> 5)) * 128 + ((j >> 2) & 7) * 16,
                                           make_uint4(0u, 0u, 0u, 0u));
                 }
                 if (failed) continue;
-                ptx::fence_proxy_async_all();
+                ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster(p_full);
             }
@@ -466,17 +522,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             // the unnormalised partial
             if (!failed && !warp_wait(kPbPvDone, (x - 1) & 1)) failed = true;
             ptx::tc_fence_after();
-            sX[half * kPfHalf + r] = l;
-            failed = ptx::named_bar_red_or(grp, 64u, failed);
-            const float lt = l + sX[(half ^ 1) * kPfHalf + r];
-            ptx::named_bar_sync(grp, 64u);
+            sX[part * kPfHalf + r] = l;
+            failed = ptx::named_bar_red_or(grp, 128u, failed);
+            const float lt = (sX[r] + sX[kPfHalf + r]) + (sX[2 * kPfHalf + r] + sX[3 * kPfHalf + r]);
             const int64_t row0 = w.tile * kPfRows + rank * kPfHalf + (quad & 1) * 32;  // the warp's first row
             const int live = p.rows - row0 < 32 ? static_cast<int>(p.rows - row0) : 32;  // rows of the warp, if any
             const bool whole = w.b0 == 0 && w.b1 == p.nblk;
-            const int64_t slot = 2 * static_cast<int64_t>(run) + (p.work * run / p.runs / p.nblk == w.tile ? 0 : 1);
-            const int64_t prow0 = slot * p.slot_rows + rank * kPfHalf + (quad & 1) * 32;
+            const int64_t prow0 = (2 * static_cast<int64_t>(run) + (w.first ? 0 : 1)) * p.slot_rows + rank * kPfHalf + (quad & 1) * 32;
             const float inv = lt > 0.f || lt != lt ? 1.0f / lt : 0.f;
-            if (!failed && lane < live && half == 0) {
+            if (!failed && lane < live && part == 0) {
                 if (whole) {
                     p.lse[row0 + lane] = lt == 0.f ? -CUDART_INF_F : (m + log2f(lt)) * 0.69314718055994531f;
                 } else {
@@ -484,60 +538,64 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     p.part_ml[2 * (prow0 + lane) + 1] = lt;
                 }
             }
-            // 32 rows x 128 bytes at a time through this warp's quarter of P's buffer (free until the
-            // next block's P): rows of whole lines, where a row per lane would touch 32 lines at once
+            // 32 rows x 64 bytes at a time through this warp's eighth of P's buffer (free until the
+            // next block's P): whole sectors, where a row per lane would touch 32 lines at once
             if (!failed && live > 0) {
-                const uint32_t stage = sbase + L::kOffP + (warp - 2) * 32 * 128;
+                const uint32_t stage = sbase + L::kOffP + (warp - 2) * 32 * 64;
                 auto put = [&](int e, uint4 v) {
-                    ptx::st_shared_v4(stage + lane * 128 + ((static_cast<uint32_t>(e) ^ static_cast<uint32_t>(lane & 7)) << 4), v);
+                    ptx::st_shared_v4(stage + lane * 64 + ((static_cast<uint32_t>(e) ^ static_cast<uint32_t>((lane >> 1) & 3)) << 4), v);
                 };
                 auto copy_out = [&](char* dst, int64_t pitch) {
                     __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int rr = 4 * e + (lane >> 3);
-                        const uint4 v = ptx::ld_shared_v4(stage + rr * 128 + ((static_cast<uint32_t>(lane & 7) ^ static_cast<uint32_t>(rr & 7)) << 4));
-                        if (rr < live) *reinterpret_cast<uint4*>(dst + rr * pitch + (lane & 7) * 16) = v;
+                    for (int e = 0; e < 4; ++e) {
+                        const int rr = 8 * e + (lane >> 2);
+                        const uint4 v = ptx::ld_shared_v4(stage + rr * 64 + ((static_cast<uint32_t>(lane & 3) ^ static_cast<uint32_t>((rr >> 1) & 3)) << 4));
+                        if (rr < live) *reinterpret_cast<uint4*>(dst + rr * pitch + (lane & 3) * 16) = v;
                     }
                     __syncwarp();
                 };
-                if (whole) {
+                // 64 columns of O are read at a time
 #pragma unroll 1
-                    for (int cc = 0; cc < 4; ++cc) {
-                        uint32_t ov[64];
+                for (int cc = 0; cc < 2; ++cc) {
+                    uint32_t ov[64];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) SMLA_TMEM_LD16(tmem + lane_base + L::kColO + cc * 64 + 16 * q, ov + 16 * q);
-                        ptx::tmem_wait_ld();
+                    for (int q = 0; q < 4; ++q) SMLA_TMEM_LD16(tmem + lane_base + ocol0 + cc * 64 + 16 * q, ov + 16 * q);
+                    ptx::tmem_wait_ld();
+                    const int64_t d0 = 256 * half + 128 * sub + 64 * cc;
+                    if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            uint32_t u[4];
+                        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                u[j] = pack_bf16x2(__uint_as_float(ov[8 * e + 2 * j]) * inv, __uint_as_float(ov[8 * e + 2 * j + 1]) * inv);
-                            put(e, make_uint4(u[0], u[1], u[2], u[3]));
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t v[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    v[j] = ptx::cvt_bf16x2(__uint_as_float(ov[32 * u + 8 * e + 2 * j]) * inv,
+                                                           __uint_as_float(ov[32 * u + 8 * e + 2 * j + 1]) * inv);
+                                put(e, make_uint4(v[0], v[1], v[2], v[3]));
+                            }
+                            copy_out(reinterpret_cast<char*>(p.out + row0 * kDV + d0 + 32 * u), kDV * 2);
                         }
-                        copy_out(reinterpret_cast<char*>(p.out + row0 * kDV + 256 * half + 64 * cc), kDV * 2);
-                    }
-                } else {
-#pragma unroll 1
-                    for (int cc = 0; cc < 8; ++cc) {
-                        uint32_t ov[32];
+                    } else {
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) SMLA_TMEM_LD16(tmem + lane_base + L::kColO + cc * 32 + 16 * q, ov + 16 * q);
-                        ptx::tmem_wait_ld();
+                        for (int u = 0; u < 4; ++u) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) put(e, make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]));
-                        copy_out(reinterpret_cast<char*>(p.part_o + prow0 * kDV + 256 * half + 32 * cc), kDV * 4);
+                            for (int e = 0; e < 4; ++e)
+                                put(e, make_uint4(ov[16 * u + 4 * e], ov[16 * u + 4 * e + 1], ov[16 * u + 4 * e + 2], ov[16 * u + 4 * e + 3]));
+                            copy_out(reinterpret_cast<char*>(p.part_o + prow0 * kDV + d0 + 16 * u), kDV * 4);
+                        }
                     }
                 }
             }
             ptx::tc_fence_before();  // before the next piece's first PV overwrites O
             // every warp's staging is read before the next P is written over it; and all leave together
-            failed = ptx::named_bar_red_or(3u, 128u, failed);
+            failed = ptx::named_bar_red_or(3u, 32u * kPfSoftmaxWarps, failed);
         }
     }
     // ---- both CTAs are done with each other's shared memory, barriers and TMEM
     ptx::tc_fence_before();
+    __syncwarp();
     ptx::cluster_sync();
     if (warp == 1) {
         ptx::tc_fence_after();
