@@ -1153,8 +1153,8 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
     const void* rows_at = fp8 ? ws + pl.off_expanded : kv_cache;
     const int64_t num_rows = fp8 ? pl.npages * smla::kPfPage : num_slots;
     CUresult r = make(&tm_q, q, rows, smla::kPfHalf, smla::kPanels);
-    if (r == CUDA_SUCCESS) r = make(&tm_k, rows_at, num_rows, smla::kPfPage, smla::kPanels / smla::kPfGroups);
-    if (r == CUDA_SUCCESS) r = make(&tm_v, rows_at, num_rows, smla::kPfPage, 4);
+    if (r == CUDA_SUCCESS) r = make(&tm_k, rows_at, num_rows, smla::kPfPage, smla::kPfGroupA);
+    if (r == CUDA_SUCCESS) r = make(&tm_v, rows_at, num_rows, smla::kPfPage, smla::kPfGroupB);
     if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/kv_cache failed (%d)", (int)r);
     pp.kv = kv_cache;
     pp.expanded = fp8 ? reinterpret_cast<__nv_bfloat16*>(ws + pl.off_expanded) : nullptr;

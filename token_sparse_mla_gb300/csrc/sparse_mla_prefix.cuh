@@ -15,13 +15,15 @@
 // (two pages):
 //   S[128, 128]  = Q . K^T     A: each CTA's 64 rows of Q; B: each CTA's page of 64 keys, all 576 dims
 //   O[128, 512] += P . V       A: each CTA's 64 rows of P; B: both pages, each CTA's 256 dims
-// An MMA of this form takes 45 cycles at N = 64 and at N = 128, and 64.5 at N = 256 (measured back to
-// back), so a block is 36 * 45 + 16 * 64.5 = 2652 cycles, 82 % of the dense rate; blocks of 64 keys
-// would be 4272 cycles per 128 keys (and measured 2.2 us per 64).  The price is shared memory: Q 72 KB, K 72 KB,
-// V 64 KB and P 16 KB leave one stage of each, so K is refilled in three groups of three panels and V
-// in two pages, each as soon as its last MMA is done: K has the time of a PV and an S to arrive, V
-// that of an S.  (The half of V that lies in a CTA's own K tile is loaded again: the MMA wants the
-// same keys at the same offset in both CTAs, and K wants different ones.)
+// Back to back, an MMA of this form takes 32 cycles at N = 128 and 64.5 at N = 256 (4060 multiply-adds a
+// cycle and SM, the dense rate), 25 at N = 64, so blocks of 64 keys would lose a third of S; a block
+// is 36 * 32 + 16 * 64.5 = 2190 cycles.  It also moves 280 KB through shared memory's 128 bytes a
+// cycle (operands 148 KB + 96 KB... of S and PV, 136 KB written by TMA): 3000 cycles, the nearer bound.
+// The price of the shape is room: Q 72 KB, K 72 KB,
+// V 64 KB and P 16 KB leave one stage of each, so K is refilled in two groups of panels and V in two
+// pages, each as soon as its last MMA is done: K has the time of a PV and an S to arrive, V that of
+// an S.  (The half of V that lies in a CTA's own K tile is loaded again: the MMA wants the same keys at
+// the same offset in both CTAs, and K wants different ones.)
 //
 // fp8 rows are first expanded to bf16 rows in the workspace (sparse_mla_prefix_expand_kernel), in
 // prefix order: dequantising in the main kernel would be repeated for every 128 query rows, and with
@@ -36,15 +38,15 @@
 // are multiplied: 0 times whatever the page holds there must stay 0.  A page number outside the
 // cache masks its page; rows of a page past the cache's end are masked.
 //
-// Roles (352 threads):
+// Roles (384 threads):
 //   warp 0      TMA producer (one thread).
-//   warp 1      S issuer (one thread of the even CTA) and TMEM owner.
+//   warp 1      S issuer (one thread of the even CTA) for dims 0 .. 319, and TMEM owner.
 //   warps 2-9   softmax, rescaling and output, two warps per TMEM lane quadrant: row r = lane % 64,
 //               page lane / 64 of a block and 32 of its keys, dims 256 (lane / 64) .. + 255 of O and
 //               128 of those.  The running max is moved only when it grows by more than 2^8; the four
 //               warps of a row vote per block and swap maxima only then.  (One warp per quadrant took
 //               2.4 us a block, longer than the block's MMAs.)
-//   warp 10     PV issuer (one thread of the even CTA).
+//   warp 10     PV issuer, warp 11 S issuer for dims 320 .. 575 (one thread of the even CTA each).
 // Every wait is bounded; a CTA that gives up meets the other at the final cluster barrier.
 #pragma once
 
@@ -58,11 +60,13 @@ constexpr int kPfPage = 64;                       // rows per page
 constexpr int kPfKeys = 2 * kPfPage;              // keys per block
 constexpr int kPfSoftmaxWarps = 8;
 constexpr int kPfPvWarp = 2 + kPfSoftmaxWarps;
-constexpr int kPfThreads = 32 * (kPfPvWarp + 1);
+constexpr int kPfS2Warp = kPfPvWarp + 1;
+constexpr int kPfThreads = 32 * (kPfS2Warp + 1);
 constexpr int kPfPanel = 64 * 128;                // 64 rows x 64 bf16, SW128
 constexpr int kPfQBytes = kPanels * kPfPanel;
-constexpr int kPfGroups = 3;                      // K is refilled in groups of panels
-constexpr int kPfGroupBytes = (kPanels / kPfGroups) * kPfPanel;
+constexpr int kPfGroupA = 5;                      // K in two groups of panels, 0 .. 4 and 5 .. 8, each with an
+constexpr int kPfGroupB = kPanels - kPfGroupA;    // issuing thread, a refill and an accumulator of its own
+static_assert(kPfGroupB == 4, "the second group is loaded by V's map (four panels)");
 constexpr int kPfVPage = 4 * kPfPanel;            // one page, this CTA's 256 dims
 constexpr int kPfMergeThreads = 512;
 constexpr int kPfExpandThreads = 256;
@@ -74,12 +78,14 @@ struct PfLayout {
     static constexpr int kOffP = kOffV + 2 * kPfVPage;        // two panels; output staging between pieces
     static constexpr int kOffX = kOffP + 2 * kPfPanel;        // [4][64] values swapped by a row's four threads
     static constexpr int kOffBar = kOffX + 4 * kPfHalf * 4;
-    static constexpr int kNumBars = 20;
+    static constexpr int kNumBars = 19;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag
     static constexpr int kBytes = kOffMisc + 16;
-    // TMEM columns: O [0, 256) | S x2 [256, 384)
+    // TMEM columns: O [0, 256) | two buffers of (S of the first group, S of the second), 64 each
     static constexpr int kColO = 0;
     static constexpr int kColS = 256;
+    static constexpr int kSBuf = 2 * kPfPage;
+    static_assert(kColS + 2 * kSBuf <= 512, "TMEM columns");
     static constexpr int kTmemCols = 512;
     static_assert(kBytes <= 232448, "shared memory budget (227 KB)");
 };
@@ -88,15 +94,15 @@ enum : int {
     kPbQFull = 0,    // even CTA: both CTAs' Q landed
     kPbQEmpty = 1,   // both: the S MMAs of the piece are done
     kPbKFull = 2,    // +group, even CTA
-    kPbKEmpty = 5,   // +group, both
-    kPbVFull = 8,    // +page of the block, even CTA
-    kPbVEmpty = 10,  // +page, both
-    kPbSFull = 12,   // +buffer, both
-    kPbSEmpty = 14,  // +buffer, even CTA
-    kPbPFull = 16,   // even CTA
-    kPbPvDone = 17,  // both
-    kPbTail = 18,    // own CTA: V of a page that the prefix ends in
-    kPbDrain = 19    // even CTA: everything both issuers issued is done
+    kPbKEmpty = 4,   // +group, both
+    kPbVFull = 6,    // +page of the block, even CTA
+    kPbVEmpty = 8,   // +page, both
+    kPbSFull = 10,   // +buffer, both
+    kPbSEmpty = 12,  // +buffer, even CTA
+    kPbPFull = 14,   // +page, even CTA
+    kPbPvDone = 16,  // both
+    kPbTail = 17,    // own CTA: V of a page that the prefix ends in
+    kPbDrain = 18    // even CTA: everything the issuers issued is done
 };
 
 struct PfParams {
@@ -189,8 +195,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (threadIdx.x == 0) {
         *sAbort = 0;
         for (int i = 0; i < L::kNumBars; ++i) {
-            const bool by_warps = i == kPbSEmpty || i == kPbSEmpty + 1 || i == kPbPFull;  // both CTAs' softmax warps
-            ptx::mbar_init(bar(i), by_warps ? 2 * kPfSoftmaxWarps : i == kPbDrain ? 2 : 1);
+            const bool by_warps = i == kPbSEmpty || i == kPbSEmpty + 1;                // both CTAs' softmax warps
+            const bool by_half = i == kPbPFull || i == kPbPFull + 1;                   // those of the page
+            const bool by_two = i == kPbQEmpty || i == kPbSFull || i == kPbSFull + 1;  // both S issuers
+            ptx::mbar_init(bar(i), by_warps ? 2 * kPfSoftmaxWarps : by_half ? kPfSoftmaxWarps : i == kPbDrain ? 3 : by_two ? 2 : 1);
         }
         ptx::fence_mbarrier_init();
     }
@@ -259,11 +267,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 }
                 for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
                     const int mine = rank == 0 ? row[0] : row[1];
-                    for (int g = 0; ok && g < kPfGroups; ++g) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
                         if (x > 0 && !(ok = wait(kPbKEmpty + g, (x - 1) & 1))) break;
-                        if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbKFull + g), 2u * kPfGroupBytes);
-                        ptx::tma_load_3d_pair(sbase + L::kOffK + g * kPfGroupBytes, &tm_k, 0, mine, g * (kPanels / kPfGroups),
-                                              even_bar(kPbKFull + g));
+                        const uint32_t bytes = static_cast<uint32_t>((g ? kPfGroupB : kPfGroupA) * kPfPanel);
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbKFull + g), 2u * bytes);
+                        ptx::tma_load_3d_pair(sbase + L::kOffK + g * kPfGroupA * kPfPanel, g ? &tm_v : &tm_k, 0, mine,
+                                              g * kPfGroupA, even_bar(kPbKFull + g));
                     }
                     const int next0 = page_row(2 * b + 2), next1 = page_row(2 * b + 3);  // loaded under the waits
                     if (ok && x > 0) ok = load_v(x - 1, b_v, row_v0, row_v1);
@@ -277,7 +287,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (ok && x > 0) ok = load_v(x - 1, b_v, row_v0, row_v1);
             // every copy has landed and been used, and no release of a stage is still on its way to
             // this CTA's barriers, before it leaves
-            for (int g = 0; ok && g < kPfGroups; ++g) ok = wait(kPbKEmpty + g, (x - 1) & 1);
+            for (int g = 0; ok && g < 2; ++g) ok = wait(kPbKEmpty + g, (x - 1) & 1);
             for (int i = 0; ok && i < 2; ++i) ok = wait(kPbVEmpty + i, (x - 1) & 1);
             if (ok) ok = wait(kPbQEmpty, (piece - 1) & 1);
             if (!ok) {  // gave up: copies in flight complete on the other CTA's barriers; leave them time to land
@@ -287,12 +297,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ================================================================ S issuer (TMEM owner)
+    } else if (warp == 1 || warp == kPfS2Warp) {
+        // ================================================================ S issuers
+        // Issuing an MMA costs its thread more time (45 cycles and more, its operands being moved to
+        // uniform registers each time, and as much again for waits and commits) than the tensor cores
+        // take for one of S (32), so S is two sums over the dims, each issued by a thread of its own
+        // into an accumulator of its own; the softmax adds them.
         if (rank == 0 && lane == 0) {
             constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kPfRows, kPfKeys, 0, 0);
-            const uint64_t dq = ptx::smem_desc_sw128(sbase + L::kOffQ, 16, 1024);
-            const uint64_t dk = ptx::smem_desc_sw128(sbase + L::kOffK, 16, 1024);
+            const bool ga = warp == 1;
+            const uint32_t off = ga ? 0u : static_cast<uint32_t>(kPfGroupA * kPfPanel);
+            const uint64_t dq = ptx::smem_desc_sw128(sbase + L::kOffQ + off, 16, 1024);
+            const uint64_t dk = ptx::smem_desc_sw128(sbase + L::kOffK + off, 16, 1024);
+            const uint32_t d0 = tmem + L::kColS + (ga ? 0 : kPfPage);
+            const int g = ga ? 0 : 1;
             bool ok = true;
             int x = 0, piece = 0;
             for (bool more = any; ok && more; more = w.next(), ++piece) {
@@ -300,23 +318,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
                     const int s = x & 1;
                     if (x >= 2 && !(ok = wait(kPbSEmpty + s, ((x >> 1) - 1) & 1))) break;
-                    const uint32_t d = tmem + L::kColS + s * kPfPage;
+                    if (!(ok = wait(kPbKFull + g, x & 1))) break;
+                    ptx::tc_fence_after();
+                    const uint32_t d = d0 + s * L::kSBuf;
 #pragma unroll
-                    for (int g = 0; g < kPfGroups; ++g) {
-                        if (!(ok = wait(kPbKFull + g, x & 1))) break;
-                        ptx::tc_fence_after();
+                    for (int pn = 0; pn < kPfGroupB; ++pn)
 #pragma unroll
-                        for (int j = 0; j < kPanels / kPfGroups; ++j)
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_bf16_ss_pair(d, dq + ((pn * kPfPanel + k * 32) >> 4), dk + ((pn * kPfPanel + k * 32) >> 4),
+                                                  kIdescS, (pn | k) != 0);
+                    if (ga) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int pn = g * (kPanels / kPfGroups) + j;
-                                ptx::mma_bf16_ss_pair(d, dq + ((pn * kPfPanel + k * 32) >> 4), dk + ((pn * kPfPanel + k * 32) >> 4),
-                                                      kIdescS, (pn | k) != 0);
-                            }
-                        ptx::mma_commit_pair(bar(kPbKEmpty + g));
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_bf16_ss_pair(d, dq + ((kPfGroupB * kPfPanel + k * 32) >> 4),
+                                                  dk + ((kPfGroupB * kPfPanel + k * 32) >> 4), kIdescS, 1u);
                     }
-                    if (!ok) break;
                     ptx::mma_commit_pair(bar(kPbSFull + s));
+                    ptx::mma_commit_pair(bar(kPbKEmpty + g));
                     if (b + 1 == w.b1) ptx::mma_commit_pair(bar(kPbQEmpty));
                 }
             }
@@ -327,9 +345,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         __syncwarp();
     } else if (warp == kPfPvWarp) {
         // ================================================================ PV issuer
-        // A thread of its own: issuing an MMA costs its thread more time (76 cycles for S, 120 for PV,
-        // with their operands moved to uniform registers each time) than the tensor cores take for it
-        // (32 and 64), so two threads issue side by side.
+        // A thread of its own, for the same reason.
         if (rank == 0 && lane == 0) {
             constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kPfRows, 256, 0, 1);
             const uint64_t dv = ptx::smem_desc_sw128(sbase + L::kOffV, kPfPanel, 1024);
@@ -339,9 +355,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             int x = 0;
             for (bool more = any; ok && more; more = w.next()) {
                 for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
-                    if (!(ok = wait(kPbPFull, x & 1))) break;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
+                        if (!(ok = wait(kPbPFull + i, x & 1))) break;
                         if (!pf_tail(p, 2 * b + i)) {
                             if (!(ok = wait(kPbVFull + i, (v_parity >> i) & 1u))) break;
                             v_parity ^= 1u << i;
@@ -384,7 +400,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             __syncwarp();
             return okw;
         };
-        const uint32_t s_empty0 = even_bar(kPbSEmpty), s_empty1 = even_bar(kPbSEmpty + 1), p_full = even_bar(kPbPFull);
+        const uint32_t s_empty0 = even_bar(kPbSEmpty), s_empty1 = even_bar(kPbSEmpty + 1), p_full = even_bar(kPbPFull + half);
         const uint32_t p_row = sbase + L::kOffP + half * kPfPanel + r * 128;
         const int ocol0 = L::kColO + 128 * sub;
         bool failed = false;
@@ -401,13 +417,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (!failed && !warp_wait(kPbSFull + s, (x >> 1) & 1)) failed = true;
                 if (!failed) {
                     ptx::tc_fence_after();
+                    uint32_t sw[32];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        SMLA_TMEM_LD16(tmem + lane_base + L::kColS + s * kPfPage + 32 * sub + 16 * q, sv + 16 * q);
+                    for (int q = 0; q < 2; ++q) {
+                        SMLA_TMEM_LD16(tmem + lane_base + L::kColS + s * L::kSBuf + 32 * sub + 16 * q, sv + 16 * q);
+                        SMLA_TMEM_LD16(tmem + lane_base + L::kColS + s * L::kSBuf + kPfPage + 32 * sub + 16 * q, sw + 16 * q);
+                    }
                     ptx::tmem_wait_ld();
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(s ? s_empty1 : s_empty0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 y = ptx::add2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])),
+                                                   make_float2(__uint_as_float(sw[2 * i]), __uint_as_float(sw[2 * i + 1])));
+                        sv[2 * i] = __float_as_uint(y.x);
+                        sv[2 * i + 1] = __float_as_uint(y.y);
+                    }
                     if (flip) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) sv[i] ^= 0x80000000u;
@@ -489,8 +515,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     pk[i] = ptx::cvt_bf16x2(pp.x, pp.y);
                 }
                 l += ((la[0].x + la[0].y) + (la[1].x + la[1].y)) + ((la[2].x + la[2].y) + (la[3].x + la[3].y));
-                // P is one buffer: PV(x - 1) has read it
-                if (x > 0 && !warp_wait(kPbPvDone, (x - 1) & 1)) {
+                // P's panel of this page is one buffer: the page's MMAs of PV(x - 1) have read it
+                if (x > 0 && !warp_wait(kPbVEmpty + half, (x - 1) & 1)) {
                     failed = true;
                     continue;  // the next reduction (or the one after the loop) takes the group out
                 }
@@ -498,22 +524,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 for (int q = 0; q < 4; ++q)
                     ptx::st_shared_v4(p_row + ((static_cast<uint32_t>(4 * sub + q) ^ static_cast<uint32_t>(r & 7)) << 4),
                                       make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
-                for (int i = 0; i < 2; ++i) {
-                    if (!pf_tail(p, 2 * b + i)) continue;
-                    // the page's rows past the prefix's end, zeroed in this CTA's V tile
+                if (pf_tail(p, 2 * b + half)) {
+                    // the page's rows past the prefix's end, zeroed in this CTA's V tile by the page's warps
                     if (!warp_wait(kPbTail, tails & 1)) {
                         failed = true;
-                        break;
+                        continue;
                     }
                     ++tails;
                     const int first = static_cast<int>(p.prefix % kPfPage);
-                    const int tid = (warp - 2) * 32 + lane;
-                    const uint32_t vt = sbase + L::kOffV + i * kPfVPage;
-                    for (int j = tid; j < (kPfPage - first) * 32; j += 32 * kPfSoftmaxWarps)
+                    const int tid = (2 * sub + (quad & 1)) * 32 + lane;
+                    const uint32_t vt = sbase + L::kOffV + half * kPfVPage;
+                    for (int j = tid; j < (kPfPage - first) * 32; j += 128)
                         ptx::st_shared_v4(vt + (j & 3) * kPfPanel + (first + (j >> 5)) * 128 + ((j >> 2) & 7) * 16,
                                           make_uint4(0u, 0u, 0u, 0u));
                 }
-                if (failed) continue;
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_cluster(p_full);
