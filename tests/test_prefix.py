@@ -300,11 +300,11 @@ def test_no_tokens_is_a_noop(lib):
 
 
 def test_workspace_bytes(lib):
-    """None where no tile is cut, else two slots of a tile's rows per CTA pair (152 SMs assumed without
-    a device), rounded up to 256 bytes."""
+    """None where no tile is cut, else two slots of a tile's rows, in groups of 32, per CTA pair (152
+    SMs assumed without a device), rounded up to 256 bytes."""
 
     def partials(runs, rows):
-        return -(-2 * runs * rows * 514 * 4 // 256) * 256
+        return -(-2 * runs * (-(-rows // 32) * 32) * 514 * 4 // 256) * 256
 
     assert smla.prefix_workspace_bytes(0, 8, 100) == 0 and smla.prefix_workspace_bytes(1, 8, 0) == 0
     assert smla.prefix_workspace_bytes(1, 8, 128) == 0

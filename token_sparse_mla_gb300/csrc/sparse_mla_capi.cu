@@ -445,7 +445,7 @@ smla_status launch(const void* q, const void* kv, const int32_t* idx, int32_t T,
 // CTA pair; and its workspace: the partials of cut tiles, if any, and the expanded rows of an fp8 cache.
 struct PrefixPlan {
     int64_t rows = 0, tiles = 0, npages = 0, nblk = 0, work = 0;
-    int runs = 0, slot_rows = 0;
+    int runs = 0, slot_groups = 0;
     bool cut = false;
     size_t off_ml = 0, off_expanded = 0, bytes = 0;
 };
@@ -459,10 +459,12 @@ PrefixPlan prefix_plan(int64_t rows, int64_t prefix, bool fp8, int num_sms) {
     pl.work = pl.tiles * pl.nblk;
     if (pl.work == 0) return pl;
     const int64_t pairs = num_sms / 2;
-    pl.runs = static_cast<int>(pl.work < pairs ? pl.work : pairs);
-    pl.slot_rows = static_cast<int>(rows < smla::kPfRows ? rows : smla::kPfRows);
+    // as few runs as keep the longest one's length: each run of a cut tile costs a partial
+    const int64_t longest = (pl.work + pairs - 1) / pairs;
+    pl.runs = static_cast<int>((pl.work + longest - 1) / longest);
+    pl.slot_groups = static_cast<int>(((rows < smla::kPfRows ? rows : smla::kPfRows) + 31) / 32);
     for (int k = 1; k < pl.runs && !pl.cut; ++k) pl.cut = (pl.work * k / pl.runs) % pl.nblk != 0;
-    const size_t slots = pl.cut ? static_cast<size_t>(pl.runs) * 2 * pl.slot_rows : 0;
+    const size_t slots = pl.cut ? static_cast<size_t>(pl.runs) * 2 * pl.slot_groups * 32 : 0;  // rows in all slots
     pl.off_ml = slots * smla::kDV * 4;
     pl.off_expanded = align256(pl.off_ml + slots * 2 * 4);
     pl.bytes = pl.off_expanded + (fp8 ? static_cast<size_t>(pl.npages) * smla::kPfPage * smla::kDQK * 2 : 0);
@@ -1101,7 +1103,7 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
     if (!aligned(block_table, 4) || !aligned(lse, 4))
         return fail(SMLA_ERR_INVALID_ARG, "block_table and lse must be 4-byte aligned");
     const int64_t rows = static_cast<int64_t>(T) * h;
-    if (rows > 0x7fffff00LL) return fail(SMLA_ERR_INVALID_ARG, "T * h too large (%d, %d)", T, h);
+    if (rows > 0x7f000000LL) return fail(SMLA_ERR_INVALID_ARG, "T * h too large (%d, %d)", T, h);
     int dev = 0;
     DeviceState* ds = nullptr;
     smla_status st = device_state(&dev, &ds);
@@ -1167,7 +1169,7 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
     pp.npages = static_cast<int32_t>(pl.npages);
     pp.nblk = static_cast<int32_t>(pl.nblk);
     pp.runs = pl.runs;
-    pp.slot_rows = pl.slot_rows;
+    pp.slot_groups = pl.slot_groups;
     pp.sm_scale_log2 = scale * 1.4426950408889634f;
     if (fp8) {
         cfg.gridDim = dim3(static_cast<unsigned>(pl.npages * smla::kPfPage / (smla::kPfExpandThreads / 32)), 1, 1);
@@ -1187,7 +1189,7 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
     if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
     if (pl.cut) {
         cfg.numAttrs = 1;
-        cfg.gridDim = dim3(static_cast<unsigned>(rows), 1, 1);
+        cfg.gridDim = dim3(static_cast<unsigned>((rows + 31) / 32 * (smla::kDV / smla::kPfMergeDims)), 1, 1);
         cfg.blockDim = dim3(smla::kPfMergeThreads, 1, 1);
         cfg.dynamicSmemBytes = 0;
         e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel, pp);

@@ -68,7 +68,11 @@ constexpr int kPfGroupA = 5;                      // K in two groups of panels, 
 constexpr int kPfGroupB = kPanels - kPfGroupA;    // issuing thread, a refill and an accumulator of its own
 static_assert(kPfGroupB == 4, "the second group is loaded by V's map (four panels)");
 constexpr int kPfVPage = 4 * kPfPanel;            // one page, this CTA's 256 dims
-constexpr int kPfMergeThreads = 512;
+constexpr int kPfAhead = 3;                       // blocks between a page's prefetch into L2 and its load
+constexpr int kPfMergeChunks = 4;                 // four dims each
+constexpr int kPfMergeParts = 4;                  // warps that share a chunk's pieces
+constexpr int kPfMergeThreads = 32 * kPfMergeChunks * kPfMergeParts;
+constexpr int kPfMergeDims = 4 * kPfMergeChunks;
 constexpr int kPfExpandThreads = 256;
 
 struct PfLayout {
@@ -111,14 +115,16 @@ struct PfParams {
     const int32_t* pages;        // [npages]
     __nv_bfloat16* out;          // [rows, 512]
     float* lse;                  // [rows]
-    float* part_o;               // [2 * runs][slot_rows][512]
-    float* part_ml;              // [2 * runs][slot_rows][2]: running max (log2 units), sum
+    // partials of cut tiles, rows in groups of 32 with neighbouring rows next to each other, so that a
+    // warp (a lane per row) stores and loads whole lines
+    float* part_o;               // [2 * runs][slot_groups][128][32][4]: dims 4 j .. 4 j + 3 of 32 rows
+    float* part_ml;              // [2 * runs][slot_groups][2][32]: running max (log2 units), sum
     int64_t rows;                // T * h
     int64_t prefix;              // P
     int64_t num_slots;
     int64_t work;                // tiles * nblk
     int32_t npages, nblk, runs;
-    int32_t slot_rows;           // min(128, rows)
+    int32_t slot_groups;         // groups of 32 rows in a tile: ceil(min(128, rows) / 32)
     float sm_scale_log2;
 };
 
@@ -253,6 +259,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 }
                 return true;
             };
+            // this CTA's pages a few blocks ahead, into L2: K of a block is loaded one block before its use,
+            // and from HBM that is too late (8 tiles x 65536 rows: 2.2 us a block, 1.5 from L2)
+            auto prefetch = [&](int b) {
+                if (p.expanded != nullptr || b >= p.nblk) return;
+                const int i = 2 * b + rank;
+                const int page = pf_page(p, i);
+                const int n = pf_valid(p, i, page);
+                if (n > 0)
+                    ptx::bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(p.kv) + static_cast<int64_t>(page) * kPfPage * kDQK,
+                                          static_cast<uint32_t>(n * kDQK * 2));
+            };
             bool ok = true;
             int x = 0, piece = 0, b_v = 0;
             int row_v0 = 0, row_v1 = 0;
@@ -275,6 +292,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         ptx::tma_load_3d_pair(sbase + L::kOffK + g * kPfGroupA * kPfPanel, g ? &tm_v : &tm_k, 0, mine,
                                               g * kPfGroupA, even_bar(kPbKFull + g));
                     }
+                    if (x == 0)
+                        for (int a = 1; a < kPfAhead; ++a) prefetch(b + a);
+                    prefetch(b + kPfAhead);
                     const int next0 = page_row(2 * b + 2), next1 = page_row(2 * b + 3);  // loaded under the waits
                     if (ok && x > 0) ok = load_v(x - 1, b_v, row_v0, row_v1);
                     row_v0 = row[0];
@@ -552,42 +572,30 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const int64_t row0 = w.tile * kPfRows + rank * kPfHalf + (quad & 1) * 32;  // the warp's first row
             const int live = p.rows - row0 < 32 ? static_cast<int>(p.rows - row0) : 32;  // rows of the warp, if any
             const bool whole = w.b0 == 0 && w.b1 == p.nblk;
-            const int64_t prow0 = (2 * static_cast<int64_t>(run) + (w.first ? 0 : 1)) * p.slot_rows + rank * kPfHalf + (quad & 1) * 32;
+            const int64_t pgroup = (2 * static_cast<int64_t>(run) + (w.first ? 0 : 1)) * p.slot_groups + 2 * rank + (quad & 1);
             const float inv = lt > 0.f || lt != lt ? 1.0f / lt : 0.f;
             if (!failed && lane < live && part == 0) {
                 if (whole) {
                     p.lse[row0 + lane] = lt == 0.f ? -CUDART_INF_F : (m + log2f(lt)) * 0.69314718055994531f;
                 } else {
-                    p.part_ml[2 * (prow0 + lane)] = m;
-                    p.part_ml[2 * (prow0 + lane) + 1] = lt;
+                    p.part_ml[64 * pgroup + lane] = m;
+                    p.part_ml[64 * pgroup + 32 + lane] = lt;
                 }
             }
-            // 32 rows x 64 bytes at a time through this warp's eighth of P's buffer (free until the
-            // next block's P): whole sectors, where a row per lane would touch 32 lines at once
+            // Out: 32 rows x 64 bytes at a time through this warp's eighth of P's buffer (free until the
+            // next block's P): whole sectors, where a row per lane would touch 32 lines at once.  Partials
+            // go as they are, each instruction 512 contiguous bytes.
             if (!failed && live > 0) {
                 const uint32_t stage = sbase + L::kOffP + (warp - 2) * 32 * 64;
-                auto put = [&](int e, uint4 v) {
-                    ptx::st_shared_v4(stage + lane * 64 + ((static_cast<uint32_t>(e) ^ static_cast<uint32_t>((lane >> 1) & 3)) << 4), v);
-                };
-                auto copy_out = [&](char* dst, int64_t pitch) {
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int rr = 8 * e + (lane >> 2);
-                        const uint4 v = ptx::ld_shared_v4(stage + rr * 64 + ((static_cast<uint32_t>(lane & 3) ^ static_cast<uint32_t>((rr >> 1) & 3)) << 4));
-                        if (rr < live) *reinterpret_cast<uint4*>(dst + rr * pitch + (lane & 3) * 16) = v;
-                    }
-                    __syncwarp();
-                };
-                // 64 columns of O are read at a time
+                float4* part = reinterpret_cast<float4*>(p.part_o) + (pgroup * 128 + 64 * half + 32 * sub) * 32 + lane;
 #pragma unroll 1
-                for (int cc = 0; cc < 2; ++cc) {
+                for (int cc = 0; cc < 2; ++cc) {  // 64 columns of O are read at a time
                     uint32_t ov[64];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) SMLA_TMEM_LD16(tmem + lane_base + ocol0 + cc * 64 + 16 * q, ov + 16 * q);
                     ptx::tmem_wait_ld();
-                    const int64_t d0 = 256 * half + 128 * sub + 64 * cc;
                     if (whole) {
+                        __nv_bfloat16* dst = p.out + row0 * kDV + 256 * half + 128 * sub + 64 * cc + (lane & 3) * 8;
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -597,18 +605,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                                 for (int j = 0; j < 4; ++j)
                                     v[j] = ptx::cvt_bf16x2(__uint_as_float(ov[32 * u + 8 * e + 2 * j]) * inv,
                                                            __uint_as_float(ov[32 * u + 8 * e + 2 * j + 1]) * inv);
-                                put(e, make_uint4(v[0], v[1], v[2], v[3]));
+                                ptx::st_shared_v4(stage + lane * 64 + ((static_cast<uint32_t>(e) ^ static_cast<uint32_t>((lane >> 1) & 3)) << 4),
+                                                  make_uint4(v[0], v[1], v[2], v[3]));
                             }
-                            copy_out(reinterpret_cast<char*>(p.out + row0 * kDV + d0 + 32 * u), kDV * 2);
-                        }
-                    } else {
+                            __syncwarp();
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                put(e, make_uint4(ov[16 * u + 4 * e], ov[16 * u + 4 * e + 1], ov[16 * u + 4 * e + 2], ov[16 * u + 4 * e + 3]));
-                            copy_out(reinterpret_cast<char*>(p.part_o + prow0 * kDV + d0 + 16 * u), kDV * 4);
+                            for (int e = 0; e < 4; ++e) {
+                                const int rr = 8 * e + (lane >> 2);
+                                const uint4 v = ptx::ld_shared_v4(stage + rr * 64 + ((static_cast<uint32_t>(lane & 3) ^ static_cast<uint32_t>((rr >> 1) & 3)) << 4));
+                                if (rr < live) *reinterpret_cast<uint4*>(dst + rr * kDV + 32 * u) = v;
+                            }
+                            __syncwarp();
                         }
+                    } else if (lane < live) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            part[(16 * cc + e) * 32] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                                                   __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
                     }
                 }
             }
@@ -655,72 +668,104 @@ __global__ void __launch_bounds__(kPfExpandThreads) sparse_mla_prefix_expand_ker
     if (lane < 8) dst[64 + lane] = rope;
 }
 
-// Joins the pieces of cut tiles, one CTA per query row: weights 2^(m_k - M) of the running maxima.
-// Four groups of 128 threads take every fourth piece each (their loads in flight together) and meet
-// in shared memory, in a fixed order.  Reads what the pieces wrote once (from L2 as a rule).
+// Joins the pieces of cut tiles by log-sum-exp weights.  A CTA takes 32 query rows (a lane each) and 16
+// dims; four warps share the pieces of four dims, each every fourth piece in order with all loads of a
+// batch in flight together, and meet in shared memory in a fixed order.  Every load is a whole line, and
+// what the pieces wrote is read once, from L2 as a rule.  (One warp over all pieces of its dims took
+// 20 us for 38 pieces of 256 rows: a round of latency per eight pieces, twice.)
 __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kernel(const PfParams p) {
-    __shared__ float4 s_acc[3][128];
-    __shared__ float s_l[4];
+    __shared__ float4 s_acc[kPfMergeParts][kPfMergeChunks][32];
+    __shared__ float s_m[kPfMergeParts][32], s_l[kPfMergeParts][32];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int64_t row = blockIdx.x;
-    const int64_t tile = row / kPfRows;
-    const int rt = static_cast<int>(row % kPfRows);
+    const int lane = threadIdx.x & 31;
+    const int chunk = (threadIdx.x >> 5) % kPfMergeChunks, part = (threadIdx.x >> 5) / kPfMergeChunks;
+    constexpr int kDimGroups = kDV / kPfMergeDims;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x / kDimGroups) * 32;
+    const int dg = static_cast<int>(blockIdx.x % kDimGroups);
+    const int64_t tile = row0 / kPfRows;
+    const int group = static_cast<int>(row0 % kPfRows) / 32;
     auto run_of = [&](int64_t b) -> int { return static_cast<int>(((b + 1) * p.runs - 1) / p.work); };
     const int k0 = run_of(tile * p.nblk), k1 = run_of((tile + 1) * p.nblk - 1);
     if (k0 == k1) return;  // the tile lies inside one run, which wrote it
     // this tile is the first piece of every run that starts inside it; the run that it begins in
     // keeps it in its second slot, unless that run starts with it
     const int first_slot = 2 * k0 + (p.work * k0 / p.runs == tile * p.nblk ? 0 : 1);
-    auto slot_row = [&](int k) -> int64_t {
-        return static_cast<int64_t>(k == k0 ? first_slot : 2 * k) * p.slot_rows + rt;
+    auto group_of = [&](int k) -> int64_t {
+        return static_cast<int64_t>(k == k0 ? first_slot : 2 * k) * p.slot_groups + group;
     };
-    const int grp = threadIdx.x >> 7, tid = threadIdx.x & 127;
-    float m = -CUDART_INF_F;
-    for (int k = k0; k <= k1; ++k) m = fmaxf(m, p.part_ml[2 * slot_row(k)]);
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int live = p.rows - row0 < 32 ? static_cast<int>(p.rows - row0) : 32;
+    const int at = lane < live ? lane : live - 1;  // a lane past the last row repeats it and stores nothing
+    const float4* part_o = reinterpret_cast<const float4*>(p.part_o) + (dg * kPfMergeChunks + chunk) * 32 + at;
     constexpr int kFlight = 6;
-    for (int kk = k0 + grp; kk <= k1; kk += 4 * kFlight) {
+    float m = -CUDART_INF_F, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int kk = k0 + part; kk <= k1; kk += kPfMergeParts * kFlight) {
         float4 v[kFlight];
-        float wt[kFlight], lk[kFlight];
+        float mk[kFlight], lk[kFlight];
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const int k = kk + 4 * u;
-            const int64_t sr = slot_row(k <= k1 ? k : k1);
-            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * sr);
-            wt[u] = k > k1 || ml.x == -CUDART_INF_F ? 0.f : ptx::ex2_approx(ml.x - m);
-            lk[u] = k > k1 ? 0.f : ml.y;
-            v[u] = reinterpret_cast<const float4*>(p.part_o + sr * kDV)[tid];
-            if (k > k1) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int64_t g = group_of(min(kk + kPfMergeParts * u, k1));
+            mk[u] = __ldg(p.part_ml + 64 * g + at);
+            lk[u] = __ldg(p.part_ml + 64 * g + 32 + at);
+            v[u] = __ldg(part_o + g * (128 * 32));
         }
+        float mn = m;
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            l += wt[u] * lk[u];
-            // a piece without a key has the sum 0 and zero rows: P was 0 and V had no NaN
-            acc.x += wt[u] * v[u].x;
-            acc.y += wt[u] * v[u].y;
-            acc.z += wt[u] * v[u].z;
-            acc.w += wt[u] * v[u].w;
+            const bool past = kk + kPfMergeParts * u > k1;
+            if (past) {
+                mk[u] = -CUDART_INF_F;
+                lk[u] = 0.f;
+                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            mn = fmaxf(mn, mk[u]);
+        }
+        // a piece without a key has the sum 0 and zero rows: P was 0 and V had no NaN
+        const float keep = m == -CUDART_INF_F ? 0.f : ptx::ex2_approx(m - mn);
+        m = mn;
+        l *= keep;
+        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const float wt = mk[u] == -CUDART_INF_F ? 0.f : ptx::ex2_approx(mk[u] - m);
+            l += wt * lk[u];
+            acc.x += wt * v[u].x;
+            acc.y += wt * v[u].y;
+            acc.z += wt * v[u].z;
+            acc.w += wt * v[u].w;
         }
     }
-    if (grp > 0) s_acc[grp - 1][tid] = acc;
-    if (tid == 0) s_l[grp] = l;
+    s_acc[part][chunk][lane] = acc;
+    if (chunk == 0) {
+        s_m[part][lane] = m;
+        s_l[part][lane] = l;
+    }
     __syncthreads();
-    if (grp > 0) return;
-    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+    if (part > 0) return;
+    float mp[kPfMergeParts];
 #pragma unroll
-    for (int g = 0; g < 3; ++g) {
-        const float4 o = s_acc[g][tid];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
+    for (int q = 0; q < kPfMergeParts; ++q) mp[q] = s_m[q][lane];
+    m = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < kPfMergeParts; ++q) {
+        const float wt = mp[q] == -CUDART_INF_F ? 0.f : ptx::ex2_approx(mp[q] - m);
+        const float4 o = s_acc[q][chunk][lane];
+        l += wt * s_l[q][lane];
+        acc.x += wt * o.x;
+        acc.y += wt * o.y;
+        acc.z += wt * o.z;
+        acc.w += wt * o.w;
     }
     const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-    reinterpret_cast<uint2*>(p.out + row * kDV)[tid] =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (tid == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+    if (lane < live) {
+        reinterpret_cast<uint2*>(p.out + (row0 + lane) * kDV + dg * kPfMergeDims)[chunk] =
+            make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
+        if (dg == 0 && chunk == 0)
+            p.lse[row0 + lane] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+    }
 }
 
 // The result over no keys: O = 0, LSE = -inf.
