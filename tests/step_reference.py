@@ -1,8 +1,25 @@
 """Plain 64-bit forms of the operators around the attention (append, q_up, prefix), written from
-their definitions in include/sparse_mla.h.  CPU, numpy; no code of the library."""
+their definitions in include/sparse_mla.h (CPU, numpy; no code of the library), and what their
+tests share."""
 
 import numpy as np
+import pytest
 import torch
+
+from tests import test_binding_marshal as marshal
+from token_sparse_mla_gb300 import _binding
+
+CUDA0, STREAM, _d = marshal.CUDA0, marshal.STREAM, marshal._d
+base_fake = marshal.fake
+
+
+@pytest.fixture
+def fake(base_fake, monkeypatch):
+    """The recording library of the marshalling tests, with the raw handle of the current stream."""
+    monkeypatch.setattr(_binding, "_current_handle", lambda dev: STREAM)
+    _binding._prefix_workspace_bytes.cache_clear()
+    yield base_fake
+    _binding._prefix_workspace_bytes.cache_clear()
 
 
 def to64(x: torch.Tensor) -> np.ndarray:

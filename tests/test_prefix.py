@@ -15,7 +15,7 @@ import torch
 
 import token_sparse_mla_gb300 as smla
 from tests import step_reference as ref
-from tests.test_binding_marshal import CUDA0, STREAM, _d, fake  # noqa: F401
+from tests.step_reference import CUDA0, STREAM, _d, base_fake, fake  # noqa: F401
 
 DEV = "cuda:0"
 SCALE = 576 ** -0.5

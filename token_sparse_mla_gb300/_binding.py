@@ -376,13 +376,60 @@ def sparse_mla_masked_mha(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mas
     return out, lse
 
 
+# ---- append, q_up and prefix.  A decode step makes these calls once per layer, so what they cost on the
+# host counts: a call of theirs reads each tensor's attributes once, takes the raw stream handle and
+# enters no context when the device is already current.
+
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _current_handle(dev: torch.device) -> int:
+    """Raw handle of torch's current stream on dev (a stream object costs 2 us to make)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _call(dev: torch.device, stream, fn, *args) -> None:
+    """fn(*args, stream handle) with dev current; raises on a status other than OK."""
+    handle = _current_handle(dev) if stream is None else _stream_handle(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != 0:
+        _check(st)
+
+
+def _together(dev: torch.device, **tensors) -> None:
+    """All tensors on the CUDA device dev."""
+    for name, t in tensors.items():
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+
+
+def _cuda_device(name: str, t: torch.Tensor) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    return t.device
+
+
 def _positions_and_table(T: int, positions: torch.Tensor, cos_sin: torch.Tensor) -> int:
-    if positions.shape != (T,) or positions.dtype != torch.int32 or not positions.is_contiguous():
+    if positions.shape != (T,) or positions.dtype != _I32 or not positions.is_contiguous():
         raise ValueError(f"positions must be a contiguous [{T}] int32 tensor")
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != D_QK - D_V or cos_sin.dtype != torch.float32 \
-            or not cos_sin.is_contiguous():
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != D_QK - D_V or cos_sin.dtype != _F32 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous [max_pos, 64] fp32 tensor")
-    return int(cos_sin.shape[0])
+    return cos_sin.shape[0]
+
+
+def _cache_rows(kv_cache: torch.Tensor, kv_format: str) -> int:
+    """num_slots of a cache tensor of the given format."""
+    if kv_format not in KV_FORMATS:
+        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
+    row, dtype = (D_QK, _BF16) if kv_format == "bf16" else (FP8_ROW_BYTES, _U8)
+    if kv_cache.dim() != 2 or kv_cache.shape[1] != row or kv_cache.dtype != dtype or not kv_cache.is_contiguous():
+        raise ValueError(f"{kv_format} kv_cache must be a contiguous [num_slots, {row}] {dtype} tensor, got "
+                         f"{tuple(kv_cache.shape)} {kv_cache.dtype}")
+    return kv_cache.shape[0]
 
 
 def sparse_mla_append(kv: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor, kv_cache: torch.Tensor,
@@ -398,34 +445,30 @@ def sparse_mla_append(kv: torch.Tensor, positions: torch.Tensor, slots: torch.Te
     -1 must be distinct.  A slot or position out of range writes nothing and makes the next
     sync_status() raise SMLA_ERR_INDEX_RANGE.
     """
-    if kv.dim() != 2 or kv.shape[1] != D_QK or kv.dtype != torch.bfloat16:
+    if kv.dim() != 2 or kv.shape[1] != D_QK or kv.dtype != _BF16:
         raise ValueError(f"kv must be [T, 576] bf16, got {tuple(kv.shape)} {kv.dtype}")
-    T = int(kv.shape[0])
-    row_stride = int(kv.stride(0)) if T > 1 else D_QK
-    if kv.stride(1) != 1 or row_stride < D_QK or row_stride % 8:
+    T = kv.shape[0]
+    row_stride, inner = kv.stride()
+    if T <= 1:
+        row_stride = D_QK
+    if inner != 1 or row_stride < D_QK or row_stride % 8:
         raise ValueError(f"kv rows must be contiguous and a multiple of 8 elements (>= 576) apart, "
                          f"got strides {tuple(kv.stride())}")
-    if slots.shape != (T,) or slots.dtype != torch.int32 or not slots.is_contiguous():
+    if slots.shape != (T,) or slots.dtype != _I32 or not slots.is_contiguous():
         raise ValueError(f"slots must be a contiguous [{T}] int32 tensor")
     max_pos = _positions_and_table(T, positions, cos_sin)
-    if kv_format not in KV_FORMATS:
-        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
-    row, dtype = (D_QK, torch.bfloat16) if kv_format == "bf16" else (FP8_ROW_BYTES, torch.uint8)
-    if kv_cache.dim() != 2 or kv_cache.shape[1] != row or kv_cache.dtype != dtype or not kv_cache.is_contiguous():
-        raise ValueError(f"{kv_format} kv_cache must be a contiguous [num_slots, {row}] {dtype} tensor, got "
-                         f"{tuple(kv_cache.shape)} {kv_cache.dtype}")
-    tensors = [("kv", kv), ("positions", positions), ("slots", slots), ("kv_cache", kv_cache), ("cos_sin", cos_sin)]
+    num_slots = _cache_rows(kv_cache, kv_format)
+    dev = _cuda_device("kv", kv)
+    _together(dev, positions=positions, slots=slots, kv_cache=kv_cache, cos_sin=cos_sin)
+    weight = None
     if norm_weight is not None:
-        if norm_weight.shape != (D_V,) or norm_weight.dtype != torch.bfloat16 or not norm_weight.is_contiguous():
+        if norm_weight.shape != (D_V,) or norm_weight.dtype != _BF16 or not norm_weight.is_contiguous():
             raise ValueError("norm_weight must be a contiguous [512] bf16 tensor")
-        tensors.append(("norm_weight", norm_weight))
-    dev = _device_of(tensors)
-    with _on(dev):
-        st = library().sparse_mla_append(
-            kv.data_ptr(), row_stride, positions.data_ptr(), slots.data_ptr(), T, cos_sin.data_ptr(), max_pos,
-            int(bool(interleaved)), None if norm_weight is None else norm_weight.data_ptr(), float(eps),
-            kv_cache.data_ptr(), int(kv_cache.shape[0]), KV_FORMATS[kv_format], _stream_handle(stream, dev))
-    _check(st)
+        _together(dev, norm_weight=norm_weight)
+        weight = norm_weight.data_ptr()
+    _call(dev, stream, library().sparse_mla_append, kv.data_ptr(), row_stride, positions.data_ptr(), slots.data_ptr(),
+          T, cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, weight, eps, kv_cache.data_ptr(), num_slots,
+          KV_FORMATS[kv_format])
     return kv_cache
 
 
@@ -439,26 +482,30 @@ def sparse_mla_q_up(q: torch.Tensor, w: torch.Tensor, positions: torch.Tensor, c
     sparse_mla_append; returns out [T, h, 576] bf16.  Any other position out of range gives zero rope
     dims and makes the next sync_status() raise SMLA_ERR_INDEX_RANGE.
     """
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+    if q.dim() != 3 or q.dtype != _BF16 or not q.is_contiguous():
         raise ValueError("q must be a contiguous [T, h, dn + 64] bf16 tensor")
-    T, h, d = (int(x) for x in q.shape)
+    T, h, d = q.shape
     dn = d - (D_QK - D_V)
-    if w.shape != (h, dn, D_V) or w.dtype != torch.bfloat16 or not w.is_contiguous():
+    if w.shape != (h, dn, D_V) or w.dtype != _BF16 or not w.is_contiguous():
         raise ValueError(f"w must be a contiguous [{h}, {dn}, 512] bf16 tensor")
     max_pos = _positions_and_table(T, positions, cos_sin)
-    dev = _device_of((("q", q), ("w", w), ("positions", positions), ("cos_sin", cos_sin)))
+    dev = _cuda_device("q", q)
+    _together(dev, w=w, positions=positions, cos_sin=cos_sin)
     if out is None:
-        out = torch.empty((T, h, D_QK), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, h, D_QK), dtype=_BF16, device=dev)
     else:
-        if out.shape != (T, h, D_QK) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        if out.shape != (T, h, D_QK) or out.dtype != _BF16 or not out.is_contiguous():
             raise ValueError("out must be a contiguous [T, h, 576] bf16 tensor")
-        _device_of((("q", q), ("out", out)))
-    with _on(dev):
-        st = library().sparse_mla_q_up(
-            q.data_ptr(), w.data_ptr(), positions.data_ptr(), T, h, dn, cos_sin.data_ptr(), max_pos,
-            int(bool(interleaved)), out.data_ptr(), _stream_handle(stream, dev))
-    _check(st)
+        _together(dev, out=out)
+    _call(dev, stream, library().sparse_mla_q_up, q.data_ptr(), w.data_ptr(), positions.data_ptr(), T, h, dn,
+          cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, out.data_ptr())
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_workspace_bytes(device_index: int, T: int, h: int, prefix_len: int, fmt: int) -> int:
+    """The library's answer for the device that is current, asked once per shape and device."""
+    return int(library().sparse_mla_prefix_workspace_bytes(T, h, prefix_len, fmt))
 
 
 def prefix_workspace_bytes(T: int, h: int, prefix_len: int, kv_format: str = "bf16") -> int:
@@ -476,59 +523,62 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
 
     Returns out [T, h, 512] bf16 and lse [T, h] fp32, which sparse_mla_merge joins with each token's
     own part.  scale defaults to 576 ** -0.5.  workspace: a uint8 tensor of prefix_workspace_bytes(T,
-    h, prefix_len, kv_format) bytes for callers that keep one (calls that may overlap need their own); allocated
-    here otherwise, from torch's allocator on the stream of the call.
+    h, prefix_len, kv_format) bytes for callers that keep one (calls that may overlap need their own);
+    allocated here otherwise, from torch's allocator on the stream of the call.
     """
-    if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != torch.bfloat16 or not q.is_contiguous():
+    if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != _BF16 or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous [T, h, 576] bf16 tensor, got {tuple(q.shape)} {q.dtype}")
-    T, h = int(q.shape[0]), int(q.shape[1])
+    T, h, _ = q.shape
     prefix_len = int(prefix_len)
-    if kv_format not in KV_FORMATS:
-        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
-    row, dtype = (D_QK, torch.bfloat16) if kv_format == "bf16" else (FP8_ROW_BYTES, torch.uint8)
-    if kv_cache.dim() != 2 or kv_cache.shape[1] != row or kv_cache.dtype != dtype or not kv_cache.is_contiguous():
-        raise ValueError(f"{kv_format} kv_cache must be a contiguous [num_slots, {row}] {dtype} tensor, got "
-                         f"{tuple(kv_cache.shape)} {kv_cache.dtype}")
-    if prefix_len < 0 or block_table.dim() != 1 or block_table.dtype != torch.int32 \
+    num_slots = _cache_rows(kv_cache, kv_format)
+    if prefix_len < 0 or block_table.dim() != 1 or block_table.dtype != _I32 \
             or block_table.numel() * 64 < prefix_len or not block_table.is_contiguous():
         raise ValueError("block_table must be a contiguous [ceil(prefix_len / 64)] int32 tensor, prefix_len >= 0")
-    dev = _device_of((("q", q), ("kv_cache", kv_cache), ("block_table", block_table)))
+    dev = _cuda_device("q", q)
+    _together(dev, kv_cache=kv_cache, block_table=block_table)
     if scale is None:
         scale = D_QK ** -0.5
     if out is None:
-        out = torch.empty((T, h, D_V), dtype=torch.bfloat16, device=dev)
-    elif out.shape != (T, h, D_V) or out.dtype != torch.bfloat16 or not out.is_contiguous():
-        raise ValueError("out must be a contiguous [T, h, 512] bf16 tensor")
+        out = torch.empty((T, h, D_V), dtype=_BF16, device=dev)
+    else:
+        if out.shape != (T, h, D_V) or out.dtype != _BF16 or not out.is_contiguous():
+            raise ValueError("out must be a contiguous [T, h, 512] bf16 tensor")
+        _together(dev, out=out)
     if lse is None:
-        lse = torch.empty((T, h), dtype=torch.float32, device=dev)
-    elif lse.shape != (T, h) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous [T, h] fp32 tensor")
-    _device_of((("q", q), ("out", out), ("lse", lse)))
-    with _on(dev):
-        lib = library()
-        handle = _stream_handle(stream, dev)
-        if workspace is None:
-            need = int(lib.sparse_mla_prefix_workspace_bytes(T, h, prefix_len, KV_FORMATS[kv_format]))
-            if need:
-                workspace = _workspace_on(need, dev, handle)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        lse = torch.empty((T, h), dtype=_F32, device=dev)
+    else:
+        if lse.shape != (T, h) or lse.dtype != _F32 or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous [T, h] fp32 tensor")
+        _together(dev, lse=lse)
+    fmt = KV_FORMATS[kv_format]
+    ws_ptr, ws_bytes = None, 0
+    if workspace is None:
+        if torch.cuda.current_device() == dev.index:
+            ws_bytes = _prefix_workspace_bytes(dev.index, T, h, prefix_len, fmt)
+        else:
+            with torch.cuda.device(dev):
+                ws_bytes = _prefix_workspace_bytes(dev.index, T, h, prefix_len, fmt)
+        if ws_bytes:
+            workspace = _workspace_on(ws_bytes, dev, stream)
+            ws_ptr = workspace.data_ptr()
+    else:
+        if workspace.dtype != _U8 or not workspace.is_contiguous() or workspace.device != dev:
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-        st = lib.sparse_mla_prefix(
-            q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), T, h, prefix_len, int(kv_cache.shape[0]),
-            KV_FORMATS[kv_format], float(scale), out.data_ptr(), lse.data_ptr(),
-            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-            handle)
-    _check(st)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    _call(dev, stream, library().sparse_mla_prefix, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), T, h,
+          prefix_len, num_slots, fmt, scale, out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
     return out, lse
 
 
-def _workspace_on(nbytes: int, dev: torch.device, handle) -> torch.Tensor:
-    """nbytes of scratch for one call on the stream `handle`.  The allocator may hand a freed block to
-    the next request on the stream it was allocated for, so it is allocated for the call's stream."""
-    if handle == torch.cuda.current_stream(dev).cuda_stream:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle or 0, device=dev)):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+def _workspace_on(nbytes: int, dev: torch.device, stream) -> torch.Tensor:
+    """nbytes of scratch for one call on `stream` (None: the current one).  The allocator may hand a freed
+    block to the next request on the stream it was allocated for, so it is allocated for the call's."""
+    if stream is not None:
+        handle = _stream_handle(stream, dev)
+        if handle != _current_handle(dev):
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle or 0, device=dev)):
+                return torch.empty(nbytes, dtype=_U8, device=dev)
+    return torch.empty(nbytes, dtype=_U8, device=dev)
 
 
 def host_workspace_bytes(T: int, h: int, topk: int) -> int:
