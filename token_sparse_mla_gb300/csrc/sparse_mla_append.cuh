@@ -92,20 +92,22 @@ __global__ void __launch_bounds__(kAppendThreads) sparse_mla_append_kernel(const
     const int lane = threadIdx.x & 31;
     const int64_t t = (static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
     if (t >= p.T) return;
-    const int slot = __ldg(p.slots + t);
-    if (slot == -1) return;  // an unused place of a padded batch
-    const int pos = __ldg(p.positions + t);
-    if (slot < 0 || static_cast<int64_t>(slot) >= p.num_slots || pos < 0 || pos >= p.max_pos) {
-        if (lane == 0) atomicOr(&g_smla_error, kErrRowRange);
-        return;  // nothing is written for this token; the next status read says so
-    }
+    // the row's loads need neither the slot nor the position: all are in flight together (volatile, so
+    // that none sinks behind the checks)
     const __nv_bfloat16* src = p.kv + t * p.kv_stride;
     const uint4* src16 = reinterpret_cast<const uint4*>(src);
     const int c0 = KVF == 0 ? lane : 2 * lane;       // this lane's 16-byte chunks of the latent
     const int c1 = KVF == 0 ? 32 + lane : 2 * lane + 1;
     const uint4 v0 = ptx::ld_nc_v4(src16 + c0);
     const uint4 v1 = ptx::ld_nc_v4(src16 + c1);
-    const uint32_t pair = __ldg(reinterpret_cast<const uint32_t*>(src + kDV) + lane);
+    const uint32_t pair = __float_as_uint(ptx::ld_nc_f32(src + kDV + 2 * lane));
+    const int slot = __ldg(p.slots + t);
+    const int pos = __ldg(p.positions + t);
+    if (slot == -1) return;  // an unused place of a padded batch
+    if (slot < 0 || static_cast<int64_t>(slot) >= p.num_slots || pos < 0 || pos >= p.max_pos) {
+        if (lane == 0) atomicOr(&g_smla_error, kErrRowRange);
+        return;  // nothing is written for this token; the next status read says so
+    }
     const float* cs = p.cos_sin + static_cast<int64_t>(pos) * 64;
     const float cosv = __ldg(cs + lane), sinv = __ldg(cs + 32 + lane);
 
@@ -142,13 +144,26 @@ __global__ void __launch_bounds__(kAppendThreads) sparse_mla_append_kernel(const
         for (int o = 1; o < 8; o <<= 1) amax = ptx::max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         float scale = __fdiv_rn(amax, 448.f);
         if (scale == 0.f) scale = 1.f;  // a tile of zeros (or of values too small for a scale): codes 0
+        // code = e4m3(x / scale), the quotient rounded to fp32 first.  Markstein's theorem: with y = 1/b
+        // correctly rounded, q = a y, r = a - b q (exact in an fma) and q + r y rounds as a / b does, three
+        // operations per value where the scale is far from the ends of the range (a division per value
+        // made the kernel compute-bound).  Where r would underflow, the code is 0 either way.
+        float q[16];
+        if (scale > 0x1p-100f && scale < 0x1p100f) {
+            const float y = __fdiv_rn(1.f, scale);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float q0 = x[i] * y;
+                q[i] = fmaf(fmaf(-q0, scale, x[i]), y, q0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(x[i], scale);
+        }
         uint32_t code[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = pack_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale));
-            const uint32_t hi = pack_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale));
-            code[i] = lo | (hi << 16);
-        }
+        for (int i = 0; i < 4; ++i)
+            code[i] = pack_e4m3x2(q[4 * i], q[4 * i + 1]) | (pack_e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16);
         uint8_t* row = static_cast<uint8_t*>(p.cache) + static_cast<int64_t>(slot) * kFp8RowBytes;
         reinterpret_cast<uint4*>(row)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
         if ((lane & 7) == 0) reinterpret_cast<float*>(row + kDV)[lane >> 3] = scale;

@@ -1172,7 +1172,7 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
     pp.slot_groups = pl.slot_groups;
     pp.sm_scale_log2 = scale * 1.4426950408889634f;
     if (fp8) {
-        cfg.gridDim = dim3(static_cast<unsigned>(pl.npages * smla::kPfPage / (smla::kPfExpandThreads / 32)), 1, 1);
+        cfg.gridDim = dim3(static_cast<unsigned>(pl.npages * smla::kPfPage / (smla::kPfExpandThreads / 32 * smla::kPfExpandRows)), 1, 1);
         cfg.blockDim = dim3(smla::kPfExpandThreads, 1, 1);
         e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_expand_kernel, pp);
         if (e != cudaSuccess) return cuda_fail(e, "prefix expand kernel launch");
@@ -1189,10 +1189,13 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
     if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
     if (pl.cut) {
         cfg.numAttrs = 1;
-        cfg.gridDim = dim3(static_cast<unsigned>((rows + 31) / 32 * (smla::kDV / smla::kPfMergeDims)), 1, 1);
+        const bool many = pl.runs > 6 * pl.tiles;  // pieces of a tile: about runs / tiles + 1
+        const int dims = smla::kPfMergeThreads / 32 * 4 / (many ? 4 : 1);
+        cfg.gridDim = dim3(static_cast<unsigned>((rows + 31) / 32 * (smla::kDV / dims)), 1, 1);
         cfg.blockDim = dim3(smla::kPfMergeThreads, 1, 1);
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel, pp);
+        e = many ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel<4>, pp)
+                 : cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel<1>, pp);
         if (e != cudaSuccess) return cuda_fail(e, "prefix merge kernel launch");
     }
     return SMLA_OK;

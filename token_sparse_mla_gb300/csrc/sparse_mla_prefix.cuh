@@ -69,11 +69,9 @@ constexpr int kPfGroupB = kPanels - kPfGroupA;    // issuing thread, a refill an
 static_assert(kPfGroupB == 4, "the second group is loaded by V's map (four panels)");
 constexpr int kPfVPage = 4 * kPfPanel;            // one page, this CTA's 256 dims
 constexpr int kPfAhead = 3;                       // blocks between a page's prefetch into L2 and its load
-constexpr int kPfMergeChunks = 4;                 // four dims each
-constexpr int kPfMergeParts = 4;                  // warps that share a chunk's pieces
-constexpr int kPfMergeThreads = 32 * kPfMergeChunks * kPfMergeParts;
-constexpr int kPfMergeDims = 4 * kPfMergeChunks;
+constexpr int kPfMergeThreads = 512;
 constexpr int kPfExpandThreads = 256;
+constexpr int kPfExpandRows = 4;                  // rows per warp
 
 struct PfLayout {
     static constexpr int kOffQ = 0;
@@ -641,48 +639,68 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 }
 
 // The prefix's fp8 rows as bf16 rows in prefix order (e4m3 -> fp32 x scale -> bf16, as in the forward),
-// zeros for rows that take no part; one warp per row, 656 bytes in and 1152 out.
+// zeros for rows that take no part: 656 bytes in and 1152 out.  A warp takes four rows of a page, their
+// loads in flight together.
 __global__ void __launch_bounds__(kPfExpandThreads) sparse_mla_prefix_expand_kernel(const PfParams p) {
+    constexpr int kRows = kPfExpandRows;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kPfExpandThreads + threadIdx.x) >> 5;
+    const int64_t i = ((static_cast<int64_t>(blockIdx.x) * kPfExpandThreads + threadIdx.x) >> 5) * kRows;
     if (i >= static_cast<int64_t>(p.npages) * kPfPage) return;
     const int pg = static_cast<int>(i / kPfPage), in_page = static_cast<int>(i % kPfPage);
     const int page = __ldg(p.pages + pg);
-    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo, rope = lo;
-    if (in_page < pf_valid(p, pg, page)) {
-        const uint8_t* row = static_cast<const uint8_t*>(p.kv) + (static_cast<int64_t>(page) * kPfPage + in_page) * kFp8RowBytes;
-        // lane l: codes [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8), so that both stores are 512 contiguous bytes
-        const uint2 a = __ldg(reinterpret_cast<const uint2*>(row) + lane), b = __ldg(reinterpret_cast<const uint2*>(row) + 32 + lane);
-        const float sa = ptx::ld_nc_f32(row + 512 + 4 * (lane >> 4)), sb = ptx::ld_nc_f32(row + 520 + 4 * (lane >> 4));
-        if (lane < 8) rope = ptx::ld_nc_v4(row + 528 + 16 * lane);
-        lo = make_uint4(ptx::e4m3x2_scaled_bf16x2(a.x & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a.x >> 16, sa),
-                        ptx::e4m3x2_scaled_bf16x2(a.y & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a.y >> 16, sa));
-        hi = make_uint4(ptx::e4m3x2_scaled_bf16x2(b.x & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b.x >> 16, sb),
-                        ptx::e4m3x2_scaled_bf16x2(b.y & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b.y >> 16, sb));
+    const int valid = pf_valid(p, pg, page);
+    const uint8_t* row0 = static_cast<const uint8_t*>(p.kv) + (static_cast<int64_t>(page) * kPfPage + in_page) * kFp8RowBytes;
+    // lane l: codes [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8), so that both stores are 512 contiguous bytes
+    uint2 a[kRows], b[kRows];
+    float sa[kRows], sb[kRows];
+    uint32_t rope[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        a[u] = b[u] = make_uint2(0u, 0u);
+        sa[u] = sb[u] = 0.f;
+        rope[u] = 0u;
+        if (in_page + u < valid) {
+            const uint8_t* row = row0 + u * kFp8RowBytes;
+            a[u] = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+            b[u] = __ldg(reinterpret_cast<const uint2*>(row) + 32 + lane);
+            sa[u] = __ldg(reinterpret_cast<const float*>(row + 512) + (lane >> 4));
+            sb[u] = __ldg(reinterpret_cast<const float*>(row + 520) + (lane >> 4));
+            rope[u] = __ldg(reinterpret_cast<const uint32_t*>(row + 528) + lane);
+        }
     }
-    uint4* dst = reinterpret_cast<uint4*>(p.expanded + i * kDQK);
-    dst[lane] = lo;
-    dst[32 + lane] = hi;
-    if (lane < 8) dst[64 + lane] = rope;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        uint4* dst = reinterpret_cast<uint4*>(p.expanded + (i + u) * kDQK);
+        dst[lane] = make_uint4(ptx::e4m3x2_scaled_bf16x2(a[u].x & 0xFFFFu, sa[u]), ptx::e4m3x2_scaled_bf16x2(a[u].x >> 16, sa[u]),
+                               ptx::e4m3x2_scaled_bf16x2(a[u].y & 0xFFFFu, sa[u]), ptx::e4m3x2_scaled_bf16x2(a[u].y >> 16, sa[u]));
+        dst[32 + lane] = make_uint4(ptx::e4m3x2_scaled_bf16x2(b[u].x & 0xFFFFu, sb[u]), ptx::e4m3x2_scaled_bf16x2(b[u].x >> 16, sb[u]),
+                                    ptx::e4m3x2_scaled_bf16x2(b[u].y & 0xFFFFu, sb[u]), ptx::e4m3x2_scaled_bf16x2(b[u].y >> 16, sb[u]));
+        reinterpret_cast<uint32_t*>(dst + 64)[lane] = rope[u];
+    }
 }
 
-// Joins the pieces of cut tiles by log-sum-exp weights.  A CTA takes 32 query rows (a lane each) and 16
-// dims; four warps share the pieces of four dims, each every fourth piece in order with all loads of a
-// batch in flight together, and meet in shared memory in a fixed order.  Every load is a whole line, and
-// what the pieces wrote is read once, from L2 as a rule.  (One warp over all pieces of its dims took
-// 20 us for 38 pieces of 256 rows: a round of latency per eight pieces, twice.)
+// Joins the pieces of cut tiles by log-sum-exp weights.  A CTA takes 32 query rows (a lane each) and
+// 64 / PARTS dims, four per warp; PARTS warps share the pieces of four dims, each every PARTS-th piece in
+// order with the loads of a batch in flight together, and meet in shared memory in a fixed order.  Every
+// load is a whole line, and what the pieces wrote is read once, from L2 as a rule.  PARTS = 4 where tiles
+// are cut into many pieces (one warp over all 38 pieces of 256 rows took 20 us: a round of latency per
+// eight pieces, twice; four take 5), PARTS = 1 where they are few.
+template <int PARTS>
 __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kernel(const PfParams p) {
-    __shared__ float4 s_acc[kPfMergeParts][kPfMergeChunks][32];
-    __shared__ float s_m[kPfMergeParts][32], s_l[kPfMergeParts][32];
+    constexpr int kChunks = kPfMergeThreads / 32 / PARTS;  // of four dims
+    constexpr int kDims = 4 * kChunks;
+    constexpr int kFlight = PARTS == 1 ? 4 : 6;
+    __shared__ float4 s_acc[PARTS][kChunks][32];
+    __shared__ float s_m[PARTS][32], s_l[PARTS][32];
+    __shared__ uint2 s_out[32][kChunks + 1];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int chunk = (threadIdx.x >> 5) % kPfMergeChunks, part = (threadIdx.x >> 5) / kPfMergeChunks;
-    constexpr int kDimGroups = kDV / kPfMergeDims;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / kDimGroups) * 32;
-    const int dg = static_cast<int>(blockIdx.x % kDimGroups);
+    const int chunk = (threadIdx.x >> 5) % kChunks, part = (threadIdx.x >> 5) / kChunks;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x / (kDV / kDims)) * 32;
+    const int dg = static_cast<int>(blockIdx.x % (kDV / kDims));
     const int64_t tile = row0 / kPfRows;
     const int group = static_cast<int>(row0 % kPfRows) / 32;
     auto run_of = [&](int64_t b) -> int { return static_cast<int>(((b + 1) * p.runs - 1) / p.work); };
@@ -696,16 +714,15 @@ __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kerne
     };
     const int live = p.rows - row0 < 32 ? static_cast<int>(p.rows - row0) : 32;
     const int at = lane < live ? lane : live - 1;  // a lane past the last row repeats it and stores nothing
-    const float4* part_o = reinterpret_cast<const float4*>(p.part_o) + (dg * kPfMergeChunks + chunk) * 32 + at;
-    constexpr int kFlight = 6;
+    const float4* part_o = reinterpret_cast<const float4*>(p.part_o) + (dg * kChunks + chunk) * 32 + at;
     float m = -CUDART_INF_F, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int kk = k0 + part; kk <= k1; kk += kPfMergeParts * kFlight) {
+    for (int kk = k0 + part; kk <= k1; kk += PARTS * kFlight) {
         float4 v[kFlight];
         float mk[kFlight], lk[kFlight];
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const int64_t g = group_of(min(kk + kPfMergeParts * u, k1));
+            const int64_t g = group_of(min(kk + PARTS * u, k1));
             mk[u] = __ldg(p.part_ml + 64 * g + at);
             lk[u] = __ldg(p.part_ml + 64 * g + 32 + at);
             v[u] = __ldg(part_o + g * (128 * 32));
@@ -713,8 +730,7 @@ __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kerne
         float mn = m;
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const bool past = kk + kPfMergeParts * u > k1;
-            if (past) {
+            if (kk + PARTS * u > k1) {
                 mk[u] = -CUDART_INF_F;
                 lk[u] = 0.f;
                 v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -736,36 +752,40 @@ __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kerne
             acc.w += wt * v[u].w;
         }
     }
-    s_acc[part][chunk][lane] = acc;
-    if (chunk == 0) {
-        s_m[part][lane] = m;
-        s_l[part][lane] = l;
-    }
-    __syncthreads();
-    if (part > 0) return;
-    float mp[kPfMergeParts];
+    if constexpr (PARTS > 1) {
+        s_acc[part][chunk][lane] = acc;
+        if (chunk == 0) {
+            s_m[part][lane] = m;
+            s_l[part][lane] = l;
+        }
+        __syncthreads();
+        m = -CUDART_INF_F;
 #pragma unroll
-    for (int q = 0; q < kPfMergeParts; ++q) mp[q] = s_m[q][lane];
-    m = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
-    l = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < PARTS; ++q) m = fmaxf(m, s_m[q][lane]);
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (part == 0) {
 #pragma unroll
-    for (int q = 0; q < kPfMergeParts; ++q) {
-        const float wt = mp[q] == -CUDART_INF_F ? 0.f : ptx::ex2_approx(mp[q] - m);
-        const float4 o = s_acc[q][chunk][lane];
-        l += wt * s_l[q][lane];
-        acc.x += wt * o.x;
-        acc.y += wt * o.y;
-        acc.z += wt * o.z;
-        acc.w += wt * o.w;
+            for (int q = 0; q < PARTS; ++q) {
+                const float wt = s_m[q][lane] == -CUDART_INF_F ? 0.f : ptx::ex2_approx(s_m[q][lane] - m);
+                const float4 o = s_acc[q][chunk][lane];
+                l += wt * s_l[q][lane];
+                acc.x += wt * o.x;
+                acc.y += wt * o.y;
+                acc.z += wt * o.z;
+                acc.w += wt * o.w;
+            }
+        }
     }
-    const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-    if (lane < live) {
-        reinterpret_cast<uint2*>(p.out + (row0 + lane) * kDV + dg * kPfMergeDims)[chunk] =
-            make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
-        if (dg == 0 && chunk == 0)
+    if (part == 0) {
+        const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+        s_out[lane][chunk] = make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
+        if (dg == 0 && chunk == 0 && lane < live)
             p.lse[row0 + lane] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
     }
+    __syncthreads();
+    const int r = threadIdx.x / kChunks, c = threadIdx.x % kChunks;  // neighbouring threads store a row's bytes
+    if (r < live) reinterpret_cast<uint2*>(p.out + (row0 + r) * kDV + dg * kDims)[c] = s_out[r][c];
 }
 
 // The result over no keys: O = 0, LSE = -inf.
