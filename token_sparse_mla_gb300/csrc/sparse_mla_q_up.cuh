@@ -26,7 +26,7 @@
 //   warp 0       TMA producer (one thread): slices of W, token panels into the ring.
 //   warp 1       MMA issuer (one thread) and TMEM owner.
 //   warps 2-9    epilogue: two warps per TMEM lane quadrant, every other accumulator each.
-//   warps 10-13  the rotated dims of this slice's share of the tile, up to 16 tokens at a time.
+//   warps 10-13  the rotated dims, a token per warp.
 // Every wait is bounded; a CTA that gives up drains its copies and MMAs before it leaves.
 #pragma once
 
@@ -122,54 +122,54 @@ __device__ __forceinline__ uint4 turn_eight(const uint4 x, const float4 cs, cons
     return pack_bf16x8(y);
 }
 
-// The rotated dims of this CTA's items, on warp rw of kQupRopeWarps.  Eight lanes per token, 16 bytes
-// each (a pair per lane spent 4 us on a pass of 16 tokens, in the latency of its instructions), and
-// up to 16 tokens' loads in flight; their positions are loaded an item ahead, one per lane.  Loads
-// have no branch -- an unused token reads row 0 of the table, a token past the last reads the last
-// one's -- because a conditional load made each token wait for its own.
-template <int DN, int SLICES, bool INTER>
-__device__ __forceinline__ void turn_items(const QupParams& p, int nh, int hh, int j, int nt, int rw, int lane) {
-    constexpr int kOwn = kQupRows / SLICES / kQupRopeWarps;  // tokens of an item per warp: 8, 16 or 32
-    constexpr int kPer = kOwn < 16 ? kOwn : 16;
-    const int tok = lane >> 3, l8 = lane & 7;
-    auto first = [&](int jj) -> int64_t { return static_cast<int64_t>(jj) * kQupRows + (nh * kQupRopeWarps + rw) * kOwn; };
-    auto load_pos = [&](int jj) -> int {
-        const int64_t t = first(jj) + lane;
-        return lane < kOwn && t < p.T ? __ldg(p.positions + t) : -1;
+// The rotated dims: they need no product, so they are dealt over the warps of the whole grid by tokens,
+// all heads of a token to one warp, which then reads the token's angles once (dealt like the items, a
+// head at a time, the angles alone were 256 bytes per (token, head), as much as is read and written
+// here).  Eight lanes per head, 16 bytes each, and up to 32 heads' loads in flight; the next token's
+// angles are loaded meanwhile.  Loads have no branch -- an unused token reads row 0 of the table, a lane
+// past the last head the last head's -- because a conditional load made each wait for its own.
+template <int DN, bool INTER>
+__device__ __forceinline__ void turn_tokens(const QupParams& p, int first, int step, int lane) {
+    constexpr int kFlight = 8;
+    const int hd = lane >> 3, l8 = lane & 7;
+    auto position = [&](int64_t t) -> int {
+        const int pos = t < p.T ? __ldg(p.positions + t) : -1;
+        const bool bad = pos != -1 && (pos < 0 || pos >= p.max_pos);
+        if (bad && lane == 0) atomicOr(&g_smla_error, kErrRowRange);
+        return bad ? -1 : pos;
     };
-    int next = nt > 0 ? load_pos(j) : -1;
-    for (int i = 0; i < nt; ++i, hh += j == 0) {
-        const int64_t t0 = first(j);
-        const int mine = next;
-        if (++j == p.mtiles) j = 0;
-        if (i + 1 < nt) next = load_pos(j);
-        const bool bad = mine != -1 && (mine < 0 || mine >= p.max_pos);
-        if (bad) atomicOr(&g_smla_error, kErrRowRange);
-        const int good = bad ? -1 : mine;
+    auto angles = [&](int pos, int off) -> float4 {
+        const uint4 v = ptx::ld_nc_v4(p.cos_sin + static_cast<int64_t>(max(pos, 0)) * 64 + off + 4 * l8);
+        return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+    };
+    int64_t t = first;
+    if (t >= p.T) return;
+    int pos = position(t);
+    float4 cs = angles(pos, 0), sn = angles(pos, 32);
+    int pos1 = position(t + step);
+    for (; t < p.T; t += step) {
+        const int pos2 = position(t + 2 * static_cast<int64_t>(step));
+        const float4 cs1 = angles(pos1, 0), sn1 = angles(pos1, 32);
 #pragma unroll 1
-        for (int u = 0; u < kOwn; u += kPer) {
-            uint4 x[kPer / 4], cs[kPer / 4], sn[kPer / 4];
+        for (int h0 = 0; h0 < p.h; h0 += 4 * kFlight) {
+            uint4 x[kFlight];
 #pragma unroll
-            for (int e = 0; e < kPer / 4; ++e) {
-                const int pos = max(__shfl_sync(0xffffffffu, good, u + 4 * e + tok), 0);
-                const int64_t t = min(t0 + u + 4 * e + tok, static_cast<int64_t>(p.T) - 1);
+            for (int e = 0; e < kFlight; ++e) {
+                const int hh = min(h0 + 4 * e + hd, p.h - 1);
                 x[e] = ptx::ld_nc_v4(p.q + (t * p.h + hh) * (DN + 64) + DN + 8 * l8);
-                cs[e] = ptx::ld_nc_v4(p.cos_sin + static_cast<int64_t>(pos) * 64 + 4 * l8);
-                sn[e] = ptx::ld_nc_v4(p.cos_sin + static_cast<int64_t>(pos) * 64 + 32 + 4 * l8);
             }
 #pragma unroll
-            for (int e = 0; e < kPer / 4; ++e) {
-                const bool used = __shfl_sync(0xffffffffu, good, u + 4 * e + tok) >= 0;
-                const float4 c4 = make_float4(__uint_as_float(cs[e].x), __uint_as_float(cs[e].y), __uint_as_float(cs[e].z),
-                                              __uint_as_float(cs[e].w));
-                const float4 s4 = make_float4(__uint_as_float(sn[e].x), __uint_as_float(sn[e].y), __uint_as_float(sn[e].z),
-                                              __uint_as_float(sn[e].w));
-                uint4 r = turn_eight<INTER>(x[e], c4, s4, lane);
-                if (!used) r = make_uint4(0u, 0u, 0u, 0u);
-                const int64_t t = t0 + u + 4 * e + tok;
-                if (t < p.T) __stcs(reinterpret_cast<uint4*>(p.out + (t * p.h + hh) * kDQK + kDV) + l8, r);
+            for (int e = 0; e < kFlight; ++e) {
+                const int hh = h0 + 4 * e + hd;
+                uint4 r = turn_eight<INTER>(x[e], cs, sn, lane);
+                if (pos < 0) r = make_uint4(0u, 0u, 0u, 0u);
+                if (hh < p.h) __stcs(reinterpret_cast<uint4*>(p.out + (t * p.h + hh) * kDQK + kDV) + l8, r);
             }
         }
+        pos = pos1;
+        cs = cs1;
+        sn = sn1;
+        pos1 = pos2;
     }
 }
 
@@ -369,10 +369,12 @@ __global__ void __launch_bounds__(kQupThreads, 1)
         }
     } else {
         // ================================================================ the rotated dims
+        const int first = static_cast<int>(blockIdx.x) * kQupRopeWarps + warp - 2 - kQupEpiWarps;
+        const int step = static_cast<int>(gridDim.x) * kQupRopeWarps;
         if (p.interleaved != 0)
-            turn_items<DN, L::kSlices, true>(p, nh, h0, j0, nt, warp - 2 - kQupEpiWarps, lane);
+            turn_tokens<DN, true>(p, first, step, lane);
         else
-            turn_items<DN, L::kSlices, false>(p, nh, h0, j0, nt, warp - 2 - kQupEpiWarps, lane);
+            turn_tokens<DN, false>(p, first, step, lane);
     }
     ptx::tc_fence_before();
     __syncthreads();
