@@ -85,11 +85,9 @@ cudaError_t set_kernel_attrs() {
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_masked_mha_kernel<256, 128>, smla::MmLayout<256, 128>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_masked_mha_kernel<256, 256>, smla::MmLayout<256, 256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<128, 128>, smla::QupLayout<128, 128>::kBytes);
-    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<128, 512>, smla::QupLayout<128, 512>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<192, 128>, smla::QupLayout<192, 128>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<192, 256>, smla::QupLayout<192, 256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256, 128>, smla::QupLayout<256, 128>::kBytes);
-    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256, 256>, smla::QupLayout<256, 256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_prefix_kernel, smla::PfLayout::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_scatter_mask_kernel, smla::kScatterMaxS / 32 * 4);
     return e;
@@ -1044,10 +1042,10 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
     qp.max_pos = max_pos;
     qp.interleaved = interleaved != 0;
     qp.mtiles = static_cast<int32_t>((static_cast<int64_t>(T) + smla::kQupRows - 1) / smla::kQupRows);
-    // wide slices (q read once or twice) once a head's tiles fill the SMs, 128-dim slices below that
-    const int wide = dn == 128 ? 512 : 256;
     qp.items = static_cast<int64_t>(h) * qp.mtiles;
-    const int ns = qp.items * (smla::kDV / wide) >= ds->num_sms ? wide : 128;
+    // 256-dim slices with 192 nope dims once they fill the SMs, 128-dim slices otherwise (the kernel's
+    // comment has the times)
+    const int ns = dn == 192 && qp.items * 2 >= ds->num_sms ? 256 : 128;
     const int slices = smla::kDV / ns;
     const int64_t runs = qp.items < ds->num_sms / slices ? qp.items : ds->num_sms / slices;
     cudaLaunchConfig_t cfg = {};
@@ -1064,12 +1062,10 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
         cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
         e = cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_w, qp);
     };
-    if (dn == 128 && ns == 128) go(smla::sparse_mla_q_up_kernel<128, 128>, smla::QupLayout<128, 128>::kBytes);
-    else if (dn == 128) go(smla::sparse_mla_q_up_kernel<128, 512>, smla::QupLayout<128, 512>::kBytes);
-    else if (dn == 192 && ns == 128) go(smla::sparse_mla_q_up_kernel<192, 128>, smla::QupLayout<192, 128>::kBytes);
-    else if (dn == 192) go(smla::sparse_mla_q_up_kernel<192, 256>, smla::QupLayout<192, 256>::kBytes);
-    else if (ns == 128) go(smla::sparse_mla_q_up_kernel<256, 128>, smla::QupLayout<256, 128>::kBytes);
-    else go(smla::sparse_mla_q_up_kernel<256, 256>, smla::QupLayout<256, 256>::kBytes);
+    if (dn == 128) go(smla::sparse_mla_q_up_kernel<128, 128>, smla::QupLayout<128, 128>::kBytes);
+    else if (dn == 256) go(smla::sparse_mla_q_up_kernel<256, 128>, smla::QupLayout<256, 128>::kBytes);
+    else if (ns == 128) go(smla::sparse_mla_q_up_kernel<192, 128>, smla::QupLayout<192, 128>::kBytes);
+    else go(smla::sparse_mla_q_up_kernel<192, 256>, smla::QupLayout<192, 256>::kBytes);
     if (e != cudaSuccess) return cuda_fail(e, "q_up kernel launch");
     return SMLA_OK;
 }

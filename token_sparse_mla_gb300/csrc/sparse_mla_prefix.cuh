@@ -260,13 +260,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             // this CTA's pages a few blocks ahead, into L2: K of a block is loaded one block before its use,
             // and from HBM that is too late (8 tiles x 65536 rows: 2.2 us a block, 1.5 from L2)
             auto prefetch = [&](int b) {
-                if (p.expanded != nullptr || b >= p.nblk) return;
                 const int i = 2 * b + rank;
-                const int page = pf_page(p, i);
-                const int n = pf_valid(p, i, page);
-                if (n > 0)
-                    ptx::bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(p.kv) + static_cast<int64_t>(page) * kPfPage * kDQK,
-                                          static_cast<uint32_t>(n * kDQK * 2));
+                if (i >= p.npages) return;
+                const __nv_bfloat16* src = p.expanded + static_cast<int64_t>(i) * kPfPage * kDQK;
+                int n = kPfPage;
+                if (p.expanded == nullptr) {
+                    const int page = pf_page(p, i);
+                    n = pf_valid(p, i, page);
+                    src = static_cast<const __nv_bfloat16*>(p.kv) + static_cast<int64_t>(page) * kPfPage * kDQK;
+                }
+                if (n > 0) ptx::bulk_prefetch_l2(src, static_cast<uint32_t>(n * kDQK * 2));
             };
             bool ok = true;
             int x = 0, piece = 0, b_v = 0;

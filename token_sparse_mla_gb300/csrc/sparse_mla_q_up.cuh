@@ -12,9 +12,10 @@
 // against 1024 DN flops, so at the measured rates the products take about a third of the stores'
 // time.  A GEMM per head: M = 128 tokens, K = DN, and a slice of NS latent dims per CTA whose part of
 // W stays in shared memory as the MN-major operand, while token panels stream through a TMA ring.
-// The wider the slice, the fewer times q is read (512 / NS) and the fewer CTAs share a head's tile:
-//   NS = 512 (DN 128) or 256 (DN 192, 256, where 512 dims of W do not fit)   once the tiles fill the SMs
-//   NS = 128                                                                 below that, for latency
+// A wider slice reads q fewer times from L2 but leaves the ring less room.  Measured, 128- against
+// 256-dim slices: 128 nope dims, 64 heads x 16384 tokens 282 / 295 us (512: 293); 192, 32 x 8192
+// 90 / 82 us; 256, 16 x 16384 108 / 112 us.  So 256-dim slices for 192 nope dims, once their items fill
+// the SMs, and 128-dim slices otherwise.
 // The (head, token tile) items are dealt in equal contiguous runs, one CTA per SM; the CTAs of a
 // run's slices go through it side by side, so that q leaves HBM once, and a run that crosses into
 // another head reloads W.  The fp32 accumulators are four TMEM buffers of 128 dims, taken in turn.
@@ -46,7 +47,7 @@ constexpr int kQupMaxStages = 6;
 template <int DN, int NS>
 struct QupLayout {
     static_assert(DN == 128 || DN == 192 || DN == 256, "nope dims");
-    static_assert(NS == 128 || NS == 256 || NS == 512, "slice width");
+    static_assert(NS == 128 || NS == 256, "slice width");
     static constexpr int kPanelsK = DN / 64;
     static constexpr int kSlices = kDV / NS;
     static constexpr int kChunks = NS / kQupN;
