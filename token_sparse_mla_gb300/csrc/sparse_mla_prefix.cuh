@@ -15,24 +15,26 @@
 // (two pages):
 //   S[128, 128]  = Q . K^T     A: each CTA's 64 rows of Q; B: each CTA's page of 64 keys, all 576 dims
 //   O[128, 512] += P . V       A: each CTA's 64 rows of P; B: both pages, each CTA's 256 dims
-// Back to back, an MMA of this form takes 32 cycles at N = 128 and 64.5 at N = 256 (4060 multiply-adds a
-// cycle and SM, the dense rate), 25 at N = 64, so blocks of 64 keys would lose a third of S; a block
-// is 36 * 32 + 16 * 64.5 = 2190 cycles.  It also moves 280 KB through shared memory's 128 bytes a
-// cycle (operands 148 KB + 96 KB... of S and PV, 136 KB written by TMA): 3000 cycles, the nearer bound.
-// The price of the shape is room: Q 72 KB, K 72 KB,
-// V 64 KB and P 16 KB leave one stage of each, so K is refilled in two groups of panels and V in two
-// pages, each as soon as its last MMA is done: K has the time of a PV and an S to arrive, V that of
-// an S.  (The half of V that lies in a CTA's own K tile is loaded again: the MMA wants the same keys at
-// the same offset in both CTAs, and K wants different ones.)
+// Back to back, an MMA of this form takes 32 cycles at N = 128 and 64 at N = 256 (4060 multiply-adds a
+// cycle and SM, the dense rate) but 25 at N = 64, so blocks of one page would lose a third of S; a block
+// of two is 36 * 32 + 16 * 64 = 2190 cycles.  The nearer bound is shared memory: operands of S 144 KB
+// and of PV 96 KB, 136 KB written by TMA and P's 16 KB are 3100 cycles at 128 bytes a cycle; measured
+// (76 tiles x 8192 keys, rows in L2) 1.5 us a block at 1.94 GHz, 1620 TFLOP/s.  What the shape costs is
+// room: Q 72 KB, K 72 KB, V 64 KB and P 16 KB leave one stage of each, so K is refilled in two groups of
+// panels and V and P page by page, each as soon as its last MMA is done.  (The half of V that lies in a
+// CTA's own K tile is loaded again: the MMA wants the same keys at the same offset in both CTAs, and K
+// wants different ones.)
 //
 // fp8 rows are first expanded to bf16 rows in the workspace (sparse_mla_prefix_expand_kernel), in
 // prefix order: dequantising in the main kernel would be repeated for every 128 query rows, and with
-// eight warps at it a block of 64 keys took 3.7 us.
+// eight warps at it a block of 64 keys took 3.7 us.  The product code x scale is rounded to bf16, the
+// MMA's operand type, as in the forward.
 //
 // Work: the (row tile, block) sequence, tile-major, is cut into equal contiguous runs, one per CTA
-// pair.  A tile that lies inside one run is written out directly; a cut tile leaves an fp32 partial
-// (O, running max, sum) per piece in the workspace, at most two per run, which a second kernel
-// joins by log-sum-exp weights in run order (so results do not depend on timing).
+// pair (no more of them than the longest one needs: 256 rows x 16384 keys took 26 us in 76 runs, 21 in
+// 64).  A tile that lies inside one run is written out directly; a cut tile leaves an fp32 partial (O,
+// running max, sum) per piece in the workspace, at most two per run, which a second kernel joins by
+// log-sum-exp weights in run order (so results do not depend on timing).
 //
 // Rows past the prefix's end in its last page are masked in S, and zeroed in the V tile before they
 // are multiplied: 0 times whatever the page holds there must stay 0.  A page number outside the
@@ -68,7 +70,7 @@ constexpr int kPfGroupA = 5;                      // K in two groups of panels, 
 constexpr int kPfGroupB = kPanels - kPfGroupA;    // issuing thread, a refill and an accumulator of its own
 static_assert(kPfGroupB == 4, "the second group is loaded by V's map (four panels)");
 constexpr int kPfVPage = 4 * kPfPanel;            // one page, this CTA's 256 dims
-constexpr int kPfAhead = 3;                       // blocks between a page's prefetch into L2 and its load
+constexpr int kPfAhead = 2;                       // blocks between a page's prefetch into L2 and its load
 constexpr int kPfMergeThreads = 512;
 constexpr int kPfExpandThreads = 256;
 constexpr int kPfExpandRows = 4;                  // rows per warp
