@@ -311,6 +311,11 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
+// Arrival on a barrier of either CTA, with the order that it needs there: what it announces (an operand
+// in this CTA's shared memory, fenced by its writers for the async proxy; a TMEM tile that has been read)
+// is next touched by this SM's own tensor core, not by the thread that waits.  A release to the whole
+// cluster would also drain the thread's other traffic (prefix attention of 76 tiles x 8192 keys: 162 us
+// instead of 108).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
