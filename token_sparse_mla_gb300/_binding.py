@@ -467,7 +467,7 @@ def sparse_mla_append(kv: torch.Tensor, positions: torch.Tensor, slots: torch.Te
         _together(dev, norm_weight=norm_weight)
         weight = norm_weight.data_ptr()
     _call(dev, stream, library().sparse_mla_append, kv.data_ptr(), row_stride, positions.data_ptr(), slots.data_ptr(),
-          T, cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, weight, eps, kv_cache.data_ptr(), num_slots,
+          T, cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, weight, float(eps), kv_cache.data_ptr(), num_slots,
           KV_FORMATS[kv_format])
     return kv_cache
 
@@ -566,7 +566,7 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
     _call(dev, stream, library().sparse_mla_prefix, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), T, h,
-          prefix_len, num_slots, fmt, scale, out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
+          prefix_len, num_slots, fmt, float(scale), out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
     return out, lse
 
 
