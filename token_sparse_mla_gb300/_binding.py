@@ -400,8 +400,8 @@ def _call(dev: torch.device, stream, fn, *args) -> None:
         _check(st)
 
 
-def _together(dev: torch.device, **tensors) -> None:
-    """All tensors on the CUDA device dev."""
+def _apart(dev: torch.device, **tensors) -> None:
+    """Names the first tensor that is not on dev."""
     for name, t in tensors.items():
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
@@ -459,12 +459,14 @@ def sparse_mla_append(kv: torch.Tensor, positions: torch.Tensor, slots: torch.Te
     max_pos = _positions_and_table(T, positions, cos_sin)
     num_slots = _cache_rows(kv_cache, kv_format)
     dev = _cuda_device("kv", kv)
-    _together(dev, positions=positions, slots=slots, kv_cache=kv_cache, cos_sin=cos_sin)
+    if not dev == positions.device == slots.device == kv_cache.device == cos_sin.device:
+        _apart(dev, positions=positions, slots=slots, kv_cache=kv_cache, cos_sin=cos_sin)
     weight = None
     if norm_weight is not None:
         if norm_weight.shape != (D_V,) or norm_weight.dtype != _BF16 or not norm_weight.is_contiguous():
             raise ValueError("norm_weight must be a contiguous [512] bf16 tensor")
-        _together(dev, norm_weight=norm_weight)
+        if norm_weight.device != dev:
+            _apart(dev, norm_weight=norm_weight)
         weight = norm_weight.data_ptr()
     _call(dev, stream, library().sparse_mla_append, kv.data_ptr(), row_stride, positions.data_ptr(), slots.data_ptr(),
           T, cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, weight, float(eps), kv_cache.data_ptr(), num_slots,
@@ -490,13 +492,15 @@ def sparse_mla_q_up(q: torch.Tensor, w: torch.Tensor, positions: torch.Tensor, c
         raise ValueError(f"w must be a contiguous [{h}, {dn}, 512] bf16 tensor")
     max_pos = _positions_and_table(T, positions, cos_sin)
     dev = _cuda_device("q", q)
-    _together(dev, w=w, positions=positions, cos_sin=cos_sin)
+    if not dev == w.device == positions.device == cos_sin.device:
+        _apart(dev, w=w, positions=positions, cos_sin=cos_sin)
     if out is None:
         out = torch.empty((T, h, D_QK), dtype=_BF16, device=dev)
     else:
         if out.shape != (T, h, D_QK) or out.dtype != _BF16 or not out.is_contiguous():
             raise ValueError("out must be a contiguous [T, h, 576] bf16 tensor")
-        _together(dev, out=out)
+        if out.device != dev:
+            _apart(dev, out=out)
     _call(dev, stream, library().sparse_mla_q_up, q.data_ptr(), w.data_ptr(), positions.data_ptr(), T, h, dn,
           cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, out.data_ptr())
     return out
@@ -535,7 +539,8 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
             or block_table.numel() * 64 < prefix_len or not block_table.is_contiguous():
         raise ValueError("block_table must be a contiguous [ceil(prefix_len / 64)] int32 tensor, prefix_len >= 0")
     dev = _cuda_device("q", q)
-    _together(dev, kv_cache=kv_cache, block_table=block_table)
+    if not dev == kv_cache.device == block_table.device:
+        _apart(dev, kv_cache=kv_cache, block_table=block_table)
     if scale is None:
         scale = D_QK ** -0.5
     if out is None:
@@ -543,13 +548,15 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
     else:
         if out.shape != (T, h, D_V) or out.dtype != _BF16 or not out.is_contiguous():
             raise ValueError("out must be a contiguous [T, h, 512] bf16 tensor")
-        _together(dev, out=out)
+        if out.device != dev:
+            _apart(dev, out=out)
     if lse is None:
         lse = torch.empty((T, h), dtype=_F32, device=dev)
     else:
         if lse.shape != (T, h) or lse.dtype != _F32 or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous [T, h] fp32 tensor")
-        _together(dev, lse=lse)
+        if lse.device != dev:
+            _apart(dev, lse=lse)
     fmt = KV_FORMATS[kv_format]
     ws_ptr, ws_bytes = None, 0
     if workspace is None:
