@@ -92,8 +92,8 @@ def prefix(q, row_values: np.ndarray, pages, prefix_len: int, scale: float):
     if not slots:
         return np.zeros((T, h, 512)), np.full((T, h), -np.inf)
     rows = row_values[slots]
-    s = np.einsum("thd,pd->thp", x, rows) * scale
+    s = (x @ rows.T) * scale
     m = s.max(axis=2, keepdims=True)
     e = np.exp(s - m)
     z = e.sum(axis=2, keepdims=True)
-    return np.einsum("thp,pd->thd", e / z, rows[:, :512]), (m + np.log(z))[:, :, 0]
+    return (e / z) @ rows[:, :512], (m + np.log(z))[:, :, 0]

@@ -61,11 +61,11 @@ def _check(out, lse, q, cache, pages, P, fmt, scale=SCALE):
         assert np.all(out == 0) and np.all(np.isneginf(lse))
         return
     k, x = np.abs(rows[slots]), np.abs(ref.to64(q))
-    e = 576 * 2.0 ** -23 * abs(scale) * np.einsum("thd,pd->thp", x, k).max(axis=2)
+    e = 576 * 2.0 ** -23 * abs(scale) * (x @ k.T).max(axis=2)
     assert np.all(np.abs(lse - want_l) <= e + 2.0 ** -22 * np.abs(want_l) + 2.0 ** -20)
-    s = np.einsum("thd,pd->thp", ref.to64(q), rows[slots]) * scale
+    s = (ref.to64(q) @ rows[slots].T) * scale
     p = np.exp(s - want_l[:, :, None])
-    pv = np.einsum("thp,pd->thd", p, k[:, :512])
+    pv = p @ k[:, :512]
     tol = (2.0 ** -8 + 2 * e[:, :, None]) * pv + 2.0 ** -8 * np.abs(want_o) + 1e-30
     assert np.all(np.abs(out - want_o) <= tol), float((np.abs(out - want_o) - tol).max())
 
@@ -86,7 +86,8 @@ def _run(q, cache, pages, P, fmt, scale=SCALE, **kw):
 
 
 SHAPES = [(1, 16, 64), (1, 1, 1), (1, 16, 63), (2, 8, 65), (1, 16, 1000), (5, 13, 129), (16, 8, 500), (17, 8, 4096), (8, 16, 128), (130, 1, 257),
-          (40, 16, 777), (64, 64, 70), (100, 64, 200), (3, 128, 640), (333, 8, 320)]
+          (40, 16, 777), (64, 64, 70), (100, 64, 200), (3, 128, 640), (333, 8, 320), (1300, 8, 130),
+          (170, 64, 300)]
 
 
 @pytest.mark.gpu

@@ -1161,6 +1161,7 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
     pp.part_ml = pl.cut ? reinterpret_cast<float*>(ws + pl.off_ml) : nullptr;
     pp.prefix = prefix_len;
     pp.num_slots = num_slots;
+    pp.tiles = pl.tiles;
     pp.work = pl.work;
     pp.npages = static_cast<int32_t>(pl.npages);
     pp.nblk = static_cast<int32_t>(pl.nblk);
@@ -1187,7 +1188,8 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
         cfg.numAttrs = 1;
         const bool many = pl.runs > 6 * pl.tiles;  // pieces of a tile: about runs / tiles + 1
         const int dims = smla::kPfMergeThreads / 32 * 4 / (many ? 4 : 1);
-        cfg.gridDim = dim3(static_cast<unsigned>((rows + 31) / 32 * (smla::kDV / dims)), 1, 1);
+        const int64_t candidates = pl.tiles > pl.runs ? pl.runs - 1 : pl.tiles;
+        cfg.gridDim = dim3(static_cast<unsigned>(candidates * pl.slot_groups * (smla::kDV / dims)), 1, 1);
         cfg.blockDim = dim3(smla::kPfMergeThreads, 1, 1);
         cfg.dynamicSmemBytes = 0;
         e = many ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel<4>, pp)

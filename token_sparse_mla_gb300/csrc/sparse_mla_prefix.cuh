@@ -122,6 +122,7 @@ struct PfParams {
     int64_t rows;                // T * h
     int64_t prefix;              // P
     int64_t num_slots;
+    int64_t tiles;               // ceil(rows / 128)
     int64_t work;                // tiles * nblk
     int32_t npages, nblk, runs;
     int32_t slot_groups;         // groups of 32 rows in a tile: ceil(min(128, rows) / 32)
@@ -704,10 +705,19 @@ __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kerne
     ptx::grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int chunk = (threadIdx.x >> 5) % kChunks, part = (threadIdx.x >> 5) / kChunks;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / (kDV / kDims)) * 32;
     const int dg = static_cast<int>(blockIdx.x % (kDV / kDims));
-    const int64_t tile = row0 / kPfRows;
-    const int group = static_cast<int>(row0 % kPfRows) / 32;
+    const int group = static_cast<int>(blockIdx.x / (kDV / kDims)) % p.slot_groups;
+    // the tile: with more tiles than runs most are whole, and the candidates are those that the runs'
+    // boundaries fall into (the first boundary of a tile stands for it)
+    int64_t tile = blockIdx.x / (kDV / kDims) / p.slot_groups;
+    if (p.tiles > p.runs) {
+        const int64_t k = tile + 1;
+        const int64_t at = p.work * k / p.runs;
+        tile = at / p.nblk;
+        if (at % p.nblk == 0 || p.work * (k - 1) / p.runs > tile * p.nblk) return;
+    }
+    const int64_t row0 = tile * kPfRows + group * 32;
+    if (row0 >= p.rows) return;
     auto run_of = [&](int64_t b) -> int { return static_cast<int>(((b + 1) * p.runs - 1) / p.work); };
     const int k0 = run_of(tile * p.nblk), k1 = run_of((tile + 1) * p.nblk - 1);
     if (k0 == k1) return;  // the tile lies inside one run, which wrote it
