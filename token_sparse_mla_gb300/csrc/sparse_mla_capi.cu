@@ -1186,14 +1186,17 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
     if (e != cudaSuccess) return cuda_fail(e, "prefix kernel launch");
     if (pl.cut) {
         cfg.numAttrs = 1;
-        const bool many = pl.runs > 6 * pl.tiles;  // pieces of a tile: about runs / tiles + 1
-        const int dims = smla::kPfMergeThreads / 32 * 4 / (many ? 4 : 1);
+        // 64 / parts dims per CTA, and no more than three CTAs per SM
         const int64_t candidates = pl.tiles > pl.runs ? pl.runs - 1 : pl.tiles;
-        cfg.gridDim = dim3(static_cast<unsigned>(candidates * pl.slot_groups * (smla::kDV / dims)), 1, 1);
+        const int64_t groups = candidates * pl.slot_groups;
+        const int64_t most = static_cast<int64_t>(ds->num_sms) * 3;
+        const int parts = groups * 32 <= most ? 4 : groups * 16 <= most ? 2 : 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(groups * 8 * parts), 1, 1);
         cfg.blockDim = dim3(smla::kPfMergeThreads, 1, 1);
         cfg.dynamicSmemBytes = 0;
-        e = many ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel<4>, pp)
-                 : cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel<1>, pp);
+        e = parts == 4   ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel<4>, pp)
+            : parts == 2 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel<2>, pp)
+                         : cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel<1>, pp);
         if (e != cudaSuccess) return cuda_fail(e, "prefix merge kernel launch");
     }
     return SMLA_OK;

@@ -223,15 +223,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // launched as a programmatic dependent: nothing above touched global memory
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    auto page_row = [&](int i) -> int {  // first row of page i; one that is not there loads as zeros, from rows below 0
-        if (p.expanded != nullptr) return i < p.npages ? i * kPfPage : -kPfPage;
-        const int page = pf_page(p, i);
-        return pf_in_cache(p, page) ? page * kPfPage : -kPfPage;
-    };
-    int row[2] = {0, 0};
+    // the producer's page numbers are loaded ahead and looked at only where their rows are asked for
+    // (the first two under the cluster barrier)
+    int pg0 = -1, pg1 = -1;
     if (warp == 0 && lane == 0) {
-        row[0] = page_row(2 * w.b0);
-        row[1] = page_row(2 * w.b0 + 1);
+        pg0 = pf_page(p, 2 * w.b0);
+        pg1 = pf_page(p, 2 * w.b0 + 1);
     }
     ptx::tc_fence_before();
     __syncwarp();         // the cluster barrier wants its warps whole
@@ -274,6 +271,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 }
                 if (n > 0) ptx::bulk_prefetch_l2(src, static_cast<uint32_t>(n * kDQK * 2));
             };
+            auto first_row = [&](int i, int page) -> int {  // of page i; one that is not there loads as zeros, from rows below 0
+                if (p.expanded != nullptr) return i < p.npages ? i * kPfPage : -kPfPage;
+                return pf_in_cache(p, page) ? page * kPfPage : -kPfPage;
+            };
             bool ok = true;
             int x = 0, piece = 0, b_v = 0;
             int row_v0 = 0, row_v1 = 0;
@@ -283,11 +284,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 ptx::tma_load_3d_pair(sbase + L::kOffQ, &tm_q, 0, static_cast<int>(w.tile * kPfRows + rank * kPfHalf), 0,
                                       even_bar(kPbQFull));
                 if (piece > 0) {
-                    row[0] = page_row(2 * w.b0);
-                    row[1] = page_row(2 * w.b0 + 1);
+                    pg0 = pf_page(p, 2 * w.b0);
+                    pg1 = pf_page(p, 2 * w.b0 + 1);
                 }
                 for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
-                    const int mine = rank == 0 ? row[0] : row[1];
+                    const int row0 = first_row(2 * b, pg0), row1 = first_row(2 * b + 1, pg1);
+                    const int mine = rank == 0 ? row0 : row1;
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         if (x > 0 && !(ok = wait(kPbKEmpty + g, (x - 1) & 1))) break;
@@ -299,13 +301,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     if (x == 0)
                         for (int a = 1; a < kPfAhead; ++a) prefetch(b + a);
                     prefetch(b + kPfAhead);
-                    const int next0 = page_row(2 * b + 2), next1 = page_row(2 * b + 3);  // loaded under the waits
+                    pg0 = pf_page(p, 2 * b + 2);  // in flight under the waits
+                    pg1 = pf_page(p, 2 * b + 3);
                     if (ok && x > 0) ok = load_v(x - 1, b_v, row_v0, row_v1);
-                    row_v0 = row[0];
-                    row_v1 = row[1];
+                    row_v0 = row0;
+                    row_v1 = row1;
                     b_v = b;
-                    row[0] = next0;
-                    row[1] = next1;
                 }
             }
             if (ok && x > 0) ok = load_v(x - 1, b_v, row_v0, row_v1);
@@ -690,14 +691,16 @@ __global__ void __launch_bounds__(kPfExpandThreads) sparse_mla_prefix_expand_ker
 // Joins the pieces of cut tiles by log-sum-exp weights.  A CTA takes 32 query rows (a lane each) and
 // 64 / PARTS dims, four per warp; PARTS warps share the pieces of four dims, each every PARTS-th piece in
 // order with the loads of a batch in flight together, and meet in shared memory in a fixed order.  Every
-// load is a whole line, and what the pieces wrote is read once, from L2 as a rule.  PARTS = 4 where tiles
-// are cut into many pieces (one warp over all 38 pieces of 256 rows took 20 us: a round of latency per
-// eight pieces, twice; four take 5), PARTS = 1 where they are few.
+// load is a whole line, and what the pieces wrote is read once, from L2 as a rule.  PARTS is the largest
+// of 4, 2 and 1 with which the grid is at most three CTAs per SM (two run at a time; held to 40 registers
+// for three, 256 rows x 16384 keys took 23.7 us in all instead of 20.2): few tiles are cut into many
+// pieces (one warp over all 38 pieces of 256 rows took 20 us, a round of latency per eight pieces, twice;
+// four take 5), many tiles into few.
 template <int PARTS>
 __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kernel(const PfParams p) {
     constexpr int kChunks = kPfMergeThreads / 32 / PARTS;  // of four dims
     constexpr int kDims = 4 * kChunks;
-    constexpr int kFlight = PARTS == 1 ? 4 : 6;
+    constexpr int kFlight = 4;
     __shared__ float4 s_acc[PARTS][kChunks][32];
     __shared__ float s_m[PARTS][32], s_l[PARTS][32];
     __shared__ uint2 s_out[32][kChunks + 1];
