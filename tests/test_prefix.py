@@ -310,11 +310,13 @@ def test_workspace_bytes(lib):
     assert smla.prefix_workspace_bytes(0, 8, 100) == 0 and smla.prefix_workspace_bytes(1, 8, 0) == 0
     assert smla.prefix_workspace_bytes(1, 8, 128) == 0
     assert smla.prefix_workspace_bytes(16 * 76, 8, 128 * 5) == 0
-    assert smla.prefix_workspace_bytes(1, 16, 129) == partials(2, 16)
+    assert smla.prefix_workspace_bytes(1, 16, 129) == 0  # two blocks: not worth a merge
+    assert smla.prefix_workspace_bytes(1, 16, 1000) == partials(8, 16)
+    assert smla.prefix_workspace_bytes(8, 16, 8192) == partials(32, 128)  # two blocks a run
     assert smla.prefix_workspace_bytes(128, 64, 32768) == partials(76, 128)
     # an fp8 prefix also has its whole pages as bf16 rows
     assert smla.prefix_workspace_bytes(1, 8, 100, "fp8") == 128 * 1152
-    assert smla.prefix_workspace_bytes(1, 16, 129, "fp8") == partials(2, 16) + 192 * 1152
+    assert smla.prefix_workspace_bytes(1, 16, 1000, "fp8") == partials(8, 16) + 1024 * 1152
 
 
 def _args(T=3, h=8, P=130):

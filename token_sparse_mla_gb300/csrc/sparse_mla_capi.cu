@@ -456,10 +456,23 @@ PrefixPlan prefix_plan(int64_t rows, int64_t prefix, bool fp8, int num_sms) {
     pl.nblk = (prefix + smla::kPfKeys - 1) / smla::kPfKeys;
     pl.work = pl.tiles * pl.nblk;
     if (pl.work == 0) return pl;
+    // Either equal runs for all pairs, whose longest sets the time, or every tile in the same number of
+    // runs, so that none crosses into another tile.  Costs in hundredths of a microsecond: a block 1.5 us, a
+    // crossing 4 us (queries, a first block and an epilogue again), the merge 3.5 us and 0.08 us for each
+    // partial of a row.  A tile in one run needs no merge.  Against as many equal runs as there are pairs:
+    // 16 rows x 256 keys 9.1 / 8.0 us, 128 x 8192 16.1 / 14.1, 384 x 8192 22.5 / 18.9, 6400 x 2048
+    // 42.4 / 31.6; 128 x 8192 by runs per tile: 16 16.3 us, 22 15.8, 32 14.3, 64 16.0.
     const int64_t pairs = num_sms / 2;
-    // as few runs as keep the longest one's length: each run of a cut tile costs a partial
     const int64_t longest = (pl.work + pairs - 1) / pairs;
     pl.runs = static_cast<int>((pl.work + longest - 1) / longest);
+    int64_t best = 150 * longest + 400 + 350 + 8 * (pl.nblk / longest + 1);
+    for (int64_t s = 1; s <= pl.nblk && s * pl.tiles <= pairs; ++s) {
+        const int64_t cost = 150 * ((pl.nblk + s - 1) / s) + (s == 1 ? 0 : 350 + 8 * s);
+        if (cost <= best) {
+            best = cost;
+            pl.runs = static_cast<int>(s * pl.tiles);
+        }
+    }
     pl.slot_groups = static_cast<int>(((rows < smla::kPfRows ? rows : smla::kPfRows) + 31) / 32);
     for (int k = 1; k < pl.runs && !pl.cut; ++k) pl.cut = (pl.work * k / pl.runs) % pl.nblk != 0;
     const size_t slots = pl.cut ? static_cast<size_t>(pl.runs) * 2 * pl.slot_groups * 32 : 0;  // rows in all slots

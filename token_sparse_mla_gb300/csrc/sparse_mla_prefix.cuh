@@ -31,8 +31,8 @@
 // MMA's operand type, as in the forward.
 //
 // Work: the (row tile, block) sequence, tile-major, is cut into equal contiguous runs, one per CTA
-// pair (no more of them than the longest one needs: 256 rows x 16384 keys took 26 us in 76 runs, 21 in
-// 64).  A tile that lies inside one run is written out directly; a cut tile leaves an fp32 partial (O,
+// pair: as many as there are pairs, or the same number for each tile where that is shorter (the host's
+// plan weighs them: 256 rows x 16384 keys took 26 us in 76 runs, 20 in 64).  A tile that lies inside one run is written out directly; a cut tile leaves an fp32 partial (O,
 // running max, sum) per piece in the workspace, at most two per run, which a second kernel joins by
 // log-sum-exp weights in run order (so results do not depend on timing).
 //
