@@ -386,6 +386,7 @@ smla_status sparse_mla_q_up(const void* q, const void* w, const int32_t* positio
  *                prefix as bf16 rows if the cache is fp8.  Calls that may overlap
  *                in time need workspaces of their own.  NULL when that function
  *                returns 0 (it asks the current device)
+ * out, lse and workspace must overlap neither each other nor the inputs.
  * A row whose every position is masked, or prefix_len = 0, gives O = 0 and
  * LSE = -inf.  Repeated calls with the same arguments give identical bytes.
  * T = 0 is a no-op.  Allocates nothing; asynchronous on `stream`.  Errors:

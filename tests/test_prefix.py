@@ -87,7 +87,7 @@ def _run(q, cache, pages, P, fmt, scale=SCALE, **kw):
 
 SHAPES = [(1, 16, 64), (1, 1, 1), (1, 16, 63), (2, 8, 65), (1, 16, 1000), (5, 13, 129), (16, 8, 500), (17, 8, 4096), (8, 16, 128), (130, 1, 257),
           (40, 16, 777), (64, 64, 70), (100, 64, 200), (3, 128, 640), (333, 8, 320), (1300, 8, 130),
-          (170, 64, 300)]
+          (170, 64, 300), (450, 8, 5100)]  # the last: runs that cross from a tile into the next, three pieces a tile
 
 
 @pytest.mark.gpu
@@ -314,6 +314,8 @@ def test_workspace_bytes(lib):
     assert smla.prefix_workspace_bytes(1, 16, 1000) == partials(8, 16)
     assert smla.prefix_workspace_bytes(8, 16, 8192) == partials(32, 128)  # two blocks a run
     assert smla.prefix_workspace_bytes(128, 64, 32768) == partials(76, 128)
+    with pytest.raises(ValueError, match="kv_format"):
+        smla.prefix_workspace_bytes(1, 8, 128, "int8")
     # an fp8 prefix also has its whole pages as bf16 rows
     assert smla.prefix_workspace_bytes(1, 8, 100, "fp8") == 128 * 1152
     assert smla.prefix_workspace_bytes(1, 16, 1000, "fp8") == partials(8, 16) + 1024 * 1152

@@ -514,6 +514,8 @@ def _prefix_workspace_bytes(device_index: int, T: int, h: int, prefix_len: int, 
 
 def prefix_workspace_bytes(T: int, h: int, prefix_len: int, kv_format: str = "bf16") -> int:
     """Bytes of workspace that sparse_mla_prefix needs on the current device (0: none)."""
+    if kv_format not in KV_FORMATS:
+        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
     return int(library().sparse_mla_prefix_workspace_bytes(T, h, prefix_len, KV_FORMATS[kv_format]))
 
 
