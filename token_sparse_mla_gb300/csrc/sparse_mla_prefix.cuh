@@ -70,9 +70,8 @@ constexpr int kPfGroupA = 5;                      // K in two groups of panels, 
 constexpr int kPfGroupB = kPanels - kPfGroupA;    // issuing thread, a refill and an accumulator of its own
 static_assert(kPfGroupB == 4, "the second group is loaded by V's map (four panels)");
 constexpr int kPfVPage = 4 * kPfPanel;            // one page, this CTA's 256 dims
-constexpr int kPfAhead = 2;                       // blocks between a page's prefetch into L2 and its load
 constexpr int kPfMergeThreads = 512;
-constexpr int kPfExpandThreads = 256;
+constexpr int kPfExpandThreads = 128;
 constexpr int kPfExpandRows = 4;                  // rows per warp
 
 struct PfLayout {
@@ -257,8 +256,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 }
                 return true;
             };
-            // this CTA's pages a few blocks ahead, into L2: K of a block is loaded one block before its use,
-            // and from HBM that is too late (8 tiles x 65536 rows: 2.2 us a block, 1.5 from L2)
+            // this CTA's page of the next block, into L2 while the current one is waited for: loaded from HBM
+            // only when K's buffer is free it would be too late (1024 rows x 65536 keys: 129 us without, 105
+            // with; two blocks ahead 106, three 107, 1 row x 131072 50 / 42 / 44 / 48: the first blocks wait
+            // behind them)
             auto prefetch = [&](int b) {
                 const int i = 2 * b + rank;
                 if (i >= p.npages) return;
@@ -298,9 +299,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         ptx::tma_load_3d_pair(sbase + L::kOffK + g * kPfGroupA * kPfPanel, g ? &tm_v : &tm_k, 0, mine,
                                               g * kPfGroupA, even_bar(kPbKFull + g));
                     }
-                    if (x == 0)
-                        for (int a = 1; a < kPfAhead; ++a) prefetch(b + a);
-                    prefetch(b + kPfAhead);
+                    prefetch(b + 1);
                     pg0 = pf_page(p, 2 * b + 2);  // in flight under the waits
                     pg1 = pf_page(p, 2 * b + 3);
                     if (ok && x > 0) ok = load_v(x - 1, b_v, row_v0, row_v1);
