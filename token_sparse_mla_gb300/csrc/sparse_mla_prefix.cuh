@@ -500,22 +500,28 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     }
                     if (b > w.b0 && __any_sync(0xffffffffu, grow)) {
                         // O is complete up to the last block
-                        if (!warp_wait(kPbPvDone, (x - 1) & 1)) {
-                            failed = true;
-                            continue;  // the next reduction takes the group out
-                        }
-                        ptx::tc_fence_after();
+                        if (!warp_wait(kPbPvDone, (x - 1) & 1)) failed = true;
+                        if (!failed) {
+                            ptx::tc_fence_after();
 #pragma unroll 1
-                        for (int cc = 0; cc < 8; ++cc) {
-                            uint32_t ov[16];
-                            SMLA_TMEM_LD16(tmem + lane_base + ocol0 + cc * 16, ov);
-                            ptx::tmem_wait_ld();
+                            for (int cc = 0; cc < 8; ++cc) {
+                                uint32_t ov[16];
+                                SMLA_TMEM_LD16(tmem + lane_base + ocol0 + cc * 16, ov);
+                                ptx::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                            SMLA_TMEM_ST16(tmem + lane_base + ocol0 + cc * 16, ov);
+                                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                SMLA_TMEM_ST16(tmem + lane_base + ocol0 + cc * 16, ov);
+                            }
+                            ptx::tmem_wait_st();
+                            ptx::tc_fence_before();
                         }
-                        ptx::tmem_wait_st();
-                        ptx::tc_fence_before();
+                        // Page 0's MMAs add to all 512 dims, also to the lanes of the page 1 warps, but its
+                        // barrier counts the page 0 warps only.  So the rows' four warps meet here: a store of
+                        // any of them comes before this barrier, this before the page 0 warps' arrival on
+                        // kPbPFull, that (both row groups', both CTAs') before the issuer's MMAs.  The branch
+                        // is the same in the four: a row's max, and with it `grow`, is the same in its threads.
+                        failed = ptx::named_bar_red_or(grp, 128u, failed);
+                        if (failed) break;
                     }
                 }
                 // P = 2^(c s - m) as bf16, the operand of PV (its rounding averages out over the keys;
