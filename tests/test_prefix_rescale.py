@@ -123,3 +123,20 @@ def test_gpu_max_that_grows_after_masked_blocks(T, h, P, skip, fmt):
     away[:skip] = -1
     out, lse = _run(q, cache, away, P, fmt)
     _check(out, lse, q, cache, pages, P, fmt, skip)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("P", [50, 128, 190, 256, 385])
+def test_gpu_many_short_pieces_in_a_run(P, fmt):
+    """300 tiles of one to four blocks: a CTA pair ends a piece and begins the next again and again, the
+    accumulator read and then overwritten."""
+    T, h = 600, 64
+    q, cache, pages = _case(T, h, P, fmt, "page", P)
+    out, lse = _run(q, cache, pages, P, fmt)
+    _check(out, lse, q, cache, pages, P, fmt)
+    d = [x.to(DEV) for x in (q, cache, pages)]
+    for _ in range(3):
+        o, l = smla.sparse_mla_prefix(*d, P, kv_format=fmt)
+        assert torch.equal(o.cpu(), out) and torch.equal(l.cpu(), lse)
+    smla.sync_status()

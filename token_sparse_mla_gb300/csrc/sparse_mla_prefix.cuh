@@ -81,7 +81,7 @@ struct PfLayout {
     static constexpr int kOffP = kOffV + 2 * kPfVPage;        // two panels; output staging between pieces
     static constexpr int kOffX = kOffP + 2 * kPfPanel;        // [4][64] values swapped by a row's four threads
     static constexpr int kOffBar = kOffX + 4 * kPfHalf * 4;
-    static constexpr int kNumBars = 19;
+    static constexpr int kNumBars = 18;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tmem base, abort flag
     static constexpr int kBytes = kOffMisc + 16;
     // TMEM columns: O [0, 256) | two buffers of (S of the first group, S of the second), 64 each
@@ -99,13 +99,12 @@ enum : int {
     kPbKFull = 2,    // +group, even CTA
     kPbKEmpty = 4,   // +group, both
     kPbVFull = 6,    // +page of the block, even CTA
-    kPbVEmpty = 8,   // +page, both
+    kPbVEmpty = 8,   // +page, both: the page's PV MMAs and all before them are done
     kPbSFull = 10,   // +buffer, both
     kPbSEmpty = 12,  // +buffer, even CTA
     kPbPFull = 14,   // +page, even CTA
-    kPbPvDone = 16,  // both
-    kPbTail = 17,    // own CTA: V of a page that the prefix ends in
-    kPbDrain = 18    // even CTA: everything the issuers issued is done
+    kPbTail = 16,    // own CTA: V of a page that the prefix ends in
+    kPbDrain = 17    // even CTA: everything the issuers issued is done
 };
 
 struct PfParams {
@@ -396,7 +395,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                                                       (b != w.b0 || i > 0 || k > 0) ? 1u : 0u);
                         ptx::mma_commit_pair(bar(kPbVEmpty + i));
                     }
-                    if (ok) ptx::mma_commit_pair(bar(kPbPvDone));
                 }
             }
             // nothing is in flight when TMEM is freed, also after giving up
@@ -499,8 +497,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         l *= alpha;
                     }
                     if (b > w.b0 && __any_sync(0xffffffffu, grow)) {
-                        // O is complete up to the last block
-                        if (!warp_wait(kPbPvDone, (x - 1) & 1)) failed = true;
+                        // O is complete up to the last block: page 1 of PV(x - 1) is done.  The wait cannot pass
+                        // on the phase of PV(x - 2): the page 1 warps saw that one complete in block x - 1 and
+                        // have since met this warp in the vote above.  (A page 0 warp has waited for page 0
+                        // only, so on a barrier that no warp follows block by block it could be two phases
+                        // behind, which a parity cannot tell.)
+                        if (!warp_wait(kPbVEmpty + 1, (x - 1) & 1)) failed = true;
                         if (!failed) {
                             ptx::tc_fence_after();
 #pragma unroll 1
@@ -574,10 +576,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             // ---- the piece's rows: O / l as bf16 and the natural-log LSE if the tile is whole, else
             // the unnormalised partial
-            if (!failed && !warp_wait(kPbPvDone, (x - 1) & 1)) failed = true;
-            ptx::tc_fence_after();
             sX[part * kPfHalf + r] = l;
             failed = ptx::named_bar_red_or(grp, 128u, failed);
+            // O is complete: page 1 of the last PV is done (after the barrier, for the reason given at the rescale)
+            if (!failed && !warp_wait(kPbVEmpty + 1, (x - 1) & 1)) failed = true;
+            ptx::tc_fence_after();
             const float lt = (sX[r] + sX[kPfHalf + r]) + (sX[2 * kPfHalf + r] + sX[3 * kPfHalf + r]);
             const int64_t row0 = w.tile * kPfRows + rank * kPfHalf + (quad & 1) * 32;  // the warp's first row
             const int live = p.rows - row0 < 32 ? static_cast<int>(p.rows - row0) : 32;  // rows of the warp, if any
