@@ -131,6 +131,28 @@ def _stream_handle(stream, device: Optional[torch.device] = None) -> Optional[in
     return stream.cuda_stream
 
 
+def _current_handle(dev: torch.device) -> int:
+    """Raw handle of torch's current stream on dev (a stream object costs 2 us to make)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _empty(shape, dtype: torch.dtype, dev: torch.device, stream, result: bool = True) -> torch.Tensor:
+    """An uninitialised tensor that a call on `stream` (None: the current one) writes.  A block of torch's
+    allocator may still be in use by work pending on the stream that it was allocated for, and a freed one
+    goes to the next request on that stream: so the tensor is allocated for the call's stream, and a
+    result's use by the caller's current stream is recorded (scratch is used by the call alone)."""
+    if stream is not None:
+        handle = _stream_handle(stream, dev) or 0
+        if handle != _current_handle(dev):
+            # (1 is the legacy default stream's other name)
+            with torch.cuda.stream(torch.cuda.ExternalStream(0 if handle == 1 else handle, device=dev)):
+                t = torch.empty(shape, dtype=dtype, device=dev)
+            if result:
+                t.record_stream(torch.cuda.current_stream(dev))
+            return t
+    return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def version() -> int:
     return int(library().sparse_mla_version())
 
@@ -177,9 +199,9 @@ def sparse_mla_fwd(q: torch.Tensor, kv_cache: torch.Tensor, indices: torch.Tenso
     if scale is None:
         scale = D_QK ** -0.5
     if out is None:
-        out = torch.empty((T, h, D_V), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, h, D_V), torch.bfloat16, dev, stream)
     if lse is None:
-        lse = torch.empty((T, h), dtype=torch.float32, device=dev)
+        lse = _empty((T, h), torch.float32, dev, stream)
     if out.shape != (T, h, D_V) or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous [T, h, 512] bf16 tensor")
     if lse.shape != (T, h) or lse.dtype != torch.float32 or not lse.is_contiguous():
@@ -237,9 +259,9 @@ def sparse_mla_merge(o_parts: torch.Tensor, lse_parts: torch.Tensor, *,
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     if out is None:
-        out = torch.empty((T, h, D_V), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, h, D_V), torch.bfloat16, dev, stream)
     if lse is None:
-        lse = torch.empty((T, h), dtype=torch.float32, device=dev)
+        lse = _empty((T, h), torch.float32, dev, stream)
     if out.shape != (T, h, D_V) or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous [T, h, 512] bf16 tensor")
     if lse.shape != (T, h) or lse.dtype != torch.float32 or not lse.is_contiguous():
@@ -268,7 +290,7 @@ def sparse_mla_v_up(o: torch.Tensor, w: torch.Tensor, *, out: Optional[torch.Ten
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     if out is None:
-        out = torch.empty((T, h, v), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, h, v), torch.bfloat16, dev, stream)
     if out.shape != (T, h, v) or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous [T, h, v] bf16 tensor")
     _device_of((("o", o), ("out", out)))
@@ -300,7 +322,7 @@ def sparse_mla_topk(scores: torch.Tensor, lengths: torch.Tensor, topk: int, *,
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     if out is None:
-        out = torch.empty((T, topk), dtype=torch.int32, device=dev)
+        out = _empty((T, topk), torch.int32, dev, stream)
     if out.shape != (T, topk) or out.dtype != torch.int32 or not out.is_contiguous():
         raise ValueError("out must be a contiguous [T, topk] int32 tensor")
     _device_of((("scores", scores), ("out", out)))
@@ -325,7 +347,7 @@ def sparse_mla_scatter_mask(indices: torch.Tensor, S: int, *, out: Optional[torc
     if not indices.is_contiguous():
         raise ValueError("indices must be contiguous")
     if out is None:
-        out = torch.empty((T, W), dtype=torch.int32, device=dev)
+        out = _empty((T, W), torch.int32, dev, stream)
     if out.shape != (T, W) or out.dtype != torch.int32 or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous [T, {W}] int32 tensor")
     _device_of((("indices", indices), ("out", out)))
@@ -360,9 +382,9 @@ def sparse_mla_masked_mha(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mas
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     if out is None:
-        out = torch.empty((T, h, dv), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, h, dv), torch.bfloat16, dev, stream)
     if lse is None:
-        lse = torch.empty((T, h), dtype=torch.float32, device=dev)
+        lse = _empty((T, h), torch.float32, dev, stream)
     if out.shape != (T, h, dv) or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous [T, h, {dv}] bf16 tensor")
     if lse.shape != (T, h) or lse.dtype != torch.float32 or not lse.is_contiguous():
@@ -381,11 +403,6 @@ def sparse_mla_masked_mha(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mas
 # enters no context when the device is already current.
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-
-
-def _current_handle(dev: torch.device) -> int:
-    """Raw handle of torch's current stream on dev (a stream object costs 2 us to make)."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _call(dev: torch.device, stream, fn, *args) -> None:
@@ -495,7 +512,7 @@ def sparse_mla_q_up(q: torch.Tensor, w: torch.Tensor, positions: torch.Tensor, c
     if not dev == w.device == positions.device == cos_sin.device:
         _apart(dev, w=w, positions=positions, cos_sin=cos_sin)
     if out is None:
-        out = torch.empty((T, h, D_QK), dtype=_BF16, device=dev)
+        out = _empty((T, h, D_QK), _BF16, dev, stream)
     else:
         if out.shape != (T, h, D_QK) or out.dtype != _BF16 or not out.is_contiguous():
             raise ValueError("out must be a contiguous [T, h, 576] bf16 tensor")
@@ -530,7 +547,7 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
     Returns out [T, h, 512] bf16 and lse [T, h] fp32, which sparse_mla_merge joins with each token's
     own part.  scale defaults to 576 ** -0.5.  workspace: a uint8 tensor of prefix_workspace_bytes(T,
     h, prefix_len, kv_format) bytes for callers that keep one (calls that may overlap need their own);
-    allocated here otherwise, from torch's allocator on the stream of the call.
+    allocated here otherwise, from torch's allocator on the stream of the call, as out and lse are.
     """
     if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != _BF16 or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous [T, h, 576] bf16 tensor, got {tuple(q.shape)} {q.dtype}")
@@ -546,14 +563,14 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
     if scale is None:
         scale = D_QK ** -0.5
     if out is None:
-        out = torch.empty((T, h, D_V), dtype=_BF16, device=dev)
+        out = _empty((T, h, D_V), _BF16, dev, stream)
     else:
         if out.shape != (T, h, D_V) or out.dtype != _BF16 or not out.is_contiguous():
             raise ValueError("out must be a contiguous [T, h, 512] bf16 tensor")
         if out.device != dev:
             _apart(dev, out=out)
     if lse is None:
-        lse = torch.empty((T, h), dtype=_F32, device=dev)
+        lse = _empty((T, h), _F32, dev, stream)
     else:
         if lse.shape != (T, h) or lse.dtype != _F32 or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous [T, h] fp32 tensor")
@@ -568,7 +585,7 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
             with torch.cuda.device(dev):
                 ws_bytes = _prefix_workspace_bytes(dev.index, T, h, prefix_len, fmt)
         if ws_bytes:
-            workspace = _workspace_on(ws_bytes, dev, stream)
+            workspace = _empty((ws_bytes,), _U8, dev, stream, result=False)
             ws_ptr = workspace.data_ptr()
     else:
         if workspace.dtype != _U8 or not workspace.is_contiguous() or workspace.device != dev:
@@ -577,17 +594,6 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
     _call(dev, stream, library().sparse_mla_prefix, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), T, h,
           prefix_len, num_slots, fmt, float(scale), out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
     return out, lse
-
-
-def _workspace_on(nbytes: int, dev: torch.device, stream) -> torch.Tensor:
-    """nbytes of scratch for one call on `stream` (None: the current one).  The allocator may hand a freed
-    block to the next request on the stream it was allocated for, so it is allocated for the call's."""
-    if stream is not None:
-        handle = _stream_handle(stream, dev)
-        if handle != _current_handle(dev):
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle or 0, device=dev)):
-                return torch.empty(nbytes, dtype=_U8, device=dev)
-    return torch.empty(nbytes, dtype=_U8, device=dev)
 
 
 def host_workspace_bytes(T: int, h: int, topk: int) -> int:
