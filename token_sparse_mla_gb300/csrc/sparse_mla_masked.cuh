@@ -54,7 +54,7 @@ namespace smla {
 constexpr int kMmBM = 128;                     // queries per tile (MMA M)
 constexpr int kMmBN = 64;                      // keys per tile
 constexpr int kMmMaxStages = 4;               // K/V ring depth: as many as shared memory holds, up to 4
-constexpr int kMmNumBars = 26;
+constexpr int kMmNumBars = 25;
 constexpr int kMmParts = 2;                    // softmax warps per TMEM lane quadrant
 constexpr int kMmSoftmaxWarps = 4 * kMmParts;
 constexpr int kMmThreads = 96 + 32 * kMmSoftmaxWarps;  // producer, S issuer, softmax warps, PV issuer
@@ -110,11 +110,10 @@ enum : int {
     kMbSFull = 16,
     kMbSEmpty = 17,  // the softmax warps hold S in registers: the next S may be written
     kMbPFull = 18,   // +buffer
-    kMbPEmpty = 20,  // +buffer
-    kMbPvDone = 22,
-    kMbDrain = 23,
-    kMbQFull = 24,   // the softmax warps have written Q into TMEM
-    kMbQLoad = 25    // Q landed in shared memory
+    kMbPEmpty = 20,  // +buffer: PV of the tile, and all before it, is done
+    kMbDrain = 22,
+    kMbQFull = 23,   // the softmax warps have written Q into TMEM
+    kMbQLoad = 24    // Q landed in shared memory
 };
 
 struct ScatterParams {
@@ -208,7 +207,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             ptx::mbar_init(bar(kMbPFull + b), kMmSoftmaxWarps);
             ptx::mbar_init(bar(kMbPEmpty + b), 1);
         }
-        ptx::mbar_init(bar(kMbPvDone), 1);
         ptx::mbar_init(bar(kMbDrain), 2);  // one commit from each issuing thread
         ptx::fence_mbarrier_init();
     }
@@ -404,7 +402,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                                      (j > 0 || k > 0) ? 1u : 0u);
                 ptx::mma_commit(bar(kMbVEmpty + s));
                 ptx::mma_commit(bar(kMbPEmpty + (j & 1)));
-                ptx::mma_commit(bar(kMbPvDone));
             }
         }
         if (lane == 0) {
@@ -526,7 +523,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 mx = fmaxf(fmaxf(fmaxf(mxa[0], mxa[1]), fmaxf(mxa[2], mxa[3])),
                            fmaxf(fmaxf(mxa[4], mxa[5]), fmaxf(mxa[6], mxa[7])));
             }
-            bool pv_waited = false;
             if (ptx::named_bar_red_or(grp_bar, kGroup, failed || mx > m + kRescaleLog2)) {
                 // the row's max over the group's keys (NaN: a warp of the group gave up)
                 const float v = group_max(failed ? CUDART_NAN_F : mx);
@@ -548,11 +544,13 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         l *= alpha;
                     }
                     if (j > 0) {
-                        if (!warp_wait(kMbPvDone, (j - 1) & 1)) {
+                        // (the buffer's barrier, whose phase of PV(j - 3) this warp waited for in block
+                        // j - 1: on one barrier for all blocks it could be two phases behind, when V(j - 2)
+                        // is late, and the parity of PV(j - 3) would pass for that of PV(j - 1))
+                        if (!warp_wait(kMbPEmpty + ((j - 1) & 1), ((j - 1) >> 1) & 1)) {
                             failed = true;
                             continue;  // the next reduction takes the whole group out
                         }
-                        pv_waited = true;
                         ptx::tc_fence_after();
 #pragma unroll 1
                         for (int cc = 0; cc < kOCols / 16; ++cc) {
@@ -584,7 +582,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 pk[i] = pack_bf16x2(pp.x, pp.y);
             }
             l += ((la[0].x + la[0].y) + (la[1].x + la[1].y)) + ((la[2].x + la[2].y) + (la[3].x + la[3].y));
-            if (j >= 2 && !pv_waited) {
+            if (j >= 2) {  // by every warp in every block, so that none misses a phase
                 if (!warp_wait(kMbPEmpty + (j & 1), ((j >> 1) - 1) & 1)) {
                     failed = true;
                     continue;
@@ -608,7 +606,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         // loop).
         bool have_o = nact > 0 && !failed;
         if (have_o) {
-            have_o = warp_wait(kMbPvDone, (nact - 1) & 1);
+            have_o = warp_wait(kMbPEmpty + ((nact - 1) & 1), ((nact - 1) >> 1) & 1);
             if (have_o) ptx::tc_fence_after();
         }
         ptx::named_bar_sync(grp_bar, kGroup);  // every read of sX in the loop is done
