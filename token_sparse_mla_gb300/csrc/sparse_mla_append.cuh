@@ -148,10 +148,11 @@ __global__ void __launch_bounds__(kAppendThreads) sparse_mla_append_kernel(const
         for (int o = 1; o < 8; o <<= 1) amax = ptx::max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         float scale = __fdiv_rn(amax, 448.f);
         if (scale == 0.f) scale = 1.f;  // a tile of zeros (or of values too small for a scale): codes 0
-        // code = e4m3(x / scale), the quotient rounded to fp32 first.  Markstein's theorem: with y = 1/b
-        // correctly rounded, q = a y, r = a - b q (exact in an fma) and q + r y rounds as a / b does, three
-        // operations per value where the scale is far from the ends of the range (a division per value
-        // made the kernel compute-bound).  Where r would underflow, the code is 0 either way.
+        // code = e4m3(x / scale), the quotient rounded to fp32 first, by Markstein's correction: with y = 1/b
+        // correctly rounded, q = a y (off by two units at most) and r = a - b q in an fma, q + r y is a / b to
+        // 2^-45 before its one rounding, three operations per value where the scale is far from the ends of
+        // the range (a division per value made the kernel compute-bound).  Where r would underflow, the code
+        // is 0 either way.
         float q[16];
         if (scale > 0x1p-100f && scale < 0x1p100f) {
             const float y = __fdiv_rn(1.f, scale);

@@ -18,9 +18,9 @@
 // Back to back, an MMA of this form takes 32 cycles at N = 128 and 64 at N = 256 (4060 multiply-adds a
 // cycle and SM, the dense rate) but 25 at N = 64, so blocks of one page would lose a third of S; a block
 // of two is 36 * 32 + 16 * 64 = 2190 cycles.  The nearer bound is shared memory: operands of S 144 KB
-// and of PV 96 KB, 136 KB written by TMA and P's 16 KB are 3100 cycles at 128 bytes a cycle; measured
-// (76 tiles x 8192 keys, rows in L2) 1.5 us a block at 1.94 GHz, 1620 TFLOP/s.  What the shape costs is
-// room: Q 72 KB, K 72 KB, V 64 KB and P 16 KB leave one stage of each, so K is refilled in two groups of
+// and of PV 96 KB, 136 KB written by TMA and P's 16 KB are 3140 cycles at 128 bytes a cycle; measured
+// (76 tiles, 16384 keys against 8192) 1.73 us a block, 3260 cycles at the 1.89 GHz of a run of seconds, and
+// 1.6 us, 1700 TFLOP/s, in a short one.  What the shape costs is room: Q 72 KB, K 72 KB, V 64 KB and P 16 KB leave one stage of each, so K is refilled in two groups of
 // panels and V and P page by page, each as soon as its last MMA is done.  (The half of V that lies in a
 // CTA's own K tile is loaded again: the MMA wants the same keys at the same offset in both CTAs, and K
 // wants different ones.)
