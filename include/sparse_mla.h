@@ -400,6 +400,59 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
                               float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * sparse_mla_tree -- attention of a batch of sequences over each one's own cached
+ * rows, for a tree of drafted tokens per sequence (speculative decoding; one
+ * token per sequence is the plain decode step over the whole context).  Sequence
+ * b has lengths[b] cached rows and the tokens starts[b] .. starts[b + 1] - 1 of q;
+ * the row of its j-th token has been appended at position lengths[b] + j.
+ * Position i of sequence b is cache slot block_tables[b][i / 64] * 64 + i % 64.
+ * Token t sees every cached row of its sequence and the j-th drafted token if bit
+ * j % 32 of word j / 32 of mask[t] is set (sparse_mla_scatter_mask writes such
+ * words from lists of ancestors); without a mask, in a chain, those up to itself:
+ *     s_p = scale * <q, kv[slot p, :]>  (576 dims),  O = softmax(s) . kv[slot p, 0:512],
+ *     LSE = ln sum exp(s_p)
+ * over the positions p that it sees.  The part of the context in sparse_mla_merge's
+ * form, if another part (lists, a shared prefix) is computed apart.  bf16 products, fp32
+ * softmax and accumulation on the tcgen05 tensor cores, O rounded to bf16; fp8 rows are
+ * dequantised to bf16 as in sparse_mla_fwd.
+ *   q             device, [T, h, 576] bf16, 16-byte aligned; any h >= 1
+ *   kv_cache      device, num_slots rows as in sparse_mla_fwd, 16-byte aligned
+ *   block_tables  device, [seqs, blocks] int32.  Positions past blocks * 64 do not
+ *                 exist.  An entry outside the cache masks its 64 positions, and
+ *                 positions that fall on slots >= num_slots are masked
+ *   lengths       device, [seqs] int32, brought into [0, blocks * 64]
+ *   starts        device, [seqs + 1] int32, ascending, brought into [0, T].  A
+ *                 sequence may have no tokens.  Tokens outside
+ *                 [starts[0], starts[seqs]) belong to no sequence: their out and
+ *                 lse are left as they are (places of a padded batch)
+ *   mask          device, [T, mask_words] uint32, or NULL: chains.  Drafted tokens
+ *                 past its 32 * mask_words bits are seen by none
+ *   out           device, [T, h, 512] bf16, caller-owned, 16-byte aligned
+ *   lse           device, [T, h] fp32, caller-owned
+ *   workspace     device, at least sparse_mla_tree_workspace_bytes(T, h, seqs,
+ *                 kv_format) bytes, 256-byte aligned, caller-owned: partial results
+ *                 of row tiles that several CTAs share, and fp8 rows as bf16 on
+ *                 their way.  Calls that may overlap in time need workspaces of
+ *                 their own, and so do captured ones that may
+ * out, lse and workspace must overlap neither each other nor the inputs.  What rows
+ * past a sequence's end hold does not matter, nor what drafted rows hold that a
+ * token does not see, infinities and NaN included.  (Of a drafted row with infinities a
+ * token that sees it gets NaN, or 0 times it where its logit is -infinity.)
+ * A token that sees no position gives O = 0 and LSE = -inf.  Lengths, starts and tables
+ * are read on the device when the call runs, so that a captured call serves a batch
+ * that grows.  Repeated calls with the same arguments give identical bytes.
+ * T = 0 or seqs = 0 is a no-op.  Allocates nothing; asynchronous on `stream`.  Errors:
+ * SMLA_ERR_INVALID_ARG for bad sizes, format, scale or workspace, a null pointer or
+ * misalignment; SMLA_ERR_CUDA if a tensor map or a launch fails; a bounded wait that
+ * ran out is reported by sparse_mla_sync_status().
+ */
+size_t sparse_mla_tree_workspace_bytes(int32_t T, int32_t h, int32_t seqs, int32_t kv_format);
+smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths,
+                            const int32_t* starts, const uint32_t* mask, int32_t T, int32_t h, int32_t seqs, int32_t blocks,
+                            int32_t mask_words, int64_t num_slots, int32_t kv_format, float scale, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * sparse_mla_fwd_host -- the same forward pass taking HOST buffers for the
  * per-step inputs and outputs, for callers whose q/indices live in host memory.
  * It queues on `stream`: copies of q_host and indices_host into `workspace`,

@@ -40,8 +40,10 @@ from ._binding import (  # noqa: F401
     sparse_mla_q_up,
     sparse_mla_scatter_mask,
     sparse_mla_topk,
+    sparse_mla_tree,
     sparse_mla_v_up,
     sync_status,
+    tree_workspace_bytes,
     version,
 )
 
@@ -66,7 +68,9 @@ __all__ = [
     "sparse_mla_q_up",
     "sparse_mla_scatter_mask",
     "sparse_mla_topk",
+    "sparse_mla_tree",
     "sparse_mla_v_up",
     "sync_status",
+    "tree_workspace_bytes",
     "version",
 ]

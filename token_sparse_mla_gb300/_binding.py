@@ -23,6 +23,7 @@ EXPORTED = ("sparse_mla_fwd", "sparse_mla_fwd_ex", "sparse_mla_fwd_checked", "sp
             "sparse_mla_host_workspace_bytes", "sparse_mla_merge",
             "sparse_mla_v_up", "sparse_mla_topk", "sparse_mla_scatter_mask", "sparse_mla_masked_mha",
             "sparse_mla_append", "sparse_mla_q_up", "sparse_mla_prefix", "sparse_mla_prefix_workspace_bytes",
+            "sparse_mla_tree", "sparse_mla_tree_workspace_bytes",
             "sparse_mla_sync_status",
             "sparse_mla_launch_info", "sparse_mla_last_error", "sparse_mla_version")
 
@@ -78,6 +79,10 @@ def library() -> ctypes.CDLL:
     lib.sparse_mla_prefix_workspace_bytes.argtypes = [i32, i32, i64, i32]
     lib.sparse_mla_prefix.restype = ctypes.c_int
     lib.sparse_mla_prefix.argtypes = [vp, vp, vp, i32, i32, i64, i64, i32, f32, vp, vp, vp, sz, vp]
+    lib.sparse_mla_tree_workspace_bytes.restype = sz
+    lib.sparse_mla_tree_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.sparse_mla_tree.restype = ctypes.c_int
+    lib.sparse_mla_tree.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i64, i32, f32, vp, vp, vp, sz, vp]
     lib.sparse_mla_host_io_layout.restype = ctypes.c_int
     lib.sparse_mla_host_io_layout.argtypes = [i32, i32, i32, vp, vp, vp, vp]
     lib.sparse_mla_fwd_host_packed.restype = ctypes.c_int
@@ -523,6 +528,20 @@ def sparse_mla_q_up(q: torch.Tensor, w: torch.Tensor, positions: torch.Tensor, c
     return out
 
 
+def _workspace(dev: torch.device, stream, workspace: Optional[torch.Tensor], bytes_of, *shape) -> Optional[torch.Tensor]:
+    """The caller's workspace, or one for a call on `stream` of bytes_of(device, *shape) bytes (None: needs none)."""
+    if workspace is not None:
+        if workspace.dtype != _U8 or not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+        return workspace
+    if torch.cuda.current_device() == dev.index:
+        n = bytes_of(dev.index, *shape)
+    else:
+        with torch.cuda.device(dev):
+            n = bytes_of(dev.index, *shape)
+    return _empty((n,), _U8, dev, stream, result=False) if n else None
+
+
 @functools.lru_cache(maxsize=1024)
 def _prefix_workspace_bytes(device_index: int, T: int, h: int, prefix_len: int, fmt: int) -> int:
     """The library's answer for the device that is current, asked once per shape and device."""
@@ -577,22 +596,104 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
         if lse.device != dev:
             _apart(dev, lse=lse)
     fmt = KV_FORMATS[kv_format]
-    ws_ptr, ws_bytes = None, 0
-    if workspace is None:
-        if torch.cuda.current_device() == dev.index:
-            ws_bytes = _prefix_workspace_bytes(dev.index, T, h, prefix_len, fmt)
-        else:
-            with torch.cuda.device(dev):
-                ws_bytes = _prefix_workspace_bytes(dev.index, T, h, prefix_len, fmt)
-        if ws_bytes:
-            workspace = _empty((ws_bytes,), _U8, dev, stream, result=False)
-            ws_ptr = workspace.data_ptr()
-    else:
-        if workspace.dtype != _U8 or not workspace.is_contiguous() or workspace.device != dev:
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    workspace = _workspace(dev, stream, workspace, _prefix_workspace_bytes, T, h, prefix_len, fmt)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _call(dev, stream, library().sparse_mla_prefix, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), T, h,
           prefix_len, num_slots, fmt, float(scale), out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
+    return out, lse
+
+
+# ---- a batch of sequences, each over its own rows
+
+@functools.lru_cache(maxsize=1024)
+def _tree_workspace_bytes(device_index: int, T: int, h: int, seqs: int, fmt: int) -> int:
+    """The library's answer for the device that is current, asked once per shape and device."""
+    return int(library().sparse_mla_tree_workspace_bytes(T, h, seqs, fmt))
+
+
+def tree_workspace_bytes(T: int, h: int, seqs: int, kv_format: str = "bf16") -> int:
+    """Bytes of workspace that sparse_mla_tree needs on the current device."""
+    if kv_format not in KV_FORMATS:
+        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
+    return int(library().sparse_mla_tree_workspace_bytes(T, h, seqs, KV_FORMATS[kv_format]))
+
+
+def _batch(dev: torch.device, block_tables: torch.Tensor, lengths: torch.Tensor) -> Tuple[int, int]:
+    """Sequences and blocks per sequence of a batch's tables."""
+    if block_tables.dim() != 2 or block_tables.dtype != _I32 or not block_tables.is_contiguous() or block_tables.shape[1] < 1:
+        raise ValueError("block_tables must be a contiguous [seqs, blocks] int32 tensor of at least one block")
+    seqs, blocks = block_tables.shape
+    if lengths.shape != (seqs,) or lengths.dtype != _I32 or not lengths.is_contiguous():
+        raise ValueError(f"lengths must be a contiguous [{seqs}] int32 tensor")
+    if not dev == block_tables.device == lengths.device:
+        _apart(dev, block_tables=block_tables, lengths=lengths)
+    return seqs, blocks
+
+
+def _tokens(dev: torch.device, T: int, seqs: int, starts: torch.Tensor, mask: Optional[torch.Tensor]):
+    """Checks starts and the mask; the mask's pointer and words per token."""
+    if starts.shape != (seqs + 1,) or starts.dtype != _I32 or not starts.is_contiguous():
+        raise ValueError(f"starts must be a contiguous [{seqs + 1}] int32 tensor")
+    if starts.device != dev:
+        _apart(dev, starts=starts)
+    if mask is None:
+        return None, 0
+    if mask.dim() != 2 or mask.shape[0] != T or mask.shape[1] < 1 or mask.dtype != _I32 or not mask.is_contiguous():
+        raise ValueError(f"mask must be a contiguous [{T}, words] int32 tensor of at least one word")
+    if mask.device != dev:
+        _apart(dev, mask=mask)
+    return mask.data_ptr(), mask.shape[1]
+
+
+def sparse_mla_tree(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tensor, lengths: torch.Tensor,
+                    starts: torch.Tensor, scale: Optional[float] = None, *, mask: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, kv_format: str = "bf16",
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of each sequence's drafted tokens over its cached rows and the tree that they form
+    (include/sparse_mla.h).
+
+    q [T, h, 576] bf16, kv_cache as in sparse_mla_fwd, block_tables [seqs, blocks] int32, lengths [seqs]
+    int32 (cached rows before the drafted ones), starts [seqs + 1] int32: sequence b's tokens are
+    starts[b] .. starts[b + 1] - 1, the row of its j-th one at position lengths[b] + j.  mask [T, words]
+    int32 bit words (as sparse_mla_scatter_mask writes them): bit j of a token's words lets it see
+    drafted token j of its sequence; None: chains, each token sees those up to itself.
+
+    Returns out [T, h, 512] bf16 and lse [T, h] fp32; tokens of no sequence are left as they are.
+    scale defaults to 576 ** -0.5.  workspace: a uint8 tensor of tree_workspace_bytes(T, h, seqs,
+    kv_format) bytes for callers that keep one (calls that may overlap need their own); allocated here
+    otherwise, from torch's allocator on the stream of the call, as out and lse are.
+    """
+    if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != _BF16 or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous [T, h, 576] bf16 tensor, got {tuple(q.shape)} {q.dtype}")
+    T, h, _ = q.shape
+    num_slots = _cache_rows(kv_cache, kv_format)
+    dev = _cuda_device("q", q)
+    if kv_cache.device != dev:
+        _apart(dev, kv_cache=kv_cache)
+    seqs, blocks = _batch(dev, block_tables, lengths)
+    mask_ptr, words = _tokens(dev, T, seqs, starts, mask)
+    if scale is None:
+        scale = D_QK ** -0.5
+    if out is None:
+        out = _empty((T, h, D_V), _BF16, dev, stream)
+    else:
+        if out.shape != (T, h, D_V) or out.dtype != _BF16 or not out.is_contiguous():
+            raise ValueError("out must be a contiguous [T, h, 512] bf16 tensor")
+        if out.device != dev:
+            _apart(dev, out=out)
+    if lse is None:
+        lse = _empty((T, h), _F32, dev, stream)
+    else:
+        if lse.shape != (T, h) or lse.dtype != _F32 or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous [T, h] fp32 tensor")
+        if lse.device != dev:
+            _apart(dev, lse=lse)
+    fmt = KV_FORMATS[kv_format]
+    workspace = _workspace(dev, stream, workspace, _tree_workspace_bytes, T, h, seqs, fmt)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _call(dev, stream, library().sparse_mla_tree, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
+          lengths.data_ptr(), starts.data_ptr(), mask_ptr, T, h, seqs, blocks, words, num_slots, fmt, float(scale),
+          out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
     return out, lse
 
 

@@ -18,6 +18,7 @@
 #include "sparse_mla_merge.cuh"
 #include "sparse_mla_v_up.cuh"
 #include "sparse_mla_topk.cuh"
+#include "sparse_mla_tree.cuh"
 #include "sparse_mla_masked.cuh"
 #include "sparse_mla_append.cuh"
 #include "sparse_mla_q_up.cuh"
@@ -89,6 +90,8 @@ cudaError_t set_kernel_attrs() {
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<192, 256>, smla::QupLayout<192, 256>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_q_up_kernel<256, 128>, smla::QupLayout<256, 128>::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_prefix_kernel, smla::PfLayout::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_tree_kernel<0>, smla::TrLayout::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_tree_kernel<1>, smla::TrLayout::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_scatter_mask_kernel, smla::kScatterMaxS / 32 * 4);
     return e;
 }
@@ -479,6 +482,79 @@ PrefixPlan prefix_plan(int64_t rows, int64_t prefix, bool fp8, int num_sms) {
     pl.off_ml = slots * smla::kDV * 4;
     pl.off_expanded = align256(pl.off_ml + slots * 2 * 4);
     pl.bytes = pl.off_expanded + (fp8 ? static_cast<size_t>(pl.npages) * smla::kPfPage * smla::kDQK * 2 : 0);
+    return pl;
+}
+
+// What the calls on a batch of sequences check alike.
+smla_status check_batch(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths, const int32_t* starts,
+                        const uint32_t* mask, int32_t T, int32_t h, int32_t seqs, int32_t blocks, int32_t mask_words, int64_t num_slots,
+                        int32_t kv_format, float scale) {
+    if (T < 0 || h < 1 || seqs < 0) return fail(SMLA_ERR_INVALID_ARG, "T and seqs must be >= 0 and h >= 1 (got %d, %d, %d)", T, seqs, h);
+    if (blocks < 1 || blocks > smla::kMaxBlocks)
+        return fail(SMLA_ERR_INVALID_ARG, "blocks per sequence must be in [1, %d] (got %d)", smla::kMaxBlocks, blocks);
+    if (num_slots < 1 || num_slots > 0x7fffffffLL)
+        return fail(SMLA_ERR_INVALID_ARG, "num_slots must be in [1, 2^31-1] (got %lld)", static_cast<long long>(num_slots));
+    if (kv_format != SMLA_KV_BF16 && kv_format != SMLA_KV_FP8)
+        return fail(SMLA_ERR_INVALID_ARG, "unknown kv_format %d", kv_format);
+    if (!std::isfinite(scale)) return fail(SMLA_ERR_INVALID_ARG, "scale must be finite");
+    if (mask != nullptr && mask_words < 1) return fail(SMLA_ERR_INVALID_ARG, "mask_words must be >= 1 (got %d)", mask_words);
+    if (static_cast<int64_t>(T) * h > 0x7f000000LL) return fail(SMLA_ERR_INVALID_ARG, "T * h too large (%d, %d)", T, h);
+    if (T == 0 || seqs == 0) return SMLA_OK;
+    if (!q || !kv_cache || !block_tables || !lengths || !starts) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(q, 16) || !aligned(kv_cache, 16)) return fail(SMLA_ERR_INVALID_ARG, "q and kv_cache must be 16-byte aligned");
+    if (!aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(starts, 4) || !aligned(mask, 4))
+        return fail(SMLA_ERR_INVALID_ARG, "block_tables, lengths, starts and mask must be 4-byte aligned");
+    return SMLA_OK;
+}
+
+smla::BatchParams batch_params(const void* kv_cache, const int32_t* block_tables, const int32_t* lengths, const int32_t* starts,
+                               const uint32_t* mask, int32_t T, int32_t h, int32_t seqs, int32_t blocks, int32_t mask_words,
+                               int64_t num_slots) {
+    smla::BatchParams bp = {};
+    bp.kv = kv_cache;
+    bp.tables = block_tables;
+    bp.lengths = lengths;
+    bp.starts = starts;
+    bp.mask = mask;
+    bp.num_slots = num_slots;
+    bp.B = seqs;
+    bp.nb = blocks;
+    bp.words = mask_words;
+    bp.T = T;
+    bp.h = h;
+    return bp;
+}
+
+// [n, 576] bf16 rows viewed as (64 dims, n, 9 panels): one box lands as SW128 panels one after another.
+CUresult row_map(EncodeTiledFn enc, CUtensorMap* tm, const void* base, int64_t n, uint32_t box_rows, uint32_t box_panels) {
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(n), smla::kPanels};
+    const cuuint64_t strides[2] = {smla::kDQK * 2, 128};
+    const cuuint32_t box[3] = {64, box_rows, box_panels};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// sparse_mla_tree's workspace: partials of cut tiles (two slots per CTA pair), the notes for their join, and
+// the ring of expanded rows of an fp8 cache.
+struct TreePlan {
+    int pairs = 0, slot_groups = 0, jobs = 0;
+    bool by_tile = false;
+    size_t off_ml = 0, off_jobs = 0, off_ring = 0, bytes = 0;
+};
+
+TreePlan tree_plan(int64_t rows, int64_t seqs, bool fp8, int num_sms) {
+    TreePlan pl;
+    pl.pairs = num_sms / 2;
+    pl.slot_groups = static_cast<int>(((rows < smla::kPfRows ? rows : smla::kPfRows) + 31) / 32);
+    const int64_t tiles = rows / smla::kPfRows + seqs;  // at most
+    pl.by_tile = tiles <= pl.pairs;
+    pl.jobs = static_cast<int>(pl.by_tile ? tiles : pl.pairs);
+    const size_t slots = static_cast<size_t>(pl.pairs) * 2 * pl.slot_groups * 32;  // rows in all slots
+    pl.off_ml = slots * smla::kDV * 4;
+    pl.off_jobs = align256(pl.off_ml + slots * 2 * 4);
+    pl.off_ring = align256(pl.off_jobs + static_cast<size_t>(pl.jobs) * sizeof(int4));
+    pl.bytes = pl.off_ring + (fp8 ? static_cast<size_t>(pl.pairs) * smla::kTrRing * smla::kTrBlockRows * smla::kDQK * 2 : 0);
     return pl;
 }
 
@@ -1212,6 +1288,90 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
                          : cudaLaunchKernelEx(&cfg, smla::sparse_mla_prefix_merge_kernel<1>, pp);
         if (e != cudaSuccess) return cuda_fail(e, "prefix merge kernel launch");
     }
+    return SMLA_OK;
+}
+
+
+size_t sparse_mla_tree_workspace_bytes(int32_t T, int32_t h, int32_t seqs, int32_t kv_format) {
+    if (T <= 0 || h <= 0 || seqs <= 0) return 0;
+    int num_sms = 152;
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    if (device_state(&dev, &ds) == SMLA_OK) num_sms = ds->num_sms;
+    return tree_plan(static_cast<int64_t>(T) * h, seqs, kv_format == SMLA_KV_FP8, num_sms).bytes;
+}
+
+smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths,
+                            const int32_t* starts, const uint32_t* mask, int32_t T, int32_t h, int32_t seqs, int32_t blocks,
+                            int32_t mask_words, int64_t num_slots, int32_t kv_format, float scale, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    smla_status st = check_batch(q, kv_cache, block_tables, lengths, starts, mask, T, h, seqs, blocks, mask_words, num_slots, kv_format, scale);
+    if (st != SMLA_OK || T == 0 || seqs == 0) return st;
+    if (!out || !lse) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(out, 16) || !aligned(lse, 4)) return fail(SMLA_ERR_INVALID_ARG, "out must be 16-byte and lse 4-byte aligned");
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&dev, &ds)) != SMLA_OK) return st;
+    const bool fp8 = kv_format == SMLA_KV_FP8;
+    const int64_t rows = static_cast<int64_t>(T) * h;
+    const TreePlan pl = tree_plan(rows, seqs, fp8, ds->num_sms);
+    if (!workspace || !aligned(workspace, 256)) return fail(SMLA_ERR_INVALID_ARG, "workspace must be given, 256-byte aligned");
+    if (workspace_bytes < pl.bytes)
+        return fail(SMLA_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, pl.bytes);
+    EncodeTiledFn enc = nullptr;
+    if ((st = encode_fn(&enc)) != SMLA_OK) return st;
+    char* ws = static_cast<char*>(workspace);
+    const void* rows_at = fp8 ? ws + pl.off_ring : kv_cache;
+    const int64_t num_rows = fp8 ? static_cast<int64_t>(pl.pairs) * smla::kTrRing * smla::kTrBlockRows : num_slots;
+    alignas(64) CUtensorMap tm_q;
+    alignas(64) CUtensorMap tm_k;
+    alignas(64) CUtensorMap tm_v;
+    CUresult r = row_map(enc, &tm_q, q, rows, smla::kPfHalf, smla::kPanels);
+    if (r == CUDA_SUCCESS) r = row_map(enc, &tm_k, rows_at, num_rows, smla::kPfPage, smla::kPfGroupA);
+    if (r == CUDA_SUCCESS) r = row_map(enc, &tm_v, rows_at, num_rows, smla::kPfPage, smla::kPfGroupB);
+    if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/kv_cache failed (%d)", (int)r);
+    smla::TrParams tp = {};
+    tp.bp = batch_params(kv_cache, block_tables, lengths, starts, mask, T, h, seqs, blocks, mask_words, num_slots);
+    tp.ring = fp8 ? reinterpret_cast<__nv_bfloat16*>(ws + pl.off_ring) : nullptr;
+    tp.out = static_cast<__nv_bfloat16*>(out);
+    tp.lse = lse;
+    tp.part_o = reinterpret_cast<float*>(ws);
+    tp.part_ml = reinterpret_cast<float*>(ws + pl.off_ml);
+    tp.job_list = reinterpret_cast<int4*>(ws + pl.off_jobs);
+    tp.pairs = pl.pairs;
+    tp.jobs = pl.jobs;
+    tp.by_tile = pl.by_tile;
+    tp.slot_groups = pl.slot_groups;
+    tp.sm_scale_log2 = scale * 1.4426950408889634f;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pl.pairs), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(fp8 ? smla::tree_threads<1>() : smla::tree_threads<0>()), 1, 1);
+    cfg.dynamicSmemBytes = smla::TrLayout::kBytes;
+    cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_kernel<1>, tm_q, tm_k, tm_v, tp)
+                        : cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_kernel<0>, tm_q, tm_k, tm_v, tp);
+    if (e != cudaSuccess) return cuda_fail(e, "tree kernel launch");
+    // the join: 64 / parts dims per CTA, as in the prefix attention
+    cfg.numAttrs = 1;
+    const int64_t groups = static_cast<int64_t>(pl.jobs) * pl.slot_groups;
+    const int64_t most = static_cast<int64_t>(ds->num_sms) * 3;
+    const int parts = groups * 32 <= most ? 4 : groups * 16 <= most ? 2 : 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(groups * 8 * parts), 1, 1);
+    cfg.blockDim = dim3(smla::kPfMergeThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    e = parts == 4   ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_merge_kernel<4>, tp)
+        : parts == 2 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_merge_kernel<2>, tp)
+                     : cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_merge_kernel<1>, tp);
+    if (e != cudaSuccess) return cuda_fail(e, "tree merge kernel launch");
     return SMLA_OK;
 }
 

@@ -705,42 +705,29 @@ __global__ void __launch_bounds__(kPfExpandThreads) sparse_mla_prefix_expand_ker
 // pieces (one warp over all 38 pieces of 256 rows took 20 us, a round of latency per eight pieces, twice;
 // four take 5), many tiles into few.
 template <int PARTS>
-__global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kernel(const PfParams p) {
-    constexpr int kChunks = kPfMergeThreads / 32 / PARTS;  // of four dims
-    constexpr int kDims = 4 * kChunks;
+struct PfJoin {
+    static constexpr int kChunks = kPfMergeThreads / 32 / PARTS;  // of four dims
+    static constexpr int kDims = 4 * kChunks;                     // per CTA
+};
+
+// One CTA's share of a cut tile: rows 32 group .. (`live` of them, from out / lse on), dims kDims dg .. .  Piece
+// k0 lies in slot first_slot, piece k of k0 + 1 .. k1 in slot 2 k.
+template <int PARTS>
+__device__ __forceinline__ void pf_join(const float* slots_o, const float* slots_ml, int slot_groups, int group, int dg, int k0, int k1,
+                                        int first_slot, int live, __nv_bfloat16* out, float* lse) {
+    constexpr int kChunks = PfJoin<PARTS>::kChunks;
+    constexpr int kDims = PfJoin<PARTS>::kDims;
     constexpr int kFlight = 4;
     __shared__ float4 s_acc[PARTS][kChunks][32];
     __shared__ float s_m[PARTS][32], s_l[PARTS][32];
     __shared__ uint2 s_out[32][kChunks + 1];
-    ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int chunk = (threadIdx.x >> 5) % kChunks, part = (threadIdx.x >> 5) / kChunks;
-    const int dg = static_cast<int>(blockIdx.x % (kDV / kDims));
-    const int group = static_cast<int>(blockIdx.x / (kDV / kDims)) % p.slot_groups;
-    // the tile: with more tiles than runs most are whole, and the candidates are those that the runs'
-    // boundaries fall into (the first boundary of a tile stands for it)
-    int64_t tile = blockIdx.x / (kDV / kDims) / p.slot_groups;
-    if (p.tiles > p.runs) {
-        const int64_t k = tile + 1;
-        const int64_t at = p.work * k / p.runs;
-        tile = at / p.nblk;
-        if (at % p.nblk == 0 || p.work * (k - 1) / p.runs > tile * p.nblk) return;
-    }
-    const int64_t row0 = tile * kPfRows + group * 32;
-    if (row0 >= p.rows) return;
-    auto run_of = [&](int64_t b) -> int { return static_cast<int>(((b + 1) * p.runs - 1) / p.work); };
-    const int k0 = run_of(tile * p.nblk), k1 = run_of((tile + 1) * p.nblk - 1);
-    if (k0 == k1) return;  // the tile lies inside one run, which wrote it
-    // this tile is the first piece of every run that starts inside it; the run that it begins in
-    // keeps it in its second slot, unless that run starts with it
-    const int first_slot = 2 * k0 + (p.work * k0 / p.runs == tile * p.nblk ? 0 : 1);
     auto group_of = [&](int k) -> int64_t {
-        return static_cast<int64_t>(k == k0 ? first_slot : 2 * k) * p.slot_groups + group;
+        return static_cast<int64_t>(k == k0 ? first_slot : 2 * k) * slot_groups + group;
     };
-    const int live = p.rows - row0 < 32 ? static_cast<int>(p.rows - row0) : 32;
     const int at = lane < live ? lane : live - 1;  // a lane past the last row repeats it and stores nothing
-    const float4* part_o = reinterpret_cast<const float4*>(p.part_o) + (dg * kChunks + chunk) * 32 + at;
+    const float4* part_o = reinterpret_cast<const float4*>(slots_o) + (dg * kChunks + chunk) * 32 + at;
     float m = -CUDART_INF_F, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int kk = k0 + part; kk <= k1; kk += PARTS * kFlight) {
@@ -749,8 +736,8 @@ __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kerne
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             const int64_t g = group_of(min(kk + PARTS * u, k1));
-            mk[u] = __ldg(p.part_ml + 64 * g + at);
-            lk[u] = __ldg(p.part_ml + 64 * g + 32 + at);
+            mk[u] = __ldg(slots_ml + 64 * g + at);
+            lk[u] = __ldg(slots_ml + 64 * g + 32 + at);
             v[u] = __ldg(part_o + g * (128 * 32));
         }
         float mn = m;
@@ -807,11 +794,39 @@ __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kerne
         const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
         s_out[lane][chunk] = make_uint2(ptx::cvt_bf16x2(acc.x * inv, acc.y * inv), ptx::cvt_bf16x2(acc.z * inv, acc.w * inv));
         if (dg == 0 && chunk == 0 && lane < live)
-            p.lse[row0 + lane] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+            lse[lane] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
     }
     __syncthreads();
     const int r = threadIdx.x / kChunks, c = threadIdx.x % kChunks;  // neighbouring threads store a row's bytes
-    if (r < live) reinterpret_cast<uint2*>(p.out + (row0 + r) * kDV + dg * kDims)[c] = s_out[r][c];
+    if (r < live) reinterpret_cast<uint2*>(out + static_cast<int64_t>(r) * kDV + dg * kDims)[c] = s_out[r][c];
+}
+
+template <int PARTS>
+__global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_prefix_merge_kernel(const PfParams p) {
+    constexpr int kDims = PfJoin<PARTS>::kDims;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int dg = static_cast<int>(blockIdx.x % (kDV / kDims));
+    const int group = static_cast<int>(blockIdx.x / (kDV / kDims)) % p.slot_groups;
+    // the tile: with more tiles than runs most are whole, and the candidates are those that the runs'
+    // boundaries fall into (the first boundary of a tile stands for it)
+    int64_t tile = blockIdx.x / (kDV / kDims) / p.slot_groups;
+    if (p.tiles > p.runs) {
+        const int64_t k = tile + 1;
+        const int64_t at = p.work * k / p.runs;
+        tile = at / p.nblk;
+        if (at % p.nblk == 0 || p.work * (k - 1) / p.runs > tile * p.nblk) return;
+    }
+    const int64_t row0 = tile * kPfRows + group * 32;
+    if (row0 >= p.rows) return;
+    auto run_of = [&](int64_t b) -> int { return static_cast<int>(((b + 1) * p.runs - 1) / p.work); };
+    const int k0 = run_of(tile * p.nblk), k1 = run_of((tile + 1) * p.nblk - 1);
+    if (k0 == k1) return;  // the tile lies inside one run, which wrote it
+    // this tile is the first piece of every run that starts inside it; the run that it begins in
+    // keeps it in its second slot, unless that run starts with it
+    const int first_slot = 2 * k0 + (p.work * k0 / p.runs == tile * p.nblk ? 0 : 1);
+    const int live = p.rows - row0 < 32 ? static_cast<int>(p.rows - row0) : 32;
+    pf_join<PARTS>(p.part_o, p.part_ml, p.slot_groups, group, dg, k0, k1, first_slot, live, p.out + row0 * kDV, p.lse + row0);
 }
 
 // The result over no keys: O = 0, LSE = -inf.
