@@ -453,6 +453,38 @@ smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* 
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * sparse_mla_weights -- the attention weight that every row of a batch's caches has
+ * gathered, what sparse_mla_evict ranks them by.  With the arguments of a
+ * sparse_mla_tree call and the lse that it gave, for every position p of sequence b
+ *     out[b][p] = decay * weights[b][p]                     (p < lengths[b])
+ *               + sum over its tokens t that see p, and over heads, of
+ *                 exp(scale * <q[t], kv[slot p, :]> - lse[t])
+ * in fp32, and 0 for the positions past the sequence's last drafted token.  A
+ * sequence without tokens keeps its decayed weights.  The probabilities are those of
+ * that attention (fp8 rows dequantised to bf16); with the lse of a merge they are those of
+ * the whole that was merged.  Rows whose lse is -infinity add nothing.
+ *   q, kv_cache, block_tables, lengths, starts, mask   as in sparse_mla_tree
+ *   lse        device, [T, h] fp32
+ *   weights    device, [seqs, blocks * 64] fp32, or NULL: zeros (decay is then ignored)
+ *   decay      finite
+ *   out        device, [seqs, blocks * 64] fp32, caller-owned; every element is
+ *              written.  May be `weights` itself, but not overlap it in part
+ *   workspace  device, at least sparse_mla_weights_workspace_bytes(kv_format)
+ *              bytes, 256-byte aligned, caller-owned: fp8 rows as bf16 on their way.
+ *              Calls that may overlap in time need workspaces of their own.  NULL
+ *              when that function returns 0
+ * Lengths, starts and tables are read on the device when the call runs.  Repeated
+ * calls with the same arguments give identical bytes (no atomics).  seqs = 0 is a no-op.
+ * Allocates nothing; asynchronous on `stream`.  Errors as in sparse_mla_tree, and
+ * SMLA_ERR_INVALID_ARG for a decay that is not finite.
+ */
+size_t sparse_mla_weights_workspace_bytes(int32_t kv_format);
+smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths,
+                               const int32_t* starts, const uint32_t* mask, const float* lse, const float* weights, float decay,
+                               int32_t T, int32_t h, int32_t seqs, int32_t blocks, int32_t mask_words, int64_t num_slots,
+                               int32_t kv_format, float scale, float* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * sparse_mla_fwd_host -- the same forward pass taking HOST buffers for the
  * per-step inputs and outputs, for callers whose q/indices live in host memory.
  * It queues on `stream`: copies of q_host and indices_host into `workspace`,

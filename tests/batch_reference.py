@@ -123,3 +123,25 @@ def tree(batch, scale=SCALE):
             tol_l[t] = err + 2.0 ** -22 * np.abs(lse[t]) + 2.0 ** -20
             tol_o[t] = (2.0 ** -8 + 2 * err[:, None]) * (p @ np.abs(k[:, :512])) + 2.0 ** -8 * np.abs(out[t]) + 1e-30
     return out, lse, tol_o, tol_l
+
+
+def weights(batch, lse, prev, decay, scale=SCALE):
+    """out [seqs, blocks * 64] in fp64 and its tolerance, by the arithmetic of tests/test_weights.py; lse [T, h] fp32."""
+    rows, q, lse = batch.rows(), ref.to64(batch.q), ref.to64(lse)
+    width = batch.blocks * 64
+    out, tol = np.zeros((len(batch.seqs), width)), np.zeros((len(batch.seqs), width))
+    for b, (n, d) in enumerate(batch.seqs):
+        n = min(n, width)
+        if prev is not None:
+            out[b, :n] = decay * ref.to64(prev)[b, :n]
+        for t, slots, sees in batch.tokens(b):
+            at = np.nonzero(sees)[0]
+            k = rows[slots[at]]
+            fin = ~np.isneginf(lse[t])
+            y = (q[t][fin] @ k.T) * scale - lse[t][fin, None]
+            p = np.exp(y)
+            err = 576 * 2.0 ** -23 * abs(scale) * (np.abs(q[t][fin]) @ np.abs(k).T)
+            out[b, at] += p.sum(axis=0)
+            tol[b, at] += (p * (np.expm1(err + np.abs(y) * 2.0 ** -23) + 2.0 ** -22)).sum(axis=0)
+        tol[b] += (d * batch.h + 3) * 2.0 ** -24 * np.abs(out[b])
+    return out, tol

@@ -42,9 +42,11 @@ from ._binding import (  # noqa: F401
     sparse_mla_topk,
     sparse_mla_tree,
     sparse_mla_v_up,
+    sparse_mla_weights,
     sync_status,
     tree_workspace_bytes,
     version,
+    weights_workspace_bytes,
 )
 
 __all__ = [
@@ -70,7 +72,9 @@ __all__ = [
     "sparse_mla_topk",
     "sparse_mla_tree",
     "sparse_mla_v_up",
+    "sparse_mla_weights",
     "sync_status",
     "tree_workspace_bytes",
     "version",
+    "weights_workspace_bytes",
 ]

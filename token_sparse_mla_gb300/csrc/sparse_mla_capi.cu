@@ -19,6 +19,7 @@
 #include "sparse_mla_v_up.cuh"
 #include "sparse_mla_topk.cuh"
 #include "sparse_mla_tree.cuh"
+#include "sparse_mla_weights.cuh"
 #include "sparse_mla_masked.cuh"
 #include "sparse_mla_append.cuh"
 #include "sparse_mla_q_up.cuh"
@@ -92,6 +93,8 @@ cudaError_t set_kernel_attrs() {
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_prefix_kernel, smla::PfLayout::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_tree_kernel<0>, smla::TrLayout::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_tree_kernel<1>, smla::TrLayout::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_weights_kernel<0>, smla::WtLayout::kBytes);
+    if (e == cudaSuccess) e = set_smem(smla::sparse_mla_weights_kernel<1>, smla::WtLayout::kBytes);
     if (e == cudaSuccess) e = set_smem(smla::sparse_mla_scatter_mask_kernel, smla::kScatterMaxS / 32 * 4);
     return e;
 }
@@ -486,9 +489,8 @@ PrefixPlan prefix_plan(int64_t rows, int64_t prefix, bool fp8, int num_sms) {
 }
 
 // What the calls on a batch of sequences check alike.
-smla_status check_batch(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths, const int32_t* starts,
-                        const uint32_t* mask, int32_t T, int32_t h, int32_t seqs, int32_t blocks, int32_t mask_words, int64_t num_slots,
-                        int32_t kv_format, float scale) {
+smla_status check_batch_sizes(const uint32_t* mask, int32_t T, int32_t h, int32_t seqs, int32_t blocks, int32_t mask_words, int64_t num_slots,
+                              int32_t kv_format, float scale) {
     if (T < 0 || h < 1 || seqs < 0) return fail(SMLA_ERR_INVALID_ARG, "T and seqs must be >= 0 and h >= 1 (got %d, %d, %d)", T, seqs, h);
     if (blocks < 1 || blocks > smla::kMaxBlocks)
         return fail(SMLA_ERR_INVALID_ARG, "blocks per sequence must be in [1, %d] (got %d)", smla::kMaxBlocks, blocks);
@@ -499,8 +501,12 @@ smla_status check_batch(const void* q, const void* kv_cache, const int32_t* bloc
     if (!std::isfinite(scale)) return fail(SMLA_ERR_INVALID_ARG, "scale must be finite");
     if (mask != nullptr && mask_words < 1) return fail(SMLA_ERR_INVALID_ARG, "mask_words must be >= 1 (got %d)", mask_words);
     if (static_cast<int64_t>(T) * h > 0x7f000000LL) return fail(SMLA_ERR_INVALID_ARG, "T * h too large (%d, %d)", T, h);
-    if (T == 0 || seqs == 0) return SMLA_OK;
-    if (!q || !kv_cache || !block_tables || !lengths || !starts) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+    return SMLA_OK;
+}
+
+smla_status check_batch_pointers(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths,
+                                 const int32_t* starts, const uint32_t* mask, int32_t T) {
+    if ((T > 0 && !q) || !kv_cache || !block_tables || !lengths || !starts) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned(q, 16) || !aligned(kv_cache, 16)) return fail(SMLA_ERR_INVALID_ARG, "q and kv_cache must be 16-byte aligned");
     if (!aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(starts, 4) || !aligned(mask, 4))
         return fail(SMLA_ERR_INVALID_ARG, "block_tables, lengths, starts and mask must be 4-byte aligned");
@@ -1305,8 +1311,9 @@ smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* 
                             const int32_t* starts, const uint32_t* mask, int32_t T, int32_t h, int32_t seqs, int32_t blocks,
                             int32_t mask_words, int64_t num_slots, int32_t kv_format, float scale, void* out, float* lse,
                             void* workspace, size_t workspace_bytes, void* stream) {
-    smla_status st = check_batch(q, kv_cache, block_tables, lengths, starts, mask, T, h, seqs, blocks, mask_words, num_slots, kv_format, scale);
+    smla_status st = check_batch_sizes(mask, T, h, seqs, blocks, mask_words, num_slots, kv_format, scale);
     if (st != SMLA_OK || T == 0 || seqs == 0) return st;
+    if ((st = check_batch_pointers(q, kv_cache, block_tables, lengths, starts, mask, T)) != SMLA_OK) return st;
     if (!out || !lse) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned(out, 16) || !aligned(lse, 4)) return fail(SMLA_ERR_INVALID_ARG, "out must be 16-byte and lse 4-byte aligned");
     int dev = 0;
@@ -1372,6 +1379,78 @@ smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* 
         : parts == 2 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_merge_kernel<2>, tp)
                      : cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_merge_kernel<1>, tp);
     if (e != cudaSuccess) return cuda_fail(e, "tree merge kernel launch");
+    return SMLA_OK;
+}
+
+
+size_t sparse_mla_weights_workspace_bytes(int32_t kv_format) {
+    int num_sms = 152;
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    if (device_state(&dev, &ds) == SMLA_OK) num_sms = ds->num_sms;
+    return kv_format == SMLA_KV_FP8 ? static_cast<size_t>(num_sms / 2 * 2) * smla::kWtRing * smla::kWtHalf * smla::kDQK * 2 : 0;
+}
+
+smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths,
+                               const int32_t* starts, const uint32_t* mask, const float* lse, const float* weights, float decay,
+                               int32_t T, int32_t h, int32_t seqs, int32_t blocks, int32_t mask_words, int64_t num_slots,
+                               int32_t kv_format, float scale, float* out, void* workspace, size_t workspace_bytes, void* stream) {
+    smla_status st = check_batch_sizes(mask, T, h, seqs, blocks, mask_words, num_slots, kv_format, scale);
+    if (st != SMLA_OK) return st;
+    if (!std::isfinite(decay)) return fail(SMLA_ERR_INVALID_ARG, "decay must be finite");
+    if (seqs == 0) return SMLA_OK;
+    if ((st = check_batch_pointers(q, kv_cache, block_tables, lengths, starts, mask, T)) != SMLA_OK) return st;
+    if (!out || (T > 0 && !lse)) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(out, 4) || !aligned(lse, 4) || !aligned(weights, 4))
+        return fail(SMLA_ERR_INVALID_ARG, "lse, weights and out must be 4-byte aligned");
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&dev, &ds)) != SMLA_OK) return st;
+    const bool fp8 = kv_format == SMLA_KV_FP8;
+    const int pairs = ds->num_sms / 2;
+    const size_t need = fp8 ? static_cast<size_t>(2 * pairs) * smla::kWtRing * smla::kWtHalf * smla::kDQK * 2 : 0;
+    if (need > 0) {
+        if (!workspace || !aligned(workspace, 256))
+            return fail(SMLA_ERR_INVALID_ARG, "workspace must be given, 256-byte aligned");
+        if (workspace_bytes < need) return fail(SMLA_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, need);
+    }
+    EncodeTiledFn enc = nullptr;
+    if ((st = encode_fn(&enc)) != SMLA_OK) return st;
+    const int64_t rows = static_cast<int64_t>(T) * h;
+    alignas(64) CUtensorMap tm_q;
+    alignas(64) CUtensorMap tm_k;
+    // (without tokens nothing is loaded by q's map)
+    CUresult r = T > 0 ? row_map(enc, &tm_q, q, rows, smla::kWtHalf, 1) : row_map(enc, &tm_q, kv_cache, 1, smla::kWtHalf, 1);
+    if (r == CUDA_SUCCESS)
+        r = fp8 ? row_map(enc, &tm_k, workspace, static_cast<int64_t>(2 * pairs) * smla::kWtRing * smla::kWtHalf, smla::kPage, 1)
+                : row_map(enc, &tm_k, kv_cache, num_slots, smla::kPage, 1);
+    if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/kv_cache failed (%d)", (int)r);
+    smla::WtParams wp = {};
+    wp.bp = batch_params(kv_cache, block_tables, lengths, starts, mask, T, h, seqs, blocks, mask_words, num_slots);
+    wp.lse = lse;
+    wp.prev = weights;
+    wp.out = out;
+    wp.ring = fp8 ? static_cast<__nv_bfloat16*>(workspace) : nullptr;
+    wp.pairs = pairs;
+    wp.scale = scale;
+    wp.decay = decay;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(fp8 ? smla::weights_threads<1>() : smla::weights_threads<0>()), 1, 1);
+    cfg.dynamicSmemBytes = smla::WtLayout::kBytes;
+    const cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_weights_kernel<1>, tm_q, tm_k, wp)
+                              : cudaLaunchKernelEx(&cfg, smla::sparse_mla_weights_kernel<0>, tm_q, tm_k, wp);
+    if (e != cudaSuccess) return cuda_fail(e, "weights kernel launch");
     return SMLA_OK;
 }
 

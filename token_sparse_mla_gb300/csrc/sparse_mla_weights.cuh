@@ -1,0 +1,518 @@
+// The attention weight that every cached row of a batch has gathered, on tcgen05 tensor cores (sm_103a):
+//
+//   out[b][p] = decay * prev[b][p] (cached rows) + sum over sequence b's tokens t and heads of exp(s - lse[t])
+//   s = scale q.k over 576 dims, for the rows p that token t sees (sparse_mla_tree.cuh), lse from that attention
+//
+// The second look at the keys that the sums need: an LSE is known only when its row's attention is done.
+//
+// The product is turned round: keys are the MMA's rows, so that a key's probabilities lie in one TMEM lane
+// and its sum is a thread's own, without atomics and in a fixed order.  A CTA pair takes 256 keys of a
+// sequence (cta_group::2, M = 256: 128 keys per CTA) against up to 256 rows (token, head), half of which each
+// CTA holds; the 576 dims go through in nine panels of 64.
+//
+// One operand of a pair stays in shared memory, the other streams through a ring of four panels:
+//   up to 256 rows in the sequence: its queries stay, keys stream.  Bound by HBM, 1152 bytes a key: 256 keys
+//     are 3.3 us for 76 pairs at 6.8 TB/s, the MMAs at most 36 * 128 cycles = 2.4 us.
+//   more: a tile of keys stays and the queries stream from L2, tile after tile, so that a key's sum still is
+//     one thread's.  Bound by the MMAs.
+// Both operands have the same layout (128 rows x 9 panels, SW128), so the two forms differ in who loads what
+// and in which descriptor is A.
+//
+// Work: tiles of 256 keys, each whole in one pair, in equal shares of their cost (kWt... below).
+//
+// fp8 rows are expanded ahead of the loads by four more warps, each CTA its own 128 keys, into two tiles per
+// CTA in global memory that stay in L2 (sparse_mla_tree.cuh says why).
+//
+// Roles (384 threads, 512 with fp8):
+//   warps 0-7    sums: TMEM quadrant warp % 4 (32 keys), half warp / 4 of the tile's columns
+//   warp 8       TMA producer (one thread)
+//   warp 9       MMA issuer (one thread of the even CTA), and TMEM owner
+//   warps 10-11  the elements without work: positions past the end, sequences without tokens
+//   warps 12-15  expansion of fp8 rows
+// Every wait is bounded; a CTA that gives up meets the other at the final cluster barrier.
+#pragma once
+
+#include "sparse_mla_batch.cuh"
+
+namespace smla {
+
+constexpr int kWtKeys = 256;      // keys per tile (pair)
+constexpr int kWtHalf = 128;      // per CTA
+constexpr int kWtRows = 256;      // rows (token, head) per tile
+constexpr int kWtStages = 4;
+constexpr int kWtPanel = 128 * 128;  // 128 rows x 64 bf16, SW128
+constexpr int kWtSumWarps = 8;
+constexpr int kWtTmaWarp = 8, kWtMmaWarp = 9, kWtFillWarp = 10, kWtExpandWarp = 12;
+constexpr int kWtExpandWarps = 4;
+constexpr int kWtRing = 2;        // expanded tiles per CTA
+// costs in tenths of a microsecond: a sequence's queries and first keys; a tile whose keys stream; one whose
+// keys stay, and each of its row tiles
+constexpr int kWtCostSeq = 30, kWtCostStream = 34, kWtCostStay = 20, kWtCostRows = 24;
+
+template <int KVF>
+__host__ __device__ constexpr int weights_threads() {
+    return 32 * (kWtExpandWarp + (KVF ? kWtExpandWarps : 0));
+}
+
+enum : int {
+    kWbStayFull = 0,                       // even CTA: both CTAs' part of the operand that stays
+    kWbStayEmpty = 1,                      // both
+    kWbFull = 2,                           // +stage, even CTA
+    kWbEmpty = kWbFull + kWtStages,        // +stage, both
+    kWbSFull = kWbEmpty + kWtStages,       // +buffer, both
+    kWbSEmpty = kWbSFull + 2,              // +buffer, even CTA
+    kWbDrain = kWbSEmpty + 2,              // even CTA
+    kWbRowsFull = kWbDrain + 1,            // +tile, own CTA: expanded rows
+    kWbRowsFree = kWbRowsFull + kWtRing,   // +tile, both
+    kWbCount = kWbRowsFree + kWtRing
+};
+
+struct WtLayout {
+    static constexpr int kOffStay = 0;
+    static constexpr int kOffRing = kPanels * kWtPanel;
+    static constexpr int kOffLse = kOffRing + kWtStages * kWtPanel;  // [2][256]: minus the rows' LSE
+    static constexpr int kOffX = kOffLse + 2 * kWtRows * 4;          // [2][128]: sums of the columns' second half; the plan's sums
+    static constexpr int kOffBar = kOffX + 2 * kWtHalf * 4;
+    static constexpr int kOffMisc = kOffBar + kWbCount * 8;          // tmem base, abort flag, the run's start
+    static constexpr int kBytes = kOffMisc + 8 + 40;
+    static_assert(kBytes <= 232448, "shared memory budget (227 KB)");
+};
+
+struct WtStart {
+    int64_t at, end, seq_at;  // the run [at, end) in cost units; where its first sequence begins
+    int32_t b;
+};
+
+struct WtParams {
+    BatchParams bp;
+    const float* lse;      // [T, h]
+    const float* prev;     // [B, nb * 64] or nullptr
+    float* out;            // [B, nb * 64]
+    __nv_bfloat16* ring;   // fp8: [CTAs][kWtRing][128][576]
+    int32_t pairs;
+    float scale, decay;
+};
+
+__device__ __forceinline__ int weights_row_tiles(const WtParams& p, const Seq& s) {
+    return static_cast<int>((static_cast<int64_t>(s.n) * p.bp.h + kWtRows - 1) / kWtRows);
+}
+__device__ __forceinline__ int weights_tile_cost(int row_tiles) {
+    return row_tiles <= 1 ? kWtCostStream : kWtCostStay + kWtCostRows * row_tiles;
+}
+__device__ __forceinline__ int weights_key_tiles(const Seq& s) { return s.n == 0 ? 0 : (s.keys + kWtKeys - 1) / kWtKeys; }
+
+// All threads of the CTA: the start of pair `run`'s share, into *start (shared memory).
+__device__ __forceinline__ void weights_plan(const WtParams& p, int run, int threads, int64_t* scratch, WtStart* start) {
+    const int per = (p.bp.B + threads - 1) / threads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.bp.B), b1 = min(b0 + per, p.bp.B);
+    auto cost_of = [&](const Seq& s) -> int64_t {
+        return s.n == 0 ? 0 : kWtCostSeq + static_cast<int64_t>(weights_key_tiles(s)) * weights_tile_cost(weights_row_tiles(p, s));
+    };
+    int64_t cost = 0;
+    for (int b = b0; b < b1; ++b) cost += cost_of(load_seq(p.bp, b));
+    int64_t at, total;
+    block_prefix(cost, scratch, threads / 32, at, total);
+    const int64_t from = total * run / p.pairs, to = total * (run + 1) / p.pairs;
+    if (from >= to) {
+        if (threadIdx.x == 0) *start = WtStart{0, 0, 0, p.bp.B};
+    } else if (at <= from && from < at + cost) {
+        int b = b0;
+        for (;; ++b) {
+            const int64_t c = cost_of(load_seq(p.bp, b));
+            if (from < at + c) break;
+            at += c;
+        }
+        *start = WtStart{from, to, at, b};
+    }
+    __syncthreads();
+}
+
+// The pieces of a run, the same for every role: key tiles [k0, k1) of sequence b.  A tile belongs to the
+// run that its first cost unit lies in.
+struct WtWalk {
+    int64_t at, end;  // relative to the sequence's first unit
+    Seq s;
+    int b, row_tiles, cost, key_tiles;
+    int k0, k1;
+    bool begun;
+    __device__ __forceinline__ WtWalk(const WtParams& p, const WtStart& st) : b(st.b), begun(false) {
+        at = st.at - st.seq_at;
+        end = st.end - st.seq_at;
+        if (b < p.bp.B) load(p);
+    }
+    __device__ __forceinline__ void load(const WtParams& p) {
+        s = load_seq(p.bp, b);
+        row_tiles = weights_row_tiles(p, s);
+        cost = weights_tile_cost(row_tiles);
+        key_tiles = weights_key_tiles(s);
+    }
+    __device__ __forceinline__ bool next(const WtParams& p) {
+        for (;;) {
+            if (begun) {
+                if (s.n) {
+                    end -= kWtCostSeq + static_cast<int64_t>(key_tiles) * cost;
+                    at = 0;
+                }
+                if (end <= 0 || ++b >= p.bp.B) return false;
+                load(p);
+            } else if (at >= end) {
+                return false;
+            }
+            begun = true;
+            k0 = first_from(at);
+            k1 = first_from(end);
+            if (k1 > k0) return true;
+        }
+    }
+    // the first tile whose first unit lies at x or later
+    __device__ __forceinline__ int first_from(int64_t x) const {
+        const int64_t y = x - kWtCostSeq;
+        return y <= 0 ? 0 : static_cast<int>(min((y + cost - 1) / cost, static_cast<int64_t>(key_tiles)));
+    }
+    // rows of row tile i, and the MMA's columns for them
+    __device__ __forceinline__ int rows(const WtParams& p, int i) const {
+        return static_cast<int>(min(static_cast<int64_t>(s.n) * p.bp.h - static_cast<int64_t>(i) * kWtRows, static_cast<int64_t>(kWtRows)));
+    }
+    __device__ __forceinline__ int columns(const WtParams& p, int i) const { return (rows(p, i) + 31) & ~31; }
+};
+
+template <int KVF>
+__global__ void __launch_bounds__(weights_threads<KVF>(), 1)
+    sparse_mla_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WtParams p) {
+    using L = WtLayout;
+    constexpr int kThreads = weights_threads<KVF>();
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = ptx::smem_u32(smem);
+    if (sbase & 1023u) {  // uniform across the grid: every CTA leaves before any barrier
+        if (threadIdx.x == 0) atomicOr(&g_smla_error, kErrLayout);
+        return;
+    }
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(ptx::cluster_ctarank());
+    const int run = static_cast<int>(blockIdx.x >> 1);
+    volatile int* sAbort = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+    WtStart* start = reinterpret_cast<WtStart*>(smem + L::kOffMisc + 8);
+    auto bar = [&](int i) -> uint32_t { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
+    auto even_bar = [&](int i) -> uint32_t { return ptx::map_shared_rank(bar(i), 0); };
+    auto wait = [&](int i, uint32_t parity) -> bool {
+        return ptx::mbar_wait(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
+    };
+
+    if (threadIdx.x == 0) {
+        *sAbort = 0;
+        for (int i = 0; i < kWbCount; ++i) {
+            const bool by_warps = i == kWbSEmpty || i == kWbSEmpty + 1;                // both CTAs' sum warps
+            const bool by_expand = i >= kWbRowsFull && i < kWbRowsFull + kWtRing;      // this CTA's expansion warps
+            ptx::mbar_init(bar(i), by_warps ? 2 * kWtSumWarps : by_expand ? kWtExpandWarps : 1);
+        }
+        ptx::fence_mbarrier_init();
+    }
+    if (warp == kWtMmaWarp) {
+        ptx::tmem_alloc_pair(sbase + L::kOffMisc, 512);
+        ptx::tmem_relinquish_pair();
+    }
+    if (warp == kWtTmaWarp && lane == 0) {
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+    }
+    // launched as a programmatic dependent: nothing above touched global memory
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    weights_plan(p, run, kThreads, reinterpret_cast<int64_t*>(smem + L::kOffX), start);
+    WtWalk w(p, *start);
+    const bool any = w.next(p);
+    ptx::tc_fence_before();
+    __syncwarp();         // the cluster barrier wants its warps whole
+    ptx::cluster_sync();  // both CTAs' barriers are initialised before anyone signals them
+    ptx::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
+
+    if (warp == kWtTmaWarp) {
+        // ================================================================ TMA producer
+        // The even CTA's thread expects both CTAs' bytes on its barrier, each CTA's thread issues its own copies.
+        if (lane == 0) {
+            bool ok = true;
+            int stays = 0, loads = 0, t = 0;  // operands that stay, ring panels, key tiles so far
+            const int ring0 = static_cast<int>(blockIdx.x) * kWtRing * kWtHalf;
+            int row0 = 0, row1 = 0;           // rows of the tile's two pages
+            auto begin_stay = [&]() -> bool {
+                if (stays > 0 && !wait(kWbStayEmpty, (stays - 1) & 1)) return false;
+                ++stays;
+                if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbStayFull), 2u * kPanels * kWtPanel);
+                return true;
+            };
+            auto begin_stage = [&](int& st) -> bool {
+                st = loads % kWtStages;
+                if (loads >= kWtStages && !wait(kWbEmpty + st, (loads / kWtStages - 1) & 1)) return false;
+                ++loads;
+                if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbFull + st), 2u * kWtPanel);
+                return true;
+            };
+            auto load_keys = [&](uint32_t dst, int pn, uint32_t b) {
+                ptx::tma_load_3d_pair(dst, &tm_k, 0, row0, pn, b);
+                ptx::tma_load_3d_pair(dst + kWtPanel / 2, &tm_k, 0, row1, pn, b);
+            };
+            // a page that is not there loads as zeros, from rows below 0
+            auto first_row = [&](int page) -> int { return page_in_cache(p.bp, page) ? page * kPage : -kPage; };
+            auto prefetch = [&](int i) {  // page i, into L2
+                const int pg = page_of(p.bp, w.b, w.s, i);
+                const int n = page_rows(p.bp, w.s, i, pg);
+                if (n > 0)
+                    ptx::bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(p.bp.kv) + static_cast<int64_t>(pg) * kPage * kDQK,
+                                          static_cast<uint32_t>(n * kDQK * 2));
+            };
+            for (bool more = any; ok && more; more = w.next(p)) {
+                const bool stream_keys = w.row_tiles == 1;
+                const int q0 = w.s.first * p.bp.h;
+                if (stream_keys) {
+                    if (!(ok = begin_stay())) break;
+                    for (int pn = 0; pn < kPanels; ++pn)
+                        ptx::tma_load_3d_pair(sbase + L::kOffStay + pn * kWtPanel, &tm_q, 0, q0 + rank * (w.columns(p, 0) / 2), pn,
+                                              even_bar(kWbStayFull));
+                }
+                for (int k = w.k0; ok && k < w.k1; ++k, ++t) {
+                    if constexpr (KVF == 0) {
+                        const int i = 4 * k + 2 * rank;
+                        row0 = first_row(page_of(p.bp, w.b, w.s, i));
+                        row1 = first_row(page_of(p.bp, w.b, w.s, i + 1));
+                        if (k + 1 < w.k1) {
+                            prefetch(i + 4);
+                            prefetch(i + 5);
+                        }
+                    } else {
+                        row0 = ring0 + (t % kWtRing) * kWtHalf;
+                        row1 = row0 + kPage;
+                        if (!(ok = wait(kWbRowsFull + t % kWtRing, (t / kWtRing) & 1))) break;
+                        ptx::fence_proxy_async_all();
+                    }
+                    int st;
+                    if (stream_keys) {
+                        for (int pn = 0; ok && pn < kPanels; ++pn)
+                            if ((ok = begin_stage(st))) load_keys(sbase + L::kOffRing + st * kWtPanel, pn, even_bar(kWbFull + st));
+                    } else {
+                        if (!(ok = begin_stay())) break;
+                        for (int pn = 0; pn < kPanels; ++pn) load_keys(sbase + L::kOffStay + pn * kWtPanel, pn, even_bar(kWbStayFull));
+                        for (int i = 0; ok && i < w.row_tiles; ++i) {
+                            const int row = q0 + i * kWtRows + rank * (w.columns(p, i) / 2);
+                            for (int pn = 0; ok && pn < kPanels; ++pn)
+                                if ((ok = begin_stage(st)))
+                                    ptx::tma_load_3d_pair(sbase + L::kOffRing + st * kWtPanel, &tm_q, 0, row, pn, even_bar(kWbFull + st));
+                        }
+                    }
+                }
+            }
+            // every copy has landed and been used, and no release is still on its way to this CTA's barriers,
+            // before it leaves
+            for (int y = max(loads - kWtStages, 0); ok && y < loads; ++y) ok = wait(kWbEmpty + y % kWtStages, (y / kWtStages) & 1);
+            if (ok && stays > 0) ok = wait(kWbStayEmpty, (stays - 1) & 1);
+            if (!ok) {  // gave up: copies in flight complete on the other CTA's barriers; leave them time to land
+                const uint64_t t0 = ptx::globaltimer_ns();
+                while (ptx::globaltimer_ns() - t0 < 2000000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kWtMmaWarp) {
+        // ================================================================ MMA issuer
+        if (rank == 0 && lane == 0) {
+            const uint64_t d_stay = ptx::smem_desc_sw128(sbase + L::kOffStay, 16, 1024);
+            const uint64_t d_ring = ptx::smem_desc_sw128(sbase + L::kOffRing, 16, 1024);
+            bool ok = true;
+            int stays = 0, loads = 0, item = 0, t = 0;
+            for (bool more = any; ok && more; more = w.next(p)) {
+                const bool stream_keys = w.row_tiles == 1;
+                if (stream_keys && !(ok = wait(kWbStayFull, stays++ & 1))) break;
+                for (int k = w.k0; ok && k < w.k1; ++k, ++t) {
+                    if (!stream_keys && !(ok = wait(kWbStayFull, stays++ & 1))) break;
+                    for (int i = 0; ok && i < w.row_tiles; ++i, ++item) {
+                        const int buf = item & 1;
+                        if (item >= 2 && !(ok = wait(kWbSEmpty + buf, ((item >> 1) - 1) & 1))) break;
+                        const uint32_t idesc = ptx::idesc_bf16_f32(kWtKeys, w.columns(p, i), 0, 0);
+                        const uint32_t d = tmem + buf * kWtRows;
+                        for (int pn = 0; pn < kPanels; ++pn, ++loads) {
+                            const int st = loads % kWtStages;
+                            if (!(ok = wait(kWbFull + st, (loads / kWtStages) & 1))) break;
+                            ptx::tc_fence_after();
+                            const uint64_t stay = d_stay + ((pn * kWtPanel) >> 4), ring = d_ring + ((st * kWtPanel) >> 4);
+                            const uint64_t a = stream_keys ? ring : stay, b = stream_keys ? stay : ring;
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                ptx::mma_bf16_ss_pair(d, a + ((kk * 32) >> 4), b + ((kk * 32) >> 4), idesc, (pn | kk) != 0);
+                            ptx::mma_commit_pair(bar(kWbEmpty + st));
+                        }
+                        if (ok) ptx::mma_commit_pair(bar(kWbSFull + buf));
+                    }
+                    if (ok && !stream_keys) ptx::mma_commit_pair(bar(kWbStayEmpty));
+                    if (ok && KVF == 1) ptx::mma_commit_pair(bar(kWbRowsFree + t % kWtRing));
+                }
+                if (ok && stream_keys) ptx::mma_commit_pair(bar(kWbStayEmpty));
+            }
+            // nothing is in flight when TMEM is freed, also after giving up
+            ptx::mma_commit_pair_local(bar(kWbDrain));
+            ptx::mbar_wait(bar(kWbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
+        }
+        __syncwarp();
+    } else if (warp >= kWtExpandWarp) {
+        // ================================================================ expansion of fp8 rows
+        if constexpr (KVF == 1) {
+            constexpr int kRows = kWtHalf / kWtExpandWarps;  // rows per warp, half a page
+            const int row = kRows * (warp - kWtExpandWarp);
+            __nv_bfloat16* ring = p.ring + (static_cast<int64_t>(blockIdx.x) * kWtRing * kWtHalf + row) * kDQK;
+            bool ok = true;
+            int t = 0;
+            for (bool more = any; ok && more; more = w.next(p)) {
+                for (int k = w.k0; k < w.k1; ++k, ++t) {
+                    const int i = 4 * k + 2 * rank + row / kPage, slot = t % kWtRing;
+                    const int page = page_of(p.bp, w.b, w.s, i);
+                    const int n = page_rows(p.bp, w.s, i, page) - row % kPage;
+                    const uint8_t* src = static_cast<const uint8_t*>(p.bp.kv) + (static_cast<int64_t>(page) * kPage + row % kPage) * kFp8RowBytes;
+                    if (t >= kWtRing) {  // this slot's last tile has been multiplied
+                        if (lane == 0) ok = wait(kWbRowsFree + slot, (t / kWtRing - 1) & 1);
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
+                    }
+                    __nv_bfloat16* dst = ring + static_cast<int64_t>(slot) * kWtHalf * kDQK;
+#pragma unroll 1
+                    for (int u = 0; u < kRows; u += 4) expand_rows4(src + u * kFp8RowBytes, n - u, dst + u * kDQK);
+                    ptx::fence_proxy_async_all();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(kWbRowsFull + slot));
+                }
+            }
+            // no release is still on its way to this CTA's barriers when it leaves
+            for (int y = max(t - kWtRing, 0); ok && y < t; ++y) {
+                if (lane == 0) ok = wait(kWbRowsFree + y % kWtRing, (y / kWtRing) & 1);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+            }
+        }
+    } else if (warp >= kWtFillWarp) {
+        // ================================================================ elements that no tile covers
+        const int width = p.bp.nb * kPage;
+        const int tid = (warp - kWtFillWarp) * 32 + lane;
+        // (B, 4096 positions) chunks over the grid
+        const int chunks = (width + 4095) / 4096;
+        for (int64_t c = blockIdx.x; c < static_cast<int64_t>(p.bp.B) * chunks; c += gridDim.x) {
+            const int b = static_cast<int>(c / chunks), c0 = static_cast<int>(c % chunks) * 4096, c1 = min(c0 + 4096, width);
+            const Seq s = load_seq(p.bp, b);
+            const int from = s.n ? max(s.keys, c0) : c0;
+            float* out = p.out + static_cast<int64_t>(b) * width;
+            const float* prev = p.prev ? p.prev + static_cast<int64_t>(b) * width : nullptr;
+            for (int i = from + tid; i < c1; i += 64) out[i] = i < s.len && prev ? p.decay * prev[i] : 0.f;
+        }
+    } else {
+        // ================================================================ sums
+        const int quad = warp & 3, half = warp >> 2;
+        const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+        const int tid = threadIdx.x;  // 0 .. 255
+        volatile float* sX = reinterpret_cast<volatile float*>(smem + L::kOffX);
+        const uint32_t s_lse = sbase + L::kOffLse;
+        const float2 scale2 = make_float2(p.scale, p.scale);
+        const float2 log2e2 = make_float2(1.4426950408889634f, 1.4426950408889634f);
+        const int width = p.bp.nb * kPage;
+        const uint32_t s_empty0 = even_bar(kWbSEmpty), s_empty1 = even_bar(kWbSEmpty + 1);
+        auto warp_wait = [&](int i, uint32_t parity) -> bool {
+            bool okw = true;
+            if (lane == 0) okw = wait(i, parity);
+            okw = __shfl_sync(0xffffffffu, okw, 0);
+            __syncwarp();
+            return okw;
+        };
+        // minus the LSE of row tid of row tile i: the table's entry (a row that saw nothing adds nothing: -inf)
+        auto entry = [&](int i) -> float {
+            if (tid >= w.rows(p, i)) return -CUDART_INF_F;
+            const float x = __ldg(p.lse + static_cast<int64_t>(w.s.first) * p.bp.h + static_cast<int64_t>(i) * kWtRows + tid);
+            return x == -CUDART_INF_F ? x : -x;
+        };
+        bool failed = false;
+        int item = 0, t = 0, tables = 0;
+        for (bool more = any; !failed && more; more = w.next(p)) {
+            float mine = entry(0);
+            for (int k = w.k0; !failed && k < w.k1; ++k, ++t) {
+                const int key = k * kWtKeys + rank * kWtHalf + 32 * quad + lane;
+                const int i_page = (k * kWtKeys + rank * kWtHalf + 32 * quad) / kPage;
+                const bool valid = (key % kPage) < page_rows(p.bp, w.s, i_page, page_of(p.bp, w.b, w.s, i_page));
+                float* dst = p.out + static_cast<int64_t>(w.b) * width + key;
+                float before = 0.f;
+                if (half == 0 && key < w.s.len && p.prev) before = p.decay * p.prev[static_cast<int64_t>(w.b) * width + key];
+                const bool tail = k * kWtKeys + rank * kWtHalf + 32 * quad + 32 > w.s.len;  // drafted rows among the warp's keys
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                for (int i = 0; i < w.row_tiles; ++i, ++item) {
+                    if (w.row_tiles > 1 || k == w.k0) {  // the row tile's table, the next one's entry on its way
+                        reinterpret_cast<volatile float*>(smem + L::kOffLse)[(tables & 1) * kWtRows + tid] = mine;
+                        ++tables;
+                        if (w.row_tiles > 1) mine = entry(i + 1 < w.row_tiles ? i + 1 : 0);
+                        failed = ptx::named_bar_red_or(1u, 32u * kWtSumWarps, failed);
+                        if (failed) break;
+                    }
+                    const uint32_t table = s_lse + ((tables - 1) & 1) * kWtRows * 4;
+                    const int buf = item & 1;
+                    const int columns = w.columns(p, i) / 2, c_first = half * columns;
+                    const int limit = min(w.rows(p, i) - c_first, columns);  // this half's columns that are rows
+                    if (!failed && !warp_wait(kWbSFull + buf, (item >> 1) & 1)) failed = true;
+                    if (failed) continue;
+                    ptx::tc_fence_after();
+                    for (int c = 0; c < limit; c += 16) {
+                        uint32_t sv[16];
+                        SMLA_TMEM_LD16(tmem + lane_base + buf * kWtRows + c_first + c, sv);
+                        float4 nl[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 v = ptx::ld_shared_v4(table + (c_first + c + 4 * e) * 4);
+                            nl[e] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+                        }
+                        ptx::tmem_wait_ld();
+                        float pr[16];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 l2 = e & 1 ? make_float2(nl[e >> 1].z, nl[e >> 1].w) : make_float2(nl[e >> 1].x, nl[e >> 1].y);
+                            const float2 y = ptx::mul2(
+                                ptx::fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), scale2, l2), log2e2);
+                            pr[2 * e] = ptx::ex2_approx(y.x);
+                            pr[2 * e + 1] = ptx::ex2_approx(y.y);
+                        }
+                        if (c + 16 > limit) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (c + e >= limit) pr[e] = 0.f;
+                        }
+                        if (tail) {
+                            int row = i * kWtRows + c_first + c, token = row / p.bp.h;
+                            row -= token * p.bp.h;
+#pragma unroll 1
+                            for (int e = 0; e < 16; ++e) {
+                                const bool sees = (seen_bits(p.bp, w.s, min(token, w.s.n - 1), key) & 1u) != 0u;
+#pragma unroll
+                                for (int u = 0; u < 16; ++u)
+                                    if (u == e && !sees) pr[u] = 0.f;
+                                if (++row == p.bp.h) {
+                                    row = 0;
+                                    ++token;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[e & 1] = ptx::add2(acc[e & 1], make_float2(pr[2 * e], pr[2 * e + 1]));
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(buf ? s_empty1 : s_empty0);
+                }
+                const float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                if (half == 1) sX[(t & 1) * kWtHalf + 32 * quad + lane] = sum;
+                failed = ptx::named_bar_red_or(1u, 32u * kWtSumWarps, failed);
+                if (!failed && half == 0 && key < w.s.keys) *dst = before + (valid ? sum + sX[(t & 1) * kWtHalf + 32 * quad + lane] : 0.f);
+            }
+        }
+    }
+    // ---- both CTAs are done with each other's shared memory, barriers and TMEM
+    ptx::tc_fence_before();
+    __syncwarp();
+    ptx::cluster_sync();
+    if (warp == kWtMmaWarp) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+}  // namespace smla
