@@ -18,7 +18,10 @@
  * sparse_mla_topk builds the index lists from per-position scores.
  * sparse_mla_append writes new tokens' rows into the cache, and
  * sparse_mla_q_up brings their queries into its space, and sparse_mla_prefix is
- * the attention over rows that a whole batch shares.
+ * the attention over rows that a whole batch shares.  sparse_mla_tree is the attention
+ * of a batch of sequences, each over its own cached rows and a tree of drafted tokens,
+ * sparse_mla_weights the attention weight that every row has gathered, and
+ * sparse_mla_evict keeps the rows with the most of it.
  *
  * Sources (page title, section):
  *   vLLM PR #60220 "FlashMLA sparse: stage fp8 mixed-batch q/out in the
@@ -80,8 +83,9 @@ typedef enum smla_status {
     SMLA_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed */
     SMLA_ERR_TIMEOUT = 4,      /* a bounded wait inside a kernel gave up */
     SMLA_ERR_INDEX_RANGE = 5   /* checked mode: a list entry other than -1 was outside
-                                  [0, num_slots) (it was masked); or sparse_mla_append or
-                                  sparse_mla_q_up met a slot or position out of range */
+                                  [0, num_slots) (it was masked); or sparse_mla_append,
+                                  sparse_mla_q_up or sparse_mla_evict met a slot or
+                                  position out of range */
 } smla_status;
 
 typedef enum smla_kv_format {
@@ -485,6 +489,41 @@ smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_
                                int32_t kv_format, float scale, float* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * sparse_mla_evict -- shrink the caches of a batch of sequences to `budget` rows each,
+ * by the attention weight that the rows have gathered (sparse_mla_weights).  Sequence
+ * b with n = lengths[b] rows keeps all of them if n <= budget; else its first `sinks`
+ * and last `recent` rows and, of those between, the ones with the largest weights, ties
+ * to the lower position (-0 and +0 are equal; NaN ranks below everything).  The kept
+ * rows, in order, are copied to positions 0, 1, ... of new_tables[b], and their weights
+ * to new_weights: what the next sparse_mla_tree and sparse_mla_weights calls take.  (The rows
+ * carry their rotation, so that their new places do not change what attention over
+ * them gives.)
+ *   kv_cache      device, num_slots rows as in sparse_mla_fwd, 16-byte aligned; rows
+ *                 that new_tables does not name keep their bytes
+ *   block_tables  device, [seqs, blocks] int32 as in sparse_mla_tree
+ *   lengths       device, [seqs] int32, brought into [0, blocks * 64]
+ *   weights       device, [seqs, blocks * 64] fp32
+ *   new_tables    device, [seqs, new_blocks] int32: pages that no other sequence's
+ *                 rows, old or new, lie in, and none of this one's old ones (the old pages
+ *                 are only read: another sequence may share them)
+ *   budget        1 .. new_blocks * 64;  sinks, recent >= 0, together <= budget
+ *   kept          device, [seqs, budget] int32, caller-owned: the positions kept,
+ *                 ascending, then -1
+ *   new_lengths   device, [seqs] int32, caller-owned: min(n, budget)
+ *   new_weights   device, [seqs, new_blocks * 64] fp32, caller-owned, zero behind the
+ *                 kept rows'; must not overlap weights
+ * A kept row that lies outside the cache, or would be copied to outside it, is not copied,
+ * and the next sparse_mla_sync_status() returns SMLA_ERR_INDEX_RANGE.  Exact, and
+ * repeated calls give identical bytes.  seqs = 0 is a no-op.  Allocates nothing;
+ * asynchronous on `stream`.  Errors: SMLA_ERR_INVALID_ARG for bad sizes or format, a
+ * null pointer or misalignment; SMLA_ERR_CUDA if a launch fails.
+ */
+smla_status sparse_mla_evict(void* kv_cache, const int32_t* block_tables, const int32_t* lengths, const float* weights,
+                             const int32_t* new_tables, int32_t seqs, int32_t blocks, int32_t new_blocks, int32_t budget, int32_t sinks,
+                             int32_t recent, int64_t num_slots, int32_t kv_format, int32_t* kept, int32_t* new_lengths,
+                             float* new_weights, void* stream);
+
+/*
  * sparse_mla_fwd_host -- the same forward pass taking HOST buffers for the
  * per-step inputs and outputs, for callers whose q/indices live in host memory.
  * It queues on `stream`: copies of q_host and indices_host into `workspace`,
@@ -531,8 +570,8 @@ smla_status sparse_mla_fwd_host_packed(const void* in_host, const void* kv_cache
  * kernel gave up on a bounded wait since the last call (the device is then
  * synchronised and the barrier words of every merge scratch on it cleared),
  * else SMLA_ERR_INDEX_RANGE if a sparse_mla_fwd_checked launch met a list
- * entry other than -1 outside [0, num_slots) or a sparse_mla_append or
- * sparse_mla_q_up launch a slot or position out of range, SMLA_ERR_CUDA if the
+ * entry other than -1 outside [0, num_slots) or a sparse_mla_append,
+ * sparse_mla_q_up or sparse_mla_evict launch a slot or position out of range, SMLA_ERR_CUDA if the
  * synchronisation failed, SMLA_OK otherwise.  The word is per device, so a
  * report covers every launch on the device since the last read.  Not for the
  * hot path.

@@ -14,7 +14,9 @@ the (out, lse) of lists split into parts (the DCP merge); sparse_mla_v_up applie
 per-head value up-projection to out on the tensor cores; sparse_mla_topk builds the
 index lists from per-position scores; sparse_mla_append writes new tokens' rows into the cache
 and sparse_mla_q_up brings their queries into its space; sparse_mla_prefix is the attention over a
-prefix that the whole batch shares; sparse_mla_scatter_mask and sparse_mla_masked_mha are
+prefix that the whole batch shares; sparse_mla_tree is the attention of a batch's drafted tokens
+over each sequence's own rows, sparse_mla_weights the attention weight that the rows gather, and
+sparse_mla_evict keeps the heaviest of them; sparse_mla_scatter_mask and sparse_mla_masked_mha are
 the masked dense route for short prefills (the lists as a bit mask, then dense MHA over per-head
 K and V under that mask).
 """
@@ -29,6 +31,7 @@ from ._binding import (  # noqa: F401
     lib_path,
     library,
     sparse_mla_append,
+    sparse_mla_evict,
     sparse_mla_fwd,
     sparse_mla_fwd_host,
     sparse_mla_fwd_host_packed,
@@ -59,6 +62,7 @@ __all__ = [
     "lib_path",
     "library",
     "sparse_mla_append",
+    "sparse_mla_evict",
     "sparse_mla_fwd",
     "sparse_mla_fwd_host",
     "sparse_mla_fwd_host_packed",

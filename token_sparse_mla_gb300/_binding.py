@@ -24,7 +24,7 @@ EXPORTED = ("sparse_mla_fwd", "sparse_mla_fwd_ex", "sparse_mla_fwd_checked", "sp
             "sparse_mla_v_up", "sparse_mla_topk", "sparse_mla_scatter_mask", "sparse_mla_masked_mha",
             "sparse_mla_append", "sparse_mla_q_up", "sparse_mla_prefix", "sparse_mla_prefix_workspace_bytes",
             "sparse_mla_tree", "sparse_mla_tree_workspace_bytes",
-            "sparse_mla_weights", "sparse_mla_weights_workspace_bytes",
+            "sparse_mla_weights", "sparse_mla_weights_workspace_bytes", "sparse_mla_evict",
             "sparse_mla_sync_status",
             "sparse_mla_launch_info", "sparse_mla_last_error", "sparse_mla_version")
 
@@ -88,6 +88,8 @@ def library() -> ctypes.CDLL:
     lib.sparse_mla_weights_workspace_bytes.argtypes = [i32]
     lib.sparse_mla_weights.restype = ctypes.c_int
     lib.sparse_mla_weights.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, f32, i32, i32, i32, i32, i32, i64, i32, f32, vp, vp, sz, vp]
+    lib.sparse_mla_evict.restype = ctypes.c_int
+    lib.sparse_mla_evict.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64, i32, vp, vp, vp, vp]
     lib.sparse_mla_host_io_layout.restype = ctypes.c_int
     lib.sparse_mla_host_io_layout.argtypes = [i32, i32, i32, vp, vp, vp, vp]
     lib.sparse_mla_fwd_host_packed.restype = ctypes.c_int
@@ -764,6 +766,53 @@ def sparse_mla_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: to
           lengths.data_ptr(), starts.data_ptr(), mask_ptr, lse.data_ptr(), prev, float(decay), T, h, seqs, blocks, words,
           num_slots, fmt, float(scale), out.data_ptr(), ws_ptr, ws_bytes)
     return out
+
+
+def sparse_mla_evict(kv_cache: torch.Tensor, block_tables: torch.Tensor, lengths: torch.Tensor, weights: torch.Tensor,
+                     new_tables: torch.Tensor, budget: int, *, sinks: int = 0, recent: int = 0, kv_format: str = "bf16",
+                     kept: Optional[torch.Tensor] = None, new_lengths: Optional[torch.Tensor] = None,
+                     new_weights: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Shrink each sequence's cache to `budget` rows by gathered attention weight (include/sparse_mla.h):
+    the first `sinks` rows, the last `recent` ones and the heaviest between them, ties to the lower
+    position, copied in order into the pages of new_tables.
+
+    block_tables [seqs, blocks] int32, lengths [seqs] int32, weights [seqs, blocks * 64] fp32 as
+    sparse_mla_weights gives them, new_tables [seqs, new_blocks] int32: pages of the same cache that
+    hold no row of any sequence.  Returns kept [seqs, budget] int32 (positions, ascending, then -1),
+    new_lengths [seqs] int32 and new_weights [seqs, new_blocks * 64] fp32.  A row that lies or would go
+    outside the cache is not copied and makes the next sync_status() raise SMLA_ERR_INDEX_RANGE.
+    """
+    num_slots = _cache_rows(kv_cache, kv_format)
+    dev = _cuda_device("kv_cache", kv_cache)
+    seqs, blocks = _batch(dev, block_tables, lengths)
+    if weights.shape != (seqs, blocks * 64) or weights.dtype != _F32 or not weights.is_contiguous():
+        raise ValueError(f"weights must be a contiguous [{seqs}, {blocks * 64}] fp32 tensor")
+    if new_tables.dim() != 2 or new_tables.shape[0] != seqs or new_tables.dtype != _I32 or not new_tables.is_contiguous():
+        raise ValueError(f"new_tables must be a contiguous [{seqs}, new_blocks] int32 tensor")
+    if not dev == weights.device == new_tables.device:
+        _apart(dev, weights=weights, new_tables=new_tables)
+    new_blocks = new_tables.shape[1]
+    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    if not 1 <= budget <= new_blocks * 64:
+        raise ValueError(f"budget must be in [1, {new_blocks * 64}], the positions of new_tables")
+    if sinks < 0 or recent < 0 or sinks + recent > budget:
+        raise ValueError("sinks and recent must be >= 0 and no more than the budget together")
+    held = []
+    for name, t, shape, dtype in (("kept", kept, (seqs, budget), _I32), ("new_lengths", new_lengths, (seqs,), _I32),
+                                  ("new_weights", new_weights, (seqs, new_blocks * 64), _F32)):
+        if t is None:
+            t = _empty(shape, dtype, dev, stream)
+        else:
+            if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
+            if t.device != dev:
+                _apart(dev, **{name: t})
+        held.append(t)
+    _call(dev, stream, library().sparse_mla_evict, kv_cache.data_ptr(), block_tables.data_ptr(), lengths.data_ptr(),
+          weights.data_ptr(), new_tables.data_ptr(), seqs, blocks, new_blocks, budget, sinks, recent, num_slots,
+          KV_FORMATS[kv_format], held[0].data_ptr(), held[1].data_ptr(), held[2].data_ptr())
+    return held[0], held[1], held[2]
 
 
 def host_workspace_bytes(T: int, h: int, topk: int) -> int:

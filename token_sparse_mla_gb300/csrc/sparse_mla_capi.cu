@@ -20,6 +20,7 @@
 #include "sparse_mla_topk.cuh"
 #include "sparse_mla_tree.cuh"
 #include "sparse_mla_weights.cuh"
+#include "sparse_mla_evict.cuh"
 #include "sparse_mla_masked.cuh"
 #include "sparse_mla_append.cuh"
 #include "sparse_mla_q_up.cuh"
@@ -1451,6 +1452,73 @@ smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_
     const cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_weights_kernel<1>, tm_q, tm_k, wp)
                               : cudaLaunchKernelEx(&cfg, smla::sparse_mla_weights_kernel<0>, tm_q, tm_k, wp);
     if (e != cudaSuccess) return cuda_fail(e, "weights kernel launch");
+    return SMLA_OK;
+}
+
+
+smla_status sparse_mla_evict(void* kv_cache, const int32_t* block_tables, const int32_t* lengths, const float* weights,
+                             const int32_t* new_tables, int32_t seqs, int32_t blocks, int32_t new_blocks, int32_t budget, int32_t sinks,
+                             int32_t recent, int64_t num_slots, int32_t kv_format, int32_t* kept, int32_t* new_lengths,
+                             float* new_weights, void* stream) {
+    if (seqs < 0) return fail(SMLA_ERR_INVALID_ARG, "seqs must be >= 0 (got %d)", seqs);
+    if (blocks < 1 || blocks > smla::kMaxBlocks || new_blocks < 1 || new_blocks > smla::kMaxBlocks)
+        return fail(SMLA_ERR_INVALID_ARG, "blocks per sequence must be in [1, %d] (got %d and %d)", smla::kMaxBlocks, blocks, new_blocks);
+    if (budget < 1 || budget > static_cast<int64_t>(new_blocks) * smla::kPage)
+        return fail(SMLA_ERR_INVALID_ARG, "budget must be in [1, new_blocks * 64] (got %d)", budget);
+    if (sinks < 0 || recent < 0 || static_cast<int64_t>(sinks) + recent > budget)
+        return fail(SMLA_ERR_INVALID_ARG, "sinks and recent must be >= 0 and no more than the budget together (got %d, %d)", sinks, recent);
+    if (num_slots < 1 || num_slots > 0x7fffffffLL)
+        return fail(SMLA_ERR_INVALID_ARG, "num_slots must be in [1, 2^31-1] (got %lld)", static_cast<long long>(num_slots));
+    if (kv_format != SMLA_KV_BF16 && kv_format != SMLA_KV_FP8)
+        return fail(SMLA_ERR_INVALID_ARG, "unknown kv_format %d", kv_format);
+    if (seqs == 0) return SMLA_OK;
+    if (seqs > 0x7fffffff / smla::kEvCluster) return fail(SMLA_ERR_INVALID_ARG, "seqs too large (%d)", seqs);
+    const int rows = kv_format == SMLA_KV_FP8 ? 8 : 4;
+    const int64_t groups = (static_cast<int64_t>(budget) + rows - 1) / rows * seqs;
+    const int64_t ctas = (groups + smla::kEvCopyThreads / 32 - 1) / (smla::kEvCopyThreads / 32);
+    if (ctas > 0x7fffffffLL) return fail(SMLA_ERR_INVALID_ARG, "seqs * budget too large (%d, %d)", seqs, budget);
+    if (!kv_cache || !block_tables || !lengths || !weights || !new_tables || !kept || !new_lengths || !new_weights)
+        return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(kv_cache, 16)) return fail(SMLA_ERR_INVALID_ARG, "kv_cache must be 16-byte aligned");
+    if (!aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(weights, 4) || !aligned(new_tables, 4) || !aligned(kept, 4) ||
+        !aligned(new_lengths, 4) || !aligned(new_weights, 4))
+        return fail(SMLA_ERR_INVALID_ARG, "tables, lengths, weights and kept must be 4-byte aligned");
+    int dev = 0;
+    DeviceState* ds = nullptr;
+    const smla_status st = device_state(&dev, &ds);
+    if (st != SMLA_OK) return st;
+    smla::EvParams ep = {};
+    ep.tables = block_tables;
+    ep.lengths = lengths;
+    ep.weights = weights;
+    ep.new_tables = new_tables;
+    ep.kept = kept;
+    ep.new_lengths = new_lengths;
+    ep.new_weights = new_weights;
+    ep.cache = kv_cache;
+    ep.num_slots = num_slots;
+    ep.B = seqs;
+    ep.nb = blocks;
+    ep.new_nb = new_blocks;
+    ep.budget = budget;
+    ep.sinks = sinks;
+    ep.recent = recent;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(seqs) * smla::kEvCluster, 1, 1);
+    cfg.blockDim = dim3(smla::kEvThreads, 1, 1);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_evict_select_kernel, ep);
+    if (e != cudaSuccess) return cuda_fail(e, "evict selection kernel launch");
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(smla::kEvCopyThreads, 1, 1);
+    e = kv_format == SMLA_KV_FP8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_evict_copy_kernel<1>, ep)
+                                 : cudaLaunchKernelEx(&cfg, smla::sparse_mla_evict_copy_kernel<0>, ep);
+    if (e != cudaSuccess) return cuda_fail(e, "evict copy kernel launch");
     return SMLA_OK;
 }
 
