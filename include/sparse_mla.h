@@ -473,20 +473,15 @@ smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* 
  *   decay      finite
  *   out        device, [seqs, blocks * 64] fp32, caller-owned; every element is
  *              written.  May be `weights` itself, but not overlap it in part
- *   workspace  device, at least sparse_mla_weights_workspace_bytes(kv_format)
- *              bytes, 256-byte aligned, caller-owned: fp8 rows as bf16 on their way.
- *              Calls that may overlap in time need workspaces of their own.  NULL
- *              when that function returns 0
  * Lengths, starts and tables are read on the device when the call runs.  Repeated
  * calls with the same arguments give identical bytes (no atomics).  seqs = 0 is a no-op.
  * Allocates nothing; asynchronous on `stream`.  Errors as in sparse_mla_tree, and
  * SMLA_ERR_INVALID_ARG for a decay that is not finite.
  */
-size_t sparse_mla_weights_workspace_bytes(int32_t kv_format);
 smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths,
                                const int32_t* starts, const uint32_t* mask, const float* lse, const float* weights, float decay,
                                int32_t T, int32_t h, int32_t seqs, int32_t blocks, int32_t mask_words, int64_t num_slots,
-                               int32_t kv_format, float scale, float* out, void* workspace, size_t workspace_bytes, void* stream);
+                               int32_t kv_format, float scale, float* out, void* stream);
 
 /*
  * sparse_mla_evict -- shrink the caches of a batch of sequences to `budget` rows each,

@@ -42,12 +42,9 @@ def _run(batch, lse, prev, decay, scale=SCALE, in_place=False, **kw):
         if in_place:
             held.copy_(before)
             before = held
-    need = smla.weights_workspace_bytes(batch.fmt)
-    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
-    out = smla.sparse_mla_weights(**d, lse=lse.to(DEV), scale=scale, weights=before, decay=decay, out=held, kv_format=batch.fmt,
-                                  workspace=ws, **kw)
+    out = smla.sparse_mla_weights(**d, lse=lse.to(DEV), scale=scale, weights=before, decay=decay, out=held, kv_format=batch.fmt, **kw)
     smla.sync_status()
-    assert guard[0].eq(2.5).all() and guard[-1].eq(2.5).all() and ws[need:].eq(0xFF).all()
+    assert guard[0].eq(2.5).all() and guard[-1].eq(2.5).all()
     return out.cpu()
 
 
@@ -178,11 +175,10 @@ def lib():
 
 def _c(lib, **kw):
     a = dict(q=0x1000, kv=0x1000, tables=0x1000, lengths=0x1000, starts=0x1000, mask=0x1000, lse=0x1000, prev=0x1000, decay=0.5, T=4, h=8,
-             seqs=2, blocks=3, words=1, num_slots=256, fmt=0, scale=0.04, out=0x1000, ws=0x1000, nws=1 << 40)
+             seqs=2, blocks=3, words=1, num_slots=256, fmt=0, scale=0.04, out=0x1000)
     a.update(kw)
     return lib.sparse_mla_weights(a["q"], a["kv"], a["tables"], a["lengths"], a["starts"], a["mask"], a["lse"], a["prev"], a["decay"],
-                                  a["T"], a["h"], a["seqs"], a["blocks"], a["words"], a["num_slots"], a["fmt"], a["scale"], a["out"],
-                                  a["ws"], a["nws"], None)
+                                  a["T"], a["h"], a["seqs"], a["blocks"], a["words"], a["num_slots"], a["fmt"], a["scale"], a["out"], None)
 
 
 @pytest.mark.parametrize("kw", [
@@ -196,20 +192,13 @@ def test_the_library_refuses(lib, kw):
 
 
 def test_no_sequences_is_a_noop(lib):
-    assert _c(lib, seqs=0, q=0, kv=0, tables=0, lengths=0, starts=0, mask=0, lse=0, prev=0, out=0, ws=0, nws=0) == 0
-
-
-def test_workspace_bytes(lib):
-    assert smla.weights_workspace_bytes() == 0
-    assert smla.weights_workspace_bytes("fp8") == 152 * 2 * 128 * 1152
-    with pytest.raises(ValueError, match="kv_format"):
-        smla.weights_workspace_bytes("int8")
+    assert _c(lib, seqs=0, q=0, kv=0, tables=0, lengths=0, starts=0, mask=0, lse=0, prev=0, out=0) == 0
 
 
 def _args():
     return dict(q=_d((3, 8, 576), torch.bfloat16), kv_cache=_d((640, 576), torch.bfloat16), block_tables=_d((2, 4), torch.int32),
                 lengths=_d((2,), torch.int32), starts=_d((3,), torch.int32), mask=_d((3, 2), torch.int32), lse=_d((3, 8), torch.float32),
-                weights=_d((2, 256), torch.float32), out=_d((2, 256), torch.float32), workspace=_d((4096,), torch.uint8))
+                weights=_d((2, 256), torch.float32), out=_d((2, 256), torch.float32))
 
 
 def test_marshalling(fake):
@@ -218,7 +207,7 @@ def test_marshalling(fake):
     p = {k: v.data_ptr() for k, v in a.items()}
     assert fake.lib.calls == [("sparse_mla_weights", (
         p["q"], p["kv_cache"], p["block_tables"], p["lengths"], p["starts"], p["mask"], p["lse"], p["weights"], 0.5, 3, 8, 2, 4, 2, 640, 0,
-        0.25, p["out"], p["workspace"], 4096, STREAM))]
+        0.25, p["out"], STREAM))]
     assert fake.entered == [CUDA0]
     a.update(kv_cache=_d((640, 656), torch.uint8), mask=None, weights=None)
     smla.sparse_mla_weights(**a, kv_format="fp8")
@@ -232,7 +221,7 @@ def test_marshalling(fake):
     dict(starts=_d((2,), torch.int32)), dict(mask=_d((3, 0), torch.int32)), dict(lse=_d((3,), torch.float32)),
     dict(lse=_d((3, 8), torch.float32, 1)), dict(lse=_d((3, 8), torch.bfloat16)), dict(weights=_d((2, 255), torch.float32)),
     dict(weights=_d((2, 256), torch.float64)), dict(weights=_d((2, 256), torch.float32, 1)), dict(out=_d((2, 512), torch.float32)),
-    dict(out=torch.zeros(2, 256)), dict(workspace=_d((4096,), torch.int32)), dict(kv_format="int8")])
+    dict(out=torch.zeros(2, 256)), dict(kv_format="int8")])
 def test_the_wrapper_refuses(fake, kw):
     a = dict(_args())
     a.update(kw)

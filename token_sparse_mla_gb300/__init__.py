@@ -49,7 +49,6 @@ from ._binding import (  # noqa: F401
     sync_status,
     tree_workspace_bytes,
     version,
-    weights_workspace_bytes,
 )
 
 __all__ = [
@@ -80,5 +79,4 @@ __all__ = [
     "sync_status",
     "tree_workspace_bytes",
     "version",
-    "weights_workspace_bytes",
 ]

@@ -24,7 +24,7 @@ EXPORTED = ("sparse_mla_fwd", "sparse_mla_fwd_ex", "sparse_mla_fwd_checked", "sp
             "sparse_mla_v_up", "sparse_mla_topk", "sparse_mla_scatter_mask", "sparse_mla_masked_mha",
             "sparse_mla_append", "sparse_mla_q_up", "sparse_mla_prefix", "sparse_mla_prefix_workspace_bytes",
             "sparse_mla_tree", "sparse_mla_tree_workspace_bytes",
-            "sparse_mla_weights", "sparse_mla_weights_workspace_bytes", "sparse_mla_evict",
+            "sparse_mla_weights", "sparse_mla_evict",
             "sparse_mla_sync_status",
             "sparse_mla_launch_info", "sparse_mla_last_error", "sparse_mla_version")
 
@@ -84,10 +84,8 @@ def library() -> ctypes.CDLL:
     lib.sparse_mla_tree_workspace_bytes.argtypes = [i32, i32, i32, i32]
     lib.sparse_mla_tree.restype = ctypes.c_int
     lib.sparse_mla_tree.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i64, i32, f32, vp, vp, vp, sz, vp]
-    lib.sparse_mla_weights_workspace_bytes.restype = sz
-    lib.sparse_mla_weights_workspace_bytes.argtypes = [i32]
     lib.sparse_mla_weights.restype = ctypes.c_int
-    lib.sparse_mla_weights.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, f32, i32, i32, i32, i32, i32, i64, i32, f32, vp, vp, sz, vp]
+    lib.sparse_mla_weights.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, f32, i32, i32, i32, i32, i32, i64, i32, f32, vp, vp]
     lib.sparse_mla_evict.restype = ctypes.c_int
     lib.sparse_mla_evict.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64, i32, vp, vp, vp, vp]
     lib.sparse_mla_host_io_layout.restype = ctypes.c_int
@@ -704,31 +702,16 @@ def sparse_mla_tree(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch
     return out, lse
 
 
-@functools.lru_cache(maxsize=64)
-def _weights_workspace_bytes(device_index: int, fmt: int) -> int:
-    return int(library().sparse_mla_weights_workspace_bytes(fmt))
-
-
-def weights_workspace_bytes(kv_format: str = "bf16") -> int:
-    """Bytes of workspace that sparse_mla_weights needs on the current device (0: none)."""
-    if kv_format not in KV_FORMATS:
-        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
-    return int(library().sparse_mla_weights_workspace_bytes(KV_FORMATS[kv_format]))
-
-
 def sparse_mla_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tensor, lengths: torch.Tensor,
                        starts: torch.Tensor, lse: torch.Tensor, scale: Optional[float] = None, *,
                        mask: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None, decay: float = 1.0,
-                       out: Optional[torch.Tensor] = None, kv_format: str = "bf16",
-                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                       out: Optional[torch.Tensor] = None, kv_format: str = "bf16", stream=None) -> torch.Tensor:
     """The attention weight that every cached row has gathered (include/sparse_mla.h): per sequence and
     position decay * weights, plus the probabilities of its tokens and heads there.
 
     q, kv_cache, block_tables, lengths, starts, scale and mask as in sparse_mla_tree, lse [T, h] fp32 as
     it returned it.  weights [seqs, blocks * 64] fp32 are what earlier calls gathered (None: nothing yet);
-    returns out of the same shape, which may be passed in and may be weights itself.  workspace: a
-    uint8 tensor of weights_workspace_bytes(kv_format) bytes for callers that keep one (calls that may
-    overlap need their own); allocated here otherwise.
+    returns out of the same shape, which may be passed in and may be weights itself.
     """
     if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != _BF16 or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous [T, h, 576] bf16 tensor, got {tuple(q.shape)} {q.dtype}")
@@ -759,12 +742,9 @@ def sparse_mla_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: to
             raise ValueError(f"out must be a contiguous [{seqs}, {blocks * 64}] fp32 tensor")
         if out.device != dev:
             _apart(dev, out=out)
-    fmt = KV_FORMATS[kv_format]
-    workspace = _workspace(dev, stream, workspace, _weights_workspace_bytes, fmt)
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _call(dev, stream, library().sparse_mla_weights, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
           lengths.data_ptr(), starts.data_ptr(), mask_ptr, lse.data_ptr(), prev, float(decay), T, h, seqs, blocks, words,
-          num_slots, fmt, float(scale), out.data_ptr(), ws_ptr, ws_bytes)
+          num_slots, KV_FORMATS[kv_format], float(scale), out.data_ptr())
     return out
 
 

@@ -94,37 +94,54 @@ __device__ __forceinline__ void block_prefix(int64_t x, int64_t* scratch, int wa
     }
 }
 
-// Four fp8 rows as bf16 rows of 1152 bytes, loads in flight together: codes x scale in fp32, rounded to
-// bf16 as in the forward.  `n` of the four take part (0 .. 4), the others are written as zeros.
-__device__ __forceinline__ void expand_rows4(const uint8_t* src, int n, __nv_bfloat16* dst) {
-    const int lane = threadIdx.x & 31;
+// Four fp8 rows on their way to bf16 rows of 1152 bytes: the loads, and, later, codes x scale in fp32 rounded to
+// bf16 as in the forward, and the stores.  `n` of the four take part (0 .. 4), the others become zeros.
+struct Fp8Rows4 {
     // lane l: codes [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8), so that both stores are 512 contiguous bytes
     uint2 a[4], b[4];
     float sa[4], sb[4];
     uint32_t rope[4];
+    __device__ __forceinline__ void load(const uint8_t* src, int n) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        a[u] = b[u] = make_uint2(0u, 0u);
-        sa[u] = sb[u] = 0.f;
-        rope[u] = 0u;
-        if (u < n) {
-            const uint8_t* row = src + u * kFp8RowBytes;
-            a[u] = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-            b[u] = __ldg(reinterpret_cast<const uint2*>(row) + 32 + lane);
-            sa[u] = __ldg(reinterpret_cast<const float*>(row + 512) + (lane >> 4));
-            sb[u] = __ldg(reinterpret_cast<const float*>(row + 520) + (lane >> 4));
-            rope[u] = __ldg(reinterpret_cast<const uint32_t*>(row + 528) + lane);
+        for (int u = 0; u < 4; ++u) {
+            a[u] = b[u] = make_uint2(0u, 0u);
+            sa[u] = sb[u] = 0.f;
+            rope[u] = 0u;
+            if (u < n) {
+                const uint8_t* row = src + u * kFp8RowBytes;
+                a[u] = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+                b[u] = __ldg(reinterpret_cast<const uint2*>(row) + 32 + lane);
+                sa[u] = __ldg(reinterpret_cast<const float*>(row + 512) + (lane >> 4));
+                sb[u] = __ldg(reinterpret_cast<const float*>(row + 520) + (lane >> 4));
+                rope[u] = __ldg(reinterpret_cast<const uint32_t*>(row + 528) + lane);
+            }
         }
     }
+    __device__ __forceinline__ void store(__nv_bfloat16* dst) const {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        uint4* out = reinterpret_cast<uint4*>(dst + u * kDQK);
-        out[lane] = make_uint4(ptx::e4m3x2_scaled_bf16x2(a[u].x & 0xFFFFu, sa[u]), ptx::e4m3x2_scaled_bf16x2(a[u].x >> 16, sa[u]),
-                               ptx::e4m3x2_scaled_bf16x2(a[u].y & 0xFFFFu, sa[u]), ptx::e4m3x2_scaled_bf16x2(a[u].y >> 16, sa[u]));
-        out[32 + lane] = make_uint4(ptx::e4m3x2_scaled_bf16x2(b[u].x & 0xFFFFu, sb[u]), ptx::e4m3x2_scaled_bf16x2(b[u].x >> 16, sb[u]),
-                                    ptx::e4m3x2_scaled_bf16x2(b[u].y & 0xFFFFu, sb[u]), ptx::e4m3x2_scaled_bf16x2(b[u].y >> 16, sb[u]));
-        reinterpret_cast<uint32_t*>(out + 64)[lane] = rope[u];
+        for (int u = 0; u < 4; ++u) {
+            uint4* out = reinterpret_cast<uint4*>(dst + u * kDQK);
+            out[lane] = make_uint4(ptx::e4m3x2_scaled_bf16x2(a[u].x & 0xFFFFu, sa[u]), ptx::e4m3x2_scaled_bf16x2(a[u].x >> 16, sa[u]),
+                                   ptx::e4m3x2_scaled_bf16x2(a[u].y & 0xFFFFu, sa[u]), ptx::e4m3x2_scaled_bf16x2(a[u].y >> 16, sa[u]));
+            out[32 + lane] = make_uint4(ptx::e4m3x2_scaled_bf16x2(b[u].x & 0xFFFFu, sb[u]), ptx::e4m3x2_scaled_bf16x2(b[u].x >> 16, sb[u]),
+                                        ptx::e4m3x2_scaled_bf16x2(b[u].y & 0xFFFFu, sb[u]), ptx::e4m3x2_scaled_bf16x2(b[u].y >> 16, sb[u]));
+            reinterpret_cast<uint32_t*>(out + 64)[lane] = rope[u];
+        }
     }
-}
+};
+
+// A warp's `rows` consecutive rows of page i of a sequence, from `row` on, and how many of them take part.
+struct Fp8Source {
+    const uint8_t* src;
+    int n;
+    __device__ __forceinline__ Fp8Source(const BatchParams& p, const Seq& s, int i, int page, int row)
+        : src(static_cast<const uint8_t*>(p.kv) + (static_cast<int64_t>(page) * kPage + row) * kFp8RowBytes), n(page_rows(p, s, i, page) - row) {}
+    __device__ __forceinline__ void prefetch(int rows) const {  // into L2
+        if (n > 0 && (threadIdx.x & 31) == 0) ptx::bulk_prefetch_l2(src, static_cast<uint32_t>(min(n, rows) * kFp8RowBytes));
+    }
+    __device__ __forceinline__ void load(Fp8Rows4& r, int u) const { r.load(src + u * kFp8RowBytes, n - u); }
+};
 
 }  // namespace smla

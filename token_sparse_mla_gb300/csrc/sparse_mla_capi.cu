@@ -1384,18 +1384,10 @@ smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* 
 }
 
 
-size_t sparse_mla_weights_workspace_bytes(int32_t kv_format) {
-    int num_sms = 152;
-    int dev = 0;
-    DeviceState* ds = nullptr;
-    if (device_state(&dev, &ds) == SMLA_OK) num_sms = ds->num_sms;
-    return kv_format == SMLA_KV_FP8 ? static_cast<size_t>(num_sms / 2 * 2) * smla::kWtRing * smla::kWtHalf * smla::kDQK * 2 : 0;
-}
-
 smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths,
                                const int32_t* starts, const uint32_t* mask, const float* lse, const float* weights, float decay,
                                int32_t T, int32_t h, int32_t seqs, int32_t blocks, int32_t mask_words, int64_t num_slots,
-                               int32_t kv_format, float scale, float* out, void* workspace, size_t workspace_bytes, void* stream) {
+                               int32_t kv_format, float scale, float* out, void* stream) {
     smla_status st = check_batch_sizes(mask, T, h, seqs, blocks, mask_words, num_slots, kv_format, scale);
     if (st != SMLA_OK) return st;
     if (!std::isfinite(decay)) return fail(SMLA_ERR_INVALID_ARG, "decay must be finite");
@@ -1409,29 +1401,21 @@ smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_
     if ((st = device_state(&dev, &ds)) != SMLA_OK) return st;
     const bool fp8 = kv_format == SMLA_KV_FP8;
     const int pairs = ds->num_sms / 2;
-    const size_t need = fp8 ? static_cast<size_t>(2 * pairs) * smla::kWtRing * smla::kWtHalf * smla::kDQK * 2 : 0;
-    if (need > 0) {
-        if (!workspace || !aligned(workspace, 256))
-            return fail(SMLA_ERR_INVALID_ARG, "workspace must be given, 256-byte aligned");
-        if (workspace_bytes < need) return fail(SMLA_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, need);
-    }
     EncodeTiledFn enc = nullptr;
     if ((st = encode_fn(&enc)) != SMLA_OK) return st;
     const int64_t rows = static_cast<int64_t>(T) * h;
     alignas(64) CUtensorMap tm_q;
     alignas(64) CUtensorMap tm_k;
     // (without tokens nothing is loaded by q's map)
-    CUresult r = T > 0 ? row_map(enc, &tm_q, q, rows, smla::kWtHalf, 1) : row_map(enc, &tm_q, kv_cache, 1, smla::kWtHalf, 1);
-    if (r == CUDA_SUCCESS)
-        r = fp8 ? row_map(enc, &tm_k, workspace, static_cast<int64_t>(2 * pairs) * smla::kWtRing * smla::kWtHalf, smla::kPage, 1)
-                : row_map(enc, &tm_k, kv_cache, num_slots, smla::kPage, 1);
+    CUresult r = T > 0 ? row_map(enc, &tm_q, q, rows, smla::kPage, 1) : row_map(enc, &tm_q, kv_cache, 1, smla::kPage, 1);
+    // (nor anything by the cache's, if its rows are fp8)
+    if (r == CUDA_SUCCESS) r = row_map(enc, &tm_k, kv_cache, fp8 ? 1 : num_slots, smla::kPage, 1);
     if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/kv_cache failed (%d)", (int)r);
     smla::WtParams wp = {};
     wp.bp = batch_params(kv_cache, block_tables, lengths, starts, mask, T, h, seqs, blocks, mask_words, num_slots);
     wp.lse = lse;
     wp.prev = weights;
     wp.out = out;
-    wp.ring = fp8 ? static_cast<__nv_bfloat16*>(workspace) : nullptr;
     wp.pairs = pairs;
     wp.scale = scale;
     wp.decay = decay;
@@ -1472,11 +1456,7 @@ smla_status sparse_mla_evict(void* kv_cache, const int32_t* block_tables, const 
     if (kv_format != SMLA_KV_BF16 && kv_format != SMLA_KV_FP8)
         return fail(SMLA_ERR_INVALID_ARG, "unknown kv_format %d", kv_format);
     if (seqs == 0) return SMLA_OK;
-    if (seqs > 0x7fffffff / smla::kEvCluster) return fail(SMLA_ERR_INVALID_ARG, "seqs too large (%d)", seqs);
-    const int rows = kv_format == SMLA_KV_FP8 ? 8 : 4;
-    const int64_t groups = (static_cast<int64_t>(budget) + rows - 1) / rows * seqs;
-    const int64_t ctas = (groups + smla::kEvCopyThreads / 32 - 1) / (smla::kEvCopyThreads / 32);
-    if (ctas > 0x7fffffffLL) return fail(SMLA_ERR_INVALID_ARG, "seqs * budget too large (%d, %d)", seqs, budget);
+    if (seqs > 0x7fffffff / smla::kEvMaxCluster) return fail(SMLA_ERR_INVALID_ARG, "seqs too large (%d)", seqs);
     if (!kv_cache || !block_tables || !lengths || !weights || !new_tables || !kept || !new_lengths || !new_weights)
         return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned(kv_cache, 16)) return fail(SMLA_ERR_INVALID_ARG, "kv_cache must be 16-byte aligned");
@@ -1503,18 +1483,32 @@ smla_status sparse_mla_evict(void* kv_cache, const int32_t* block_tables, const 
     ep.budget = budget;
     ep.sinks = sinks;
     ep.recent = recent;
-    cudaLaunchAttribute attr[1];
+    // CTAs per sequence: no more in all than SMs, and 1024 positions or more each
+    ep.cluster = 1;
+    while (ep.cluster < smla::kEvMaxCluster && static_cast<int64_t>(seqs) * ep.cluster * 2 <= ds->num_sms &&
+           static_cast<int64_t>(blocks) * smla::kPage >= 2048LL * ep.cluster)
+        ep.cluster *= 2;
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(seqs) * smla::kEvCluster, 1, 1);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ep.cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(seqs) * static_cast<unsigned>(ep.cluster), 1, 1);
     cfg.blockDim = dim3(smla::kEvThreads, 1, 1);
     cudaError_t e = cudaLaunchKernelEx(&cfg, smla::sparse_mla_evict_select_kernel, ep);
     if (e != cudaSuccess) return cuda_fail(e, "evict selection kernel launch");
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    const int rows = kv_format == SMLA_KV_FP8 ? smla::evict_copy_rows<1>() : smla::evict_copy_rows<0>();
+    const int64_t groups = (static_cast<int64_t>(budget) + rows - 1) / rows * seqs;
+    const int64_t want = (groups + smla::kEvCopyThreads / 32 - 1) / (smla::kEvCopyThreads / 32), cap = static_cast<int64_t>(ds->num_sms) * 3;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(want < cap ? want : cap), 1, 1);
     cfg.blockDim = dim3(smla::kEvCopyThreads, 1, 1);
     e = kv_format == SMLA_KV_FP8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_evict_copy_kernel<1>, ep)
                                  : cudaLaunchKernelEx(&cfg, smla::sparse_mla_evict_copy_kernel<0>, ep);

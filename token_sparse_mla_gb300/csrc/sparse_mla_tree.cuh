@@ -50,6 +50,10 @@ constexpr int kTrExpandWarps = 4;
 constexpr int kTrRing = 3;       // blocks of expanded rows per pair
 constexpr int kTrTileCost = 3;   // what a piece costs beside its blocks, in blocks
 constexpr int kTrBlockRows = kPfKeys;
+#ifndef TR_AHEAD
+#define TR_AHEAD 1
+#endif
+constexpr int kTrAhead = TR_AHEAD;
 
 template <int KVF>
 __host__ __device__ constexpr int tree_threads() {
@@ -265,6 +269,14 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             };
             // a page that is not there loads as zeros, from rows below 0
             auto first_row = [&](int page) -> int { return page_in_cache(p.bp, page) ? page * kPage : -kPage; };
+            auto prefetch = [&](int i) {
+                if (i >= 2 * w.b1) return;
+                const int pg = page_of(p.bp, w.b, w.s, i);
+                const int n = page_rows(p.bp, w.s, i, pg);
+                if (n > 0)
+                    ptx::bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(p.bp.kv) + static_cast<int64_t>(pg) * kPage * kDQK,
+                                          static_cast<uint32_t>(n * kDQK * 2));
+            };
             bool ok = true;
             int x = 0, piece = 0;
             bool tail_v0 = false, tail_v1 = false;
@@ -314,14 +326,12 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                                               g * kPfGroupA, even_bar(kPbKFull + g));
                     }
                     if constexpr (KVF == 0) {
+                        // this CTA's page of a later block, into L2 while the current one is waited for
+                        if (b == w.b0)
+                            for (int a = 1; a < kTrAhead; ++a) prefetch(2 * (b + a) + rank);
+                        prefetch(2 * (b + kTrAhead) + rank);
                         pg0 = page_of(p.bp, w.b, w.s, 2 * b + 2);
                         pg1 = page_of(p.bp, w.b, w.s, 2 * b + 3);
-                        // this CTA's page of the next block, into L2 while the current one is waited for
-                        const int pg = rank ? pg1 : pg0;
-                        const int n = page_rows(p.bp, w.s, 2 * b + 2 + rank, pg);
-                        if (n > 0)
-                            ptx::bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(p.bp.kv) + static_cast<int64_t>(pg) * kPage * kDQK,
-                                                  static_cast<uint32_t>(n * kDQK * 2));
                     }
                     if (ok && x > 0) ok = load_v(x - 1, tail_v0, tail_v1, row_v0, row_v1);
                     row_v0 = row0;
@@ -433,20 +443,34 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             bool ok = true;
             int x = 0;
             for (bool more = any; ok && more; more = w.next(p)) {
-                int page = page_of(p.bp, w.b, w.s, 2 * w.b0 + rank);
+                // four rows are loaded while the four before them are converted, across blocks too; a block's
+                // rows are brought into L2 two blocks ahead
+                auto source = [&](int b) -> Fp8Source {
+                    const int i = 2 * b + rank;
+                    return Fp8Source(p.bp, w.s, i, b < w.b1 ? page_of(p.bp, w.b, w.s, i) : -1, row);
+                };
+                Fp8Source cur = source(w.b0), next = source(w.b0 + 1);
+                next.prefetch(kRows);
+                Fp8Rows4 r[2];
+                cur.load(r[0], 0);
                 for (int b = w.b0; b < w.b1; ++b, ++x) {
-                    const int i = 2 * b + rank, slot = x % kTrRing;
-                    const int n = page_rows(p.bp, w.s, i, page) - row;
-                    const uint8_t* src = static_cast<const uint8_t*>(p.bp.kv) + (static_cast<int64_t>(page) * kPage + row) * kFp8RowBytes;
-                    page = page_of(p.bp, w.b, w.s, i + 2);
+                    const int slot = x % kTrRing;
+                    const Fp8Source after = source(b + 2);
+                    after.prefetch(kRows);
                     if (x >= kTrRing) {  // this slot's last block has been multiplied
                         if (lane == 0) ok = wait(kTbRingFree + slot, (x / kTrRing - 1) & 1);
                         ok = __shfl_sync(0xffffffffu, ok, 0);
                         if (!ok) break;
                     }
                     __nv_bfloat16* dst = ring + static_cast<int64_t>(slot) * kTrBlockRows * kDQK;
-#pragma unroll 1
-                    for (int u = 0; u < kRows; u += 4) expand_rows4(src + u * kFp8RowBytes, n - u, dst + u * kDQK);
+#pragma unroll
+                    for (int u = 0; u < kRows; u += 4) {
+                        if (u + 4 < kRows) cur.load(r[(u / 4 + 1) & 1], u + 4);
+                        else next.load(r[(u / 4 + 1) & 1], 0);
+                        r[(u / 4) & 1].store(dst + u * kDQK);
+                    }
+                    cur = next;
+                    next = after;
                     ptx::fence_proxy_async_all();
                     __syncwarp();
                     if (lane < 2) ptx::mbar_arrive_release_cluster(ptx::map_shared_rank(bar(kTbRingFull + slot), lane));

@@ -10,18 +10,21 @@
 // sequence (cta_group::2, M = 256: 128 keys per CTA) against up to 256 rows (token, head), half of which each
 // CTA holds; the 576 dims go through in nine panels of 64.
 //
-// One operand of a pair stays in shared memory, the other streams through a ring of four panels:
+// One operand of a pair stays in shared memory, the other streams through a ring of panels:
 //   up to 256 rows in the sequence: its queries stay, keys stream.  Bound by HBM, 1152 bytes a key: 256 keys
 //     are 3.3 us for 76 pairs at 6.8 TB/s, the MMAs at most 36 * 128 cycles = 2.4 us.
 //   more: a tile of keys stays and the queries stream from L2, tile after tile, so that a key's sum still is
 //     one thread's.  Bound by the MMAs.
-// Both operands have the same layout (128 rows x 9 panels, SW128), so the two forms differ in who loads what
-// and in which descriptor is A.
+// Both operands have the same layout (rows x 9 panels, SW128), so the two forms differ in who loads what and in
+// which descriptor is A.  The ring's depth sets the pace where the operand streams (64 KB in flight per CTA gave
+// 42 GB/s per SM, from HBM and from L2 alike), so it takes what the other operand leaves: eight stages if no
+// sequence of the batch has more than 128 rows, else five.
 //
 // Work: tiles of 256 keys, each whole in one pair, in equal shares of their cost (kWt... below).
 //
-// fp8 rows are expanded ahead of the loads by four more warps, each CTA its own 128 keys, into two tiles per
-// CTA in global memory that stay in L2 (sparse_mla_tree.cuh says why).
+// fp8 rows are expanded straight into the ring (or the operand that stays) by four more warps, each 32 of the
+// CTA's 128 keys, two panels of codes at a time with the next two on their way.  (Expanded into global memory
+// and loaded from there by TMA, a tile took 6.4 us: L2 took the writes no faster.)
 //
 // Roles (384 threads, 512 with fp8):
 //   warps 0-7    sums: TMEM quadrant warp % 4 (32 keys), half warp / 4 of the tile's columns
@@ -39,12 +42,12 @@ namespace smla {
 constexpr int kWtKeys = 256;      // keys per tile (pair)
 constexpr int kWtHalf = 128;      // per CTA
 constexpr int kWtRows = 256;      // rows (token, head) per tile
-constexpr int kWtStages = 4;
+constexpr int kWtStages = 5, kWtStagesFew = 8;
+constexpr int kWtRowsFew = 128;      // rows of a sequence up to which the deeper ring has room
 constexpr int kWtPanel = 128 * 128;  // 128 rows x 64 bf16, SW128
 constexpr int kWtSumWarps = 8;
 constexpr int kWtTmaWarp = 8, kWtMmaWarp = 9, kWtFillWarp = 10, kWtExpandWarp = 12;
 constexpr int kWtExpandWarps = 4;
-constexpr int kWtRing = 2;        // expanded tiles per CTA
 // costs in tenths of a microsecond: a sequence's queries and first keys; a tile whose keys stream; one whose
 // keys stay, and each of its row tiles
 constexpr int kWtCostSeq = 30, kWtCostStream = 34, kWtCostStay = 20, kWtCostRows = 24;
@@ -55,24 +58,25 @@ __host__ __device__ constexpr int weights_threads() {
 }
 
 enum : int {
-    kWbStayFull = 0,                       // even CTA: both CTAs' part of the operand that stays
-    kWbStayEmpty = 1,                      // both
-    kWbFull = 2,                           // +stage, even CTA
-    kWbEmpty = kWbFull + kWtStages,        // +stage, both
-    kWbSFull = kWbEmpty + kWtStages,       // +buffer, both
-    kWbSEmpty = kWbSFull + 2,              // +buffer, even CTA
-    kWbDrain = kWbSEmpty + 2,              // even CTA
-    kWbRowsFull = kWbDrain + 1,            // +tile, own CTA: expanded rows
-    kWbRowsFree = kWbRowsFull + kWtRing,   // +tile, both
-    kWbCount = kWbRowsFree + kWtRing
+    kWbStayFull = 0,                        // even CTA: both CTAs' part of the operand that stays, by TMA
+    kWbStayMade = 1,                        // even CTA: the same, expanded
+    kWbStayEmpty = 2,                       // both
+    kWbFull = 3,                            // +stage, even CTA: by TMA
+    kWbMade = kWbFull + kWtStagesFew,       // +stage, even CTA: expanded
+    kWbEmpty = kWbMade + kWtStagesFew,      // +stage, both
+    kWbSFull = kWbEmpty + kWtStagesFew,     // +buffer, both
+    kWbSEmpty = kWbSFull + 2,               // +buffer, even CTA
+    kWbDrain = kWbSEmpty + 2,               // even CTA
+    kWbCount = kWbDrain + 1
 };
 
 struct WtLayout {
-    static constexpr int kOffStay = 0;
-    static constexpr int kOffRing = kPanels * kWtPanel;
+    static constexpr int kOffStay = 0;                               // 9 panels of 128 rows, or of 64
+    static constexpr int kOffRing = kPanels * kWtPanel, kOffRingFew = kOffRing / 2;
     static constexpr int kOffLse = kOffRing + kWtStages * kWtPanel;  // [2][256]: minus the rows' LSE
-    static constexpr int kOffX = kOffLse + 2 * kWtRows * 4;          // [2][128]: sums of the columns' second half; the plan's sums
-    static constexpr int kOffBar = kOffX + 2 * kWtHalf * 4;
+    static_assert(kOffRingFew + kWtStagesFew * kWtPanel <= kOffLse, "ring");
+    static constexpr int kOffX = kOffLse + 2 * kWtRows * 4;          // [128]: sums of the columns' second half; the plan's sums
+    static constexpr int kOffBar = kOffX + kWtHalf * 4;
     static constexpr int kOffMisc = kOffBar + kWbCount * 8;          // tmem base, abort flag, the run's start
     static constexpr int kBytes = kOffMisc + 8 + 40;
     static_assert(kBytes <= 232448, "shared memory budget (227 KB)");
@@ -81,6 +85,7 @@ struct WtLayout {
 struct WtStart {
     int64_t at, end, seq_at;  // the run [at, end) in cost units; where its first sequence begins
     int32_t b;
+    int32_t few;              // no sequence has more than kWtRowsFew rows
 };
 
 struct WtParams {
@@ -88,7 +93,6 @@ struct WtParams {
     const float* lse;      // [T, h]
     const float* prev;     // [B, nb * 64] or nullptr
     float* out;            // [B, nb * 64]
-    __nv_bfloat16* ring;   // fp8: [CTAs][kWtRing][128][576]
     int32_t pairs;
     float scale, decay;
 };
@@ -109,12 +113,21 @@ __device__ __forceinline__ void weights_plan(const WtParams& p, int run, int thr
         return s.n == 0 ? 0 : kWtCostSeq + static_cast<int64_t>(weights_key_tiles(s)) * weights_tile_cost(weights_row_tiles(p, s));
     };
     int64_t cost = 0;
-    for (int b = b0; b < b1; ++b) cost += cost_of(load_seq(p.bp, b));
+    int most = 0;  // tokens of a sequence
+    for (int b = b0; b < b1; ++b) {
+        const Seq s = load_seq(p.bp, b);
+        cost += cost_of(s);
+        most = max(most, s.n);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((threadIdx.x & 31) == 0) scratch[32 + threadIdx.x / 32] = most;
     int64_t at, total;
     block_prefix(cost, scratch, threads / 32, at, total);
+    for (int w = 0; w < threads / 32; ++w) most = max(most, static_cast<int>(scratch[32 + w]));
+    const int few = static_cast<int64_t>(most) * p.bp.h <= kWtRowsFew;
     const int64_t from = total * run / p.pairs, to = total * (run + 1) / p.pairs;
     if (from >= to) {
-        if (threadIdx.x == 0) *start = WtStart{0, 0, 0, p.bp.B};
+        if (threadIdx.x == 0) *start = WtStart{0, 0, 0, p.bp.B, few};
     } else if (at <= from && from < at + cost) {
         int b = b0;
         for (;; ++b) {
@@ -122,7 +135,7 @@ __device__ __forceinline__ void weights_plan(const WtParams& p, int run, int thr
             if (from < at + c) break;
             at += c;
         }
-        *start = WtStart{from, to, at, b};
+        *start = WtStart{from, to, at, b, few};
     }
     __syncthreads();
 }
@@ -176,6 +189,72 @@ struct WtWalk {
     __device__ __forceinline__ int columns(const WtParams& p, int i) const { return (rows(p, i) + 31) & ~31; }
 };
 
+// A place in the ring of stages, the same for everybody who goes along it.
+struct WtStage {
+    int at, stages, round;
+    __device__ __forceinline__ explicit WtStage(int n) : at(0), stages(n), round(0) {}
+    __device__ __forceinline__ void next() {
+        if (++at == stages) {
+            at = 0;
+            ++round;
+        }
+    }
+    __device__ __forceinline__ bool used() const { return round > 0; }                 // this stage has been filled before
+    __device__ __forceinline__ uint32_t last() const { return (round - 1) & 1; }       // parity of its last release
+};
+
+// 32 rows of fp8 on their way into two panels: lane l has rows 8 i + l / 4 and of each the 16 codes from
+// 16 (l % 4) on of either panel, with their tile's scale; or the 32 bytes from 32 (l % 4) on of the rotated dims.
+struct WtCodes {
+    uint4 v[8];
+    float s[4];
+    __device__ __forceinline__ void load(const Fp8Source& from, int pair) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            v[2 * i] = v[2 * i + 1] = make_uint4(0u, 0u, 0u, 0u);
+            s[i] = 0.f;
+            if (r < from.n) {
+                const uint8_t* row = from.src + r * kFp8RowBytes;
+                if (pair < 4) {
+                    const uint4* codes = reinterpret_cast<const uint4*>(row) + 8 * pair + (lane & 3);
+                    v[2 * i] = __ldg(codes);
+                    v[2 * i + 1] = __ldg(codes + 4);
+                    s[i] = __ldg(reinterpret_cast<const float*>(row + 512) + pair);
+                } else {
+                    const uint4* rope = reinterpret_cast<const uint4*>(row + 528) + 2 * (lane & 3);
+                    v[2 * i] = __ldg(rope);
+                    v[2 * i + 1] = __ldg(rope + 1);
+                }
+            }
+        }
+    }
+    // chunk c of row r of a panel lies at 128 r + 16 (c ^ r % 8)
+    __device__ __forceinline__ static uint32_t place(uint32_t dst, int r, int c) { return dst + r * 128 + ((c ^ (r & 7)) << 4); }
+    __device__ __forceinline__ void store_codes(uint32_t dst, int j) const {
+        const int lane = threadIdx.x & 31, c = 2 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const uint4 q = v[2 * i + j];
+            ptx::st_shared_v4(place(dst, r, c), make_uint4(ptx::e4m3x2_scaled_bf16x2(q.x & 0xFFFFu, s[i]), ptx::e4m3x2_scaled_bf16x2(q.x >> 16, s[i]),
+                                                           ptx::e4m3x2_scaled_bf16x2(q.y & 0xFFFFu, s[i]), ptx::e4m3x2_scaled_bf16x2(q.y >> 16, s[i])));
+            ptx::st_shared_v4(place(dst, r, c + 1), make_uint4(ptx::e4m3x2_scaled_bf16x2(q.z & 0xFFFFu, s[i]), ptx::e4m3x2_scaled_bf16x2(q.z >> 16, s[i]),
+                                                               ptx::e4m3x2_scaled_bf16x2(q.w & 0xFFFFu, s[i]), ptx::e4m3x2_scaled_bf16x2(q.w >> 16, s[i])));
+        }
+    }
+    __device__ __forceinline__ void store_rope(uint32_t dst) const {
+        const int lane = threadIdx.x & 31, c = 2 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            ptx::st_shared_v4(place(dst, r, c), v[2 * i]);
+            ptx::st_shared_v4(place(dst, r, c + 1), v[2 * i + 1]);
+        }
+    }
+};
+
 template <int KVF>
 __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
     sparse_mla_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WtParams p) {
@@ -203,8 +282,8 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
         *sAbort = 0;
         for (int i = 0; i < kWbCount; ++i) {
             const bool by_warps = i == kWbSEmpty || i == kWbSEmpty + 1;                // both CTAs' sum warps
-            const bool by_expand = i >= kWbRowsFull && i < kWbRowsFull + kWtRing;      // this CTA's expansion warps
-            ptx::mbar_init(bar(i), by_warps ? 2 * kWtSumWarps : by_expand ? kWtExpandWarps : 1);
+            const bool by_expand = i == kWbStayMade || (i >= kWbMade && i < kWbMade + kWtStagesFew);  // both CTAs' expansion warps
+            ptx::mbar_init(bar(i), by_warps ? 2 * kWtSumWarps : by_expand ? 2 * kWtExpandWarps : 1);
         }
         ptx::fence_mbarrier_init();
     }
@@ -227,26 +306,29 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
     ptx::cluster_sync();  // both CTAs' barriers are initialised before anyone signals them
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
+    const bool few = start->few != 0;
+    const int stages = few ? kWtStagesFew : kWtStages;
+    const uint32_t ring = sbase + (few ? L::kOffRingFew : L::kOffRing);
+    const int stay_panel = few ? kWtPanel / 2 : kWtPanel;
 
     if (warp == kWtTmaWarp) {
         // ================================================================ TMA producer
         // The even CTA's thread expects both CTAs' bytes on its barrier, each CTA's thread issues its own copies.
         if (lane == 0) {
             bool ok = true;
-            int stays = 0, loads = 0, t = 0;  // operands that stay, ring panels, key tiles so far
-            const int ring0 = static_cast<int>(blockIdx.x) * kWtRing * kWtHalf;
-            int row0 = 0, row1 = 0;           // rows of the tile's two pages
+            int stays = 0;          // operands that stayed so far
+            bool others = false;    // the last piece's keys stayed
+            WtStage st(stages);
+            int row0 = 0, row1 = 0;  // rows of the tile's two pages
             auto begin_stay = [&]() -> bool {
                 if (stays > 0 && !wait(kWbStayEmpty, (stays - 1) & 1)) return false;
                 ++stays;
-                if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbStayFull), 2u * kPanels * kWtPanel);
                 return true;
             };
-            auto begin_stage = [&](int& st) -> bool {
-                st = loads % kWtStages;
-                if (loads >= kWtStages && !wait(kWbEmpty + st, (loads / kWtStages - 1) & 1)) return false;
-                ++loads;
-                if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbFull + st), 2u * kWtPanel);
+            // the stage is this thread's to fill
+            auto begin_stage = [&]() -> bool {
+                if (st.used() && !wait(kWbEmpty + st.at, st.last())) return false;
+                if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbFull + st.at), 2u * kWtPanel);
                 return true;
             };
             auto load_keys = [&](uint32_t dst, int pn, uint32_t b) {
@@ -267,11 +349,18 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 const int q0 = w.s.first * p.bp.h;
                 if (stream_keys) {
                     if (!(ok = begin_stay())) break;
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbStayFull), 2u * kPanels * static_cast<uint32_t>(stay_panel));
+                    const int row = q0 + rank * (w.columns(p, 0) / 2);
                     for (int pn = 0; pn < kPanels; ++pn)
-                        ptx::tma_load_3d_pair(sbase + L::kOffStay + pn * kWtPanel, &tm_q, 0, q0 + rank * (w.columns(p, 0) / 2), pn,
-                                              even_bar(kWbStayFull));
+                        for (int half = 0; half < (few ? 1 : 2); ++half)
+                            ptx::tma_load_3d_pair(sbase + L::kOffStay + pn * stay_panel + half * kWtPanel / 2, &tm_q, 0,
+                                                  row + half * kPage, pn, even_bar(kWbStayFull));
                 }
-                for (int k = w.k0; ok && k < w.k1; ++k, ++t) {
+                // what the expansion warps filled of the ring has been used before this thread fills it: a barrier that
+                // nobody here has followed could be more than one phase behind, which a parity cannot tell
+                if (KVF == 1 && !stream_keys && !others && stays > 0 && !(ok = wait(kWbStayEmpty, (stays - 1) & 1))) break;
+                others = !stream_keys;
+                for (int k = w.k0; ok && k < w.k1; ++k) {
                     if constexpr (KVF == 0) {
                         const int i = 4 * k + 2 * rank;
                         row0 = first_row(page_of(p.bp, w.b, w.s, i));
@@ -280,32 +369,35 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                             prefetch(i + 4);
                             prefetch(i + 5);
                         }
-                    } else {
-                        row0 = ring0 + (t % kWtRing) * kWtHalf;
-                        row1 = row0 + kPage;
-                        if (!(ok = wait(kWbRowsFull + t % kWtRing, (t / kWtRing) & 1))) break;
-                        ptx::fence_proxy_async_all();
                     }
-                    int st;
                     if (stream_keys) {
-                        for (int pn = 0; ok && pn < kPanels; ++pn)
-                            if ((ok = begin_stage(st))) load_keys(sbase + L::kOffRing + st * kWtPanel, pn, even_bar(kWbFull + st));
+                        for (int pn = 0; ok && pn < kPanels; ++pn, st.next())
+                            if (KVF == 0 && (ok = begin_stage())) load_keys(ring + st.at * kWtPanel, pn, even_bar(kWbFull + st.at));
                     } else {
-                        if (!(ok = begin_stay())) break;
-                        for (int pn = 0; pn < kPanels; ++pn) load_keys(sbase + L::kOffStay + pn * kWtPanel, pn, even_bar(kWbStayFull));
+                        if (KVF == 1) {
+                            ++stays;  // the expansion warps'
+                        } else {
+                            if (!(ok = begin_stay())) break;
+                            if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbStayFull), 2u * kPanels * kWtPanel);
+                            for (int pn = 0; pn < kPanels; ++pn) load_keys(sbase + L::kOffStay + pn * kWtPanel, pn, even_bar(kWbStayFull));
+                        }
                         for (int i = 0; ok && i < w.row_tiles; ++i) {
                             const int row = q0 + i * kWtRows + rank * (w.columns(p, i) / 2);
-                            for (int pn = 0; ok && pn < kPanels; ++pn)
-                                if ((ok = begin_stage(st)))
-                                    ptx::tma_load_3d_pair(sbase + L::kOffRing + st * kWtPanel, &tm_q, 0, row, pn, even_bar(kWbFull + st));
+                            for (int pn = 0; ok && pn < kPanels; ++pn, st.next())
+                                if ((ok = begin_stage())) {
+                                    const uint32_t dst = ring + st.at * kWtPanel, b = even_bar(kWbFull + st.at);
+                                    ptx::tma_load_3d_pair(dst, &tm_q, 0, row, pn, b);
+                                    ptx::tma_load_3d_pair(dst + kWtPanel / 2, &tm_q, 0, row + kPage, pn, b);
+                                }
                         }
                     }
                 }
             }
             // every copy has landed and been used, and no release is still on its way to this CTA's barriers,
             // before it leaves
-            for (int y = max(loads - kWtStages, 0); ok && y < loads; ++y) ok = wait(kWbEmpty + y % kWtStages, (y / kWtStages) & 1);
             if (ok && stays > 0) ok = wait(kWbStayEmpty, (stays - 1) & 1);
+            for (int u = 0; ok && u < stages; ++u, st.next())
+                if (st.used()) ok = wait(kWbEmpty + st.at, st.last());
             if (!ok) {  // gave up: copies in flight complete on the other CTA's barriers; leave them time to land
                 const uint64_t t0 = ptx::globaltimer_ns();
                 while (ptx::globaltimer_ns() - t0 < 2000000ull) {
@@ -317,34 +409,43 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
         // ================================================================ MMA issuer
         if (rank == 0 && lane == 0) {
             const uint64_t d_stay = ptx::smem_desc_sw128(sbase + L::kOffStay, 16, 1024);
-            const uint64_t d_ring = ptx::smem_desc_sw128(sbase + L::kOffRing, 16, 1024);
+            const uint64_t d_ring = ptx::smem_desc_sw128(ring, 16, 1024);
             bool ok = true;
-            int stays = 0, loads = 0, item = 0, t = 0;
+            uint32_t full = 0u, made = 0u, stay_full = 0u, stay_made = 0u;  // parities, by stage
+            int item = 0;
+            WtStage st(stages);
+            auto wait_stay = [&](bool expanded) -> bool {
+                uint32_t& parity = expanded ? stay_made : stay_full;
+                const bool r = wait(expanded ? kWbStayMade : kWbStayFull, parity);
+                parity ^= 1u;
+                return r;
+            };
             for (bool more = any; ok && more; more = w.next(p)) {
                 const bool stream_keys = w.row_tiles == 1;
-                if (stream_keys && !(ok = wait(kWbStayFull, stays++ & 1))) break;
-                for (int k = w.k0; ok && k < w.k1; ++k, ++t) {
-                    if (!stream_keys && !(ok = wait(kWbStayFull, stays++ & 1))) break;
+                const bool expanded = KVF == 1 && stream_keys;  // what streams
+                if (stream_keys && !(ok = wait_stay(false))) break;
+                for (int k = w.k0; ok && k < w.k1; ++k) {
+                    if (!stream_keys && !(ok = wait_stay(KVF == 1))) break;
                     for (int i = 0; ok && i < w.row_tiles; ++i, ++item) {
                         const int buf = item & 1;
                         if (item >= 2 && !(ok = wait(kWbSEmpty + buf, ((item >> 1) - 1) & 1))) break;
                         const uint32_t idesc = ptx::idesc_bf16_f32(kWtKeys, w.columns(p, i), 0, 0);
                         const uint32_t d = tmem + buf * kWtRows;
-                        for (int pn = 0; pn < kPanels; ++pn, ++loads) {
-                            const int st = loads % kWtStages;
-                            if (!(ok = wait(kWbFull + st, (loads / kWtStages) & 1))) break;
+                        for (int pn = 0; pn < kPanels; ++pn, st.next()) {
+                            uint32_t& parity = expanded ? made : full;
+                            if (!(ok = wait((expanded ? kWbMade : kWbFull) + st.at, (parity >> st.at) & 1u))) break;
+                            parity ^= 1u << st.at;
                             ptx::tc_fence_after();
-                            const uint64_t stay = d_stay + ((pn * kWtPanel) >> 4), ring = d_ring + ((st * kWtPanel) >> 4);
-                            const uint64_t a = stream_keys ? ring : stay, b = stream_keys ? stay : ring;
+                            const uint64_t stay = d_stay + ((pn * stay_panel) >> 4), moving = d_ring + ((st.at * kWtPanel) >> 4);
+                            const uint64_t a = stream_keys ? moving : stay, b = stream_keys ? stay : moving;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 ptx::mma_bf16_ss_pair(d, a + ((kk * 32) >> 4), b + ((kk * 32) >> 4), idesc, (pn | kk) != 0);
-                            ptx::mma_commit_pair(bar(kWbEmpty + st));
+                            ptx::mma_commit_pair(bar(kWbEmpty + st.at));
                         }
                         if (ok) ptx::mma_commit_pair(bar(kWbSFull + buf));
                     }
                     if (ok && !stream_keys) ptx::mma_commit_pair(bar(kWbStayEmpty));
-                    if (ok && KVF == 1) ptx::mma_commit_pair(bar(kWbRowsFree + t % kWtRing));
                 }
                 if (ok && stream_keys) ptx::mma_commit_pair(bar(kWbStayEmpty));
             }
@@ -356,34 +457,67 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
     } else if (warp >= kWtExpandWarp) {
         // ================================================================ expansion of fp8 rows
         if constexpr (KVF == 1) {
-            constexpr int kRows = kWtHalf / kWtExpandWarps;  // rows per warp, half a page
-            const int row = kRows * (warp - kWtExpandWarp);
-            __nv_bfloat16* ring = p.ring + (static_cast<int64_t>(blockIdx.x) * kWtRing * kWtHalf + row) * kDQK;
-            bool ok = true;
-            int t = 0;
+            const int row = 32 * (warp - kWtExpandWarp);  // this warp's first of the CTA's 128 keys
+            bool ok = true, others = false;  // the last piece's keys stayed
+            int stays = 0;
+            WtStage st(stages);
+            auto warp_wait = [&](int i, uint32_t parity) -> bool {
+                bool okw = true;
+                if (lane == 0) okw = wait(i, parity);
+                okw = __shfl_sync(0xffffffffu, okw, 0);
+                __syncwarp();
+                return okw;
+            };
+            auto done = [&](int i) {  // what this warp wrote is there for the MMAs
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(even_bar(i));
+            };
             for (bool more = any; ok && more; more = w.next(p)) {
-                for (int k = w.k0; k < w.k1; ++k, ++t) {
-                    const int i = 4 * k + 2 * rank + row / kPage, slot = t % kWtRing;
-                    const int page = page_of(p.bp, w.b, w.s, i);
-                    const int n = page_rows(p.bp, w.s, i, page) - row % kPage;
-                    const uint8_t* src = static_cast<const uint8_t*>(p.bp.kv) + (static_cast<int64_t>(page) * kPage + row % kPage) * kFp8RowBytes;
-                    if (t >= kWtRing) {  // this slot's last tile has been multiplied
-                        if (lane == 0) ok = wait(kWbRowsFree + slot, (t / kWtRing - 1) & 1);
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
-                        if (!ok) break;
+                const bool stream_keys = w.row_tiles == 1;
+                auto source = [&](int k) -> Fp8Source {
+                    const int i = 4 * k + 2 * rank + row / kPage;
+                    return Fp8Source(p.bp, w.s, i, k < w.k1 ? page_of(p.bp, w.b, w.s, i) : -1, row % kPage);
+                };
+                // (the producer's thread says why: before the ring is these warps' again, and before the first tile of
+                // keys that stays)
+                if (stays > 1 && others != !stream_keys && !(ok = warp_wait(kWbStayEmpty, stays & 1))) break;
+                if (stays > 0 && others != !stream_keys && !(ok = warp_wait(kWbStayEmpty, (stays - 1) & 1))) break;
+                others = !stream_keys;
+                Fp8Source cur = source(w.k0);
+                WtCodes now, then;
+                now.load(cur, 0);
+                for (int k = w.k0; ok && k < w.k1; ++k) {
+                    const Fp8Source next = source(k + 1);
+                    next.prefetch(32);
+                    if (!stream_keys) {
+                        if (stays > 0 && !(ok = warp_wait(kWbStayEmpty, (stays - 1) & 1))) break;
+                        ++stays;
                     }
-                    __nv_bfloat16* dst = ring + static_cast<int64_t>(slot) * kWtHalf * kDQK;
 #pragma unroll 1
-                    for (int u = 0; u < kRows; u += 4) expand_rows4(src + u * kFp8RowBytes, n - u, dst + u * kDQK);
-                    ptx::fence_proxy_async_all();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar(kWbRowsFull + slot));
+                    for (int pair = 0; ok && pair < 5; ++pair) {  // two panels of codes, or the rotated dims
+                        then.load(pair < 4 ? cur : next, pair < 4 ? pair + 1 : 0);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if (pair == 4 && j == 1) break;
+                            if (stream_keys && st.used() && !(ok = warp_wait(kWbEmpty + st.at, st.last()))) break;
+                            const uint32_t dst = (stream_keys ? ring + st.at * kWtPanel : sbase + L::kOffStay + (2 * pair + j) * kWtPanel) + row * 128;
+                            if (pair < 4) now.store_codes(dst, j);
+                            else now.store_rope(dst);
+                            if (stream_keys) {
+                                done(kWbMade + st.at);
+                                st.next();
+                            }
+                        }
+                        now = then;
+                    }
+                    if (ok && !stream_keys) {
+                        done(kWbStayMade);
+                        for (int i = 0; i < w.row_tiles * kPanels; ++i) st.next();
+                    }
+                    cur = next;
                 }
-            }
-            // no release is still on its way to this CTA's barriers when it leaves
-            for (int y = max(t - kWtRing, 0); ok && y < t; ++y) {
-                if (lane == 0) ok = wait(kWbRowsFree + y % kWtRing, (y / kWtRing) & 1);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (stream_keys) ++stays;  // the queries, the producer's
             }
         }
     } else if (warp >= kWtFillWarp) {
@@ -425,10 +559,10 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
             return x == -CUDART_INF_F ? x : -x;
         };
         bool failed = false;
-        int item = 0, t = 0, tables = 0;
+        int item = 0, tables = 0;
         for (bool more = any; !failed && more; more = w.next(p)) {
             float mine = entry(0);
-            for (int k = w.k0; !failed && k < w.k1; ++k, ++t) {
+            for (int k = w.k0; !failed && k < w.k1; ++k) {
                 const int key = k * kWtKeys + rank * kWtHalf + 32 * quad + lane;
                 const int i_page = (k * kWtKeys + rank * kWtHalf + 32 * quad) / kPage;
                 const bool valid = (key % kPage) < page_rows(p.bp, w.s, i_page, page_of(p.bp, w.b, w.s, i_page));
@@ -452,7 +586,18 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                     if (!failed && !warp_wait(kWbSFull + buf, (item >> 1) & 1)) failed = true;
                     if (failed) continue;
                     ptx::tc_fence_after();
-                    for (int c = 0; c < limit; c += 16) {
+                    // in tiles with drafted rows, word e of lane l: which of the warp's 32 keys column 32 e + l sees
+                    uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                    if (tail) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int row = i * kWtRows + c_first + 32 * e + lane;
+                            if (32 * e + lane < limit) seen[e] = seen_bits(p.bp, w.s, row / p.bp.h, key - lane);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < kWtRows / 2; c += 16) {
+                        if (c >= limit) break;
                         uint32_t sv[16];
                         SMLA_TMEM_LD16(tmem + lane_base + buf * kWtRows + c_first + c, sv);
                         float4 nl[4];
@@ -477,19 +622,9 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                                 if (c + e >= limit) pr[e] = 0.f;
                         }
                         if (tail) {
-                            int row = i * kWtRows + c_first + c, token = row / p.bp.h;
-                            row -= token * p.bp.h;
-#pragma unroll 1
-                            for (int e = 0; e < 16; ++e) {
-                                const bool sees = (seen_bits(p.bp, w.s, min(token, w.s.n - 1), key) & 1u) != 0u;
 #pragma unroll
-                                for (int u = 0; u < 16; ++u)
-                                    if (u == e && !sees) pr[u] = 0.f;
-                                if (++row == p.bp.h) {
-                                    row = 0;
-                                    ++token;
-                                }
-                            }
+                            for (int e = 0; e < 16; ++e)
+                                if (!((__shfl_sync(0xffffffffu, seen[c / 32], c % 32 + e) >> lane) & 1u)) pr[e] = 0.f;
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) acc[e & 1] = ptx::add2(acc[e & 1], make_float2(pr[2 * e], pr[2 * e + 1]));
@@ -499,9 +634,11 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                     if (lane == 0) ptx::mbar_arrive_cluster(buf ? s_empty1 : s_empty0);
                 }
                 const float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                if (half == 1) sX[(t & 1) * kWtHalf + 32 * quad + lane] = sum;
+                if (half == 1) sX[32 * quad + lane] = sum;
                 failed = ptx::named_bar_red_or(1u, 32u * kWtSumWarps, failed);
-                if (!failed && half == 0 && key < w.s.keys) *dst = before + (valid ? sum + sX[(t & 1) * kWtHalf + 32 * quad + lane] : 0.f);
+                const float other = sX[32 * quad + lane];
+                if (w.row_tiles == 1) ptx::named_bar_sync(1u, 32u * kWtSumWarps);  // (else the next table's barrier comes before the next sum)
+                if (!failed && half == 0 && key < w.s.keys) *dst = before + (valid ? sum + other : 0.f);
             }
         }
     }
