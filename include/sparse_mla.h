@@ -433,11 +433,10 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
  *                 past its 32 * mask_words bits are seen by none
  *   out           device, [T, h, 512] bf16, caller-owned, 16-byte aligned
  *   lse           device, [T, h] fp32, caller-owned
- *   workspace     device, at least sparse_mla_tree_workspace_bytes(T, h, seqs,
- *                 kv_format) bytes, 256-byte aligned, caller-owned: partial results
- *                 of row tiles that several CTAs share, and fp8 rows as bf16 on
- *                 their way.  Calls that may overlap in time need workspaces of
- *                 their own, and so do captured ones that may
+ *   workspace     device, at least sparse_mla_tree_workspace_bytes(T, h, seqs)
+ *                 bytes, 256-byte aligned, caller-owned: partial results of row
+ *                 tiles that several CTAs share.  Calls that may overlap in time
+ *                 need workspaces of their own, and so do captured ones that may
  * out, lse and workspace must overlap neither each other nor the inputs.  What rows
  * past a sequence's end hold does not matter, nor what drafted rows hold that a
  * token does not see, infinities and NaN included.  (Of a drafted row with infinities a
@@ -450,7 +449,7 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
  * misalignment; SMLA_ERR_CUDA if a tensor map or a launch fails; a bounded wait that
  * ran out is reported by sparse_mla_sync_status().
  */
-size_t sparse_mla_tree_workspace_bytes(int32_t T, int32_t h, int32_t seqs, int32_t kv_format);
+size_t sparse_mla_tree_workspace_bytes(int32_t T, int32_t h, int32_t seqs);
 smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths,
                             const int32_t* starts, const uint32_t* mask, int32_t T, int32_t h, int32_t seqs, int32_t blocks,
                             int32_t mask_words, int64_t num_slots, int32_t kv_format, float scale, void* out, float* lse,

@@ -27,7 +27,7 @@ def _run(batch, scale=SCALE, **kw):
     T, h = batch.T, batch.h
     guard_o = torch.full((T + 2, h, 512), 2.5, dtype=torch.bfloat16, device=DEV)
     guard_l = torch.full((T + 2, h), 2.5, dtype=torch.float32, device=DEV)
-    need = smla.tree_workspace_bytes(T, h, len(batch.seqs), batch.fmt)
+    need = smla.tree_workspace_bytes(T, h, len(batch.seqs))
     ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN where nothing is written
     out, lse = smla.sparse_mla_tree(**batch.to(DEV), scale=scale, out=guard_o[1:T + 1], lse=guard_l[1:T + 1], kv_format=batch.fmt,
                                     workspace=ws, **kw)
@@ -297,7 +297,7 @@ def test_no_work_is_a_noop(lib, kw):
 
 def test_workspace_bytes(lib):
     """Two slots of a tile's rows in groups of 32 for each of 76 CTA pairs (152 SMs assumed without a device), 16
-    bytes for each tile or pair; with fp8 the rings of three blocks of 128 bf16 rows."""
+    bytes for each tile or pair."""
     def up(x):
         return -(-x // 256) * 256
 
@@ -305,9 +305,7 @@ def test_workspace_bytes(lib):
     assert smla.tree_workspace_bytes(1, 8, 1) == up(152 * 32 * 514 * 4) + 256
     assert smla.tree_workspace_bytes(512, 8, 32) == up(152 * 128 * 514 * 4) + up(64 * 16)
     assert smla.tree_workspace_bytes(512, 64, 8) == up(152 * 128 * 514 * 4) + up(76 * 16)
-    assert smla.tree_workspace_bytes(5, 16, 1, "fp8") == up(152 * 96 * 514 * 4) + 256 + 76 * 3 * 128 * 1152
-    with pytest.raises(ValueError, match="kv_format"):
-        smla.tree_workspace_bytes(1, 8, 1, "int8")
+    assert smla.tree_workspace_bytes(5, 16, 1) == up(152 * 96 * 514 * 4) + 256
 
 
 def _args():

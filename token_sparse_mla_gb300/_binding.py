@@ -81,7 +81,7 @@ def library() -> ctypes.CDLL:
     lib.sparse_mla_prefix.restype = ctypes.c_int
     lib.sparse_mla_prefix.argtypes = [vp, vp, vp, i32, i32, i64, i64, i32, f32, vp, vp, vp, sz, vp]
     lib.sparse_mla_tree_workspace_bytes.restype = sz
-    lib.sparse_mla_tree_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.sparse_mla_tree_workspace_bytes.argtypes = [i32, i32, i32]
     lib.sparse_mla_tree.restype = ctypes.c_int
     lib.sparse_mla_tree.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i64, i32, f32, vp, vp, vp, sz, vp]
     lib.sparse_mla_weights.restype = ctypes.c_int
@@ -611,16 +611,14 @@ def sparse_mla_prefix(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
 # ---- a batch of sequences, each over its own rows
 
 @functools.lru_cache(maxsize=1024)
-def _tree_workspace_bytes(device_index: int, T: int, h: int, seqs: int, fmt: int) -> int:
+def _tree_workspace_bytes(device_index: int, T: int, h: int, seqs: int) -> int:
     """The library's answer for the device that is current, asked once per shape and device."""
-    return int(library().sparse_mla_tree_workspace_bytes(T, h, seqs, fmt))
+    return int(library().sparse_mla_tree_workspace_bytes(T, h, seqs))
 
 
-def tree_workspace_bytes(T: int, h: int, seqs: int, kv_format: str = "bf16") -> int:
+def tree_workspace_bytes(T: int, h: int, seqs: int) -> int:
     """Bytes of workspace that sparse_mla_tree needs on the current device."""
-    if kv_format not in KV_FORMATS:
-        raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
-    return int(library().sparse_mla_tree_workspace_bytes(T, h, seqs, KV_FORMATS[kv_format]))
+    return int(library().sparse_mla_tree_workspace_bytes(T, h, seqs))
 
 
 def _batch(dev: torch.device, block_tables: torch.Tensor, lengths: torch.Tensor) -> Tuple[int, int]:
@@ -664,9 +662,9 @@ def sparse_mla_tree(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch
     drafted token j of its sequence; None: chains, each token sees those up to itself.
 
     Returns out [T, h, 512] bf16 and lse [T, h] fp32; tokens of no sequence are left as they are.
-    scale defaults to 576 ** -0.5.  workspace: a uint8 tensor of tree_workspace_bytes(T, h, seqs,
-    kv_format) bytes for callers that keep one (calls that may overlap need their own); allocated here
-    otherwise, from torch's allocator on the stream of the call, as out and lse are.
+    scale defaults to 576 ** -0.5.  workspace: a uint8 tensor of tree_workspace_bytes(T, h, seqs) bytes
+    for callers that keep one (calls that may overlap need their own); allocated here otherwise, from
+    torch's allocator on the stream of the call, as out and lse are.
     """
     if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != _BF16 or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous [T, h, 576] bf16 tensor, got {tuple(q.shape)} {q.dtype}")
@@ -693,12 +691,11 @@ def sparse_mla_tree(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch
             raise ValueError("lse must be a contiguous [T, h] fp32 tensor")
         if lse.device != dev:
             _apart(dev, lse=lse)
-    fmt = KV_FORMATS[kv_format]
-    workspace = _workspace(dev, stream, workspace, _tree_workspace_bytes, T, h, seqs, fmt)
+    workspace = _workspace(dev, stream, workspace, _tree_workspace_bytes, T, h, seqs)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _call(dev, stream, library().sparse_mla_tree, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
-          lengths.data_ptr(), starts.data_ptr(), mask_ptr, T, h, seqs, blocks, words, num_slots, fmt, float(scale),
-          out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
+          lengths.data_ptr(), starts.data_ptr(), mask_ptr, T, h, seqs, blocks, words, num_slots, KV_FORMATS[kv_format],
+          float(scale), out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
     return out, lse
 
 

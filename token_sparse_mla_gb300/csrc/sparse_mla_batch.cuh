@@ -73,66 +73,47 @@ __device__ __forceinline__ uint32_t seen_bits(const BatchParams& p, const Seq& s
 // The first `n` of 32 bits (n may lie outside 0 .. 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
-// Sums over the CTA's threads (at most 32 warps): of the threads before this one, and of all.  `scratch`
-// holds 32 values, written only before the barrier and read only after it.
-__device__ __forceinline__ void block_prefix(int64_t x, int64_t* scratch, int warps, int64_t& before, int64_t& total) {
+// Sums of two values over the CTA's threads (at most 16 warps): of the threads before this one, and of all.
+// `scratch` holds 32 values, written only before the barrier and read only after it.
+__device__ __forceinline__ void block_prefix2(int64_t x, int64_t y, int64_t* scratch, int warps, int64_t& x_before, int64_t& x_all,
+                                              int64_t& y_before, int64_t& y_all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl = x;
+    int64_t xi = x, yi = y;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const int64_t xo = __shfl_up_sync(0xffffffffu, xi, o), yo = __shfl_up_sync(0xffffffffu, yi, o);
+        if (lane >= o) {
+            xi += xo;
+            yi += yo;
+        }
     }
-    if (lane == 31) scratch[warp] = incl;
+    if (lane == 31) {
+        scratch[2 * warp] = xi;
+        scratch[2 * warp + 1] = yi;
+    }
     __syncthreads();
-    before = incl - x;
-    total = 0;
+    x_before = xi - x;
+    y_before = yi - y;
+    x_all = y_all = 0;
+#pragma unroll 4
     for (int w = 0; w < warps; ++w) {
-        const int64_t v = scratch[w];
-        if (w < warp) before += v;
-        total += v;
+        const longlong2 v = *reinterpret_cast<const longlong2*>(scratch + 2 * w);
+        if (w < warp) {
+            x_before += v.x;
+            y_before += v.y;
+        }
+        x_all += v.x;
+        y_all += v.y;
     }
 }
 
-// Four fp8 rows on their way to bf16 rows of 1152 bytes: the loads, and, later, codes x scale in fp32 rounded to
-// bf16 as in the forward, and the stores.  `n` of the four take part (0 .. 4), the others become zeros.
-struct Fp8Rows4 {
-    // lane l: codes [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8), so that both stores are 512 contiguous bytes
-    uint2 a[4], b[4];
-    float sa[4], sb[4];
-    uint32_t rope[4];
-    __device__ __forceinline__ void load(const uint8_t* src, int n) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            a[u] = b[u] = make_uint2(0u, 0u);
-            sa[u] = sb[u] = 0.f;
-            rope[u] = 0u;
-            if (u < n) {
-                const uint8_t* row = src + u * kFp8RowBytes;
-                a[u] = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-                b[u] = __ldg(reinterpret_cast<const uint2*>(row) + 32 + lane);
-                sa[u] = __ldg(reinterpret_cast<const float*>(row + 512) + (lane >> 4));
-                sb[u] = __ldg(reinterpret_cast<const float*>(row + 520) + (lane >> 4));
-                rope[u] = __ldg(reinterpret_cast<const uint32_t*>(row + 528) + lane);
-            }
-        }
-    }
-    __device__ __forceinline__ void store(__nv_bfloat16* dst) const {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            uint4* out = reinterpret_cast<uint4*>(dst + u * kDQK);
-            out[lane] = make_uint4(ptx::e4m3x2_scaled_bf16x2(a[u].x & 0xFFFFu, sa[u]), ptx::e4m3x2_scaled_bf16x2(a[u].x >> 16, sa[u]),
-                                   ptx::e4m3x2_scaled_bf16x2(a[u].y & 0xFFFFu, sa[u]), ptx::e4m3x2_scaled_bf16x2(a[u].y >> 16, sa[u]));
-            out[32 + lane] = make_uint4(ptx::e4m3x2_scaled_bf16x2(b[u].x & 0xFFFFu, sb[u]), ptx::e4m3x2_scaled_bf16x2(b[u].x >> 16, sb[u]),
-                                        ptx::e4m3x2_scaled_bf16x2(b[u].y & 0xFFFFu, sb[u]), ptx::e4m3x2_scaled_bf16x2(b[u].y >> 16, sb[u]));
-            reinterpret_cast<uint32_t*>(out + 64)[lane] = rope[u];
-        }
-    }
-};
+// x * k / n, in 32 bits where they do (k <= n < 2^16)
+__device__ __forceinline__ int64_t share_of(int64_t x, int k, int n) {
+    if (x < (1 << 16)) return static_cast<uint32_t>(x) * static_cast<uint32_t>(k) / static_cast<uint32_t>(n);
+    return x * k / n;
+}
 
-// A warp's `rows` consecutive rows of page i of a sequence, from `row` on, and how many of them take part.
+// A warp's fp8 rows of page i of a sequence, from `row` of the page on, and how many of them take part.
 struct Fp8Source {
     const uint8_t* src;
     int n;
@@ -141,7 +122,6 @@ struct Fp8Source {
     __device__ __forceinline__ void prefetch(int rows) const {  // into L2
         if (n > 0 && (threadIdx.x & 31) == 0) ptx::bulk_prefetch_l2(src, static_cast<uint32_t>(min(n, rows) * kFp8RowBytes));
     }
-    __device__ __forceinline__ void load(Fp8Rows4& r, int u) const { r.load(src + u * kFp8RowBytes, n - u); }
 };
 
 }  // namespace smla

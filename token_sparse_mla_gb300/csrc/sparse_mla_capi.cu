@@ -542,15 +542,24 @@ CUresult row_map(EncodeTiledFn enc, CUtensorMap* tm, const void* base, int64_t n
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// sparse_mla_tree's workspace: partials of cut tiles (two slots per CTA pair), the notes for their join, and
-// the ring of expanded rows of an fp8 cache.
+// Rows of 656 bytes, boxes of `box_bytes` of `box_rows` of them.
+CUresult byte_map(EncodeTiledFn enc, CUtensorMap* tm, const void* base, int64_t n, uint32_t box_bytes, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[2] = {smla::kFp8RowBytes, static_cast<cuuint64_t>(n)};
+    const cuuint64_t strides[1] = {smla::kFp8RowBytes};
+    const cuuint32_t box[2] = {box_bytes, box_rows};
+    const cuuint32_t es[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// sparse_mla_tree's workspace: partials of cut tiles (two slots per CTA pair) and the notes for their join.
 struct TreePlan {
     int pairs = 0, slot_groups = 0, jobs = 0;
     bool by_tile = false;
-    size_t off_ml = 0, off_jobs = 0, off_ring = 0, bytes = 0;
+    size_t off_ml = 0, off_jobs = 0, bytes = 0;
 };
 
-TreePlan tree_plan(int64_t rows, int64_t seqs, bool fp8, int num_sms) {
+TreePlan tree_plan(int64_t rows, int64_t seqs, int num_sms) {
     TreePlan pl;
     pl.pairs = num_sms / 2;
     pl.slot_groups = static_cast<int>(((rows < smla::kPfRows ? rows : smla::kPfRows) + 31) / 32);
@@ -560,8 +569,7 @@ TreePlan tree_plan(int64_t rows, int64_t seqs, bool fp8, int num_sms) {
     const size_t slots = static_cast<size_t>(pl.pairs) * 2 * pl.slot_groups * 32;  // rows in all slots
     pl.off_ml = slots * smla::kDV * 4;
     pl.off_jobs = align256(pl.off_ml + slots * 2 * 4);
-    pl.off_ring = align256(pl.off_jobs + static_cast<size_t>(pl.jobs) * sizeof(int4));
-    pl.bytes = pl.off_ring + (fp8 ? static_cast<size_t>(pl.pairs) * smla::kTrRing * smla::kTrBlockRows * smla::kDQK * 2 : 0);
+    pl.bytes = align256(pl.off_jobs + static_cast<size_t>(pl.jobs) * sizeof(int4));
     return pl;
 }
 
@@ -1299,13 +1307,13 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
 }
 
 
-size_t sparse_mla_tree_workspace_bytes(int32_t T, int32_t h, int32_t seqs, int32_t kv_format) {
+size_t sparse_mla_tree_workspace_bytes(int32_t T, int32_t h, int32_t seqs) {
     if (T <= 0 || h <= 0 || seqs <= 0) return 0;
     int num_sms = 152;
     int dev = 0;
     DeviceState* ds = nullptr;
     if (device_state(&dev, &ds) == SMLA_OK) num_sms = ds->num_sms;
-    return tree_plan(static_cast<int64_t>(T) * h, seqs, kv_format == SMLA_KV_FP8, num_sms).bytes;
+    return tree_plan(static_cast<int64_t>(T) * h, seqs, num_sms).bytes;
 }
 
 smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* block_tables, const int32_t* lengths,
@@ -1322,25 +1330,25 @@ smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* 
     if ((st = device_state(&dev, &ds)) != SMLA_OK) return st;
     const bool fp8 = kv_format == SMLA_KV_FP8;
     const int64_t rows = static_cast<int64_t>(T) * h;
-    const TreePlan pl = tree_plan(rows, seqs, fp8, ds->num_sms);
+    const TreePlan pl = tree_plan(rows, seqs, ds->num_sms);
     if (!workspace || !aligned(workspace, 256)) return fail(SMLA_ERR_INVALID_ARG, "workspace must be given, 256-byte aligned");
     if (workspace_bytes < pl.bytes)
         return fail(SMLA_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", workspace_bytes, pl.bytes);
     EncodeTiledFn enc = nullptr;
     if ((st = encode_fn(&enc)) != SMLA_OK) return st;
     char* ws = static_cast<char*>(workspace);
-    const void* rows_at = fp8 ? ws + pl.off_ring : kv_cache;
-    const int64_t num_rows = fp8 ? static_cast<int64_t>(pl.pairs) * smla::kTrRing * smla::kTrBlockRows : num_slots;
     alignas(64) CUtensorMap tm_q;
     alignas(64) CUtensorMap tm_k;
     alignas(64) CUtensorMap tm_v;
     CUresult r = row_map(enc, &tm_q, q, rows, smla::kPfHalf, smla::kPanels);
-    if (r == CUDA_SUCCESS) r = row_map(enc, &tm_k, rows_at, num_rows, smla::kPfPage, smla::kPfGroupA);
-    if (r == CUDA_SUCCESS) r = row_map(enc, &tm_v, rows_at, num_rows, smla::kPfPage, smla::kPfGroupB);
+    // (by the cache's maps an fp8 cache has its rotated dims loaded, and nothing by the third)
+    if (r == CUDA_SUCCESS)
+        r = fp8 ? byte_map(enc, &tm_k, kv_cache, num_slots, 128, smla::kPfPage, CU_TENSOR_MAP_SWIZZLE_128B)
+                : row_map(enc, &tm_k, kv_cache, num_slots, smla::kPfPage, smla::kPfGroupA);
+    if (r == CUDA_SUCCESS) r = row_map(enc, &tm_v, fp8 ? q : kv_cache, fp8 ? rows : num_slots, smla::kPfPage, smla::kPfGroupB);
     if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/kv_cache failed (%d)", (int)r);
     smla::TrParams tp = {};
     tp.bp = batch_params(kv_cache, block_tables, lengths, starts, mask, T, h, seqs, blocks, mask_words, num_slots);
-    tp.ring = fp8 ? reinterpret_cast<__nv_bfloat16*>(ws + pl.off_ring) : nullptr;
     tp.out = static_cast<__nv_bfloat16*>(out);
     tp.lse = lse;
     tp.part_o = reinterpret_cast<float*>(ws);
@@ -1408,8 +1416,12 @@ smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_
     alignas(64) CUtensorMap tm_k;
     // (without tokens nothing is loaded by q's map)
     CUresult r = T > 0 ? row_map(enc, &tm_q, q, rows, smla::kPage, 1) : row_map(enc, &tm_q, kv_cache, 1, smla::kPage, 1);
-    // (nor anything by the cache's, if its rows are fp8)
-    if (r == CUDA_SUCCESS) r = row_map(enc, &tm_k, kv_cache, fp8 ? 1 : num_slots, smla::kPage, 1);
+    // (by the cache's map an fp8 cache has its rotated dims loaded)
+    if (r == CUDA_SUCCESS)
+        r = fp8 ? byte_map(enc, &tm_k, kv_cache, num_slots, 128, smla::kPage, CU_TENSOR_MAP_SWIZZLE_128B)
+                : row_map(enc, &tm_k, kv_cache, num_slots, smla::kPage, 1);
+    alignas(64) CUtensorMap tm_codes = tm_k;
+    if (r == CUDA_SUCCESS && fp8) r = byte_map(enc, &tm_codes, kv_cache, num_slots, 64, smla::kPage, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/kv_cache failed (%d)", (int)r);
     smla::WtParams wp = {};
     wp.bp = batch_params(kv_cache, block_tables, lengths, starts, mask, T, h, seqs, blocks, mask_words, num_slots);
@@ -1433,8 +1445,8 @@ smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(fp8 ? smla::weights_threads<1>() : smla::weights_threads<0>()), 1, 1);
     cfg.dynamicSmemBytes = smla::WtLayout::kBytes;
-    const cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_weights_kernel<1>, tm_q, tm_k, wp)
-                              : cudaLaunchKernelEx(&cfg, smla::sparse_mla_weights_kernel<0>, tm_q, tm_k, wp);
+    const cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_weights_kernel<1>, tm_q, tm_k, tm_codes, wp)
+                              : cudaLaunchKernelEx(&cfg, smla::sparse_mla_weights_kernel<0>, tm_q, tm_k, tm_codes, wp);
     if (e != cudaSuccess) return cuda_fail(e, "weights kernel launch");
     return SMLA_OK;
 }

@@ -25,10 +25,11 @@
 // past the end zeroed, values that are not finite in the drafted rows zeroed: a token that does see such a
 // row has its NaN from S).
 //
-// fp8.  Four more warps expand the rows ahead of the loads, each CTA one page of a block, into a ring of
-// kTrRing blocks per pair in global memory (33 MB in all, which stays in L2), and the loads take them from
-// there: shared memory has no room for a tile of codes, and the pages of a large batch expanded ahead of
-// the kernel would be three times the traffic.
+// fp8.  Shared memory has no room for a block's codes, so four more warps take them through registers: a warp has
+// 16 rows of its CTA's page, the next block's in flight as soon as this one's are written.  V is a copy of K: panels 0 .. 3 of a page are the even CTA's V tile of it, panels
+// 4 .. 7 the odd one's, in the same layout, so the TMA thread copies them there as they are, half of them
+// into the other CTA's shared memory.  (Expanded into a ring in global memory and loaded from there, a block
+// took 5.0 us: 11 TB/s of traffic through L2.)
 //
 // Roles (384 threads, 512 with fp8):
 //   warps 0-7    softmax, rescaling and output: TMEM quadrant warp % 4, keys 32 (warp / 4) .. of a page
@@ -47,13 +48,8 @@ namespace smla {
 constexpr int kTrSoftmaxWarps = 8;
 constexpr int kTrTmaWarp = 8, kTrS1Warp = 9, kTrPvWarp = 10, kTrS2Warp = 11, kTrExpandWarp = 12;
 constexpr int kTrExpandWarps = 4;
-constexpr int kTrRing = 3;       // blocks of expanded rows per pair
+constexpr int kTrExpandRows = kPage / kTrExpandWarps;
 constexpr int kTrTileCost = 3;   // what a piece costs beside its blocks, in blocks
-constexpr int kTrBlockRows = kPfKeys;
-#ifndef TR_AHEAD
-#define TR_AHEAD 1
-#endif
-constexpr int kTrAhead = TR_AHEAD;
 
 template <int KVF>
 __host__ __device__ constexpr int tree_threads() {
@@ -62,11 +58,12 @@ __host__ __device__ constexpr int tree_threads() {
 
 // Barriers of the prefix kernel, then:
 enum : int {
-    kTbTail = kPbTail,                // +page of the block, own CTA: V of a page that has to be cleaned
-    kTbDrain = kTbTail + 2,           // even CTA
-    kTbRingFull = kTbDrain + 1,       // +slot, both: the block's rows are expanded, by both CTAs
-    kTbRingFree = kTbRingFull + kTrRing,  // +slot, both: the block has been multiplied
-    kTbCount = kTbRingFree + kTrRing
+    kTbTail = kPbTail,           // +page of the block, own CTA: V of a page that has to be cleaned; fp8: of every page
+    kTbDrain = kTbTail + 2,      // even CTA
+    kTbMade = kTbDrain + 1,      // fp8, even CTA: both CTAs' K is expanded, and its rotated dims landed
+    kTbRows = kTbMade + 1,       // fp8, own CTA: this CTA's K is expanded
+    kTbCopied = kTbRows + 1,     // fp8, own CTA: both copies of this CTA's K have landed
+    kTbCount = kTbCopied + 1
 };
 
 struct TrLayout {
@@ -88,7 +85,6 @@ struct TrStart {
 
 struct TrParams {
     BatchParams bp;
-    __nv_bfloat16* ring;         // fp8: [pairs][kTrRing][128][576]
     __nv_bfloat16* out;          // [T, h, 512]
     float* lse;                  // [T, h]
     float* part_o;               // partials as in the prefix kernel, two slots per pair
@@ -115,10 +111,9 @@ __device__ __forceinline__ void tree_plan(const TrParams& p, int run, int thread
         cost += static_cast<int64_t>(t) * (tree_blocks(s) + kTrTileCost);
     }
     int64_t at, total, first_tile, all_tiles;
-    block_prefix(cost, scratch, threads / 32, at, total);
-    block_prefix(tiles, scratch + 32, threads / 32, first_tile, all_tiles);
-    const int64_t runs = min(total, static_cast<int64_t>(p.pairs));
-    const int64_t from = run < runs ? total * run / runs : total, to = run < runs ? total * (run + 1) / runs : total;
+    block_prefix2(cost, tiles, scratch, threads / 32, at, total, first_tile, all_tiles);
+    const int runs = static_cast<int>(min(total, static_cast<int64_t>(p.pairs)));
+    const int64_t from = run < runs ? share_of(total, run, runs) : total, to = run < runs ? share_of(total, run + 1, runs) : total;
     if (from >= total) {
         if (threadIdx.x == 0) *start = TrStart{total, total, total, total, p.bp.B, 0, 0, static_cast<int32_t>(all_tiles)};
     } else if (at <= from && from < at + cost) {
@@ -128,7 +123,7 @@ __device__ __forceinline__ void tree_plan(const TrParams& p, int run, int thread
             const int t = tree_tiles(p, s);
             const int64_t c = tree_blocks(s) + kTrTileCost;
             if (from < at + t * c) {
-                const int64_t i = (from - at) / c;
+                const int64_t i = from - at < (1 << 30) ? static_cast<int32_t>(from - at) / static_cast<int32_t>(c) : (from - at) / c;
                 *start = TrStart{from, to, at + i * c, total, b, static_cast<int32_t>(i), static_cast<int32_t>(first_tile + i),
                                  static_cast<int32_t>(all_tiles)};
                 break;
@@ -186,6 +181,46 @@ struct TrWalk {
 // Whether page i holds positions that V has to be cleaned of: drafted rows, or the end.
 __device__ __forceinline__ bool tree_tail(const Seq& s, int i) { return (i + 1) * kPage > s.len && i * kPage < s.keys; }
 
+// Eight rows of an fp8 page on their way to the K tile: lane l has codes [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8) of
+// every row.  (The rotated dims come by TMA.)
+struct TrCodes {
+    uint2 a[8], b[8];
+    __device__ __forceinline__ void load(const Fp8Source& from, int u0) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            a[u] = b[u] = make_uint2(0u, 0u);
+            if (u0 + u < from.n) {
+                const uint8_t* row = from.src + (u0 + u) * kFp8RowBytes;
+                a[u] = ptx::ld_nc_l1_v2(row + 8 * lane);
+                b[u] = ptx::ld_nc_l1_v2(row + 256 + 8 * lane);
+            }
+        }
+    }
+    // lane l: of row l % 16 the scales of codes [128 (l / 16), ..) and [256 + 128 (l / 16), ..)
+    __device__ __forceinline__ static float2 scales(const Fp8Source& from) {
+        static_assert(kTrExpandRows == 16, "a warp's rows and halves are its lanes");
+        const int lane = threadIdx.x & 31;
+        if ((lane & 15) >= from.n) return make_float2(0.f, 0.f);
+        const float* s = reinterpret_cast<const float*>(from.src + (lane & 15) * kFp8RowBytes + 512) + (lane >> 4);
+        return make_float2(__ldg(s), __ldg(s + 2));
+    }
+    // rows u0 .. u0 + 7 of the warp's, to eight rows of the K tile from `to` on: codes x scale in fp32 rounded to
+    // bf16 as in the forward; chunk c of a panel's row r lies at 16 (c ^ r % 8), so each store is conflict-free
+    __device__ __forceinline__ void store(int u0, uint32_t to, const float2& sc) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const float sa = __shfl_sync(0xffffffffu, sc.x, (lane & 16) + u0 + u), sb = __shfl_sync(0xffffffffu, sc.y, (lane & 16) + u0 + u);
+            const uint32_t at = to + (lane >> 3) * kPfPanel + u * 128 + (((lane & 7) ^ u) << 4);
+            ptx::st_shared_v4(at, make_uint4(ptx::e4m3x2_scaled_bf16x2(a[u].x & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a[u].x >> 16, sa),
+                                             ptx::e4m3x2_scaled_bf16x2(a[u].y & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a[u].y >> 16, sa)));
+            ptx::st_shared_v4(at + 4 * kPfPanel, make_uint4(ptx::e4m3x2_scaled_bf16x2(b[u].x & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b[u].x >> 16, sb),
+                                                            ptx::e4m3x2_scaled_bf16x2(b[u].y & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b[u].y >> 16, sb)));
+        }
+    }
+};
+
 template <int KVF>
 __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
     sparse_mla_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -216,9 +251,8 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             const bool by_warps = i == kPbSEmpty || i == kPbSEmpty + 1;                // both CTAs' softmax warps
             const bool by_half = i == kPbPFull || i == kPbPFull + 1;                   // those of the page
             const bool by_two = i == kPbQEmpty || i == kPbSFull || i == kPbSFull + 1;  // both S issuers
-            const bool by_expand = i >= kTbRingFull && i < kTbRingFull + kTrRing;      // both CTAs' expansion warps
-            ptx::mbar_init(bar(i), by_warps ? 2 * kTrSoftmaxWarps : by_half ? kTrSoftmaxWarps : by_expand ? 2 * kTrExpandWarps
-                                   : i == kTbDrain ? 3 : by_two ? 2 : 1);
+            ptx::mbar_init(bar(i), by_warps ? 2 * kTrSoftmaxWarps : by_half ? kTrSoftmaxWarps : i == kTbMade ? 2 * kTrExpandWarps + 1
+                                   : i == kTbRows ? kTrExpandWarps : i == kTbDrain ? 3 : by_two || i == kTbCopied ? 2 : 1);
         }
         ptx::fence_mbarrier_init();
     }
@@ -231,26 +265,31 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
         ptx::prefetch_tmap(&tm_k);
         ptx::prefetch_tmap(&tm_v);
     }
+    ptx::tc_fence_before();
+    __syncwarp();           // the cluster barrier wants its warps whole
+    ptx::cluster_arrive();  // both CTAs' barriers are initialised before anyone signals them
     // launched as a programmatic dependent: nothing above touched global memory
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     tree_plan(p, run, kThreads, reinterpret_cast<int64_t*>(smem + L::kOffX), start);
-    TrWalk w(p, *start);
-    const bool any = w.next(p);
-    ptx::tc_fence_before();
-    __syncwarp();         // the cluster barrier wants its warps whole
-    ptx::cluster_sync();  // both CTAs' barriers are initialised before anyone signals them
+    __syncwarp();
+    ptx::cluster_wait();
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
 
+    // fp8: 512 threads are launched with 128 registers each; the warps that issue give some of theirs to those that
+    // compute (2 * 136 + 104 + 136 = 4 * 128 for the four warpgroups)
+    if (warp >= kTrSoftmaxWarps && warp < kTrExpandWarp) {
+    if constexpr (KVF == 1) ptx::regs_down<104>();
     if (warp == kTrTmaWarp) {
         // ================================================================ TMA producer
+        TrWalk w(p, *start);
+            const bool any = w.next(p);
         // As in the prefix kernel: the even CTA's thread expects both CTAs' bytes on its barrier, K runs a
         // block ahead of V, pages are brought into L2 a block ahead.
         if (p.by_tile && run == 0 && rank == 0)
             for (int i = start->tiles + lane; i < p.jobs; i += 32) p.job_list[i] = make_int4(0, 0, 0, 0);
         if (lane == 0) {
-            const int ring0 = run * kTrRing * kTrBlockRows;  // first row of this pair's ring
             int4 job = make_int4(0, 0, 0, 0);
             auto load_v = [&](int x, bool tail0, bool tail1, int row0, int row1) -> bool {
 #pragma unroll
@@ -264,6 +303,24 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                         if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbVFull + i), 2u * kPfVPage);
                         ptx::tma_load_3d_pair(dst, &tm_v, 0, i ? row1 : row0, 4 * rank, even_bar(kPbVFull + i));
                     }
+                }
+                return true;
+            };
+            // fp8: this CTA's page of block x, once expanded, from K to both CTAs' V; then word to the CTAs whose
+            // copies have landed here
+            auto copy_v = [&](int x) -> bool {
+                if (!wait(kTbRows, x & 1)) return false;
+                if (x > 0 && !wait(kPbVEmpty + rank, (x - 1) & 1)) return false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) ptx::mbar_arrive_expect_tx(bar(kTbTail + i), static_cast<uint32_t>(kPfVPage));
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    ptx::bulk_copy_cluster(ptx::map_shared_rank(sbase + L::kOffV + rank * kPfVPage, c), sbase + L::kOffK + 4 * c * kPfPanel,
+                                           static_cast<uint32_t>(kPfVPage), ptx::map_shared_rank(bar(kTbTail + rank), c));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!wait(kTbTail + i, x & 1)) return false;
+                    ptx::mbar_arrive_cluster(ptx::map_shared_rank(bar(kTbCopied), i));
                 }
                 return true;
             };
@@ -298,24 +355,19 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                 ptx::tma_load_3d_pair(sbase + L::kOffQ, &tm_q, 0,
                                       static_cast<int>(static_cast<int64_t>(w.s.first) * p.bp.h + w.row0() + rank * kPfHalf), 0,
                                       even_bar(kPbQFull));
-                int pg0 = -1, pg1 = -1;
-                if constexpr (KVF == 0) {
-                    pg0 = page_of(p.bp, w.b, w.s, 2 * w.b0);
-                    pg1 = page_of(p.bp, w.b, w.s, 2 * w.b0 + 1);
-                }
-                for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
-                    int row0, row1;
-                    if constexpr (KVF == 0) {
-                        row0 = first_row(pg0);
-                        row1 = first_row(pg1);
-                    } else {
-                        const int slot = x % kTrRing;
-                        row0 = ring0 + slot * kTrBlockRows;
-                        row1 = row0 + kPage;
-                        if (!(ok = wait(kTbRingFull + slot, (x / kTrRing) & 1))) break;
-                        ptx::fence_acq_rel_cluster();
-                        ptx::fence_proxy_async_all();
+                if constexpr (KVF == 1) {
+                    for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
+                        if (x > 0 && !(ok = wait(kPbKEmpty + 1, (x - 1) & 1))) break;
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kTbMade), 2u * kPfPanel);
+                        ptx::tma_load_2d_pair(sbase + L::kOffK + 8 * kPfPanel, &tm_k, 528, first_row(page_of(p.bp, w.b, w.s, 2 * b + rank)),
+                                              even_bar(kTbMade));
+                        ok = copy_v(x);
                     }
+                    continue;
+                }
+                int pg0 = page_of(p.bp, w.b, w.s, 2 * w.b0), pg1 = page_of(p.bp, w.b, w.s, 2 * w.b0 + 1);
+                for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
+                    const int row0 = first_row(pg0), row1 = first_row(pg1);
                     const int mine = rank == 0 ? row0 : row1;
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
@@ -325,14 +377,9 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                         ptx::tma_load_3d_pair(sbase + L::kOffK + g * kPfGroupA * kPfPanel, g ? &tm_v : &tm_k, 0, mine,
                                               g * kPfGroupA, even_bar(kPbKFull + g));
                     }
-                    if constexpr (KVF == 0) {
-                        // this CTA's page of a later block, into L2 while the current one is waited for
-                        if (b == w.b0)
-                            for (int a = 1; a < kTrAhead; ++a) prefetch(2 * (b + a) + rank);
-                        prefetch(2 * (b + kTrAhead) + rank);
-                        pg0 = page_of(p.bp, w.b, w.s, 2 * b + 2);
-                        pg1 = page_of(p.bp, w.b, w.s, 2 * b + 3);
-                    }
+                    prefetch(2 * b + 2 + rank);
+                    pg0 = page_of(p.bp, w.b, w.s, 2 * b + 2);
+                    pg1 = page_of(p.bp, w.b, w.s, 2 * b + 3);
                     if (ok && x > 0) ok = load_v(x - 1, tail_v0, tail_v1, row_v0, row_v1);
                     row_v0 = row0;
                     row_v1 = row1;
@@ -340,12 +387,13 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                     tail_v1 = tree_tail(w.s, 2 * b + 1);
                 }
             }
-            if (ok && x > 0) ok = load_v(x - 1, tail_v0, tail_v1, row_v0, row_v1);
+            if (KVF == 0 && ok && x > 0) ok = load_v(x - 1, tail_v0, tail_v1, row_v0, row_v1);
             if (rank == 0 && !p.by_tile) p.job_list[run] = job;
             // every copy has landed and been used, and no release of a stage is still on its way to
             // this CTA's barriers, before it leaves
             if (x > 0) {
                 for (int g = 0; ok && g < 2; ++g) ok = wait(kPbKEmpty + g, (x - 1) & 1);
+                if (KVF == 1 && ok) ok = wait(kTbCopied, (x - 1) & 1);
                 for (int i = 0; ok && i < 2; ++i) ok = wait(kPbVEmpty + i, (x - 1) & 1);
                 if (ok) ok = wait(kPbQEmpty, (piece - 1) & 1);
             }
@@ -358,6 +406,8 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
         __syncwarp();
     } else if (warp == kTrS1Warp || warp == kTrS2Warp) {
         // ================================================================ S issuers, as in the prefix kernel
+        TrWalk w(p, *start);
+            const bool any = w.next(p);
         if (rank == 0 && lane == 0) {
             constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kPfRows, kPfKeys, 0, 0);
             const bool ga = warp == kTrS1Warp;
@@ -373,7 +423,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                 for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
                     const int s = x & 1;
                     if (x >= 2 && !(ok = wait(kPbSEmpty + s, ((x >> 1) - 1) & 1))) break;
-                    if (!(ok = wait(kPbKFull + g, x & 1))) break;
+                    if (!(ok = wait(KVF == 1 ? kTbMade : kPbKFull + g, x & 1))) break;
                     ptx::tc_fence_after();
                     const uint32_t d = d0 + s * PfLayout::kSBuf;
 #pragma unroll
@@ -398,8 +448,10 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             ptx::mbar_wait(bar(kTbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
         }
         __syncwarp();
-    } else if (warp == kTrPvWarp) {
+    } else {
         // ================================================================ PV issuer
+        TrWalk w(p, *start);
+            const bool any = w.next(p);
         if (rank == 0 && lane == 0) {
             constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kPfRows, 256, 0, 1);
             const uint64_t dv = ptx::smem_desc_sw128(sbase + L::kOffV, kPfPanel, 1024);
@@ -412,7 +464,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         if (!(ok = wait(kPbPFull + i, x & 1))) break;
-                        if (!tree_tail(w.s, 2 * b + i)) {
+                        if (KVF == 0 && !tree_tail(w.s, 2 * b + i)) {
                             if (!(ok = wait(kPbVFull + i, (v_parity >> i) & 1u))) break;
                             v_parity ^= 1u << i;
                         }
@@ -424,7 +476,6 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                                 ptx::mma_bf16_ss_pair(tmem + PfLayout::kColO + 128 * n, dp + ((i * kPfPanel + k * 32) >> 4),
                                                       dv + ((i * kPfVPage + 2 * n * kPfPanel + k * 2048) >> 4), kIdescPV,
                                                       (b != w.b0 || i > 0 || k > 0) ? 1u : 0u);
-                        if (KVF == 1 && i == 1) ptx::mma_commit_pair(bar(kTbRingFree + x % kTrRing));
                         ptx::mma_commit_pair(bar(kPbVEmpty + i));
                     }
                 }
@@ -434,56 +485,59 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             ptx::mbar_wait(bar(kTbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
         }
         __syncwarp();
+    }
     } else if (warp >= kTrExpandWarp) {
         // ================================================================ expansion of fp8 rows
         if constexpr (KVF == 1) {
-            constexpr int kRows = kPage / kTrExpandWarps;  // rows per warp
-            const int row = kRows * (warp - kTrExpandWarp);
-            __nv_bfloat16* ring = p.ring + (static_cast<int64_t>(run) * kTrRing * kTrBlockRows + rank * kPage + row) * kDQK;
+            ptx::regs_up<136>();
+        TrWalk w(p, *start);
+            const bool any = w.next(p);
+            const int row = kTrExpandRows * (warp - kTrExpandWarp);
+            auto warp_wait = [&](int i, uint32_t parity) -> bool {
+                return ptx::mbar_wait_warp(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
+            };
             bool ok = true;
             int x = 0;
             for (bool more = any; ok && more; more = w.next(p)) {
-                // four rows are loaded while the four before them are converted, across blocks too; a block's
-                // rows are brought into L2 two blocks ahead
-                auto source = [&](int b) -> Fp8Source {
-                    const int i = 2 * b + rank;
-                    return Fp8Source(p.bp, w.s, i, b < w.b1 ? page_of(p.bp, w.b, w.s, i) : -1, row);
-                };
-                Fp8Source cur = source(w.b0), next = source(w.b0 + 1);
-                next.prefetch(kRows);
-                Fp8Rows4 r[2];
-                cur.load(r[0], 0);
+                auto page = [&](int b) -> int { return b < w.b1 ? page_of(p.bp, w.b, w.s, 2 * b + rank) : -1; };
+                const Fp8Source cur(p.bp, w.s, 2 * w.b0 + rank, page(w.b0), row);
+                Fp8Source next(p.bp, w.s, 2 * w.b0 + 2 + rank, page(w.b0 + 1), row);
+                next.prefetch(kTrExpandRows);
+                TrCodes half0, half1;
+                half0.load(cur, 0);
+                half1.load(cur, 8);
+                float2 sc = TrCodes::scales(cur);
+                int pg = page(w.b0 + 2);
                 for (int b = w.b0; b < w.b1; ++b, ++x) {
-                    const int slot = x % kTrRing;
-                    const Fp8Source after = source(b + 2);
-                    after.prefetch(kRows);
-                    if (x >= kTrRing) {  // this slot's last block has been multiplied
-                        if (lane == 0) ok = wait(kTbRingFree + slot, (x / kTrRing - 1) & 1);
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
-                        if (!ok) break;
-                    }
-                    __nv_bfloat16* dst = ring + static_cast<int64_t>(slot) * kTrBlockRows * kDQK;
-#pragma unroll
-                    for (int u = 0; u < kRows; u += 4) {
-                        if (u + 4 < kRows) cur.load(r[(u / 4 + 1) & 1], u + 4);
-                        else next.load(r[(u / 4 + 1) & 1], 0);
-                        r[(u / 4) & 1].store(dst + u * kDQK);
-                    }
-                    cur = next;
-                    next = after;
-                    ptx::fence_proxy_async_all();
+                    const Fp8Source after(p.bp, w.s, 2 * (b + 2) + rank, pg, row);
+                    after.prefetch(kTrExpandRows);
+                    pg = page(b + 3);
+                    // the last block's S has read the K tile, and its copies to V have
+                    if (x > 0 && !(ok = warp_wait(kPbKEmpty, (x - 1) & 1) && warp_wait(kPbKEmpty + 1, (x - 1) & 1) &&
+                                        warp_wait(kTbCopied, (x - 1) & 1)))
+                        break;
+                    const uint32_t to = sbase + L::kOffK + row * 128;
+                    half0.store(0, to, sc);
+                    half1.store(8, to + 8 * 128, sc);
+                    ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane < 2) ptx::mbar_arrive_release_cluster(ptx::map_shared_rank(bar(kTbRingFull + slot), lane));
+                    if (lane == 0) {
+                        ptx::mbar_arrive_cluster(even_bar(kTbMade));
+                        ptx::mbar_arrive(bar(kTbRows));
+                    }
+                    // only now: a fence waits for the loads before it, too (5.3 us a block with these before it)
+                    half0.load(next, 0);
+                    half1.load(next, 8);
+                    sc = TrCodes::scales(next);
+                    next = after;
                 }
-            }
-            // no release is still on its way to this CTA's barriers when it leaves
-            for (int y = max(x - kTrRing, 0); ok && y < x; ++y) {
-                if (lane == 0) ok = wait(kTbRingFree + y % kTrRing, (y / kTrRing) & 1);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
         }
     } else {
         // ================================================================ softmax / output
+        if constexpr (KVF == 1) ptx::regs_up<136>();
+        TrWalk w(p, *start);
+            const bool any = w.next(p);
         const int quad = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
         const int half = quad >> 1;            // page of the block, dims 256 half .. + 255
@@ -496,11 +550,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
         const bool flip = p.sm_scale_log2 < 0.f;
         volatile float* sX = reinterpret_cast<volatile float*>(smem + L::kOffX);
         auto warp_wait = [&](int i, uint32_t parity) -> bool {
-            bool okw = true;
-            if (lane == 0) okw = wait(i, parity);
-            okw = __shfl_sync(0xffffffffu, okw, 0);
-            __syncwarp();
-            return okw;
+            return ptx::mbar_wait_warp(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
         };
         const uint32_t s_empty0 = even_bar(kPbSEmpty), s_empty1 = even_bar(kPbSEmpty + 1), p_full = even_bar(kPbPFull + half);
         const uint32_t p_row = sbase + L::kOffP + half * kPfPanel + r * 128;
@@ -510,7 +560,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
         for (bool more = any; !failed && more; more = w.next(p)) {
             float m = -CUDART_INF_F, l = 0.f;
             // (rows past the sequence's last are another's, or garbage: never stored)
-            const int token = static_cast<int>(min((w.row0() + rank * kPfHalf + r) / p.bp.h, static_cast<int64_t>(w.s.n - 1)));
+            const int token = min(static_cast<int>(w.row0() + rank * kPfHalf + r) / p.bp.h, w.s.n - 1);
             int page = page_of(p.bp, w.b, w.s, 2 * w.b0 + half);
             for (int b = w.b0; b < w.b1; ++b, ++x) {
                 const int i_page = 2 * b + half, key = i_page * kPage + 32 * sub;
@@ -635,14 +685,17 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                 for (int q = 0; q < 4; ++q)
                     ptx::st_shared_v4(p_row + ((static_cast<uint32_t>(4 * sub + q) ^ static_cast<uint32_t>(r & 7)) << 4),
                                       make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
-                if (tree_tail(w.s, i_page)) {
-                    // this CTA's V tile of the page, cleaned by the page's warps: rows past the end, and what
-                    // is not finite in the drafted rows
+                const bool tail = tree_tail(w.s, i_page);
+                if (KVF == 1 || tail) {
                     if (!warp_wait(kTbTail + half, tails & 1)) {
                         failed = true;
                         continue;
                     }
                     ++tails;
+                }
+                if (tail) {
+                    // this CTA's V tile of the page, cleaned by the page's warps: rows past the end, and what
+                    // is not finite in the drafted rows
                     const int drafted = max(w.s.len - i_page * kPage, 0), end = min(w.s.keys - i_page * kPage, kPage);
                     const int tid = (2 * sub + (quad & 1)) * 32 + lane;
                     const uint32_t vt = sbase + L::kOffV + half * kPfVPage;

@@ -18,13 +18,15 @@
 // Both operands have the same layout (rows x 9 panels, SW128), so the two forms differ in who loads what and in
 // which descriptor is A.  The ring's depth sets the pace where the operand streams (64 KB in flight per CTA gave
 // 42 GB/s per SM, from HBM and from L2 alike), so it takes what the other operand leaves: eight stages if no
-// sequence of the batch has more than 128 rows, else five.
+// sequence of the batch has more than 128 rows, else five (with fp8 six and four, beside the codes).
 //
 // Work: tiles of 256 keys, each whole in one pair, in equal shares of their cost (kWt... below).
 //
-// fp8 rows are expanded straight into the ring (or the operand that stays) by four more warps, each 32 of the
-// CTA's 128 keys, two panels of codes at a time with the next two on their way.  (Expanded into global memory
-// and loaded from there by TMA, a tile took 6.4 us: L2 took the writes no faster.)
+// fp8 codes come by TMA, 64 of every row at a time, into a ring of their own, and four more warps expand them, each 32
+// of the CTA's 128 keys, panel by panel into the ring of panels (or the operand that stays); the rotated dims come by
+// TMA as they are.  (Codes loaded into registers: 7 us a tile, because the fence after a panel's stores waits
+// for the loads that are meant to run ahead.  Expanded into global memory and loaded from there: 6.4 us, L2 took
+// the writes no faster.)
 //
 // Roles (384 threads, 512 with fp8):
 //   warps 0-7    sums: TMEM quadrant warp % 4 (32 keys), half warp / 4 of the tile's columns
@@ -42,7 +44,15 @@ namespace smla {
 constexpr int kWtKeys = 256;      // keys per tile (pair)
 constexpr int kWtHalf = 128;      // per CTA
 constexpr int kWtRows = 256;      // rows (token, head) per tile
+// stages of the ring, and of the ring of fp8 codes; Few: no sequence has more than kWtRowsFew rows
 constexpr int kWtStages = 5, kWtStagesFew = 8;
+constexpr int kWtStagesFp8 = 4, kWtStagesFewFp8 = 7;
+constexpr int kWtRaw = 2, kWtRawFew = 5;
+// The producer fills every ninth stage of an fp8 tile (the rotated dims) and waits for that stage's last release by
+// its parity, so the release before that one must be known: the codes of panel 7 - kWtRaw have been
+// expanded by then, and for that the stage kWtRaw + 1 places ahead of it had been released.
+static_assert(kWtRaw < kWtStagesFp8 && kWtRawFew < kWtStagesFewFp8, "parities of the ring");
+constexpr int kWtRawPanel = 128 * 64;  // 128 rows x 64 codes
 constexpr int kWtRowsFew = 128;      // rows of a sequence up to which the deeper ring has room
 constexpr int kWtPanel = 128 * 128;  // 128 rows x 64 bf16, SW128
 constexpr int kWtSumWarps = 8;
@@ -59,7 +69,7 @@ __host__ __device__ constexpr int weights_threads() {
 
 enum : int {
     kWbStayFull = 0,                        // even CTA: both CTAs' part of the operand that stays, by TMA
-    kWbStayMade = 1,                        // even CTA: the same, expanded
+    kWbStayMade = 1,                        // even CTA: the same, expanded, with the rotated dims by TMA
     kWbStayEmpty = 2,                       // both
     kWbFull = 3,                            // +stage, even CTA: by TMA
     kWbMade = kWbFull + kWtStagesFew,       // +stage, even CTA: expanded
@@ -67,14 +77,18 @@ enum : int {
     kWbSFull = kWbEmpty + kWtStagesFew,     // +buffer, both
     kWbSEmpty = kWbSFull + 2,               // +buffer, even CTA
     kWbDrain = kWbSEmpty + 2,               // even CTA
-    kWbCount = kWbDrain + 1
+    kWbRawFull = kWbDrain + 1,              // +stage, own CTA: codes
+    kWbRawEmpty = kWbRawFull + kWtRawFew,   // +stage, own CTA
+    kWbCount = kWbRawEmpty + kWtRawFew
 };
 
 struct WtLayout {
     static constexpr int kOffStay = 0;                               // 9 panels of 128 rows, or of 64
     static constexpr int kOffRing = kPanels * kWtPanel, kOffRingFew = kOffRing / 2;
     static constexpr int kOffLse = kOffRing + kWtStages * kWtPanel;  // [2][256]: minus the rows' LSE
+    static constexpr int kOffRaw = kOffRing + kWtStagesFp8 * kWtPanel, kOffRawFew = kOffRingFew + kWtStagesFewFp8 * kWtPanel;
     static_assert(kOffRingFew + kWtStagesFew * kWtPanel <= kOffLse, "ring");
+    static_assert(kOffRaw + kWtRaw * kWtRawPanel <= kOffLse && kOffRawFew + kWtRawFew * kWtRawPanel <= kOffLse, "codes");
     static constexpr int kOffX = kOffLse + 2 * kWtRows * 4;          // [128]: sums of the columns' second half; the plan's sums
     static constexpr int kOffBar = kOffX + kWtHalf * 4;
     static constexpr int kOffMisc = kOffBar + kWbCount * 8;          // tmem base, abort flag, the run's start
@@ -112,20 +126,16 @@ __device__ __forceinline__ void weights_plan(const WtParams& p, int run, int thr
     auto cost_of = [&](const Seq& s) -> int64_t {
         return s.n == 0 ? 0 : kWtCostSeq + static_cast<int64_t>(weights_key_tiles(s)) * weights_tile_cost(weights_row_tiles(p, s));
     };
-    int64_t cost = 0;
-    int most = 0;  // tokens of a sequence
+    int64_t cost = 0, many = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq(p.bp, b);
         cost += cost_of(s);
-        most = max(most, s.n);
+        many += static_cast<int64_t>(s.n) * p.bp.h > kWtRowsFew;
     }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if ((threadIdx.x & 31) == 0) scratch[32 + threadIdx.x / 32] = most;
-    int64_t at, total;
-    block_prefix(cost, scratch, threads / 32, at, total);
-    for (int w = 0; w < threads / 32; ++w) most = max(most, static_cast<int>(scratch[32 + w]));
-    const int few = static_cast<int64_t>(most) * p.bp.h <= kWtRowsFew;
-    const int64_t from = total * run / p.pairs, to = total * (run + 1) / p.pairs;
+    int64_t at, total, wide_before, wide;  // wide: sequences of more than kWtRowsFew rows
+    block_prefix2(cost, many, scratch, threads / 32, at, total, wide_before, wide);
+    const int few = wide == 0;
+    const int64_t from = share_of(total, run, p.pairs), to = share_of(total, run + 1, p.pairs);
     if (from >= to) {
         if (threadIdx.x == 0) *start = WtStart{0, 0, 0, p.bp.B, few};
     } else if (at <= from && from < at + cost) {
@@ -203,61 +213,10 @@ struct WtStage {
     __device__ __forceinline__ uint32_t last() const { return (round - 1) & 1; }       // parity of its last release
 };
 
-// 32 rows of fp8 on their way into two panels: lane l has rows 8 i + l / 4 and of each the 16 codes from
-// 16 (l % 4) on of either panel, with their tile's scale; or the 32 bytes from 32 (l % 4) on of the rotated dims.
-struct WtCodes {
-    uint4 v[8];
-    float s[4];
-    __device__ __forceinline__ void load(const Fp8Source& from, int pair) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2);
-            v[2 * i] = v[2 * i + 1] = make_uint4(0u, 0u, 0u, 0u);
-            s[i] = 0.f;
-            if (r < from.n) {
-                const uint8_t* row = from.src + r * kFp8RowBytes;
-                if (pair < 4) {
-                    const uint4* codes = reinterpret_cast<const uint4*>(row) + 8 * pair + (lane & 3);
-                    v[2 * i] = __ldg(codes);
-                    v[2 * i + 1] = __ldg(codes + 4);
-                    s[i] = __ldg(reinterpret_cast<const float*>(row + 512) + pair);
-                } else {
-                    const uint4* rope = reinterpret_cast<const uint4*>(row + 528) + 2 * (lane & 3);
-                    v[2 * i] = __ldg(rope);
-                    v[2 * i + 1] = __ldg(rope + 1);
-                }
-            }
-        }
-    }
-    // chunk c of row r of a panel lies at 128 r + 16 (c ^ r % 8)
-    __device__ __forceinline__ static uint32_t place(uint32_t dst, int r, int c) { return dst + r * 128 + ((c ^ (r & 7)) << 4); }
-    __device__ __forceinline__ void store_codes(uint32_t dst, int j) const {
-        const int lane = threadIdx.x & 31, c = 2 * (lane & 3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2);
-            const uint4 q = v[2 * i + j];
-            ptx::st_shared_v4(place(dst, r, c), make_uint4(ptx::e4m3x2_scaled_bf16x2(q.x & 0xFFFFu, s[i]), ptx::e4m3x2_scaled_bf16x2(q.x >> 16, s[i]),
-                                                           ptx::e4m3x2_scaled_bf16x2(q.y & 0xFFFFu, s[i]), ptx::e4m3x2_scaled_bf16x2(q.y >> 16, s[i])));
-            ptx::st_shared_v4(place(dst, r, c + 1), make_uint4(ptx::e4m3x2_scaled_bf16x2(q.z & 0xFFFFu, s[i]), ptx::e4m3x2_scaled_bf16x2(q.z >> 16, s[i]),
-                                                               ptx::e4m3x2_scaled_bf16x2(q.w & 0xFFFFu, s[i]), ptx::e4m3x2_scaled_bf16x2(q.w >> 16, s[i])));
-        }
-    }
-    __device__ __forceinline__ void store_rope(uint32_t dst) const {
-        const int lane = threadIdx.x & 31, c = 2 * (lane & 3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2);
-            ptx::st_shared_v4(place(dst, r, c), v[2 * i]);
-            ptx::st_shared_v4(place(dst, r, c + 1), v[2 * i + 1]);
-        }
-    }
-};
-
 template <int KVF>
 __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
-    sparse_mla_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WtParams p) {
+    sparse_mla_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                              const __grid_constant__ CUtensorMap tm_codes, const WtParams p) {
     using L = WtLayout;
     constexpr int kThreads = weights_threads<KVF>();
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -283,7 +242,8 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
         for (int i = 0; i < kWbCount; ++i) {
             const bool by_warps = i == kWbSEmpty || i == kWbSEmpty + 1;                // both CTAs' sum warps
             const bool by_expand = i == kWbStayMade || (i >= kWbMade && i < kWbMade + kWtStagesFew);  // both CTAs' expansion warps
-            ptx::mbar_init(bar(i), by_warps ? 2 * kWtSumWarps : by_expand ? 2 * kWtExpandWarps : 1);
+            const bool by_own = i >= kWbRawEmpty;                                                       // this CTA's
+            ptx::mbar_init(bar(i), by_warps ? 2 * kWtSumWarps : by_own ? kWtExpandWarps : by_expand ? 2 * kWtExpandWarps + (i == kWbStayMade ? 1 : 0) : 1);
         }
         ptx::fence_mbarrier_init();
     }
@@ -294,20 +254,25 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
     if (warp == kWtTmaWarp && lane == 0) {
         ptx::prefetch_tmap(&tm_q);
         ptx::prefetch_tmap(&tm_k);
+        if (KVF == 1) ptx::prefetch_tmap(&tm_codes);
     }
+    ptx::tc_fence_before();
+    __syncwarp();           // the cluster barrier wants its warps whole
+    ptx::cluster_arrive();  // both CTAs' barriers are initialised before anyone signals them
     // launched as a programmatic dependent: nothing above touched global memory
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     weights_plan(p, run, kThreads, reinterpret_cast<int64_t*>(smem + L::kOffX), start);
     WtWalk w(p, *start);
     const bool any = w.next(p);
-    ptx::tc_fence_before();
-    __syncwarp();         // the cluster barrier wants its warps whole
-    ptx::cluster_sync();  // both CTAs' barriers are initialised before anyone signals them
+    __syncwarp();
+    ptx::cluster_wait();
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
     const bool few = start->few != 0;
-    const int stages = few ? kWtStagesFew : kWtStages;
+    const int stages = KVF ? (few ? kWtStagesFewFp8 : kWtStagesFp8) : few ? kWtStagesFew : kWtStages;
+    const int raw_stages = few ? kWtRawFew : kWtRaw;
+    const uint32_t raw = sbase + (few ? L::kOffRawFew : L::kOffRaw);
     const uint32_t ring = sbase + (few ? L::kOffRingFew : L::kOffRing);
     const int stay_panel = few ? kWtPanel / 2 : kWtPanel;
 
@@ -317,7 +282,6 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
         if (lane == 0) {
             bool ok = true;
             int stays = 0;          // operands that stayed so far
-            bool others = false;    // the last piece's keys stayed
             WtStage st(stages);
             int row0 = 0, row1 = 0;  // rows of the tile's two pages
             auto begin_stay = [&]() -> bool {
@@ -331,6 +295,10 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbFull + st.at), 2u * kWtPanel);
                 return true;
             };
+            auto load_rope = [&](uint32_t dst, uint32_t b) {
+                ptx::tma_load_2d_pair(dst, &tm_k, 528, row0, b);
+                ptx::tma_load_2d_pair(dst + kWtPanel / 2, &tm_k, 528, row1, b);
+            };
             auto load_keys = [&](uint32_t dst, int pn, uint32_t b) {
                 ptx::tma_load_3d_pair(dst, &tm_k, 0, row0, pn, b);
                 ptx::tma_load_3d_pair(dst + kWtPanel / 2, &tm_k, 0, row1, pn, b);
@@ -341,8 +309,18 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 const int pg = page_of(p.bp, w.b, w.s, i);
                 const int n = page_rows(p.bp, w.s, i, pg);
                 if (n > 0)
-                    ptx::bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(p.bp.kv) + static_cast<int64_t>(pg) * kPage * kDQK,
-                                          static_cast<uint32_t>(n * kDQK * 2));
+                    ptx::bulk_prefetch_l2(static_cast<const char*>(p.bp.kv) + static_cast<int64_t>(pg) * kPage * (KVF ? kFp8RowBytes : kDQK * 2),
+                                          static_cast<uint32_t>(n * (KVF ? kFp8RowBytes : kDQK * 2)));
+            };
+            WtStage raw_st(raw_stages);
+            auto load_codes = [&](int pn) -> bool {  // panel pn's
+                if (raw_st.used() && !wait(kWbRawEmpty + raw_st.at, raw_st.last())) return false;
+                const uint32_t dst = raw + raw_st.at * kWtRawPanel, b = bar(kWbRawFull + raw_st.at);
+                ptx::mbar_arrive_expect_tx(b, static_cast<uint32_t>(kWtRawPanel));
+                ptx::tma_load_2d(dst, &tm_codes, 64 * pn, row0, b);
+                ptx::tma_load_2d(dst + kWtRawPanel / 2, &tm_codes, 64 * pn, row1, b);
+                raw_st.next();
+                return true;
             };
             for (bool more = any; ok && more; more = w.next(p)) {
                 const bool stream_keys = w.row_tiles == 1;
@@ -356,28 +334,28 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                             ptx::tma_load_3d_pair(sbase + L::kOffStay + pn * stay_panel + half * kWtPanel / 2, &tm_q, 0,
                                                   row + half * kPage, pn, even_bar(kWbStayFull));
                 }
-                // what the expansion warps filled of the ring has been used before this thread fills it: a barrier that
-                // nobody here has followed could be more than one phase behind, which a parity cannot tell
-                if (KVF == 1 && !stream_keys && !others && stays > 0 && !(ok = wait(kWbStayEmpty, (stays - 1) & 1))) break;
-                others = !stream_keys;
                 for (int k = w.k0; ok && k < w.k1; ++k) {
-                    if constexpr (KVF == 0) {
-                        const int i = 4 * k + 2 * rank;
-                        row0 = first_row(page_of(p.bp, w.b, w.s, i));
-                        row1 = first_row(page_of(p.bp, w.b, w.s, i + 1));
-                        if (k + 1 < w.k1) {
-                            prefetch(i + 4);
-                            prefetch(i + 5);
-                        }
+                    const int i_page = 4 * k + 2 * rank;
+                    row0 = first_row(page_of(p.bp, w.b, w.s, i_page));
+                    row1 = first_row(page_of(p.bp, w.b, w.s, i_page + 1));
+                    if (k + 1 < w.k1) {
+                        prefetch(i_page + 4);
+                        prefetch(i_page + 5);
                     }
                     if (stream_keys) {
-                        for (int pn = 0; ok && pn < kPanels; ++pn, st.next())
-                            if (KVF == 0 && (ok = begin_stage())) load_keys(ring + st.at * kWtPanel, pn, even_bar(kWbFull + st.at));
+                        for (int pn = 0; ok && pn < kPanels; ++pn, st.next()) {
+                            if (KVF == 1 && pn < kPanels - 1) ok = load_codes(pn);
+                            else if (!(ok = begin_stage())) break;
+                            else if (KVF == 1) load_rope(ring + st.at * kWtPanel, even_bar(kWbFull + st.at));
+                            else load_keys(ring + st.at * kWtPanel, pn, even_bar(kWbFull + st.at));
+                        }
                     } else {
+                        if (!(ok = begin_stay())) break;
                         if (KVF == 1) {
-                            ++stays;  // the expansion warps'
+                            if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbStayMade), 2u * kWtPanel);
+                            load_rope(sbase + L::kOffStay + (kPanels - 1) * kWtPanel, even_bar(kWbStayMade));
+                            for (int pn = 0; ok && pn < kPanels - 1; ++pn) ok = load_codes(pn);
                         } else {
-                            if (!(ok = begin_stay())) break;
                             if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbStayFull), 2u * kPanels * kWtPanel);
                             for (int pn = 0; pn < kPanels; ++pn) load_keys(sbase + L::kOffStay + pn * kWtPanel, pn, even_bar(kWbStayFull));
                         }
@@ -432,8 +410,9 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                         const uint32_t idesc = ptx::idesc_bf16_f32(kWtKeys, w.columns(p, i), 0, 0);
                         const uint32_t d = tmem + buf * kWtRows;
                         for (int pn = 0; pn < kPanels; ++pn, st.next()) {
-                            uint32_t& parity = expanded ? made : full;
-                            if (!(ok = wait((expanded ? kWbMade : kWbFull) + st.at, (parity >> st.at) & 1u))) break;
+                            const bool by_warps = expanded && pn < kPanels - 1;
+                            uint32_t& parity = by_warps ? made : full;
+                            if (!(ok = wait((by_warps ? kWbMade : kWbFull) + st.at, (parity >> st.at) & 1u))) break;
                             parity ^= 1u << st.at;
                             ptx::tc_fence_after();
                             const uint64_t stay = d_stay + ((pn * stay_panel) >> 4), moving = d_ring + ((st.at * kWtPanel) >> 4);
@@ -460,62 +439,74 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
             const int row = 32 * (warp - kWtExpandWarp);  // this warp's first of the CTA's 128 keys
             bool ok = true, others = false;  // the last piece's keys stayed
             int stays = 0;
-            WtStage st(stages);
+            WtStage st(stages), raw_st(raw_stages);
             auto warp_wait = [&](int i, uint32_t parity) -> bool {
-                bool okw = true;
-                if (lane == 0) okw = wait(i, parity);
-                okw = __shfl_sync(0xffffffffu, okw, 0);
-                __syncwarp();
-                return okw;
-            };
-            auto done = [&](int i) {  // what this warp wrote is there for the MMAs
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(even_bar(i));
+                return ptx::mbar_wait_warp(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
             };
             for (bool more = any; ok && more; more = w.next(p)) {
                 const bool stream_keys = w.row_tiles == 1;
-                auto source = [&](int k) -> Fp8Source {
-                    const int i = 4 * k + 2 * rank + row / kPage;
-                    return Fp8Source(p.bp, w.s, i, k < w.k1 ? page_of(p.bp, w.b, w.s, i) : -1, row % kPage);
-                };
-                // (the producer's thread says why: before the ring is these warps' again, and before the first tile of
-                // keys that stays)
-                if (stays > 1 && others != !stream_keys && !(ok = warp_wait(kWbStayEmpty, stays & 1))) break;
-                if (stays > 0 && others != !stream_keys && !(ok = warp_wait(kWbStayEmpty, (stays - 1) & 1))) break;
+                // where keys that stay and keys that stream meet, the last operand that stayed has been used: then the
+                // ring has, whose barriers these warps do not follow while queries stream
+                if (others != !stream_keys) {
+                    if (stays > 0 && !(ok = warp_wait(kWbStayEmpty, (stays - 1) & 1))) break;
+                }
                 others = !stream_keys;
-                Fp8Source cur = source(w.k0);
-                WtCodes now, then;
-                now.load(cur, 0);
+                // lane l: rows 8 i + l / 4 of the warp's, their scales, and of each row 16 of a panel's codes from 16 (l % 4) on
+                float4 sc[4];
+                auto scales = [&](int k) {
+                    const int i_page = 4 * k + 2 * rank + row / kPage;
+                    const int page = k < w.k1 ? page_of(p.bp, w.b, w.s, i_page) : -1;
+                    const int n = page_rows(p.bp, w.s, i_page, page) - row % kPage;
+                    const uint8_t* src = static_cast<const uint8_t*>(p.bp.kv) + (static_cast<int64_t>(page) * kPage + row % kPage) * kFp8RowBytes + 512;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * i + (lane >> 2);
+                        sc[i] = r < n ? __ldg(reinterpret_cast<const float4*>(src + r * kFp8RowBytes)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                };
+                scales(w.k0);
                 for (int k = w.k0; ok && k < w.k1; ++k) {
-                    const Fp8Source next = source(k + 1);
-                    next.prefetch(32);
                     if (!stream_keys) {
                         if (stays > 0 && !(ok = warp_wait(kWbStayEmpty, (stays - 1) & 1))) break;
                         ++stays;
                     }
 #pragma unroll 1
-                    for (int pair = 0; ok && pair < 5; ++pair) {  // two panels of codes, or the rotated dims
-                        then.load(pair < 4 ? cur : next, pair < 4 ? pair + 1 : 0);
+                    for (int pn = 0; pn < kPanels - 1; ++pn) {
+                        if (!(ok = warp_wait(kWbRawFull + raw_st.at, raw_st.round & 1))) break;
+                        uint4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if (pair == 4 && j == 1) break;
-                            if (stream_keys && st.used() && !(ok = warp_wait(kWbEmpty + st.at, st.last()))) break;
-                            const uint32_t dst = (stream_keys ? ring + st.at * kWtPanel : sbase + L::kOffStay + (2 * pair + j) * kWtPanel) + row * 128;
-                            if (pair < 4) now.store_codes(dst, j);
-                            else now.store_rope(dst);
-                            if (stream_keys) {
-                                done(kWbMade + st.at);
-                                st.next();
-                            }
+                        for (int i = 0; i < 4; ++i) v[i] = ptx::ld_shared_v4(raw + raw_st.at * kWtRawPanel + (row + 8 * i) * 64 + lane * 16);
+                        if (stream_keys && st.used() && !(ok = warp_wait(kWbEmpty + st.at, st.last()))) break;
+                        const uint32_t dst = (stream_keys ? ring + st.at * kWtPanel : sbase + L::kOffStay + pn * kWtPanel) + row * 128;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float s = sc[i].x;
+                            if (pn & 1) sc[i] = make_float4(sc[i].y, sc[i].z, sc[i].w, 0.f);  // the next tile of 128
+                            const int r = 8 * i + (lane >> 2), c = 2 * (lane & 3);  // chunk c of row r lies at 16 (c ^ r % 8)
+                            ptx::st_shared_v4(dst + r * 128 + ((c ^ (r & 7)) << 4),
+                                              make_uint4(ptx::e4m3x2_scaled_bf16x2(v[i].x & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(v[i].x >> 16, s),
+                                                         ptx::e4m3x2_scaled_bf16x2(v[i].y & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(v[i].y >> 16, s)));
+                            ptx::st_shared_v4(dst + r * 128 + (((c + 1) ^ (r & 7)) << 4),
+                                              make_uint4(ptx::e4m3x2_scaled_bf16x2(v[i].z & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(v[i].z >> 16, s),
+                                                         ptx::e4m3x2_scaled_bf16x2(v[i].w & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(v[i].w >> 16, s)));
                         }
-                        now = then;
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            ptx::mbar_arrive(bar(kWbRawEmpty + raw_st.at));
+                            if (stream_keys) ptx::mbar_arrive_cluster(even_bar(kWbMade + st.at));
+                        }
+                        raw_st.next();
+                        if (stream_keys) st.next();
                     }
-                    if (ok && !stream_keys) {
-                        done(kWbStayMade);
+                    if (!ok) break;
+                    scales(k + 1);  // after the last fence, which would wait for them
+                    if (stream_keys) {
+                        st.next();  // the rotated dims' stage, the producer's
+                    } else {
+                        if (lane == 0) ptx::mbar_arrive_cluster(even_bar(kWbStayMade));
                         for (int i = 0; i < w.row_tiles * kPanels; ++i) st.next();
                     }
-                    cur = next;
                 }
                 if (stream_keys) ++stays;  // the queries, the producer's
             }
@@ -546,11 +537,7 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
         const int width = p.bp.nb * kPage;
         const uint32_t s_empty0 = even_bar(kWbSEmpty), s_empty1 = even_bar(kWbSEmpty + 1);
         auto warp_wait = [&](int i, uint32_t parity) -> bool {
-            bool okw = true;
-            if (lane == 0) okw = wait(i, parity);
-            okw = __shfl_sync(0xffffffffu, okw, 0);
-            __syncwarp();
-            return okw;
+            return ptx::mbar_wait_warp(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
         };
         // minus the LSE of row tid of row tile i: the table's entry (a row that saw nothing adds nothing: -inf)
         auto entry = [&](int i) -> float {
@@ -586,48 +573,45 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                     if (!failed && !warp_wait(kWbSFull + buf, (item >> 1) & 1)) failed = true;
                     if (failed) continue;
                     ptx::tc_fence_after();
-                    // in tiles with drafted rows, word e of lane l: which of the warp's 32 keys column 32 e + l sees
-                    uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-                    if (tail) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int row = i * kWtRows + c_first + 32 * e + lane;
-                            if (32 * e + lane < limit) seen[e] = seen_bits(p.bp, w.s, row / p.bp.h, key - lane);
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < kWtRows / 2; c += 16) {
-                        if (c >= limit) break;
-                        uint32_t sv[16];
-                        SMLA_TMEM_LD16(tmem + lane_base + buf * kWtRows + c_first + c, sv);
-                        float4 nl[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint4 v = ptx::ld_shared_v4(table + (c_first + c + 4 * e) * 4);
-                            nl[e] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-                        }
-                        ptx::tmem_wait_ld();
+                    // 16 columns at a time, the next ones' logits on their way
+                    const uint32_t s_at = tmem + lane_base + buf * kWtRows + c_first;
+                    auto add = [&](const uint32_t* sv, int c0) {
                         float pr[16];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 l2 = e & 1 ? make_float2(nl[e >> 1].z, nl[e >> 1].w) : make_float2(nl[e >> 1].x, nl[e >> 1].y);
-                            const float2 y = ptx::mul2(
-                                ptx::fma2(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), scale2, l2), log2e2);
-                            pr[2 * e] = ptx::ex2_approx(y.x);
-                            pr[2 * e + 1] = ptx::ex2_approx(y.y);
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 nl = ptx::ld_shared_v4(table + (c_first + c0 + 4 * e) * 4);
+                            const float2 y0 = ptx::mul2(ptx::fma2(make_float2(__uint_as_float(sv[4 * e]), __uint_as_float(sv[4 * e + 1])), scale2,
+                                                                  make_float2(__uint_as_float(nl.x), __uint_as_float(nl.y))), log2e2);
+                            const float2 y1 = ptx::mul2(ptx::fma2(make_float2(__uint_as_float(sv[4 * e + 2]), __uint_as_float(sv[4 * e + 3])), scale2,
+                                                                  make_float2(__uint_as_float(nl.z), __uint_as_float(nl.w))), log2e2);
+                            pr[4 * e] = ptx::ex2_approx(y0.x);
+                            pr[4 * e + 1] = ptx::ex2_approx(y0.y);
+                            pr[4 * e + 2] = ptx::ex2_approx(y1.x);
+                            pr[4 * e + 3] = ptx::ex2_approx(y1.y);
                         }
-                        if (c + 16 > limit) {
+                        if (tail || c0 + 16 > limit) {
+                            // lane l < 16: which of the warp's 32 keys column c0 + l sees
+                            uint32_t seen = 0u;
+                            if (lane < 16 && c0 + lane < limit) seen = seen_bits(p.bp, w.s, (i * kWtRows + c_first + c0 + lane) / p.bp.h, key - lane);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                if (c + e >= limit) pr[e] = 0.f;
-                        }
-                        if (tail) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (!((__shfl_sync(0xffffffffu, seen[c / 32], c % 32 + e) >> lane) & 1u)) pr[e] = 0.f;
+                                if (!((__shfl_sync(0xffffffffu, seen, e) >> lane) & 1u)) pr[e] = 0.f;
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) acc[e & 1] = ptx::add2(acc[e & 1], make_float2(pr[2 * e], pr[2 * e + 1]));
+                    };
+                    uint32_t sv0[16], sv1[16];
+                    if (limit > 0) SMLA_TMEM_LD16(s_at, sv0);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < limit; c0 += 32) {
+                        ptx::tmem_wait_ld16(sv0);
+                        if (c0 + 16 < limit) SMLA_TMEM_LD16(s_at + c0 + 16, sv1);
+                        add(sv0, c0);
+                        if (c0 + 16 < limit) {
+                            ptx::tmem_wait_ld16(sv1);
+                            if (c0 + 32 < limit) SMLA_TMEM_LD16(s_at + c0 + 32, sv0);
+                            add(sv1, c0 + 16);
+                        }
                     }
                     ptx::tc_fence_before();
                     __syncwarp();
