@@ -113,15 +113,4 @@ __device__ __forceinline__ int64_t share_of(int64_t x, int k, int n) {
     return x * k / n;
 }
 
-// A warp's fp8 rows of page i of a sequence, from `row` of the page on, and how many of them take part.
-struct Fp8Source {
-    const uint8_t* src;
-    int n;
-    __device__ __forceinline__ Fp8Source(const BatchParams& p, const Seq& s, int i, int page, int row)
-        : src(static_cast<const uint8_t*>(p.kv) + (static_cast<int64_t>(page) * kPage + row) * kFp8RowBytes), n(page_rows(p, s, i, page) - row) {}
-    __device__ __forceinline__ void prefetch(int rows) const {  // into L2
-        if (n > 0 && (threadIdx.x & 31) == 0) ptx::bulk_prefetch_l2(src, static_cast<uint32_t>(min(n, rows) * kFp8RowBytes));
-    }
-};
-
 }  // namespace smla

@@ -26,10 +26,11 @@
 // row has its NaN from S).
 //
 // fp8.  Shared memory has no room for a block's codes, so four more warps take them through registers: a warp has
-// 16 rows of its CTA's page, the next block's in flight as soon as this one's are written.  V is a copy of K: panels 0 .. 3 of a page are the even CTA's V tile of it, panels
-// 4 .. 7 the odd one's, in the same layout, so the TMA thread copies them there as they are, half of them
-// into the other CTA's shared memory.  (Expanded into a ring in global memory and loaded from there, a block
-// took 5.0 us: 11 TB/s of traffic through L2.)
+// 16 rows of its CTA's page, the next block's in flight as soon as this one's are written.  V is a copy of K:
+// panels 0 .. 3 of a page are the even CTA's V tile of it, panels 4 .. 7 the odd one's, in the same layout, so the
+// same warps copy them there once the last block's V has been multiplied, half of them into the other CTA's
+// shared memory.  (Expanded into a ring in global memory and loaded from there, a block took 5.0 us: 11 TB/s of
+// traffic through L2.  V by bulk copies between shared memories took 3000 to 4700 cycles for 32 KB.)
 //
 // Roles (384 threads, 512 with fp8):
 //   warps 0-7    softmax, rescaling and output: TMEM quadrant warp % 4, keys 32 (warp / 4) .. of a page
@@ -61,9 +62,7 @@ enum : int {
     kTbTail = kPbTail,           // +page of the block, own CTA: V of a page that has to be cleaned; fp8: of every page
     kTbDrain = kTbTail + 2,      // even CTA
     kTbMade = kTbDrain + 1,      // fp8, even CTA: both CTAs' K is expanded, and its rotated dims landed
-    kTbRows = kTbMade + 1,       // fp8, own CTA: this CTA's K is expanded
-    kTbCopied = kTbRows + 1,     // fp8, own CTA: both copies of this CTA's K have landed
-    kTbCount = kTbCopied + 1
+    kTbCount = kTbMade + 1
 };
 
 struct TrLayout {
@@ -181,42 +180,60 @@ struct TrWalk {
 // Whether page i holds positions that V has to be cleaned of: drafted rows, or the end.
 __device__ __forceinline__ bool tree_tail(const Seq& s, int i) { return (i + 1) * kPage > s.len && i * kPage < s.keys; }
 
-// Eight rows of an fp8 page on their way to the K tile: lane l has codes [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8) of
-// every row.  (The rotated dims come by TMA.)
+// An expansion warp's sixteen rows of an fp8 page on their way to the K tile, in four groups: lane l has codes
+// [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8) of every row, and of row l % 16 the scales of codes [128 (l / 16), ..) and
+// [256 + 128 (l / 16), ..).  (The rotated dims come by TMA.)
 struct TrCodes {
-    uint2 a[8], b[8];
-    __device__ __forceinline__ void load(const Fp8Source& from, int u0) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            a[u] = b[u] = make_uint2(0u, 0u);
-            if (u0 + u < from.n) {
-                const uint8_t* row = from.src + (u0 + u) * kFp8RowBytes;
-                a[u] = ptx::ld_nc_l1_v2(row + 8 * lane);
-                b[u] = ptx::ld_nc_l1_v2(row + 256 + 8 * lane);
-            }
-        }
-    }
-    // lane l: of row l % 16 the scales of codes [128 (l / 16), ..) and [256 + 128 (l / 16), ..)
-    __device__ __forceinline__ static float2 scales(const Fp8Source& from) {
+    uint2 a[kTrExpandRows], b[kTrExpandRows];
+    float2 sc;
+    __device__ __forceinline__ void load(const BatchParams& p, const Seq& s, int i, int page, int row) {
         static_assert(kTrExpandRows == 16, "a warp's rows and halves are its lanes");
         const int lane = threadIdx.x & 31;
-        if ((lane & 15) >= from.n) return make_float2(0.f, 0.f);
-        const float* s = reinterpret_cast<const float*>(from.src + (lane & 15) * kFp8RowBytes + 512) + (lane >> 4);
-        return make_float2(__ldg(s), __ldg(s + 2));
-    }
-    // rows u0 .. u0 + 7 of the warp's, to eight rows of the K tile from `to` on: codes x scale in fp32 rounded to
-    // bf16 as in the forward; chunk c of a panel's row r lies at 16 (c ^ r % 8), so each store is conflict-free
-    __device__ __forceinline__ void store(int u0, uint32_t to, const float2& sc) const {
-        const int lane = threadIdx.x & 31;
+        const int n = page_rows(p, s, i, page) - row;
+        const uint8_t* src = static_cast<const uint8_t*>(p.kv) + (static_cast<int64_t>(page) * kPage + row) * kFp8RowBytes;
+        const float* scales = reinterpret_cast<const float*>(src + (lane & 15) * kFp8RowBytes + 512) + (lane >> 4);
+        if (n >= kTrExpandRows) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const float sa = __shfl_sync(0xffffffffu, sc.x, (lane & 16) + u0 + u), sb = __shfl_sync(0xffffffffu, sc.y, (lane & 16) + u0 + u);
-            const uint32_t at = to + (lane >> 3) * kPfPanel + u * 128 + (((lane & 7) ^ u) << 4);
-            ptx::st_shared_v4(at, make_uint4(ptx::e4m3x2_scaled_bf16x2(a[u].x & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a[u].x >> 16, sa),
-                                             ptx::e4m3x2_scaled_bf16x2(a[u].y & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a[u].y >> 16, sa)));
-            ptx::st_shared_v4(at + 4 * kPfPanel, make_uint4(ptx::e4m3x2_scaled_bf16x2(b[u].x & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b[u].x >> 16, sb),
-                                                            ptx::e4m3x2_scaled_bf16x2(b[u].y & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b[u].y >> 16, sb)));
+            for (int u = 0; u < kTrExpandRows; ++u) {
+                a[u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 8 * lane);
+                b[u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 256 + 8 * lane);
+            }
+            sc = make_float2(__ldg(scales), __ldg(scales + 2));
+        } else {  // rows that take no part become zeros
+#pragma unroll
+            for (int u = 0; u < kTrExpandRows; ++u) {
+                a[u] = b[u] = make_uint2(0u, 0u);
+                if (u < n) {
+                    a[u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 8 * lane);
+                    b[u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 256 + 8 * lane);
+                }
+            }
+            sc = (lane & 15) < n ? make_float2(__ldg(scales), __ldg(scales + 2)) : make_float2(0.f, 0.f);
+        }
+    }
+    // All rows, to sixteen of the K tile from `to` on: codes x scale in fp32 rounded to bf16 as in the forward; chunk
+    // c of a panel's row r lies at 16 (c ^ r % 8), so each store is conflict-free.  A loop over the groups that moves
+    // the registers along: straight-line code for all rows is fetched more slowly than it runs (3100
+    // cycles a block).
+    __device__ __forceinline__ void store(uint32_t to) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t at0 = to + (lane >> 3) * kPfPanel;
+#pragma unroll 1
+        for (int u0 = 0; u0 < kTrExpandRows; u0 += 4) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float sa = __shfl_sync(0xffffffffu, sc.x, (lane & 16) + u0 + u), sb = __shfl_sync(0xffffffffu, sc.y, (lane & 16) + u0 + u);
+                const uint32_t at = at0 + (u0 + u) * 128 + (((lane & 7) ^ ((u0 & 4) + u)) << 4);
+                ptx::st_shared_v4(at, make_uint4(ptx::e4m3x2_scaled_bf16x2(a[u].x & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a[u].x >> 16, sa),
+                                                 ptx::e4m3x2_scaled_bf16x2(a[u].y & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a[u].y >> 16, sa)));
+                ptx::st_shared_v4(at + 4 * kPfPanel, make_uint4(ptx::e4m3x2_scaled_bf16x2(b[u].x & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b[u].x >> 16, sb),
+                                                                ptx::e4m3x2_scaled_bf16x2(b[u].y & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b[u].y >> 16, sb)));
+            }
+#pragma unroll
+            for (int u = 0; u < kTrExpandRows - 4; ++u) {
+                a[u] = a[u + 4];
+                b[u] = b[u + 4];
+            }
         }
     }
 };
@@ -251,8 +268,9 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             const bool by_warps = i == kPbSEmpty || i == kPbSEmpty + 1;                // both CTAs' softmax warps
             const bool by_half = i == kPbPFull || i == kPbPFull + 1;                   // those of the page
             const bool by_two = i == kPbQEmpty || i == kPbSFull || i == kPbSFull + 1;  // both S issuers
+            const bool by_page = KVF == 1 && (i == kTbTail || i == kTbTail + 1);       // the expansion warps of the page's CTA
             ptx::mbar_init(bar(i), by_warps ? 2 * kTrSoftmaxWarps : by_half ? kTrSoftmaxWarps : i == kTbMade ? 2 * kTrExpandWarps + 1
-                                   : i == kTbRows ? kTrExpandWarps : i == kTbDrain ? 3 : by_two || i == kTbCopied ? 2 : 1);
+                                   : by_page ? kTrExpandWarps : i == kTbDrain ? 3 : by_two ? 2 : 1);
         }
         ptx::fence_mbarrier_init();
     }
@@ -306,24 +324,6 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                 }
                 return true;
             };
-            // fp8: this CTA's page of block x, once expanded, from K to both CTAs' V; then word to the CTAs whose
-            // copies have landed here
-            auto copy_v = [&](int x) -> bool {
-                if (!wait(kTbRows, x & 1)) return false;
-                if (x > 0 && !wait(kPbVEmpty + rank, (x - 1) & 1)) return false;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) ptx::mbar_arrive_expect_tx(bar(kTbTail + i), static_cast<uint32_t>(kPfVPage));
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    ptx::bulk_copy_cluster(ptx::map_shared_rank(sbase + L::kOffV + rank * kPfVPage, c), sbase + L::kOffK + 4 * c * kPfPanel,
-                                           static_cast<uint32_t>(kPfVPage), ptx::map_shared_rank(bar(kTbTail + rank), c));
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (!wait(kTbTail + i, x & 1)) return false;
-                    ptx::mbar_arrive_cluster(ptx::map_shared_rank(bar(kTbCopied), i));
-                }
-                return true;
-            };
             // a page that is not there loads as zeros, from rows below 0
             auto first_row = [&](int page) -> int { return page_in_cache(p.bp, page) ? page * kPage : -kPage; };
             auto prefetch = [&](int i) {
@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                 const int pg = page_of(p.bp, w.b, w.s, i);
                 const int n = page_rows(p.bp, w.s, i, pg);
                 if (n > 0)
-                    ptx::bulk_prefetch_l2(static_cast<const __nv_bfloat16*>(p.bp.kv) + static_cast<int64_t>(pg) * kPage * kDQK,
-                                          static_cast<uint32_t>(n * kDQK * 2));
+                    ptx::bulk_prefetch_l2(static_cast<const char*>(p.bp.kv) + static_cast<int64_t>(pg) * kPage * (KVF ? kFp8RowBytes : kDQK * 2),
+                                          static_cast<uint32_t>(n * (KVF ? kFp8RowBytes : kDQK * 2)));
             };
             bool ok = true;
             int x = 0, piece = 0;
@@ -357,11 +357,12 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                                       even_bar(kPbQFull));
                 if constexpr (KVF == 1) {
                     for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
+                        if (b == w.b0) prefetch(2 * b + 2 + rank);
+                        prefetch(2 * b + 4 + rank);
                         if (x > 0 && !(ok = wait(kPbKEmpty + 1, (x - 1) & 1))) break;
                         if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kTbMade), 2u * kPfPanel);
                         ptx::tma_load_2d_pair(sbase + L::kOffK + 8 * kPfPanel, &tm_k, 528, first_row(page_of(p.bp, w.b, w.s, 2 * b + rank)),
                                               even_bar(kTbMade));
-                        ok = copy_v(x);
                     }
                     continue;
                 }
@@ -393,8 +394,8 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             // this CTA's barriers, before it leaves
             if (x > 0) {
                 for (int g = 0; ok && g < 2; ++g) ok = wait(kPbKEmpty + g, (x - 1) & 1);
-                if (KVF == 1 && ok) ok = wait(kTbCopied, (x - 1) & 1);
-                for (int i = 0; ok && i < 2; ++i) ok = wait(kPbVEmpty + i, (x - 1) & 1);
+                // (with fp8 the softmax warps see the last of these; this thread has not followed them)
+                for (int i = 0; KVF == 0 && ok && i < 2; ++i) ok = wait(kPbVEmpty + i, (x - 1) & 1);
                 if (ok) ok = wait(kPbQEmpty, (piece - 1) & 1);
             }
             if (!ok) {  // gave up: copies in flight complete on the other CTA's barriers; leave them time to land
@@ -500,36 +501,41 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             int x = 0;
             for (bool more = any; ok && more; more = w.next(p)) {
                 auto page = [&](int b) -> int { return b < w.b1 ? page_of(p.bp, w.b, w.s, 2 * b + rank) : -1; };
-                const Fp8Source cur(p.bp, w.s, 2 * w.b0 + rank, page(w.b0), row);
-                Fp8Source next(p.bp, w.s, 2 * w.b0 + 2 + rank, page(w.b0 + 1), row);
-                next.prefetch(kTrExpandRows);
-                TrCodes half0, half1;
-                half0.load(cur, 0);
-                half1.load(cur, 8);
-                float2 sc = TrCodes::scales(cur);
-                int pg = page(w.b0 + 2);
+                TrCodes codes;
+                codes.load(p.bp, w.s, 2 * w.b0 + rank, page(w.b0), row);
+                int pg = page(w.b0 + 1);
                 for (int b = w.b0; b < w.b1; ++b, ++x) {
-                    const Fp8Source after(p.bp, w.s, 2 * (b + 2) + rank, pg, row);
-                    after.prefetch(kTrExpandRows);
-                    pg = page(b + 3);
-                    // the last block's S has read the K tile, and its copies to V have
-                    if (x > 0 && !(ok = warp_wait(kPbKEmpty, (x - 1) & 1) && warp_wait(kPbKEmpty + 1, (x - 1) & 1) &&
-                                        warp_wait(kTbCopied, (x - 1) & 1)))
-                        break;
-                    const uint32_t to = sbase + L::kOffK + row * 128;
-                    half0.store(0, to, sc);
-                    half1.store(8, to + 8 * 128, sc);
+                    // the last block's S has read the K tile
+                    if (x > 0 && !(ok = warp_wait(kPbKEmpty, (x - 1) & 1) && warp_wait(kPbKEmpty + 1, (x - 1) & 1))) break;
+                    codes.store(sbase + L::kOffK + row * 128);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        ptx::mbar_arrive_cluster(even_bar(kTbMade));
-                        ptx::mbar_arrive(bar(kTbRows));
+                    if (lane == 0) ptx::mbar_arrive_cluster(even_bar(kTbMade));
+                    // V of the last block has been multiplied: panels 0 .. 3 of these rows to the even CTA's V tile, 4 .. 7 to
+                    // the odd one's
+                    if (x > 0 && !(ok = warp_wait(kPbVEmpty + rank, (x - 1) & 1))) break;
+#pragma unroll 1
+                    for (int pn = 0; pn < 8; ++pn) {
+                        const uint32_t from = sbase + L::kOffK + pn * kPfPanel + row * 128 + lane * 16;
+                        const uint32_t into = sbase + L::kOffV + rank * kPfVPage + (pn & 3) * kPfPanel + row * 128 + lane * 16;
+                        uint4 v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = ptx::ld_shared_v4(from + j * 512);
+                        if ((pn >> 2) == rank) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) ptx::st_shared_v4(into + j * 512, v[j]);
+                        } else {
+                            const uint32_t there = ptx::map_shared_rank(into, rank ^ 1);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) ptx::st_shared_cluster_v4(there + j * 512, v[j]);
+                        }
                     }
+                    ptx::fence_proxy_async_all();
+                    __syncwarp();
+                    if (lane < 2) ptx::mbar_arrive_release_cluster(ptx::map_shared_rank(bar(kTbTail + rank), lane));
                     // only now: a fence waits for the loads before it, too (5.3 us a block with these before it)
-                    half0.load(next, 0);
-                    half1.load(next, 8);
-                    sc = TrCodes::scales(next);
-                    next = after;
+                    codes.load(p.bp, w.s, 2 * b + 2 + rank, pg, row);
+                    pg = page(b + 2);
                 }
             }
         }
@@ -692,6 +698,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                         continue;
                     }
                     ++tails;
+                    if constexpr (KVF == 1) ptx::fence_acq_rel_cluster();  // (half of it is the other CTA's doing)
                 }
                 if (tail) {
                     // this CTA's V tile of the page, cleaned by the page's warps: rows past the end, and what
