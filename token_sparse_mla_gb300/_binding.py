@@ -623,10 +623,11 @@ def tree_workspace_bytes(T: int, h: int, seqs: int) -> int:
 
 def _batch(dev: torch.device, block_tables: torch.Tensor, lengths: torch.Tensor) -> Tuple[int, int]:
     """Sequences and blocks per sequence of a batch's tables."""
-    if block_tables.dim() != 2 or block_tables.dtype != _I32 or not block_tables.is_contiguous() or block_tables.shape[1] < 1:
+    shape = block_tables.shape
+    if len(shape) != 2 or shape[1] < 1 or block_tables.dtype is not _I32 or not block_tables.is_contiguous():
         raise ValueError("block_tables must be a contiguous [seqs, blocks] int32 tensor of at least one block")
-    seqs, blocks = block_tables.shape
-    if lengths.shape != (seqs,) or lengths.dtype != _I32 or not lengths.is_contiguous():
+    seqs, blocks = shape
+    if lengths.shape != (seqs,) or lengths.dtype is not _I32 or not lengths.is_contiguous():
         raise ValueError(f"lengths must be a contiguous [{seqs}] int32 tensor")
     if not dev == block_tables.device == lengths.device:
         _apart(dev, block_tables=block_tables, lengths=lengths)
@@ -635,17 +636,30 @@ def _batch(dev: torch.device, block_tables: torch.Tensor, lengths: torch.Tensor)
 
 def _tokens(dev: torch.device, T: int, seqs: int, starts: torch.Tensor, mask: Optional[torch.Tensor]):
     """Checks starts and the mask; the mask's pointer and words per token."""
-    if starts.shape != (seqs + 1,) or starts.dtype != _I32 or not starts.is_contiguous():
+    if starts.shape != (seqs + 1,) or starts.dtype is not _I32 or not starts.is_contiguous():
         raise ValueError(f"starts must be a contiguous [{seqs + 1}] int32 tensor")
     if starts.device != dev:
         _apart(dev, starts=starts)
     if mask is None:
         return None, 0
-    if mask.dim() != 2 or mask.shape[0] != T or mask.shape[1] < 1 or mask.dtype != _I32 or not mask.is_contiguous():
+    shape = mask.shape
+    if len(shape) != 2 or shape[0] != T or shape[1] < 1 or mask.dtype is not _I32 or not mask.is_contiguous():
         raise ValueError(f"mask must be a contiguous [{T}, words] int32 tensor of at least one word")
     if mask.device != dev:
         _apart(dev, mask=mask)
-    return mask.data_ptr(), mask.shape[1]
+    return mask.data_ptr(), shape[1]
+
+
+def _queries(q: torch.Tensor, kv_cache: torch.Tensor, kv_format: str) -> Tuple[torch.device, int, int, int]:
+    """The device, tokens, heads and cache rows of a call on a batch."""
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D_QK or q.dtype is not _BF16 or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous [T, h, 576] bf16 tensor, got {tuple(shape)} {q.dtype}")
+    num_slots = _cache_rows(kv_cache, kv_format)
+    dev = _cuda_device("q", q)
+    if kv_cache.device != dev:
+        _apart(dev, kv_cache=kv_cache)
+    return dev, shape[0], shape[1], num_slots
 
 
 def sparse_mla_tree(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tensor, lengths: torch.Tensor,
@@ -666,13 +680,7 @@ def sparse_mla_tree(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch
     for callers that keep one (calls that may overlap need their own); allocated here otherwise, from
     torch's allocator on the stream of the call, as out and lse are.
     """
-    if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != _BF16 or not q.is_contiguous():
-        raise ValueError(f"q must be a contiguous [T, h, 576] bf16 tensor, got {tuple(q.shape)} {q.dtype}")
-    T, h, _ = q.shape
-    num_slots = _cache_rows(kv_cache, kv_format)
-    dev = _cuda_device("q", q)
-    if kv_cache.device != dev:
-        _apart(dev, kv_cache=kv_cache)
+    dev, T, h, num_slots = _queries(q, kv_cache, kv_format)
     seqs, blocks = _batch(dev, block_tables, lengths)
     mask_ptr, words = _tokens(dev, T, seqs, starts, mask)
     if scale is None:
@@ -710,13 +718,7 @@ def sparse_mla_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: to
     it returned it.  weights [seqs, blocks * 64] fp32 are what earlier calls gathered (None: nothing yet);
     returns out of the same shape, which may be passed in and may be weights itself.
     """
-    if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != _BF16 or not q.is_contiguous():
-        raise ValueError(f"q must be a contiguous [T, h, 576] bf16 tensor, got {tuple(q.shape)} {q.dtype}")
-    T, h, _ = q.shape
-    num_slots = _cache_rows(kv_cache, kv_format)
-    dev = _cuda_device("q", q)
-    if kv_cache.device != dev:
-        _apart(dev, kv_cache=kv_cache)
+    dev, T, h, num_slots = _queries(q, kv_cache, kv_format)
     seqs, blocks = _batch(dev, block_tables, lengths)
     mask_ptr, words = _tokens(dev, T, seqs, starts, mask)
     if lse.shape != (T, h) or lse.dtype != _F32 or not lse.is_contiguous():

@@ -73,8 +73,8 @@ __device__ __forceinline__ uint32_t seen_bits(const BatchParams& p, const Seq& s
 // The first `n` of 32 bits (n may lie outside 0 .. 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
-// Sums of two values over the CTA's threads (at most 16 warps): of the threads before this one, and of all.
-// `scratch` holds 32 values, written only before the barrier and read only after it.
+// Sums of two values over the CTA's threads: of the threads before this one, and of all.  `scratch` holds two
+// values for every warp, written only before the barrier and read only after it.
 __device__ __forceinline__ void block_prefix2(int64_t x, int64_t y, int64_t* scratch, int warps, int64_t& x_before, int64_t& x_all,
                                               int64_t& y_before, int64_t& y_all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -1376,17 +1376,19 @@ smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* 
     cudaError_t e = fp8 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_kernel<1>, tm_q, tm_k, tm_v, tp)
                         : cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_kernel<0>, tm_q, tm_k, tm_v, tp);
     if (e != cudaSuccess) return cuda_fail(e, "tree kernel launch");
-    // the join: 64 / parts dims per CTA, as in the prefix attention
+    // the join: few cut tiles by 64 / parts dims per CTA, at most three CTAs per SM, as in the prefix attention; many
+    // by warps of 32 dims
     cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
     const int64_t groups = static_cast<int64_t>(pl.jobs) * pl.slot_groups;
     const int64_t most = static_cast<int64_t>(ds->num_sms) * 3;
-    const int parts = groups * 32 <= most ? 4 : groups * 16 <= most ? 2 : 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(groups * 8 * parts), 1, 1);
-    cfg.blockDim = dim3(smla::kPfMergeThreads, 1, 1);
-    cfg.dynamicSmemBytes = 0;
+    const int parts = groups * 32 <= most ? 4 : groups * 16 <= most ? 2 : groups * 8 <= most ? 1 : 0;
+    cfg.gridDim = dim3(static_cast<unsigned>(parts ? groups * 8 * parts : groups * 2), 1, 1);
+    cfg.blockDim = dim3(parts ? smla::kPfMergeThreads : smla::kTrJoinThreads, 1, 1);
     e = parts == 4   ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_merge_kernel<4>, tp)
         : parts == 2 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_merge_kernel<2>, tp)
-                     : cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_merge_kernel<1>, tp);
+        : parts == 1 ? cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_merge_kernel<1>, tp)
+                     : cudaLaunchKernelEx(&cfg, smla::sparse_mla_tree_join_kernel, tp);
     if (e != cudaSuccess) return cuda_fail(e, "tree merge kernel launch");
     return SMLA_OK;
 }
@@ -1421,7 +1423,7 @@ smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_
         r = fp8 ? byte_map(enc, &tm_k, kv_cache, num_slots, 128, smla::kPage, CU_TENSOR_MAP_SWIZZLE_128B)
                 : row_map(enc, &tm_k, kv_cache, num_slots, smla::kPage, 1);
     alignas(64) CUtensorMap tm_codes = tm_k;
-    if (r == CUDA_SUCCESS && fp8) r = byte_map(enc, &tm_codes, kv_cache, num_slots, 64, smla::kPage, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (r == CUDA_SUCCESS && fp8) r = byte_map(enc, &tm_codes, kv_cache, num_slots, 128, smla::kPage, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (r != CUDA_SUCCESS) return fail(SMLA_ERR_CUDA, "tensor maps for q/kv_cache failed (%d)", (int)r);
     smla::WtParams wp = {};
     wp.bp = batch_params(kv_cache, block_tables, lengths, starts, mask, T, h, seqs, blocks, mask_words, num_slots);

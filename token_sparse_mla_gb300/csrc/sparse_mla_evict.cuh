@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t weight_key(float x) { return x != x ? 0u : s
 __global__ void __launch_bounds__(kEvThreads) sparse_mla_evict_select_kernel(const EvParams p) {
     __shared__ __align__(16) uint32_t s_hist[2][kEvBins];
     __shared__ uint32_t s_warp[kEvWarps], s_warp2[kEvWarps];
-    __shared__ uint32_t s_sel[2];
+    __shared__ uint32_t s_sel[3];
     __shared__ uint32_t s_count[2];  // keys above the threshold (and rows kept in any case), keys at it
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kEvThreads) sparse_mla_evict_select_kernel(con
                         if (above < need && need <= above + c4[j]) {
                             s_sel[0] = static_cast<uint32_t>(kEvBins - 4 - 4 * tid + j);
                             s_sel[1] = above;
+                            s_sel[2] = c4[j];
                         }
                         above += c4[j];
                     }
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(kEvThreads) sparse_mla_evict_select_kernel(con
             prefix |= s_sel[0] << shift;
             pmask |= digit << shift;
             need -= s_sel[1];
+            if (s_sel[2] == need) break;  // every key with this prefix is kept: the digits below do not matter
             // (s_sel and s_warp are written again after the next digit's barriers)
         }
     }
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kEvThreads) sparse_mla_evict_select_kernel(con
         if (i >= seg1) return 0;
         if (i < mid0 || i >= mid1) return 2;
         if (pmask == 0u) return 0;  // nothing of the middle
-        const uint32_t key = weight_key(x);
+        const uint32_t key = weight_key(x) & pmask;
         return key > prefix ? 2 : key == prefix ? 1 : 0;
     };
     uint32_t over = 0u, equal = 0u;

@@ -25,19 +25,19 @@
 // past the end zeroed, values that are not finite in the drafted rows zeroed: a token that does see such a
 // row has its NaN from S).
 //
-// fp8.  Shared memory has no room for a block's codes, so four more warps take them through registers: a warp has
-// 16 rows of its CTA's page, the next block's in flight as soon as this one's are written.  V is a copy of K:
+// fp8.  Shared memory has no room for a block's codes, so eight more warps take them through registers: a warp has
+// eight rows of its CTA's page, the next block's in flight as soon as this one's are written.  V is a copy of K:
 // panels 0 .. 3 of a page are the even CTA's V tile of it, panels 4 .. 7 the odd one's, in the same layout, so the
 // same warps copy them there once the last block's V has been multiplied, half of them into the other CTA's
 // shared memory.  (Expanded into a ring in global memory and loaded from there, a block took 5.0 us: 11 TB/s of
 // traffic through L2.  V by bulk copies between shared memories took 3000 to 4700 cycles for 32 KB.)
 //
-// Roles (384 threads, 512 with fp8):
+// Roles (384 threads, 640 with fp8):
 //   warps 0-7    softmax, rescaling and output: TMEM quadrant warp % 4, keys 32 (warp / 4) .. of a page
 //   warp 8       TMA producer (one thread)
 //   warp 9       S issuer for dims 0 .. 319, and TMEM owner
 //   warp 10      PV issuer, warp 11 S issuer for dims 320 .. 575 (one thread of the even CTA each)
-//   warps 12-15  expansion of fp8 rows
+//   warps 12-19  expansion of fp8 rows
 // Every wait is bounded; a CTA that gives up meets the other at the final cluster barrier.
 #pragma once
 
@@ -48,7 +48,7 @@ namespace smla {
 
 constexpr int kTrSoftmaxWarps = 8;
 constexpr int kTrTmaWarp = 8, kTrS1Warp = 9, kTrPvWarp = 10, kTrS2Warp = 11, kTrExpandWarp = 12;
-constexpr int kTrExpandWarps = 4;
+constexpr int kTrExpandWarps = 8;
 constexpr int kTrExpandRows = kPage / kTrExpandWarps;
 constexpr int kTrTileCost = 3;   // what a piece costs beside its blocks, in blocks
 
@@ -56,6 +56,13 @@ template <int KVF>
 __host__ __device__ constexpr int tree_threads() {
     return 32 * (kTrExpandWarp + (KVF ? kTrExpandWarps : 0));
 }
+
+// Registers per thread with fp8: 640 threads are launched with 96 each, and the two warpgroups that expand give some
+// of theirs to the two of the softmax.  (More than the launch's total in all would wait forever.)
+constexpr int kTrRegsLaunch = 96, kTrRegsSoftmax = 120, kTrRegsExpand = 72;
+static_assert(tree_threads<1>() * kTrRegsLaunch <= 65536, "registers of a block");
+static_assert(32 * (kTrSoftmaxWarps * kTrRegsSoftmax + 4 * kTrRegsLaunch + kTrExpandWarps * kTrRegsExpand) <= tree_threads<1>() * kTrRegsLaunch,
+              "shares of the block's registers");
 
 // Barriers of the prefix kernel, then:
 enum : int {
@@ -180,18 +187,17 @@ struct TrWalk {
 // Whether page i holds positions that V has to be cleaned of: drafted rows, or the end.
 __device__ __forceinline__ bool tree_tail(const Seq& s, int i) { return (i + 1) * kPage > s.len && i * kPage < s.keys; }
 
-// An expansion warp's sixteen rows of an fp8 page on their way to the K tile, in four groups: lane l has codes
-// [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8) of every row, and of row l % 16 the scales of codes [128 (l / 16), ..) and
-// [256 + 128 (l / 16), ..).  (The rotated dims come by TMA.)
+// An expansion warp's eight rows of an fp8 page on their way to the K tile: lane l has codes [8l, 8l + 8) and
+// [256 + 8l, 256 + 8l + 8) of every row, and of row l % 8 the scales of codes [128 (l / 16), ..) and [256 + 128 (l / 16), ..).
+// (The rotated dims come by TMA.)
 struct TrCodes {
     uint2 a[kTrExpandRows], b[kTrExpandRows];
     float2 sc;
     __device__ __forceinline__ void load(const BatchParams& p, const Seq& s, int i, int page, int row) {
-        static_assert(kTrExpandRows == 16, "a warp's rows and halves are its lanes");
         const int lane = threadIdx.x & 31;
         const int n = page_rows(p, s, i, page) - row;
         const uint8_t* src = static_cast<const uint8_t*>(p.kv) + (static_cast<int64_t>(page) * kPage + row) * kFp8RowBytes;
-        const float* scales = reinterpret_cast<const float*>(src + (lane & 15) * kFp8RowBytes + 512) + (lane >> 4);
+        const float* scales = reinterpret_cast<const float*>(src + lane % kTrExpandRows * kFp8RowBytes + 512) + (lane >> 4);
         if (n >= kTrExpandRows) {
 #pragma unroll
             for (int u = 0; u < kTrExpandRows; ++u) {
@@ -208,13 +214,12 @@ struct TrCodes {
                     b[u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 256 + 8 * lane);
                 }
             }
-            sc = (lane & 15) < n ? make_float2(__ldg(scales), __ldg(scales + 2)) : make_float2(0.f, 0.f);
+            sc = lane % kTrExpandRows < n ? make_float2(__ldg(scales), __ldg(scales + 2)) : make_float2(0.f, 0.f);
         }
     }
-    // All rows, to sixteen of the K tile from `to` on: codes x scale in fp32 rounded to bf16 as in the forward; chunk
-    // c of a panel's row r lies at 16 (c ^ r % 8), so each store is conflict-free.  A loop over the groups that moves
-    // the registers along: straight-line code for all rows is fetched more slowly than it runs (3100
-    // cycles a block).
+    // All rows, to those of the K tile from `to` on: codes x scale in fp32 rounded to bf16 as in the forward; chunk
+    // c of a panel's row r lies at 16 (c ^ r % 8), so each store is conflict-free.  A loop over groups of four that
+    // moves the registers along: straight-line code for all rows is fetched more slowly than it runs.
     __device__ __forceinline__ void store(uint32_t to) {
         const int lane = threadIdx.x & 31;
         const uint32_t at0 = to + (lane >> 3) * kPfPanel;
@@ -295,10 +300,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
 
-    // fp8: 512 threads are launched with 128 registers each; the warps that issue give some of theirs to those that
-    // compute (2 * 136 + 104 + 136 = 4 * 128 for the four warpgroups)
     if (warp >= kTrSoftmaxWarps && warp < kTrExpandWarp) {
-    if constexpr (KVF == 1) ptx::regs_down<104>();
     if (warp == kTrTmaWarp) {
         // ================================================================ TMA producer
         TrWalk w(p, *start);
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
     } else if (warp >= kTrExpandWarp) {
         // ================================================================ expansion of fp8 rows
         if constexpr (KVF == 1) {
-            ptx::regs_up<136>();
+            ptx::regs_down<kTrRegsExpand>();
         TrWalk w(p, *start);
             const bool any = w.next(p);
             const int row = kTrExpandRows * (warp - kTrExpandWarp);
@@ -518,16 +520,16 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                     for (int pn = 0; pn < 8; ++pn) {
                         const uint32_t from = sbase + L::kOffK + pn * kPfPanel + row * 128 + lane * 16;
                         const uint32_t into = sbase + L::kOffV + rank * kPfVPage + (pn & 3) * kPfPanel + row * 128 + lane * 16;
-                        uint4 v[4];
+                        uint4 v[kTrExpandRows / 4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] = ptx::ld_shared_v4(from + j * 512);
+                        for (int j = 0; j < kTrExpandRows / 4; ++j) v[j] = ptx::ld_shared_v4(from + j * 512);
                         if ((pn >> 2) == rank) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) ptx::st_shared_v4(into + j * 512, v[j]);
+                            for (int j = 0; j < kTrExpandRows / 4; ++j) ptx::st_shared_v4(into + j * 512, v[j]);
                         } else {
                             const uint32_t there = ptx::map_shared_rank(into, rank ^ 1);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) ptx::st_shared_cluster_v4(there + j * 512, v[j]);
+                            for (int j = 0; j < kTrExpandRows / 4; ++j) ptx::st_shared_cluster_v4(there + j * 512, v[j]);
                         }
                     }
                     ptx::fence_proxy_async_all();
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
         }
     } else {
         // ================================================================ softmax / output
-        if constexpr (KVF == 1) ptx::regs_up<136>();
+        if constexpr (KVF == 1) ptx::regs_up<kTrRegsSoftmax>();
         TrWalk w(p, *start);
             const bool any = w.next(p);
         const int quad = warp & 3;
@@ -820,6 +822,71 @@ __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_tree_merge_kernel(
     if (live <= 0) return;
     const int64_t row0 = static_cast<int64_t>(job.x) + 32 * group;
     pf_join<PARTS>(p.part_o, p.part_ml, p.slot_groups, group, dg, job.z >> 1, job.w, job.z, live, p.out + row0 * kDV, p.lse + row0);
+}
+
+// The same where there are many cut tiles of few pieces each: a warp takes 32 rows (a lane each) and 32 dims,
+// two pieces' loads in flight, and stores its row's 64 bytes itself.  (As small CTAs that do 64 dims and meet
+// in shared memory, 2432 of them took 17 us for 8 sequences of 4096 rows, most of it the latency of four
+// waves.)
+constexpr int kTrJoinThreads = 256;
+
+__global__ void __launch_bounds__(kTrJoinThreads) sparse_mla_tree_join_kernel(const TrParams p) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = static_cast<int>(blockIdx.x & 1);  // of the dims
+    const int group = static_cast<int>(blockIdx.x >> 1) % p.slot_groups;
+    const int4 job = __ldg(p.job_list + static_cast<int>(blockIdx.x >> 1) / p.slot_groups);
+    const int live = min(job.y - 32 * group, 32);
+    if (live <= 0) return;
+    const int at = min(lane, live - 1);  // a lane past the last row repeats it and stores nothing
+    const int first = job.z >> 1, last = job.w, chunk = 64 * part + 8 * warp;
+    float m = -CUDART_INF_F, l = 0.f;
+    float4 acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = first; k <= last; k += 2) {
+        float mk[2], lk[2];
+        float4 v[2][8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int kk = min(k + u, last);
+            const int64_t g = static_cast<int64_t>(kk == first ? job.z : 2 * kk) * p.slot_groups + group;
+            mk[u] = k + u <= last ? __ldg(p.part_ml + 64 * g + at) : -CUDART_INF_F;
+            lk[u] = __ldg(p.part_ml + 64 * g + 32 + at);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[u][e] = __ldg(reinterpret_cast<const float4*>(p.part_o) + (g * 128 + chunk + e) * 32 + at);
+        }
+        const float mn = fmaxf(m, fmaxf(mk[0], mk[1]));
+        // a piece without a key has the sum 0 and zero rows: P was 0 and V had nothing that is not finite
+        const float keep = m == -CUDART_INF_F ? 0.f : ptx::ex2_approx(m - mn);
+        m = mn;
+        l *= keep;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (mk[u] == -CUDART_INF_F) continue;
+            const float wt = ptx::ex2_approx(mk[u] - m);
+            l += wt * lk[u];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                acc[e].x += wt * v[u][e].x;
+                acc[e].y += wt * v[u][e].y;
+                acc[e].z += wt * v[u][e].z;
+                acc[e].w += wt * v[u][e].w;
+            }
+        }
+    }
+    if (lane >= live) return;
+    const int64_t row = static_cast<int64_t>(job.x) + 32 * group + lane;
+    const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+    if (chunk == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+    uint4* out = reinterpret_cast<uint4*>(p.out + row * kDV + 4 * chunk);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+        out[e / 2] = make_uint4(ptx::cvt_bf16x2(acc[e].x * inv, acc[e].y * inv), ptx::cvt_bf16x2(acc[e].z * inv, acc[e].w * inv),
+                                ptx::cvt_bf16x2(acc[e + 1].x * inv, acc[e + 1].y * inv), ptx::cvt_bf16x2(acc[e + 1].z * inv, acc[e + 1].w * inv));
 }
 
 }  // namespace smla

@@ -18,22 +18,22 @@
 // Both operands have the same layout (rows x 9 panels, SW128), so the two forms differ in who loads what and in
 // which descriptor is A.  The ring's depth sets the pace where the operand streams (64 KB in flight per CTA gave
 // 42 GB/s per SM, from HBM and from L2 alike), so it takes what the other operand leaves: eight stages if no
-// sequence of the batch has more than 128 rows, else five (with fp8 six and four, beside the codes).
+// sequence of the batch has more than 128 rows, else five (with fp8 six and three, beside the codes).
 //
 // Work: tiles of 256 keys, each whole in one pair, in equal shares of their cost (kWt... below).
 //
-// fp8 codes come by TMA, 64 of every row at a time, into a ring of their own, and four more warps expand them, each 32
-// of the CTA's 128 keys, panel by panel into the ring of panels (or the operand that stays); the rotated dims come by
-// TMA as they are.  (Codes loaded into registers: 7 us a tile, because the fence after a panel's stores waits
-// for the loads that are meant to run ahead.  Expanded into global memory and loaded from there: 6.4 us, L2 took
-// the writes no faster.)
+// fp8 codes come by TMA, 128 of every row at a time, into a ring of their own, and eight more warps expand them, each
+// 16 of the CTA's 128 keys, two panels at a time into the ring of panels (or the operand that stays); the rotated
+// dims come by TMA as they are.  (Codes loaded into registers: 7 us a tile, because the fence after a panel's
+// stores waits for the loads that are meant to run ahead.  Expanded into global memory and loaded from there:
+// 6.4 us, L2 took the writes no faster.  One panel at a time: 4.4.)
 //
-// Roles (384 threads, 512 with fp8):
+// Roles (384 threads, 640 with fp8):
 //   warps 0-7    sums: TMEM quadrant warp % 4 (32 keys), half warp / 4 of the tile's columns
 //   warp 8       TMA producer (one thread)
 //   warp 9       MMA issuer (one thread of the even CTA), and TMEM owner
 //   warps 10-11  the elements without work: positions past the end, sequences without tokens
-//   warps 12-15  expansion of fp8 rows
+//   warps 12-19  expansion of fp8 rows
 // Every wait is bounded; a CTA that gives up meets the other at the final cluster barrier.
 #pragma once
 
@@ -46,18 +46,14 @@ constexpr int kWtHalf = 128;      // per CTA
 constexpr int kWtRows = 256;      // rows (token, head) per tile
 // stages of the ring, and of the ring of fp8 codes; Few: no sequence has more than kWtRowsFew rows
 constexpr int kWtStages = 5, kWtStagesFew = 8;
-constexpr int kWtStagesFp8 = 4, kWtStagesFewFp8 = 7;
-constexpr int kWtRaw = 2, kWtRawFew = 5;
-// The producer fills every ninth stage of an fp8 tile (the rotated dims) and waits for that stage's last release by
-// its parity, so the release before that one must be known: the codes of panel 7 - kWtRaw have been
-// expanded by then, and for that the stage kWtRaw + 1 places ahead of it had been released.
-static_assert(kWtRaw < kWtStagesFp8 && kWtRawFew < kWtStagesFewFp8, "parities of the ring");
-constexpr int kWtRawPanel = 128 * 64;  // 128 rows x 64 codes
+constexpr int kWtStagesFp8 = 3, kWtStagesFewFp8 = 6;
+constexpr int kWtRaw = 2, kWtRawFew = 3;  // 128 rows x 128 codes each: two panels
 constexpr int kWtRowsFew = 128;      // rows of a sequence up to which the deeper ring has room
 constexpr int kWtPanel = 128 * 128;  // 128 rows x 64 bf16, SW128
 constexpr int kWtSumWarps = 8;
 constexpr int kWtTmaWarp = 8, kWtMmaWarp = 9, kWtFillWarp = 10, kWtExpandWarp = 12;
-constexpr int kWtExpandWarps = 4;
+constexpr int kWtExpandWarps = 8;
+constexpr int kWtExpandRows = kWtHalf / kWtExpandWarps;  // 16
 // costs in tenths of a microsecond: a sequence's queries and first keys; a tile whose keys stream; one whose
 // keys stay, and each of its row tiles
 constexpr int kWtCostSeq = 30, kWtCostStream = 34, kWtCostStay = 20, kWtCostRows = 24;
@@ -88,7 +84,7 @@ struct WtLayout {
     static constexpr int kOffLse = kOffRing + kWtStages * kWtPanel;  // [2][256]: minus the rows' LSE
     static constexpr int kOffRaw = kOffRing + kWtStagesFp8 * kWtPanel, kOffRawFew = kOffRingFew + kWtStagesFewFp8 * kWtPanel;
     static_assert(kOffRingFew + kWtStagesFew * kWtPanel <= kOffLse, "ring");
-    static_assert(kOffRaw + kWtRaw * kWtRawPanel <= kOffLse && kOffRawFew + kWtRawFew * kWtRawPanel <= kOffLse, "codes");
+    static_assert(kOffRaw + kWtRaw * kWtPanel <= kOffLse && kOffRawFew + kWtRawFew * kWtPanel <= kOffLse, "codes");
     static constexpr int kOffX = kOffLse + 2 * kWtRows * 4;          // [128]: sums of the columns' second half; the plan's sums
     static constexpr int kOffBar = kOffX + kWtHalf * 4;
     static constexpr int kOffMisc = kOffBar + kWbCount * 8;          // tmem base, abort flag, the run's start
@@ -295,10 +291,6 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbFull + st.at), 2u * kWtPanel);
                 return true;
             };
-            auto load_rope = [&](uint32_t dst, uint32_t b) {
-                ptx::tma_load_2d_pair(dst, &tm_k, 528, row0, b);
-                ptx::tma_load_2d_pair(dst + kWtPanel / 2, &tm_k, 528, row1, b);
-            };
             auto load_keys = [&](uint32_t dst, int pn, uint32_t b) {
                 ptx::tma_load_3d_pair(dst, &tm_k, 0, row0, pn, b);
                 ptx::tma_load_3d_pair(dst + kWtPanel / 2, &tm_k, 0, row1, pn, b);
@@ -313,15 +305,16 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                                           static_cast<uint32_t>(n * (KVF ? kFp8RowBytes : kDQK * 2)));
             };
             WtStage raw_st(raw_stages);
-            auto load_codes = [&](int pn) -> bool {  // panel pn's
+            auto load_codes = [&](int pair) -> bool {  // those of panels 2 pair and 2 pair + 1
                 if (raw_st.used() && !wait(kWbRawEmpty + raw_st.at, raw_st.last())) return false;
-                const uint32_t dst = raw + raw_st.at * kWtRawPanel, b = bar(kWbRawFull + raw_st.at);
-                ptx::mbar_arrive_expect_tx(b, static_cast<uint32_t>(kWtRawPanel));
-                ptx::tma_load_2d(dst, &tm_codes, 64 * pn, row0, b);
-                ptx::tma_load_2d(dst + kWtRawPanel / 2, &tm_codes, 64 * pn, row1, b);
+                const uint32_t dst = raw + raw_st.at * kWtPanel, b = bar(kWbRawFull + raw_st.at);
+                ptx::mbar_arrive_expect_tx(b, static_cast<uint32_t>(kWtPanel));
+                ptx::tma_load_2d(dst, &tm_codes, 128 * pair, row0, b);
+                ptx::tma_load_2d(dst + kWtPanel / 2, &tm_codes, 128 * pair, row1, b);
                 raw_st.next();
                 return true;
             };
+            bool others = false;  // the last piece's keys stayed
             for (bool more = any; ok && more; more = w.next(p)) {
                 const bool stream_keys = w.row_tiles == 1;
                 const int q0 = w.s.first * p.bp.h;
@@ -334,6 +327,10 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                             ptx::tma_load_3d_pair(sbase + L::kOffStay + pn * stay_panel + half * kWtPanel / 2, &tm_q, 0,
                                                   row + half * kPage, pn, even_bar(kWbStayFull));
                 }
+                // the stages that the expansion warps filled have been used before this thread fills them: barriers that it
+                // does not follow could be more than one phase behind, which a parity cannot tell
+                if (KVF == 1 && !stream_keys && !others && stays > 0 && !(ok = wait(kWbStayEmpty, (stays - 1) & 1))) break;
+                others = !stream_keys;
                 for (int k = w.k0; ok && k < w.k1; ++k) {
                     const int i_page = 4 * k + 2 * rank;
                     row0 = first_row(page_of(p.bp, w.b, w.s, i_page));
@@ -342,20 +339,17 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                         prefetch(i_page + 4);
                         prefetch(i_page + 5);
                     }
+                    if (KVF == 1)
+                        for (int pair = 0; ok && pair < 4; ++pair) ok = load_codes(pair);
+                    if (!ok) break;
                     if (stream_keys) {
-                        for (int pn = 0; ok && pn < kPanels; ++pn, st.next()) {
-                            if (KVF == 1 && pn < kPanels - 1) ok = load_codes(pn);
-                            else if (!(ok = begin_stage())) break;
-                            else if (KVF == 1) load_rope(ring + st.at * kWtPanel, even_bar(kWbFull + st.at));
-                            else load_keys(ring + st.at * kWtPanel, pn, even_bar(kWbFull + st.at));
-                        }
+                        for (int pn = 0; ok && pn < kPanels; ++pn, st.next())
+                            if (KVF == 0 && (ok = begin_stage())) load_keys(ring + st.at * kWtPanel, pn, even_bar(kWbFull + st.at));
                     } else {
-                        if (!(ok = begin_stay())) break;
                         if (KVF == 1) {
-                            if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbStayMade), 2u * kWtPanel);
-                            load_rope(sbase + L::kOffStay + (kPanels - 1) * kWtPanel, even_bar(kWbStayMade));
-                            for (int pn = 0; ok && pn < kPanels - 1; ++pn) ok = load_codes(pn);
+                            ++stays;  // the expansion warps'
                         } else {
+                            if (!(ok = begin_stay())) break;
                             if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kWbStayFull), 2u * kPanels * kWtPanel);
                             for (int pn = 0; pn < kPanels; ++pn) load_keys(sbase + L::kOffStay + pn * kWtPanel, pn, even_bar(kWbStayFull));
                         }
@@ -436,7 +430,7 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
     } else if (warp >= kWtExpandWarp) {
         // ================================================================ expansion of fp8 rows
         if constexpr (KVF == 1) {
-            const int row = 32 * (warp - kWtExpandWarp);  // this warp's first of the CTA's 128 keys
+            const int row = kWtExpandRows * (warp - kWtExpandWarp);  // this warp's first of the CTA's 128 keys
             bool ok = true, others = false;  // the last piece's keys stayed
             int stays = 0;
             WtStage st(stages), raw_st(raw_stages);
@@ -451,62 +445,91 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                     if (stays > 0 && !(ok = warp_wait(kWbStayEmpty, (stays - 1) & 1))) break;
                 }
                 others = !stream_keys;
-                // lane l: rows 8 i + l / 4 of the warp's, their scales, and of each row 16 of a panel's codes from 16 (l % 4) on
-                float4 sc[4];
-                auto scales = [&](int k) {
-                    const int i_page = 4 * k + 2 * rank + row / kPage;
-                    const int page = k < w.k1 ? page_of(p.bp, w.b, w.s, i_page) : -1;
-                    const int n = page_rows(p.bp, w.s, i_page, page) - row % kPage;
-                    const uint8_t* src = static_cast<const uint8_t*>(p.bp.kv) + (static_cast<int64_t>(page) * kPage + row % kPage) * kFp8RowBytes + 512;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 8 * i + (lane >> 2);
-                        sc[i] = r < n ? __ldg(reinterpret_cast<const float4*>(src + r * kFp8RowBytes)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
+                // Lane l has the scales of row l % 16 of the warp's; of the codes, 16 from 16 (l % 8) on of a pair of panels, in rows
+                // 4 i + l / 8.
+                auto page = [&](int k, int i) -> int { return k < w.k1 ? page_of(p.bp, w.b, w.s, 4 * k + 2 * rank + i) : -1; };
+                auto scales = [&](int k, int pg) -> float4 {
+                    const int n = page_rows(p.bp, w.s, 4 * k + 2 * rank + row / kPage, pg) - row % kPage, r = lane % kWtExpandRows;
+                    const uint8_t* src = static_cast<const uint8_t*>(p.bp.kv) + (static_cast<int64_t>(pg) * kPage + row % kPage + r) * kFp8RowBytes;
+                    return r < n ? __ldg(reinterpret_cast<const float4*>(src + 512)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 };
-                scales(w.k0);
+                const int part = lane & 7, rr = lane >> 3;
+                const bool second = part >= 4;  // of the two panels
+                int pg0 = page(w.k0, 0), pg1 = page(w.k0, 1);
+                float4 sc = scales(w.k0, row < kPage ? pg0 : pg1);
                 for (int k = w.k0; ok && k < w.k1; ++k) {
+                    // the rotated dims, by this CTA's first expansion warp
+                    auto load_rope = [&](uint32_t dst, int i) {
+                        if (lane == 0) {
+                            if (rank == 0) ptx::mbar_arrive_expect_tx(bar(i), 2u * kWtPanel);
+                            ptx::tma_load_2d_pair(dst, &tm_k, 528, page_in_cache(p.bp, pg0) ? pg0 * kPage : -kPage, even_bar(i));
+                            ptx::tma_load_2d_pair(dst + kWtPanel / 2, &tm_k, 528, page_in_cache(p.bp, pg1) ? pg1 * kPage : -kPage, even_bar(i));
+                        }
+                        __syncwarp();
+                    };
                     if (!stream_keys) {
                         if (stays > 0 && !(ok = warp_wait(kWbStayEmpty, (stays - 1) & 1))) break;
                         ++stays;
+                        if (warp == kWtExpandWarp) load_rope(sbase + L::kOffStay + (kPanels - 1) * kWtPanel, kWbStayMade);
                     }
 #pragma unroll 1
-                    for (int pn = 0; pn < kPanels - 1; ++pn) {
+                    for (int pair = 0; pair < 4; ++pair) {
                         if (!(ok = warp_wait(kWbRawFull + raw_st.at, raw_st.round & 1))) break;
-                        uint4 v[4];
+                        uint4 v[kWtExpandRows / 4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = ptx::ld_shared_v4(raw + raw_st.at * kWtRawPanel + (row + 8 * i) * 64 + lane * 16);
-                        if (stream_keys && st.used() && !(ok = warp_wait(kWbEmpty + st.at, st.last()))) break;
-                        const uint32_t dst = (stream_keys ? ring + st.at * kWtPanel : sbase + L::kOffStay + pn * kWtPanel) + row * 128;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float s = sc[i].x;
-                            if (pn & 1) sc[i] = make_float4(sc[i].y, sc[i].z, sc[i].w, 0.f);  // the next tile of 128
-                            const int r = 8 * i + (lane >> 2), c = 2 * (lane & 3);  // chunk c of row r lies at 16 (c ^ r % 8)
-                            ptx::st_shared_v4(dst + r * 128 + ((c ^ (r & 7)) << 4),
-                                              make_uint4(ptx::e4m3x2_scaled_bf16x2(v[i].x & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(v[i].x >> 16, s),
-                                                         ptx::e4m3x2_scaled_bf16x2(v[i].y & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(v[i].y >> 16, s)));
-                            ptx::st_shared_v4(dst + r * 128 + (((c + 1) ^ (r & 7)) << 4),
-                                              make_uint4(ptx::e4m3x2_scaled_bf16x2(v[i].z & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(v[i].z >> 16, s),
-                                                         ptx::e4m3x2_scaled_bf16x2(v[i].w & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(v[i].w >> 16, s)));
+                        for (int i = 0; i < kWtExpandRows / 4; ++i) v[i] = ptx::ld_shared_v4(raw + raw_st.at * kWtPanel + (row + 4 * i) * 128 + lane * 16);
+                        uint32_t dst;
+                        WtStage st2 = st;
+                        if (stream_keys) {
+                            st2.next();
+                            if (st.used() && !(ok = warp_wait(kWbEmpty + st.at, st.last()))) break;
+                            if (st2.used() && !(ok = warp_wait(kWbEmpty + st2.at, st2.last()))) break;
+                            dst = ring + (second ? st2.at : st.at) * kWtPanel;
+                        } else {
+                            dst = sbase + L::kOffStay + (2 * pair + second) * kWtPanel;
                         }
+                        dst += row * 128;
+#pragma unroll
+                        for (int i = 0; i < kWtExpandRows / 4; ++i) {
+                            // chunk c of row r lies at 16 (c ^ r % 8); the lanes of the second panel store their two chunks in the
+                            // other order, so that the eight lanes of a row hit all banks
+                            const int r = 4 * i + rr, c = 2 * (part & 3);
+                            const float s = __shfl_sync(0xffffffffu, sc.x, r);
+                            const uint32_t x0 = second ? v[i].z : v[i].x, y0 = second ? v[i].w : v[i].y;
+                            const uint32_t x1 = second ? v[i].x : v[i].z, y1 = second ? v[i].y : v[i].w;
+                            ptx::st_shared_v4(dst + r * 128 + (((c + second) ^ (r & 7)) << 4),
+                                              make_uint4(ptx::e4m3x2_scaled_bf16x2(x0 & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(x0 >> 16, s),
+                                                         ptx::e4m3x2_scaled_bf16x2(y0 & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(y0 >> 16, s)));
+                            ptx::st_shared_v4(dst + r * 128 + (((c + !second) ^ (r & 7)) << 4),
+                                              make_uint4(ptx::e4m3x2_scaled_bf16x2(x1 & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(x1 >> 16, s),
+                                                         ptx::e4m3x2_scaled_bf16x2(y1 & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(y1 >> 16, s)));
+                        }
+                        sc = make_float4(sc.y, sc.z, sc.w, 0.f);
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
-                            ptx::mbar_arrive(bar(kWbRawEmpty + raw_st.at));
-                            if (stream_keys) ptx::mbar_arrive_cluster(even_bar(kWbMade + st.at));
-                        }
+                        if (lane == 0) ptx::mbar_arrive(bar(kWbRawEmpty + raw_st.at));
                         raw_st.next();
-                        if (stream_keys) st.next();
+                        if (stream_keys) {
+                            if (lane < 2) ptx::mbar_arrive_cluster(even_bar(kWbMade + (lane ? st2.at : st.at)));
+                            st = st2;
+                            st.next();
+                        }
                     }
                     if (!ok) break;
-                    scales(k + 1);  // after the last fence, which would wait for them
                     if (stream_keys) {
-                        st.next();  // the rotated dims' stage, the producer's
+                        if (warp == kWtExpandWarp) {
+                            if (st.used() && !(ok = warp_wait(kWbEmpty + st.at, st.last()))) break;
+                            load_rope(ring + st.at * kWtPanel, kWbFull + st.at);
+                        }
+                        st.next();
                     } else {
                         if (lane == 0) ptx::mbar_arrive_cluster(even_bar(kWbStayMade));
                         for (int i = 0; i < w.row_tiles * kPanels; ++i) st.next();
                     }
+                    // (after the last fence, which would wait for these)
+                    pg0 = page(k + 1, 0);
+                    pg1 = page(k + 1, 1);
+                    sc = scales(k + 1, row < kPage ? pg0 : pg1);
                 }
                 if (stream_keys) ++stays;  // the queries, the producer's
             }
