@@ -25,12 +25,13 @@
 // past the end zeroed, values that are not finite in the drafted rows zeroed: a token that does see such a
 // row has its NaN from S).
 //
-// fp8.  Shared memory has no room for a block's codes, so eight more warps take them through registers: a warp has
-// eight rows of its CTA's page, the next block's in flight as soon as this one's are written.  V is a copy of K:
-// panels 0 .. 3 of a page are the even CTA's V tile of it, panels 4 .. 7 the odd one's, in the same layout, so the
-// same warps copy them there once the last block's V has been multiplied, half of them into the other CTA's
-// shared memory.  (Expanded into a ring in global memory and loaded from there, a block took 5.0 us: 11 TB/s of
-// traffic through L2.  V by bulk copies between shared memories took 3000 to 4700 cycles for 32 KB.)
+// fp8.  Shared memory has no room for a block's codes, so eight more warps take them through registers, eight rows of
+// each page a warp, the next block's in flight as soon as this one's are written: its own page into K, as the MMA
+// wants it, and its dims of both pages into V, once the last block's V has been multiplied (those of its own
+// page are copied from K).  So half of the codes are converted in both CTAs.  (Expanded into a ring in global
+// memory and loaded from there, a block took 5.0 us: 11 TB/s of traffic through L2.  The other CTA's half of V
+// from its K: by bulk copies 3000 to 4700 cycles for 32 KB, by stores into its shared memory 2000, and 3000
+// more until a fence and a release had waited for them.)
 //
 // Roles (384 threads, 640 with fp8):
 //   warps 0-7    softmax, rescaling and output: TMEM quadrant warp % 4, keys 32 (warp / 4) .. of a page
@@ -57,11 +58,11 @@ __host__ __device__ constexpr int tree_threads() {
     return 32 * (kTrExpandWarp + (KVF ? kTrExpandWarps : 0));
 }
 
-// Registers per thread with fp8: 640 threads are launched with 96 each, and the two warpgroups that expand give some
+// Registers per thread with fp8: 640 threads are launched with 96 each, and the warpgroups that issue and expand give some
 // of theirs to the two of the softmax.  (More than the launch's total in all would wait forever.)
-constexpr int kTrRegsLaunch = 96, kTrRegsSoftmax = 120, kTrRegsExpand = 72;
+constexpr int kTrRegsLaunch = 96, kTrRegsSoftmax = 112, kTrRegsIssue = 80, kTrRegsExpand = 88;
 static_assert(tree_threads<1>() * kTrRegsLaunch <= 65536, "registers of a block");
-static_assert(32 * (kTrSoftmaxWarps * kTrRegsSoftmax + 4 * kTrRegsLaunch + kTrExpandWarps * kTrRegsExpand) <= tree_threads<1>() * kTrRegsLaunch,
+static_assert(32 * (kTrSoftmaxWarps * kTrRegsSoftmax + 4 * kTrRegsIssue + kTrExpandWarps * kTrRegsExpand) <= tree_threads<1>() * kTrRegsLaunch,
               "shares of the block's registers");
 
 // Barriers of the prefix kernel, then:
@@ -187,57 +188,59 @@ struct TrWalk {
 // Whether page i holds positions that V has to be cleaned of: drafted rows, or the end.
 __device__ __forceinline__ bool tree_tail(const Seq& s, int i) { return (i + 1) * kPage > s.len && i * kPage < s.keys; }
 
-// An expansion warp's eight rows of an fp8 page on their way to the K tile: lane l has codes [8l, 8l + 8) and
-// [256 + 8l, 256 + 8l + 8) of every row, and of row l % 8 the scales of codes [128 (l / 16), ..) and [256 + 128 (l / 16), ..).
-// (The rotated dims come by TMA.)
+// An expansion warp's eight rows of an fp8 page, kParts * 256 codes of each, on their way to shared memory: lane l has codes
+// [8l, 8l + 8) of every part, and of row l % 8 the scales of codes [128 (l / 16), ..) of every part.  (The rotated
+// dims come by TMA.)
+template <int kParts>
 struct TrCodes {
-    uint2 a[kTrExpandRows], b[kTrExpandRows];
-    float2 sc;
-    __device__ __forceinline__ void load(const BatchParams& p, const Seq& s, int i, int page, int row) {
+    uint2 a[kParts][kTrExpandRows];
+    float sc[kParts];
+    // rows from `row` on of page i, codes from `first` (of the row's 512) on
+    __device__ __forceinline__ void load(const BatchParams& p, const Seq& s, int i, int page, int row, int first) {
         const int lane = threadIdx.x & 31;
         const int n = page_rows(p, s, i, page) - row;
         const uint8_t* src = static_cast<const uint8_t*>(p.kv) + (static_cast<int64_t>(page) * kPage + row) * kFp8RowBytes;
-        const float* scales = reinterpret_cast<const float*>(src + lane % kTrExpandRows * kFp8RowBytes + 512) + (lane >> 4);
+        const float* scales = reinterpret_cast<const float*>(src + lane % kTrExpandRows * kFp8RowBytes + 512) + first / 128 + (lane >> 4);
+        src += first + 8 * lane;
         if (n >= kTrExpandRows) {
 #pragma unroll
-            for (int u = 0; u < kTrExpandRows; ++u) {
-                a[u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 8 * lane);
-                b[u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 256 + 8 * lane);
+            for (int e = 0; e < kParts; ++e) {
+#pragma unroll
+                for (int u = 0; u < kTrExpandRows; ++u) a[e][u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 256 * e);
+                sc[e] = ptx::ld_nc_f32(scales + 2 * e);
             }
-            sc = make_float2(__ldg(scales), __ldg(scales + 2));
         } else {  // rows that take no part become zeros
 #pragma unroll
-            for (int u = 0; u < kTrExpandRows; ++u) {
-                a[u] = b[u] = make_uint2(0u, 0u);
-                if (u < n) {
-                    a[u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 8 * lane);
-                    b[u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 256 + 8 * lane);
+            for (int e = 0; e < kParts; ++e) {
+#pragma unroll
+                for (int u = 0; u < kTrExpandRows; ++u) {
+                    a[e][u] = make_uint2(0u, 0u);
+                    if (u < n) a[e][u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 256 * e);
                 }
+                sc[e] = lane % kTrExpandRows < n ? ptx::ld_nc_f32(scales + 2 * e) : 0.f;
             }
-            sc = lane % kTrExpandRows < n ? make_float2(__ldg(scales), __ldg(scales + 2)) : make_float2(0.f, 0.f);
         }
     }
-    // All rows, to those of the K tile from `to` on: codes x scale in fp32 rounded to bf16 as in the forward; chunk
-    // c of a panel's row r lies at 16 (c ^ r % 8), so each store is conflict-free.  A loop over groups of four that
-    // moves the registers along: straight-line code for all rows is fetched more slowly than it runs.
+    // All rows, to those of a tile from `to` on, four panels a part: codes x scale in fp32 rounded to bf16 as in the
+    // forward; chunk c of a panel's row r lies at 16 (c ^ r % 8), so each store is conflict-free.  A loop over groups of
+    // four that moves the registers along: straight-line code for all rows is fetched more slowly than it runs.
     __device__ __forceinline__ void store(uint32_t to) {
         const int lane = threadIdx.x & 31;
         const uint32_t at0 = to + (lane >> 3) * kPfPanel;
 #pragma unroll 1
         for (int u0 = 0; u0 < kTrExpandRows; u0 += 4) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float sa = __shfl_sync(0xffffffffu, sc.x, (lane & 16) + u0 + u), sb = __shfl_sync(0xffffffffu, sc.y, (lane & 16) + u0 + u);
-                const uint32_t at = at0 + (u0 + u) * 128 + (((lane & 7) ^ ((u0 & 4) + u)) << 4);
-                ptx::st_shared_v4(at, make_uint4(ptx::e4m3x2_scaled_bf16x2(a[u].x & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a[u].x >> 16, sa),
-                                                 ptx::e4m3x2_scaled_bf16x2(a[u].y & 0xFFFFu, sa), ptx::e4m3x2_scaled_bf16x2(a[u].y >> 16, sa)));
-                ptx::st_shared_v4(at + 4 * kPfPanel, make_uint4(ptx::e4m3x2_scaled_bf16x2(b[u].x & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b[u].x >> 16, sb),
-                                                                ptx::e4m3x2_scaled_bf16x2(b[u].y & 0xFFFFu, sb), ptx::e4m3x2_scaled_bf16x2(b[u].y >> 16, sb)));
-            }
+            for (int e = 0; e < kParts; ++e) {
 #pragma unroll
-            for (int u = 0; u < kTrExpandRows - 4; ++u) {
-                a[u] = a[u + 4];
-                b[u] = b[u + 4];
+                for (int u = 0; u < 4; ++u) {
+                    const float s = __shfl_sync(0xffffffffu, sc[e], (lane & 16) + u0 + u);
+                    const uint2 x = a[e][u];
+                    ptx::st_shared_v4(at0 + 4 * e * kPfPanel + (u0 + u) * 128 + (((lane & 7) ^ ((u0 & 4) + u)) << 4),
+                                      make_uint4(ptx::e4m3x2_scaled_bf16x2(x.x & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(x.x >> 16, s),
+                                                 ptx::e4m3x2_scaled_bf16x2(x.y & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(x.y >> 16, s)));
+                }
+#pragma unroll
+                for (int u = 0; u < kTrExpandRows - 4; ++u) a[e][u] = a[e][u + 4];
             }
         }
     }
@@ -301,6 +304,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
 
     if (warp >= kTrSoftmaxWarps && warp < kTrExpandWarp) {
+    if constexpr (KVF == 1) ptx::regs_down<kTrRegsIssue>();
     if (warp == kTrTmaWarp) {
         // ================================================================ TMA producer
         TrWalk w(p, *start);
@@ -502,42 +506,46 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             bool ok = true;
             int x = 0;
             for (bool more = any; ok && more; more = w.next(p)) {
-                auto page = [&](int b) -> int { return b < w.b1 ? page_of(p.bp, w.b, w.s, 2 * b + rank) : -1; };
-                TrCodes codes;
-                codes.load(p.bp, w.s, 2 * w.b0 + rank, page(w.b0), row);
-                int pg = page(w.b0 + 1);
+                auto page = [&](int b, int i) -> int { return b < w.b1 ? page_of(p.bp, w.b, w.s, 2 * b + i) : -1; };
+                TrCodes<2> own;    // this CTA's page, all codes: K
+                TrCodes<1> other;  // the other CTA's, those of this CTA's dims: V
+                auto load = [&](int b, int pg_own, int pg_other) {
+                    own.load(p.bp, w.s, 2 * b + rank, pg_own, row, 0);
+                    other.load(p.bp, w.s, 2 * b + (rank ^ 1), pg_other, row, 256 * rank);
+                };
+                load(w.b0, page(w.b0, rank), page(w.b0, rank ^ 1));
+                int pg_own = page(w.b0 + 1, rank), pg_other = page(w.b0 + 1, rank ^ 1);
                 for (int b = w.b0; b < w.b1; ++b, ++x) {
                     // the last block's S has read the K tile
                     if (x > 0 && !(ok = warp_wait(kPbKEmpty, (x - 1) & 1) && warp_wait(kPbKEmpty + 1, (x - 1) & 1))) break;
-                    codes.store(sbase + L::kOffK + row * 128);
+                    own.store(sbase + L::kOffK + row * 128);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(even_bar(kTbMade));
-                    // V of the last block has been multiplied: panels 0 .. 3 of these rows to the even CTA's V tile, 4 .. 7 to
-                    // the odd one's
+                    // the last block's V has been multiplied: this CTA's dims of its own page are in the K tile, panels
+                    // 4 rank .. 4 rank + 3
                     if (x > 0 && !(ok = warp_wait(kPbVEmpty + rank, (x - 1) & 1))) break;
-#pragma unroll 1
-                    for (int pn = 0; pn < 8; ++pn) {
-                        const uint32_t from = sbase + L::kOffK + pn * kPfPanel + row * 128 + lane * 16;
-                        const uint32_t into = sbase + L::kOffV + rank * kPfVPage + (pn & 3) * kPfPanel + row * 128 + lane * 16;
-                        uint4 v[kTrExpandRows / 4];
+                    {
+                        const uint32_t from = sbase + L::kOffK + 4 * rank * kPfPanel + row * 128 + lane * 16;
+                        const uint32_t into = sbase + L::kOffV + rank * kPfVPage + row * 128 + lane * 16;
+                        uint4 v[8];
 #pragma unroll
-                        for (int j = 0; j < kTrExpandRows / 4; ++j) v[j] = ptx::ld_shared_v4(from + j * 512);
-                        if ((pn >> 2) == rank) {
+                        for (int j = 0; j < 8; ++j) v[j] = ptx::ld_shared_v4(from + (j >> 1) * kPfPanel + (j & 1) * 512);
 #pragma unroll
-                            for (int j = 0; j < kTrExpandRows / 4; ++j) ptx::st_shared_v4(into + j * 512, v[j]);
-                        } else {
-                            const uint32_t there = ptx::map_shared_rank(into, rank ^ 1);
-#pragma unroll
-                            for (int j = 0; j < kTrExpandRows / 4; ++j) ptx::st_shared_cluster_v4(there + j * 512, v[j]);
-                        }
+                        for (int j = 0; j < 8; ++j) ptx::st_shared_v4(into + (j >> 1) * kPfPanel + (j & 1) * 512, v[j]);
                     }
-                    ptx::fence_proxy_async_all();
+                    ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane < 2) ptx::mbar_arrive_release_cluster(ptx::map_shared_rank(bar(kTbTail + rank), lane));
+                    if (lane == 0) ptx::mbar_arrive(bar(kTbTail + rank));
+                    if (x > 0 && !(ok = warp_wait(kPbVEmpty + (rank ^ 1), (x - 1) & 1))) break;
+                    other.store(sbase + L::kOffV + (rank ^ 1) * kPfVPage + row * 128);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(bar(kTbTail + (rank ^ 1)));
                     // only now: a fence waits for the loads before it, too (5.3 us a block with these before it)
-                    codes.load(p.bp, w.s, 2 * b + 2 + rank, pg, row);
-                    pg = page(b + 2);
+                    load(b + 1, pg_own, pg_other);
+                    pg_own = page(b + 2, rank);
+                    pg_other = page(b + 2, rank ^ 1);
                 }
             }
         }
@@ -700,7 +708,6 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                         continue;
                     }
                     ++tails;
-                    if constexpr (KVF == 1) ptx::fence_acq_rel_cluster();  // (half of it is the other CTA's doing)
                 }
                 if (tail) {
                     // this CTA's V tile of the page, cleaned by the page's warps: rows past the end, and what
