@@ -31,7 +31,7 @@
 // page are copied from K).  So half of the codes are converted in both CTAs.  (Expanded into a ring in global
 // memory and loaded from there, a block took 5.0 us: 11 TB/s of traffic through L2.  The other CTA's half of V
 // from its K: by bulk copies 3000 to 4700 cycles for 32 KB, by stores into its shared memory 2000, and 3000
-// more until a fence and a release had waited for them.)
+// more until a fence and a release had waited for them.  Four warps for K and four for V: 4.1 us; so 3.6.)
 //
 // Roles (384 threads, 640 with fp8):
 //   warps 0-7    softmax, rescaling and output: TMEM quadrant warp % 4, keys 32 (warp / 4) .. of a page
