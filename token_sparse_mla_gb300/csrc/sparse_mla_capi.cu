@@ -730,11 +730,11 @@ smla_status sparse_mla_sync_status(void* stream) {
             return fail(SMLA_ERR_CUDA, "kernel reported an error (error word 0x%x)", word);
         if (!(word & smla::kErrIndexRange))
             return fail(SMLA_ERR_INDEX_RANGE,
-                        "an append or q_up launch met a slot outside [0, num_slots) or a position outside "
+                        "an append, q_up or evict launch met a slot outside [0, num_slots) or a position outside "
                         "[0, max_pos); those rows were not written (q_up: their rotated part is zero)");
         return fail(SMLA_ERR_INDEX_RANGE,
                     "a checked launch met list entries other than -1 outside [0, num_slots); they were masked%s",
-                    (word & smla::kErrRowRange) ? "; an append or q_up launch also met an out-of-range slot or position"
+                    (word & smla::kErrRowRange) ? "; an append, q_up or evict launch also met an out-of-range slot or position"
                                                 : "");
     }
     return SMLA_OK;

@@ -20,19 +20,25 @@
 // 42 GB/s per SM, from HBM and from L2 alike), so it takes what the other operand leaves: eight stages if no
 // sequence of the batch has more than 128 rows, else five (with fp8 six and three, beside the codes).
 //
+// Issuing: a panel costs its thread 500 cycles and more (four MMAs at 70 to 100, a wait and a commit): nine of them
+// are 2.5 us a tile, 4 beside the expansion of fp8 rows.  Where no sequence has more than 128 rows, TMEM holds two
+// accumulators in each of two buffers, so two threads issue every other panel, each into its own, and the sums add
+// them (37 sequences of 8191 fp8 rows: 66 -> 60 us).  A stage of the ring is always the same thread's, which so follows
+// every phase of its barriers.  With more rows the MMAs themselves take 512 cycles a panel and one thread issues.
+//
 // Work: tiles of 256 keys, each whole in one pair, in equal shares of their cost (kWt... below).
 //
 // fp8 codes come by TMA, 128 of every row at a time, into a ring of their own, and eight more warps expand them, each
 // 16 of the CTA's 128 keys, two panels at a time into the ring of panels (or the operand that stays); the rotated
 // dims come by TMA as they are.  (Codes loaded into registers: 7 us a tile, because the fence after a panel's
 // stores waits for the loads that are meant to run ahead.  Expanded into global memory and loaded from there:
-// 6.4 us, L2 took the writes no faster.  One panel at a time: 4.4.)
+// 6.4 us, L2 took the writes no faster.  One panel at a time: 4.4; two, with one thread issuing: 4.1.  Now 3.7.)
 //
 // Roles (384 threads, 640 with fp8):
 //   warps 0-7    sums: TMEM quadrant warp % 4 (32 keys), half warp / 4 of the tile's columns
 //   warp 8       TMA producer (one thread)
-//   warp 9       MMA issuer (one thread of the even CTA), and TMEM owner
-//   warps 10-11  the elements without work: positions past the end, sequences without tokens
+//   warps 9-10   MMA issuers (one thread of the even CTA each); warp 9 owns the TMEM
+//   warp 11      the elements without work: positions past the end, sequences without tokens
 //   warps 12-19  expansion of fp8 rows
 // Every wait is bounded; a CTA that gives up meets the other at the final cluster barrier.
 #pragma once
@@ -47,11 +53,12 @@ constexpr int kWtRows = 256;      // rows (token, head) per tile
 // stages of the ring, and of the ring of fp8 codes; Few: no sequence has more than kWtRowsFew rows
 constexpr int kWtStages = 5, kWtStagesFew = 8;
 constexpr int kWtStagesFp8 = 3, kWtStagesFewFp8 = 6;
+static_assert(kWtStagesFew % 2 == 0 && kWtStagesFewFp8 % 2 == 0, "a stage is always the same issuer's");
 constexpr int kWtRaw = 2, kWtRawFew = 3;  // 128 rows x 128 codes each: two panels
 constexpr int kWtRowsFew = 128;      // rows of a sequence up to which the deeper ring has room
 constexpr int kWtPanel = 128 * 128;  // 128 rows x 64 bf16, SW128
 constexpr int kWtSumWarps = 8;
-constexpr int kWtTmaWarp = 8, kWtMmaWarp = 9, kWtFillWarp = 10, kWtExpandWarp = 12;
+constexpr int kWtTmaWarp = 8, kWtMmaWarp = 9, kWtFillWarp = 11, kWtExpandWarp = 12;
 constexpr int kWtExpandWarps = 8;
 constexpr int kWtExpandRows = kWtHalf / kWtExpandWarps;  // 16
 // costs in tenths of a microsecond: a sequence's queries and first keys; a tile whose keys stream; one whose
@@ -239,7 +246,8 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
             const bool by_warps = i == kWbSEmpty || i == kWbSEmpty + 1;                // both CTAs' sum warps
             const bool by_expand = i == kWbStayMade || (i >= kWbMade && i < kWbMade + kWtStagesFew);  // both CTAs' expansion warps
             const bool by_own = i >= kWbRawEmpty;                                                       // this CTA's
-            ptx::mbar_init(bar(i), by_warps ? 2 * kWtSumWarps : by_own ? kWtExpandWarps : by_expand ? 2 * kWtExpandWarps + (i == kWbStayMade ? 1 : 0) : 1);
+            const bool by_two = i == kWbStayEmpty || i == kWbSFull || i == kWbSFull + 1 || i == kWbDrain;  // both issuers
+            ptx::mbar_init(bar(i), by_warps ? 2 * kWtSumWarps : by_two ? 2 : by_own ? kWtExpandWarps : by_expand ? 2 * kWtExpandWarps + (i == kWbStayMade ? 1 : 0) : 1);
         }
         ptx::fence_mbarrier_init();
     }
@@ -377,9 +385,11 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
             }
         }
         __syncwarp();
-    } else if (warp == kWtMmaWarp) {
-        // ================================================================ MMA issuer
+    } else if (warp == kWtMmaWarp || warp == kWtMmaWarp + 1) {
+        // ================================================================ MMA issuers
+        // (With more than kWtRowsFew rows the first does everything, the second's releases too.)
         if (rank == 0 && lane == 0) {
+            const int me = warp - kWtMmaWarp;
             const uint64_t d_stay = ptx::smem_desc_sw128(sbase + L::kOffStay, 16, 1024);
             const uint64_t d_ring = ptx::smem_desc_sw128(ring, 16, 1024);
             bool ok = true;
@@ -392,7 +402,12 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 parity ^= 1u;
                 return r;
             };
-            for (bool more = any; ok && more; more = w.next(p)) {
+            const bool both = !few && me == 0;
+            auto commit = [&](int i) {
+                ptx::mma_commit_pair(bar(i));
+                if (both) ptx::mma_commit_pair(bar(i));
+            };
+            for (bool more = any && (few || me == 0); ok && more; more = w.next(p)) {
                 const bool stream_keys = w.row_tiles == 1;
                 const bool expanded = KVF == 1 && stream_keys;  // what streams
                 if (stream_keys && !(ok = wait_stay(false))) break;
@@ -402,25 +417,46 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                         const int buf = item & 1;
                         if (item >= 2 && !(ok = wait(kWbSEmpty + buf, ((item >> 1) - 1) & 1))) break;
                         const uint32_t idesc = ptx::idesc_bf16_f32(kWtKeys, w.columns(p, i), 0, 0);
-                        const uint32_t d = tmem + buf * kWtRows;
-                        for (int pn = 0; pn < kPanels; ++pn, st.next()) {
-                            const bool by_warps = expanded && pn < kPanels - 1;
-                            uint32_t& parity = by_warps ? made : full;
-                            if (!(ok = wait((by_warps ? kWbMade : kWbFull) + st.at, (parity >> st.at) & 1u))) break;
-                            parity ^= 1u << st.at;
-                            ptx::tc_fence_after();
-                            const uint64_t stay = d_stay + ((pn * stay_panel) >> 4), moving = d_ring + ((st.at * kWtPanel) >> 4);
-                            const uint64_t a = stream_keys ? moving : stay, b = stream_keys ? stay : moving;
+                        const uint32_t d = tmem + buf * kWtRows + me * kWtRowsFew;
+                        // Two loops on purpose: the wide one has no time to spare (a panel's MMAs take 512 cycles, its issue about
+                        // 500; with the choice of stages inside one loop the wide batches lost 4 per cent).
+                        if (!few) {
+                            for (int pn = 0; pn < kPanels; ++pn, st.next()) {
+                                const bool by_warps = expanded && pn < kPanels - 1;
+                                uint32_t& parity = by_warps ? made : full;
+                                if (!(ok = wait((by_warps ? kWbMade : kWbFull) + st.at, (parity >> st.at) & 1u))) break;
+                                parity ^= 1u << st.at;
+                                ptx::tc_fence_after();
+                                const uint64_t stay = d_stay + ((pn * stay_panel) >> 4), moving = d_ring + ((st.at * kWtPanel) >> 4);
+                                const uint64_t a = stream_keys ? moving : stay, b = stream_keys ? stay : moving;
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                ptx::mma_bf16_ss_pair(d, a + ((kk * 32) >> 4), b + ((kk * 32) >> 4), idesc, (pn | kk) != 0);
-                            ptx::mma_commit_pair(bar(kWbEmpty + st.at));
+                                for (int kk = 0; kk < 4; ++kk)
+                                    ptx::mma_bf16_ss_pair(d, a + ((kk * 32) >> 4), b + ((kk * 32) >> 4), idesc, (pn | kk) != 0);
+                                ptx::mma_commit_pair(bar(kWbEmpty + st.at));
+                            }
+                        } else {  // the keys stream past the queries; the stages of the issuer's own parity
+                            bool first = true;  // nothing issued for this item yet
+                            for (int pn = 0; pn < kPanels; ++pn, st.next()) {
+                                const bool by_warps = KVF == 1 && pn < kPanels - 1;
+                                uint32_t& parity = by_warps ? made : full;
+                                const uint32_t now = (parity >> st.at) & 1u;
+                                parity ^= 1u << st.at;
+                                if ((st.at & 1) != me) continue;
+                                if (!(ok = wait((by_warps ? kWbMade : kWbFull) + st.at, now))) break;
+                                ptx::tc_fence_after();
+                                const uint64_t stay = d_stay + ((pn * stay_panel) >> 4), moving = d_ring + ((st.at * kWtPanel) >> 4);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    ptx::mma_bf16_ss_pair(d, moving + ((kk * 32) >> 4), stay + ((kk * 32) >> 4), idesc, kk > 0 || !first);
+                                ptx::mma_commit_pair(bar(kWbEmpty + st.at));
+                                first = false;
+                            }
                         }
-                        if (ok) ptx::mma_commit_pair(bar(kWbSFull + buf));
+                        if (ok) commit(kWbSFull + buf);
                     }
-                    if (ok && !stream_keys) ptx::mma_commit_pair(bar(kWbStayEmpty));
+                    if (ok && !stream_keys) commit(kWbStayEmpty);
                 }
-                if (ok && stream_keys) ptx::mma_commit_pair(bar(kWbStayEmpty));
+                if (ok && stream_keys) commit(kWbStayEmpty);
             }
             // nothing is in flight when TMEM is freed, also after giving up
             ptx::mma_commit_pair_local(bar(kWbDrain));
@@ -537,7 +573,7 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
     } else if (warp >= kWtFillWarp) {
         // ================================================================ elements that no tile covers
         const int width = p.bp.nb * kPage;
-        const int tid = (warp - kWtFillWarp) * 32 + lane;
+        const int tid = lane;
         // (B, 4096 positions) chunks over the grid
         const int chunks = (width + 4095) / 4096;
         for (int64_t c = blockIdx.x; c < static_cast<int64_t>(p.bp.B) * chunks; c += gridDim.x) {
@@ -546,7 +582,7 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
             const int from = s.n ? max(s.keys, c0) : c0;
             float* out = p.out + static_cast<int64_t>(b) * width;
             const float* prev = p.prev ? p.prev + static_cast<int64_t>(b) * width : nullptr;
-            for (int i = from + tid; i < c1; i += 64) out[i] = i < s.len && prev ? p.decay * prev[i] : 0.f;
+            for (int i = from + tid; i < c1; i += 32) out[i] = i < s.len && prev ? p.decay * prev[i] : 0.f;
         }
     } else {
         // ================================================================ sums
@@ -624,16 +660,34 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                         for (int e = 0; e < 8; ++e) acc[e & 1] = ptx::add2(acc[e & 1], make_float2(pr[2 * e], pr[2 * e + 1]));
                     };
                     uint32_t sv0[16], sv1[16];
-                    if (limit > 0) SMLA_TMEM_LD16(s_at, sv0);
+                    if (!few) {
+                        if (limit > 0) SMLA_TMEM_LD16(s_at, sv0);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < limit; c0 += 32) {
-                        ptx::tmem_wait_ld16(sv0);
-                        if (c0 + 16 < limit) SMLA_TMEM_LD16(s_at + c0 + 16, sv1);
-                        add(sv0, c0);
-                        if (c0 + 16 < limit) {
+                        for (int c0 = 0; c0 < limit; c0 += 32) {
+                            ptx::tmem_wait_ld16(sv0);
+                            if (c0 + 16 < limit) SMLA_TMEM_LD16(s_at + c0 + 16, sv1);
+                            add(sv0, c0);
+                            if (c0 + 16 < limit) {
+                                ptx::tmem_wait_ld16(sv1);
+                                if (c0 + 32 < limit) SMLA_TMEM_LD16(s_at + c0 + 32, sv0);
+                                add(sv1, c0 + 16);
+                            }
+                        }
+                    } else {  // the two issuers' accumulators
+#pragma unroll 1
+                        for (int c0 = 0; c0 < limit; c0 += 16) {
+                            SMLA_TMEM_LD16(s_at + c0, sv0);
+                            SMLA_TMEM_LD16(s_at + kWtRowsFew + c0, sv1);
+                            ptx::tmem_wait_ld16(sv0);
                             ptx::tmem_wait_ld16(sv1);
-                            if (c0 + 32 < limit) SMLA_TMEM_LD16(s_at + c0 + 32, sv0);
-                            add(sv1, c0 + 16);
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float2 y = ptx::add2(make_float2(__uint_as_float(sv0[e]), __uint_as_float(sv0[e + 1])),
+                                                           make_float2(__uint_as_float(sv1[e]), __uint_as_float(sv1[e + 1])));
+                                sv0[e] = __float_as_uint(y.x);
+                                sv0[e + 1] = __float_as_uint(y.y);
+                            }
+                            add(sv0, c0);
                         }
                     }
                     ptx::tc_fence_before();
