@@ -1,6 +1,6 @@
-"""The operators on a batch of sequences over caches of a few rows, and over batches whose sequences differ in
-everything that chooses how they are worked: few rows (token, head) and many, no cached rows and thousands.
-Tolerances are those of each operator's own tests."""
+"""The operators on a batch of sequences over caches of a few rows, over batches whose sequences differ in
+everything that chooses how they are worked (few rows (token, head) and many, no cached rows and thousands,
+tokens and none), and over block tables of the largest width.  Tolerances are those of each operator's own tests."""
 
 import numpy as np
 import pytest
@@ -73,3 +73,46 @@ def test_gpu_eviction_in_a_cache_that_ends_inside_the_new_page(fmt):
         if b == 0:
             want[64:70] = bits[mine[:6]]
     assert torch.equal(cache.cpu(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_gpu_many_sequences_without_tokens(fmt, in_place):
+    """Some with more positions than a warp takes at once, their weights decayed beside the others' sums."""
+    rng = np.random.default_rng(6)
+    seqs = [(int(n), 0) for n in rng.integers(0, 9000, 40)]
+    seqs[3], seqs[11], seqs[25], seqs[39] = (8500, 3), (0, 2), (4097, 1), (9100, 0)
+    batch = Batch(seqs, 8, 61, fmt, extra_blocks=3)
+    lse, prev = test_weights._inputs(batch)
+    test_weights._check(batch, test_weights._run(batch, lse, prev, 0.75, in_place=in_place), lse, prev, 0.75)
+    test_weights._check(batch, test_weights._run(batch, lse, None, 0.75), lse, None, 0.75)
+
+
+@pytest.mark.gpu
+def test_gpu_block_tables_of_the_largest_width():
+    """2^31 - 16384 positions: every index is within 31 bits, loops' steps past the end included."""
+    widest = 2 ** 25 - 256
+    batch = Batch([(100, 2)], 8, 62)
+    d = batch.to(DEV)
+    want_o, want_l = smla.sparse_mla_tree(**d)
+    want_w = smla.sparse_mla_weights(**d, lse=want_l)
+    d["block_tables"] = torch.zeros(1, widest, dtype=torch.int32, device=DEV)
+    d["block_tables"][0, :batch.blocks] = batch.tables[0].to(DEV)
+    out, lse = smla.sparse_mla_tree(**d)
+    assert torch.equal(out, want_o) and torch.equal(lse, want_l)
+    w = torch.full((1, widest * 64), float("nan"), device=DEV)
+    smla.sparse_mla_weights(**d, lse=lse, out=w)
+    assert torch.equal(w[:, :want_w.shape[1]], want_w)
+    assert not w[:, want_w.shape[1]:].count_nonzero()  # (NaN counts)
+    used = set(batch.tables[0].tolist())
+    free = [p for p in range(batch.cache.shape[0] // 64) if p not in used]
+    new_tables = torch.zeros_like(d["block_tables"])
+    new_tables[0, :2] = torch.tensor(free[:2], dtype=torch.int32, device=DEV)
+    kept, lengths, weights = smla.sparse_mla_evict(d["kv_cache"], d["block_tables"], torch.tensor([100], dtype=torch.int32, device=DEV), w,
+                                                   new_tables, 100)
+    smla.sync_status()
+    assert kept.tolist() == [list(range(100))] and lengths.tolist() == [100]
+    assert torch.equal(weights[:, :100], w[:, :100]) and not weights[:, 100:].count_nonzero()
+    with pytest.raises(smla.SparseMLAError, match="blocks"):
+        smla.sparse_mla_tree(d["q"], d["kv_cache"], torch.zeros(1, widest + 1, dtype=torch.int32, device=DEV), d["lengths"], d["starts"])

@@ -9,7 +9,7 @@
 namespace smla {
 
 constexpr int kPage = 64;                   // rows per page
-constexpr int kMaxBlocks = (1 << 25) - 8;   // pages of a sequence: positions, and some past them, fit 31 bits
+constexpr int kMaxBlocks = (1 << 25) - 256;  // pages of a sequence: positions, and 16000 past them (a loop's step), fit 31 bits
 
 struct BatchParams {
     const void* kv;           // the cache

@@ -35,10 +35,11 @@
 // 6.4 us, L2 took the writes no faster.  One panel at a time: 4.4; two, with one thread issuing: 4.1.  Now 3.7.)
 //
 // Roles (384 threads, 640 with fp8):
-//   warps 0-7    sums: TMEM quadrant warp % 4 (32 keys), half warp / 4 of the tile's columns
+//   warps 0-7    elements of sequences without tokens; then sums: TMEM quadrant warp % 4 (32 keys), half warp / 4 of
+//                the tile's columns
 //   warp 8       TMA producer (one thread)
 //   warps 9-10   MMA issuers (one thread of the even CTA each); warp 9 owns the TMEM
-//   warp 11      the elements without work: positions past the end, sequences without tokens
+//   warp 11      elements past a sequence's last key
 //   warps 12-19  expansion of fp8 rows
 // Every wait is bounded; a CTA that gives up meets the other at the final cluster barrier.
 #pragma once
@@ -215,6 +216,43 @@ struct WtStage {
     __device__ __forceinline__ bool used() const { return round > 0; }                 // this stage has been filled before
     __device__ __forceinline__ uint32_t last() const { return (round - 1) & 1; }       // parity of its last release
 };
+
+// The elements that no tile covers, by warp `first` of `stride`: of sequences without tokens all (kIdle), of the others
+// those past the last key.  Chunks of 4096 positions; a lane looks at one, so that the many without work cost little.
+template <bool kIdle>
+__device__ __forceinline__ void weights_fill(const WtParams& p, int first, int stride) {
+    constexpr int kChunk = 4096, kLoads = kIdle ? 8 : 4;  // idle: loads in flight a lane, eight warps of them
+    const int lane = threadIdx.x & 31;
+    const int width = p.bp.nb * kPage, chunks = (width + kChunk - 1) / kChunk;
+    const int64_t total = static_cast<int64_t>(p.bp.B) * chunks;
+    for (int64_t c0 = first; c0 < total; c0 += 32 * static_cast<int64_t>(stride)) {
+        const int64_t c = c0 + static_cast<int64_t>(lane) * stride;
+        int b = 0, from = 0, to = 0, len = 0;
+        if (c < total) {
+            b = static_cast<int>(c / chunks);
+            from = static_cast<int>(c % chunks) * kChunk;
+            to = min(from + kChunk, width);
+            const Seq s = load_seq(p.bp, b);
+            len = s.len;
+            if (!kIdle) from = max(from, s.keys);
+            if ((s.n == 0) != kIdle) to = 0;
+        }
+        for (uint32_t left = __ballot_sync(0xffffffffu, from < to); left; left &= left - 1u) {
+            const int l = __ffs(left) - 1;
+            const int64_t row = static_cast<int64_t>(__shfl_sync(0xffffffffu, b, l)) * width;
+            const int i0 = __shfl_sync(0xffffffffu, from, l) + lane, i1 = __shfl_sync(0xffffffffu, to, l);
+            const int n = kIdle && p.prev ? __shfl_sync(0xffffffffu, len, l) : 0;
+            for (int i = i0; i < i1; i += 32 * kLoads) {
+                float x[kLoads];
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) x[u] = i + 32 * u < n ? p.prev[row + i + 32 * u] : 0.f;
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u)
+                    if (i + 32 * u < i1) p.out[row + i + 32 * u] = i + 32 * u < n ? p.decay * x[u] : 0.f;
+            }
+        }
+    }
+}
 
 template <int KVF>
 __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
@@ -572,20 +610,10 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
         }
     } else if (warp >= kWtFillWarp) {
         // ================================================================ elements that no tile covers
-        const int width = p.bp.nb * kPage;
-        const int tid = lane;
-        // (B, 4096 positions) chunks over the grid
-        const int chunks = (width + 4095) / 4096;
-        for (int64_t c = blockIdx.x; c < static_cast<int64_t>(p.bp.B) * chunks; c += gridDim.x) {
-            const int b = static_cast<int>(c / chunks), c0 = static_cast<int>(c % chunks) * 4096, c1 = min(c0 + 4096, width);
-            const Seq s = load_seq(p.bp, b);
-            const int from = s.n ? max(s.keys, c0) : c0;
-            float* out = p.out + static_cast<int64_t>(b) * width;
-            const float* prev = p.prev ? p.prev + static_cast<int64_t>(b) * width : nullptr;
-            for (int i = from + tid; i < c1; i += 32) out[i] = i < s.len && prev ? p.decay * prev[i] : 0.f;
-        }
+        weights_fill<false>(p, blockIdx.x, gridDim.x);
     } else {
         // ================================================================ sums
+        weights_fill<true>(p, static_cast<int>(blockIdx.x) * kWtSumWarps + warp, static_cast<int>(gridDim.x) * kWtSumWarps);
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
         const int tid = threadIdx.x;  // 0 .. 255
