@@ -505,7 +505,8 @@ smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_
  *                 ascending, then -1
  *   new_lengths   device, [seqs] int32, caller-owned: min(n, budget)
  *   new_weights   device, [seqs, new_blocks * 64] fp32, caller-owned, zero behind the
- *                 kept rows'; must not overlap weights
+ *                 kept rows'
+ * kept, new_lengths and new_weights must overlap neither each other nor the inputs.
  * A kept row that lies outside the cache, or would be copied to outside it, is not copied,
  * and the next sparse_mla_sync_status() returns SMLA_ERR_INDEX_RANGE.  Exact, and
  * repeated calls give identical bytes.  seqs = 0 is a no-op.  Allocates nothing;
