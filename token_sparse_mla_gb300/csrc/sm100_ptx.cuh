@@ -610,5 +610,33 @@ __device__ __forceinline__ uint32_t e4m3x2_scaled_bf16x2(uint32_t two_bytes, flo
     return out;
 }
 
+// Four of them, the products in pairs: bf16 of codes x scale, from the four bytes of x (a block of the fp8 tree attention, where
+// instructions bound it: 3.6 -> 3.4 us).
+__device__ __forceinline__ uint2 e4m3x4_scaled_bf16x4(uint32_t x, float2 scale2) {
+    uint32_t h0, h1;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(h0), "=r"(h1)
+        : "r"(x));
+    uint2 out;
+    float2 f0, f1;
+    asm("{\n\t.reg .b16 l16, h16;\n\tmov.b32 {l16, h16}, %2;\n\tcvt.f32.f16 %0, l16;\n\tcvt.f32.f16 %1, h16;\n\t}"
+        : "=f"(f0.x), "=f"(f0.y)
+        : "r"(h0));
+    asm("{\n\t.reg .b16 l16, h16;\n\tmov.b32 {l16, h16}, %2;\n\tcvt.f32.f16 %0, l16;\n\tcvt.f32.f16 %1, h16;\n\t}"
+        : "=f"(f1.x), "=f"(f1.y)
+        : "r"(h1));
+    // (mul2 would flush subnormal products)
+    asm("{\n.reg .b64 ra, rb, rd;\nmov.b64 ra, {%0, %1};\nmov.b64 rb, {%2, %3};\nmul.rn.f32x2 rd, ra, rb;\nmov.b64 {%0, %1}, rd;\n}"
+        : "+f"(f0.x), "+f"(f0.y)
+        : "f"(scale2.x), "f"(scale2.y));
+    asm("{\n.reg .b64 ra, rb, rd;\nmov.b64 ra, {%0, %1};\nmov.b64 rb, {%2, %3};\nmul.rn.f32x2 rd, ra, rb;\nmov.b64 {%0, %1}, rd;\n}"
+        : "+f"(f1.x), "+f"(f1.y)
+        : "f"(scale2.x), "f"(scale2.y));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.x) : "f"(f0.y), "f"(f0.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out.y) : "f"(f1.y), "f"(f1.x));
+    return out;
+}
+
 }  // namespace ptx
 }  // namespace smla

@@ -31,7 +31,10 @@
 // page are copied from K).  So half of the codes are converted in both CTAs.  (Expanded into a ring in global
 // memory and loaded from there, a block took 5.0 us: 11 TB/s of traffic through L2.  The other CTA's half of V
 // from its K: by bulk copies 3000 to 4700 cycles for 32 KB, by stores into its shared memory 2000, and 3000
-// more until a fence and a release had waited for them.  Four warps for K and four for V: 4.1 us; so 3.6.)
+// more until a fence and a release had waited for them.  Four warps for K and four for V: 4.1 us; so 3.4, and 3.6
+// from HBM: what bounds it is how fast the expansion warps issue, 1900 cycles for K, 1600 for V and 1100 for the copy of 6600
+// a block, in part beside S, which has shared memory to itself.  V's own part kept in registers instead of copied
+// from K was no faster.)
 //
 // Roles (384 threads, 640 with fp8):
 //   warps 0-7    softmax, rescaling and output: TMEM quadrant warp % 4, keys 32 (warp / 4) .. of a page
@@ -235,9 +238,9 @@ struct TrCodes {
                 for (int u = 0; u < 4; ++u) {
                     const float s = __shfl_sync(0xffffffffu, sc[e], (lane & 16) + u0 + u);
                     const uint2 x = a[e][u];
+                    const uint2 lo = ptx::e4m3x4_scaled_bf16x4(x.x, make_float2(s, s)), hi = ptx::e4m3x4_scaled_bf16x4(x.y, make_float2(s, s));
                     ptx::st_shared_v4(at0 + 4 * e * kPfPanel + (u0 + u) * 128 + (((lane & 7) ^ ((u0 & 4) + u)) << 4),
-                                      make_uint4(ptx::e4m3x2_scaled_bf16x2(x.x & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(x.x >> 16, s),
-                                                 ptx::e4m3x2_scaled_bf16x2(x.y & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(x.y >> 16, s)));
+                                      make_uint4(lo.x, lo.y, hi.x, hi.y));
                 }
 #pragma unroll
                 for (int u = 0; u < kTrExpandRows - 4; ++u) a[e][u] = a[e][u + 4];
@@ -509,11 +512,10 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                 auto page = [&](int b, int i) -> int { return b < w.b1 ? page_of(p.bp, w.b, w.s, 2 * b + i) : -1; };
                 TrCodes<2> own;    // this CTA's page, all codes: K
                 TrCodes<1> other;  // the other CTA's, those of this CTA's dims: V
-                auto load = [&](int b, int pg_own, int pg_other) {
-                    own.load(p.bp, w.s, 2 * b + rank, pg_own, row, 0);
-                    other.load(p.bp, w.s, 2 * b + (rank ^ 1), pg_other, row, 256 * rank);
-                };
-                load(w.b0, page(w.b0, rank), page(w.b0, rank ^ 1));
+                auto load_own = [&](int b, int pg) { own.load(p.bp, w.s, 2 * b + rank, pg, row, 0); };
+                auto load_other = [&](int b, int pg) { other.load(p.bp, w.s, 2 * b + (rank ^ 1), pg, row, 256 * rank); };
+                load_own(w.b0, page(w.b0, rank));
+                load_other(w.b0, page(w.b0, rank ^ 1));
                 int pg_own = page(w.b0 + 1, rank), pg_other = page(w.b0 + 1, rank ^ 1);
                 for (int b = w.b0; b < w.b1; ++b, ++x) {
                     // the last block's S has read the K tile
@@ -522,29 +524,31 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(even_bar(kTbMade));
+                    // A fence waits for the loads before it, too: the next block's come right behind one (4.05 us a block from HBM
+                    // with all of them behind the last fence, 3.85 so, 5.3 with all of them before it)
+                    load_own(b + 1, pg_own);
+                    pg_own = page(b + 2, rank);
                     // the last block's V has been multiplied: this CTA's dims of its own page are in the K tile, panels
                     // 4 rank .. 4 rank + 3
                     if (x > 0 && !(ok = warp_wait(kPbVEmpty + rank, (x - 1) & 1))) break;
                     {
                         const uint32_t from = sbase + L::kOffK + 4 * rank * kPfPanel + row * 128 + lane * 16;
                         const uint32_t into = sbase + L::kOffV + rank * kPfVPage + row * 128 + lane * 16;
-                        uint4 v[8];
+#pragma unroll 1
+                        for (int j = 0; j < 4; j += 2) {
+                            uint4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = ptx::ld_shared_v4(from + (j >> 1) * kPfPanel + (j & 1) * 512);
+                            for (int u = 0; u < 4; ++u) v[u] = ptx::ld_shared_v4(from + (j + (u >> 1)) * kPfPanel + (u & 1) * 512);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) ptx::st_shared_v4(into + (j >> 1) * kPfPanel + (j & 1) * 512, v[j]);
+                            for (int u = 0; u < 4; ++u) ptx::st_shared_v4(into + (j + (u >> 1)) * kPfPanel + (u & 1) * 512, v[u]);
+                        }
                     }
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar(kTbTail + rank));
                     if (x > 0 && !(ok = warp_wait(kPbVEmpty + (rank ^ 1), (x - 1) & 1))) break;
                     other.store(sbase + L::kOffV + (rank ^ 1) * kPfVPage + row * 128);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(bar(kTbTail + (rank ^ 1)));
-                    // only now: a fence waits for the loads before it, too (5.3 us a block with these before it)
-                    load(b + 1, pg_own, pg_other);
-                    pg_own = page(b + 2, rank);
+                    if (lane < 2) ptx::mbar_arrive(bar(kTbTail + lane));
+                    load_other(b + 1, pg_other);
                     pg_other = page(b + 2, rank ^ 1);
                 }
             }
@@ -762,18 +766,19 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
             // next block's P): whole sectors, where a row per lane would touch 32 lines at once.  Partials
             // go as they are, each instruction 512 contiguous bytes.
             if (!failed && live > 0) {
+                constexpr int kCols = KVF == 1 ? 32 : 64;
                 const uint32_t stage = sbase + L::kOffP + warp * 32 * 64;
                 float4* part = reinterpret_cast<float4*>(p.part_o) + (pgroup * 128 + 64 * half + 32 * sub) * 32 + lane;
 #pragma unroll 1
-                for (int cc = 0; cc < 2; ++cc) {  // 64 columns of O are read at a time
-                    uint32_t ov[64];
+                for (int cc = 0; cc < 128 / kCols; ++cc) {  // 64 columns of O are read at a time (with fp8 32, for registers)
+                    uint32_t ov[kCols];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) SMLA_TMEM_LD16(tmem + lane_base + ocol0 + cc * 64 + 16 * q, ov + 16 * q);
+                    for (int q = 0; q < kCols / 16; ++q) SMLA_TMEM_LD16(tmem + lane_base + ocol0 + cc * kCols + 16 * q, ov + 16 * q);
                     ptx::tmem_wait_ld();
                     if (whole) {
-                        __nv_bfloat16* dst = p.out + row0 * kDV + 256 * half + 128 * sub + 64 * cc + (lane & 3) * 8;
+                        __nv_bfloat16* dst = p.out + row0 * kDV + 256 * half + 128 * sub + kCols * cc + (lane & 3) * 8;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
+                        for (int u = 0; u < kCols / 32; ++u) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 uint32_t v[4];
@@ -795,8 +800,8 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
                         }
                     } else if (lane < live) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            part[(16 * cc + e) * 32] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                        for (int e = 0; e < kCols / 4; ++e)
+                            part[(kCols / 4 * cc + e) * 32] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
                                                                    __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
                     }
                 }

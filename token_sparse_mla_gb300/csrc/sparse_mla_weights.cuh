@@ -32,7 +32,8 @@
 // 16 of the CTA's 128 keys, two panels at a time into the ring of panels (or the operand that stays); the rotated
 // dims come by TMA as they are.  (Codes loaded into registers: 7 us a tile, because the fence after a panel's
 // stores waits for the loads that are meant to run ahead.  Expanded into global memory and loaded from there:
-// 6.4 us, L2 took the writes no faster.  One panel at a time: 4.4; two, with one thread issuing: 4.1.  Now 3.7.)
+// 6.4 us, L2 took the writes no faster.  One panel at a time: 4.4; two, with one thread issuing: 4.1.  With two 3.7,
+// and 3.5 with the products in pairs.)
 //
 // Roles (384 threads, 640 with fp8):
 //   warps 0-7    elements of sequences without tokens; then sums: TMEM quadrant warp % 4 (32 keys), half warp / 4 of
@@ -571,12 +572,10 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                             const float s = __shfl_sync(0xffffffffu, sc.x, r);
                             const uint32_t x0 = second ? v[i].z : v[i].x, y0 = second ? v[i].w : v[i].y;
                             const uint32_t x1 = second ? v[i].x : v[i].z, y1 = second ? v[i].y : v[i].w;
-                            ptx::st_shared_v4(dst + r * 128 + (((c + second) ^ (r & 7)) << 4),
-                                              make_uint4(ptx::e4m3x2_scaled_bf16x2(x0 & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(x0 >> 16, s),
-                                                         ptx::e4m3x2_scaled_bf16x2(y0 & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(y0 >> 16, s)));
-                            ptx::st_shared_v4(dst + r * 128 + (((c + !second) ^ (r & 7)) << 4),
-                                              make_uint4(ptx::e4m3x2_scaled_bf16x2(x1 & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(x1 >> 16, s),
-                                                         ptx::e4m3x2_scaled_bf16x2(y1 & 0xFFFFu, s), ptx::e4m3x2_scaled_bf16x2(y1 >> 16, s)));
+                            const uint2 a0 = ptx::e4m3x4_scaled_bf16x4(x0, make_float2(s, s)), b0 = ptx::e4m3x4_scaled_bf16x4(y0, make_float2(s, s));
+                            ptx::st_shared_v4(dst + r * 128 + (((c + second) ^ (r & 7)) << 4), make_uint4(a0.x, a0.y, b0.x, b0.y));
+                            const uint2 a1 = ptx::e4m3x4_scaled_bf16x4(x1, make_float2(s, s)), b1 = ptx::e4m3x4_scaled_bf16x4(y1, make_float2(s, s));
+                            ptx::st_shared_v4(dst + r * 128 + (((c + !second) ^ (r & 7)) << 4), make_uint4(a1.x, a1.y, b1.x, b1.y));
                         }
                         sc = make_float4(sc.y, sc.z, sc.w, 0.f);
                         ptx::fence_proxy_async_smem();
