@@ -427,6 +427,15 @@ def _call(dev: torch.device, stream, fn, *args) -> None:
         _check(st)
 
 
+def _given(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, dev: torch.device) -> torch.Tensor:
+    """A result tensor that the caller passed, checked."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
+    if t.device != dev:
+        _apart(dev, **{name: t})
+    return t
+
+
 def _apart(dev: torch.device, **tensors) -> None:
     """Names the first tensor that is not on dev."""
     for name, t in tensors.items():
@@ -777,21 +786,15 @@ def sparse_mla_evict(kv_cache: torch.Tensor, block_tables: torch.Tensor, lengths
         raise ValueError(f"budget must be in [1, {new_blocks * 64}], the positions of new_tables")
     if sinks < 0 or recent < 0 or sinks + recent > budget:
         raise ValueError("sinks and recent must be >= 0 and no more than the budget together")
-    held = []
-    for name, t, shape, dtype in (("kept", kept, (seqs, budget), _I32), ("new_lengths", new_lengths, (seqs,), _I32),
-                                  ("new_weights", new_weights, (seqs, new_blocks * 64), _F32)):
-        if t is None:
-            t = _empty(shape, dtype, dev, stream)
-        else:
-            if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
-            if t.device != dev:
-                _apart(dev, **{name: t})
-        held.append(t)
+    kept = _empty((seqs, budget), _I32, dev, stream) if kept is None else _given("kept", kept, (seqs, budget), _I32, dev)
+    new_lengths = _empty((seqs,), _I32, dev, stream) if new_lengths is None else _given("new_lengths", new_lengths, (seqs,), _I32, dev)
+    width = new_blocks * 64
+    new_weights = (_empty((seqs, width), _F32, dev, stream) if new_weights is None
+                   else _given("new_weights", new_weights, (seqs, width), _F32, dev))
     _call(dev, stream, library().sparse_mla_evict, kv_cache.data_ptr(), block_tables.data_ptr(), lengths.data_ptr(),
           weights.data_ptr(), new_tables.data_ptr(), seqs, blocks, new_blocks, budget, sinks, recent, num_slots,
-          KV_FORMATS[kv_format], held[0].data_ptr(), held[1].data_ptr(), held[2].data_ptr())
-    return held[0], held[1], held[2]
+          KV_FORMATS[kv_format], kept.data_ptr(), new_lengths.data_ptr(), new_weights.data_ptr())
+    return kept, new_lengths, new_weights
 
 
 def host_workspace_bytes(T: int, h: int, topk: int) -> int:
