@@ -14,11 +14,11 @@
 //   up to 256 rows in the sequence: its queries stay, keys stream.  Bound by HBM, 1152 bytes a key: 256 keys
 //     are 3.3 us for 76 pairs at 6.8 TB/s, the MMAs at most 36 * 128 cycles = 2.4 us.
 //   more: a tile of keys stays and the queries stream from L2, tile after tile, so that a key's sum still is
-//     one thread's.  Bound by the MMAs.
+//     one thread's.  Bound by that stream, 295 KB a row tile and pair: 3.9 us, where the MMAs take 2.4.
 // Both operands have the same layout (rows x 9 panels, SW128), so the two forms differ in who loads what and in
 // which descriptor is A.  The ring's depth sets the pace where the operand streams (64 KB in flight per CTA gave
 // 42 GB/s per SM, from HBM and from L2 alike), so it takes what the other operand leaves: eight stages if no
-// sequence of the batch has more than 128 rows, else five (with fp8 six and three, beside the codes).
+// sequence of the batch has more than 128 rows, else five (with fp8 five and three, beside the codes).
 //
 // Issuing: a panel costs its thread 500 cycles and more (four MMAs at 70 to 100, a wait and a commit): nine of them
 // are 2.5 us a tile, 4 beside the expansion of fp8 rows.  Where no sequence has more than 128 rows, TMEM holds two
@@ -33,7 +33,10 @@
 // dims come by TMA as they are.  (Codes loaded into registers: 7 us a tile, because the fence after a panel's
 // stores waits for the loads that are meant to run ahead.  Expanded into global memory and loaded from there:
 // 6.4 us, L2 took the writes no faster.  One panel at a time: 4.4; two, with one thread issuing: 4.1.  With two 3.7,
-// and 3.5 with the products in pairs.)
+// and 3.5 with the products in pairs.)  Where no sequence has more than 128 rows, each half of the warps has every other
+// pair of panels and a slot of the ring for it, which the issuer of the slot waits for and frees as one, 32 rows a
+// warp: half as many waits and fences a tile, and one half's waits beside the other's work (57.6 -> 55 us, L2: 3.1 to
+// 3.6 us a tile).  The codes' ring is far enough ahead without a prefetch into L2 (one tile ahead 56.3, two 60).
 //
 // Roles (384 threads, 640 with fp8):
 //   warps 0-7    elements of sequences without tokens; then sums: TMEM quadrant warp % 4 (32 keys), half warp / 4 of
@@ -54,9 +57,10 @@ constexpr int kWtHalf = 128;      // per CTA
 constexpr int kWtRows = 256;      // rows (token, head) per tile
 // stages of the ring, and of the ring of fp8 codes; Few: no sequence has more than kWtRowsFew rows
 constexpr int kWtStages = 5, kWtStagesFew = 8;
-constexpr int kWtStagesFp8 = 3, kWtStagesFewFp8 = 6;
-static_assert(kWtStagesFew % 2 == 0 && kWtStagesFewFp8 % 2 == 0, "a stage is always the same issuer's");
-constexpr int kWtRaw = 2, kWtRawFew = 3;  // 128 rows x 128 codes each: two panels
+constexpr int kWtStagesFp8 = 3, kWtStagesFewFp8 = 5;  // the latter: two pairs of panels, and one for the rotated dims
+static_assert(kWtStagesFew % 2 == 0, "a stage is always the same issuer's");
+constexpr int kWtRopeAt = kWtStagesFewFp8 - 1;
+constexpr int kWtRaw = 2, kWtRawFew = 4;  // 128 rows x 128 codes each: two panels
 constexpr int kWtRowsFew = 128;      // rows of a sequence up to which the deeper ring has room
 constexpr int kWtPanel = 128 * 128;  // 128 rows x 64 bf16, SW128
 constexpr int kWtSumWarps = 8;
@@ -362,6 +366,7 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 return true;
             };
             bool others = false;  // the last piece's keys stayed
+            int tiles = 0;
             for (bool more = any; ok && more; more = w.next(p)) {
                 const bool stream_keys = w.row_tiles == 1;
                 const int q0 = w.s.first * p.bp.h;
@@ -378,11 +383,11 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 // does not follow could be more than one phase behind, which a parity cannot tell
                 if (KVF == 1 && !stream_keys && !others && stays > 0 && !(ok = wait(kWbStayEmpty, (stays - 1) & 1))) break;
                 others = !stream_keys;
-                for (int k = w.k0; ok && k < w.k1; ++k) {
+                for (int k = w.k0; ok && k < w.k1; ++k, ++tiles) {
                     const int i_page = 4 * k + 2 * rank;
                     row0 = first_row(page_of(p.bp, w.b, w.s, i_page));
                     row1 = first_row(page_of(p.bp, w.b, w.s, i_page + 1));
-                    if (k + 1 < w.k1) {
+                    if (KVF == 0 && k + 1 < w.k1) {
                         prefetch(i_page + 4);
                         prefetch(i_page + 5);
                     }
@@ -415,8 +420,13 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
             // every copy has landed and been used, and no release is still on its way to this CTA's barriers,
             // before it leaves
             if (ok && stays > 0) ok = wait(kWbStayEmpty, (stays - 1) & 1);
-            for (int u = 0; ok && u < stages; ++u, st.next())
-                if (st.used()) ok = wait(kWbEmpty + st.at, st.last());
+            if (KVF == 1 && few) {
+                for (int slot = 0; ok && stays > 0 && slot < 2; ++slot) ok = wait(kWbEmpty + 2 * slot, 1u);  // (two uses a tile)
+                if (ok && stays > 0) ok = wait(kWbEmpty + kWtRopeAt, (tiles - 1) & 1);
+            } else {
+                for (int u = 0; ok && u < stages; ++u, st.next())
+                    if (st.used()) ok = wait(kWbEmpty + st.at, st.last());
+            }
             if (!ok) {  // gave up: copies in flight complete on the other CTA's barriers; leave them time to land
                 const uint64_t t0 = ptx::globaltimer_ns();
                 while (ptx::globaltimer_ns() - t0 < 2000000ull) {
@@ -473,15 +483,36 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                                     ptx::mma_bf16_ss_pair(d, a + ((kk * 32) >> 4), b + ((kk * 32) >> 4), idesc, (pn | kk) != 0);
                                 ptx::mma_commit_pair(bar(kWbEmpty + st.at));
                             }
+                        } else if (KVF == 1) {  // pairs of panels, each issuer those of its slot; the rotated dims are the second's
+                            const uint64_t moving = d_ring + ((2 * me * kWtPanel) >> 4);
+                            if (me == 1) {
+                                if (!(ok = wait(kWbFull + kWtRopeAt, item & 1))) break;
+                                ptx::tc_fence_after();
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    ptx::mma_bf16_ss_pair(d, d_ring + ((kWtRopeAt * kWtPanel + kk * 32) >> 4),
+                                                          d_stay + (((kPanels - 1) * (kWtPanel / 2) + kk * 32) >> 4), idesc, kk > 0);
+                                ptx::mma_commit_pair(bar(kWbEmpty + kWtRopeAt));
+                            }
+#pragma unroll 1
+                            for (uint32_t h = 0; h < 2; ++h) {
+                                if (!(ok = wait(kWbMade + 2 * me, h))) break;
+                                ptx::tc_fence_after();
+                                const uint64_t stay = d_stay + (((4 * h + 2 * me) * (kWtPanel / 2)) >> 4);
+                                const bool more_of_it = me == 1 || h > 0;
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk)
+                                    ptx::mma_bf16_ss_pair(d, moving + (((kk >> 2) * kWtPanel + (kk & 3) * 32) >> 4),
+                                                          stay + (((kk >> 2) * (kWtPanel / 2) + (kk & 3) * 32) >> 4), idesc, kk > 0 || more_of_it);
+                                ptx::mma_commit_pair(bar(kWbEmpty + 2 * me));
+                            }
                         } else {  // the keys stream past the queries; the stages of the issuer's own parity
                             bool first = true;  // nothing issued for this item yet
                             for (int pn = 0; pn < kPanels; ++pn, st.next()) {
-                                const bool by_warps = KVF == 1 && pn < kPanels - 1;
-                                uint32_t& parity = by_warps ? made : full;
-                                const uint32_t now = (parity >> st.at) & 1u;
-                                parity ^= 1u << st.at;
+                                const uint32_t now = (full >> st.at) & 1u;
+                                full ^= 1u << st.at;
                                 if ((st.at & 1) != me) continue;
-                                if (!(ok = wait((by_warps ? kWbMade : kWbFull) + st.at, now))) break;
+                                if (!(ok = wait(kWbFull + st.at, now))) break;
                                 ptx::tc_fence_after();
                                 const uint64_t stay = d_stay + ((pn * stay_panel) >> 4), moving = d_ring + ((st.at * kWtPanel) >> 4);
 #pragma unroll
@@ -505,9 +536,11 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
     } else if (warp >= kWtExpandWarp) {
         // ================================================================ expansion of fp8 rows
         if constexpr (KVF == 1) {
-            const int row = kWtExpandRows * (warp - kWtExpandWarp);  // this warp's first of the CTA's 128 keys
+            // this warp's rows of the CTA's 128 keys; few: of every other pair of panels, twice as many
+            const int slot = (warp - kWtExpandWarp) >> 2, rows = few ? 2 * kWtExpandRows : kWtExpandRows;
+            const int row = few ? rows * ((warp - kWtExpandWarp) & 3) : rows * (warp - kWtExpandWarp);
             bool ok = true, others = false;  // the last piece's keys stayed
-            int stays = 0;
+            int stays = 0, tile = 0;
             WtStage st(stages), raw_st(raw_stages);
             auto warp_wait = [&](int i, uint32_t parity) -> bool {
                 return ptx::mbar_wait_warp(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
@@ -520,11 +553,11 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                     if (stays > 0 && !(ok = warp_wait(kWbStayEmpty, (stays - 1) & 1))) break;
                 }
                 others = !stream_keys;
-                // Lane l has the scales of row l % 16 of the warp's; of the codes, 16 from 16 (l % 8) on of a pair of panels, in rows
+                // Lane l has the scales of row l % rows of the warp's; of the codes, 16 from 16 (l % 8) on of a pair of panels, in rows
                 // 4 i + l / 8.
                 auto page = [&](int k, int i) -> int { return k < w.k1 ? page_of(p.bp, w.b, w.s, 4 * k + 2 * rank + i) : -1; };
                 auto scales = [&](int k, int pg) -> float4 {
-                    const int n = page_rows(p.bp, w.s, 4 * k + 2 * rank + row / kPage, pg) - row % kPage, r = lane % kWtExpandRows;
+                    const int n = page_rows(p.bp, w.s, 4 * k + 2 * rank + row / kPage, pg) - row % kPage, r = lane & (rows - 1);
                     const uint8_t* src = static_cast<const uint8_t*>(p.bp.kv) + (static_cast<int64_t>(pg) * kPage + row % kPage + r) * kFp8RowBytes;
                     return r < n ? __ldg(reinterpret_cast<const float4*>(src + 512)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 };
@@ -532,7 +565,8 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 const bool second = part >= 4;  // of the two panels
                 int pg0 = page(w.k0, 0), pg1 = page(w.k0, 1);
                 float4 sc = scales(w.k0, row < kPage ? pg0 : pg1);
-                for (int k = w.k0; ok && k < w.k1; ++k) {
+                int next0 = page(w.k0 + 1, 0), next1 = page(w.k0 + 1, 1);
+                for (int k = w.k0; ok && k < w.k1; ++k, ++tile) {
                     // the rotated dims, by this CTA's first expansion warp
                     auto load_rope = [&](uint32_t dst, int i) {
                         if (lane == 0) {
@@ -546,30 +580,22 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                         if (stays > 0 && !(ok = warp_wait(kWbStayEmpty, (stays - 1) & 1))) break;
                         ++stays;
                         if (warp == kWtExpandWarp) load_rope(sbase + L::kOffStay + (kPanels - 1) * kWtPanel, kWbStayMade);
+                    } else if (few && warp == kWtExpandWarp) {
+                        if (tile > 0 && !(ok = warp_wait(kWbEmpty + kWtRopeAt, (tile - 1) & 1))) break;
+                        load_rope(ring + kWtRopeAt * kWtPanel, kWbFull + kWtRopeAt);
                     }
-#pragma unroll 1
-                    for (int pair = 0; pair < 4; ++pair) {
-                        if (!(ok = warp_wait(kWbRawFull + raw_st.at, raw_st.round & 1))) break;
+                    // 16 rows from r0 of the warp's on: codes at `from`, panels at `into`, the rows' scale `s_of` of lane r0 + their index
+                    auto expand = [&](uint32_t from, uint32_t into, int r0, float s_of) {
                         uint4 v[kWtExpandRows / 4];
 #pragma unroll
-                        for (int i = 0; i < kWtExpandRows / 4; ++i) v[i] = ptx::ld_shared_v4(raw + raw_st.at * kWtPanel + (row + 4 * i) * 128 + lane * 16);
-                        uint32_t dst;
-                        WtStage st2 = st;
-                        if (stream_keys) {
-                            st2.next();
-                            if (st.used() && !(ok = warp_wait(kWbEmpty + st.at, st.last()))) break;
-                            if (st2.used() && !(ok = warp_wait(kWbEmpty + st2.at, st2.last()))) break;
-                            dst = ring + (second ? st2.at : st.at) * kWtPanel;
-                        } else {
-                            dst = sbase + L::kOffStay + (2 * pair + second) * kWtPanel;
-                        }
-                        dst += row * 128;
+                        for (int i = 0; i < kWtExpandRows / 4; ++i) v[i] = ptx::ld_shared_v4(from + (row + r0 + 4 * i) * 128 + lane * 16);
+                        const uint32_t dst = into + second * kWtPanel + (row + r0) * 128;
 #pragma unroll
                         for (int i = 0; i < kWtExpandRows / 4; ++i) {
                             // chunk c of row r lies at 16 (c ^ r % 8); the lanes of the second panel store their two chunks in the
                             // other order, so that the eight lanes of a row hit all banks
                             const int r = 4 * i + rr, c = 2 * (part & 3);
-                            const float s = __shfl_sync(0xffffffffu, sc.x, r);
+                            const float s = __shfl_sync(0xffffffffu, s_of, r0 + r);
                             const uint32_t x0 = second ? v[i].z : v[i].x, y0 = second ? v[i].w : v[i].y;
                             const uint32_t x1 = second ? v[i].x : v[i].z, y1 = second ? v[i].y : v[i].w;
                             const uint2 a0 = ptx::e4m3x4_scaled_bf16x4(x0, make_float2(s, s)), b0 = ptx::e4m3x4_scaled_bf16x4(y0, make_float2(s, s));
@@ -577,32 +603,69 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                             const uint2 a1 = ptx::e4m3x4_scaled_bf16x4(x1, make_float2(s, s)), b1 = ptx::e4m3x4_scaled_bf16x4(y1, make_float2(s, s));
                             ptx::st_shared_v4(dst + r * 128 + (((c + !second) ^ (r & 7)) << 4), make_uint4(a1.x, a1.y, b1.x, b1.y));
                         }
-                        sc = make_float4(sc.y, sc.z, sc.w, 0.f);
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(bar(kWbRawEmpty + raw_st.at));
-                        raw_st.next();
-                        if (stream_keys) {
-                            if (lane < 2) ptx::mbar_arrive_cluster(even_bar(kWbMade + (lane ? st2.at : st.at)));
-                            st = st2;
-                            st.next();
+                    };
+                    if (few) {
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            const int pair = 2 * h + slot, use = 2 * tile + h;  // of the pair's slot
+                            if (!(ok = warp_wait(kWbRawFull + pair, tile & 1))) break;
+                            if (use > 0 && !(ok = warp_wait(kWbEmpty + 2 * slot, (use - 1) & 1))) break;
+                            const float s = h ? (slot ? sc.w : sc.z) : (slot ? sc.y : sc.x);
+#pragma unroll 1
+                            for (int r0 = 0; r0 < 2 * kWtExpandRows; r0 += kWtExpandRows)
+                                expand(raw + pair * kWtPanel, ring + 2 * slot * kWtPanel, r0, s);
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            // (twice each: the barriers count eight warps a CTA)
+                            if (lane < 2) {
+                                ptx::mbar_arrive_cluster(even_bar(kWbMade + 2 * slot));
+                                ptx::mbar_arrive(bar(kWbRawEmpty + pair));
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int pair = 0; pair < 4; ++pair) {
+                            if (!(ok = warp_wait(kWbRawFull + raw_st.at, raw_st.round & 1))) break;
+                            WtStage st2 = st;
+                            uint32_t into = sbase + L::kOffStay + 2 * pair * kWtPanel;
+                            int apart = 0;  // how much further than the next the second panel lies
+                            if (stream_keys) {
+                                st2.next();
+                                if (st.used() && !(ok = warp_wait(kWbEmpty + st.at, st.last()))) break;
+                                if (st2.used() && !(ok = warp_wait(kWbEmpty + st2.at, st2.last()))) break;
+                                into = ring + st.at * kWtPanel;
+                                apart = second ? (st2.at - st.at - 1) * kWtPanel : 0;
+                            }
+                            expand(raw + raw_st.at * kWtPanel, into + apart, 0, sc.x);
+                            sc = make_float4(sc.y, sc.z, sc.w, 0.f);
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(bar(kWbRawEmpty + raw_st.at));
+                            raw_st.next();
+                            if (stream_keys) {
+                                if (lane < 2) ptx::mbar_arrive_cluster(even_bar(kWbMade + (lane ? st2.at : st.at)));
+                                st = st2;
+                                st.next();
+                            }
                         }
                     }
                     if (!ok) break;
-                    if (stream_keys) {
+                    if (!few && stream_keys) {
                         if (warp == kWtExpandWarp) {
                             if (st.used() && !(ok = warp_wait(kWbEmpty + st.at, st.last()))) break;
                             load_rope(ring + st.at * kWtPanel, kWbFull + st.at);
                         }
                         st.next();
-                    } else {
+                    } else if (!stream_keys) {
                         if (lane == 0) ptx::mbar_arrive_cluster(even_bar(kWbStayMade));
                         for (int i = 0; i < w.row_tiles * kPanels; ++i) st.next();
                     }
                     // (after the last fence, which would wait for these)
-                    pg0 = page(k + 1, 0);
-                    pg1 = page(k + 1, 1);
+                    pg0 = next0;
+                    pg1 = next1;
                     sc = scales(k + 1, row < kPage ? pg0 : pg1);
+                    next0 = page(k + 2, 0);
+                    next1 = page(k + 2, 1);
                 }
                 if (stream_keys) ++stays;  // the queries, the producer's
             }
