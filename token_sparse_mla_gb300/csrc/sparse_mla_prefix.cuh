@@ -750,7 +750,8 @@ __device__ __forceinline__ void pf_join(const float* slots_o, const float* slots
             }
             mn = fmaxf(mn, mk[u]);
         }
-        // a piece without a key has the sum 0 and zero rows: P was 0 and V had no NaN
+        // a piece without a key has the sum 0 and zero rows: P was 0 and V had no NaN (one whose logits are all NaN has no max
+        // either, and its NaN stays: 0 times it)
         const float keep = m == -CUDART_INF_F ? 0.f : ptx::ex2_approx(m - mn);
         m = mn;
         l *= keep;

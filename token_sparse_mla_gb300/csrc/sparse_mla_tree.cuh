@@ -864,13 +864,20 @@ __global__ void __launch_bounds__(kTrJoinThreads) sparse_mla_tree_join_kernel(co
         for (int u = 0; u < 2; ++u) {
             const int kk = min(k + u, last);
             const int64_t g = static_cast<int64_t>(kk == first ? job.z : 2 * kk) * p.slot_groups + group;
-            mk[u] = k + u <= last ? __ldg(p.part_ml + 64 * g + at) : -CUDART_INF_F;
+            mk[u] = __ldg(p.part_ml + 64 * g + at);
             lk[u] = __ldg(p.part_ml + 64 * g + 32 + at);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[u][e] = __ldg(reinterpret_cast<const float4*>(p.part_o) + (g * 128 + chunk + e) * 32 + at);
         }
+        if (k + 1 > last) {  // no second piece
+            mk[1] = -CUDART_INF_F;
+            lk[1] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[1][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         const float mn = fmaxf(m, fmaxf(mk[0], mk[1]));
-        // a piece without a key has the sum 0 and zero rows: P was 0 and V had nothing that is not finite
+        // A piece without a max weighs 0 and is added all the same: without a key its sum and rows are 0 (P was 0 and V had
+        // nothing that is not finite), but where all that a row sees of it is NaN, they are NaN, and 0 times that stays.
         const float keep = m == -CUDART_INF_F ? 0.f : ptx::ex2_approx(m - mn);
         m = mn;
         l *= keep;
@@ -878,8 +885,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) sparse_mla_tree_join_kernel(co
         for (int e = 0; e < 8; ++e) acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            if (mk[u] == -CUDART_INF_F) continue;
-            const float wt = ptx::ex2_approx(mk[u] - m);
+            const float wt = mk[u] == -CUDART_INF_F ? 0.f : ptx::ex2_approx(mk[u] - m);
             l += wt * lk[u];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
