@@ -506,12 +506,13 @@ smla_status sparse_mla_weights(const void* q, const void* kv_cache, const int32_
  *   new_lengths   device, [seqs] int32, caller-owned: min(n, budget)
  *   new_weights   device, [seqs, new_blocks * 64] fp32, caller-owned, zero behind the
  *                 kept rows'
- * kept, new_lengths and new_weights must overlap neither each other nor the inputs.
+ * kept, new_lengths and new_weights must overlap neither each other nor the inputs
+ * (refused): lengths are not updated in place.
  * A kept row that lies outside the cache, or would be copied to outside it, is not copied,
  * and the next sparse_mla_sync_status() returns SMLA_ERR_INDEX_RANGE.  Exact, and
  * repeated calls give identical bytes.  seqs = 0 is a no-op.  Allocates nothing;
  * asynchronous on `stream`.  Errors: SMLA_ERR_INVALID_ARG for bad sizes or format, a
- * null pointer or misalignment; SMLA_ERR_CUDA if a launch fails.
+ * null pointer, misalignment or overlap; SMLA_ERR_CUDA if a launch fails.
  */
 smla_status sparse_mla_evict(void* kv_cache, const int32_t* block_tables, const int32_t* lengths, const float* weights,
                              const int32_t* new_tables, int32_t seqs, int32_t blocks, int32_t new_blocks, int32_t budget, int32_t sinks,

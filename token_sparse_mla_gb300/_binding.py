@@ -768,7 +768,8 @@ def sparse_mla_evict(kv_cache: torch.Tensor, block_tables: torch.Tensor, lengths
     block_tables [seqs, blocks] int32, lengths [seqs] int32, weights [seqs, blocks * 64] fp32 as
     sparse_mla_weights gives them, new_tables [seqs, new_blocks] int32: pages of the same cache that
     hold no row of any sequence.  Returns kept [seqs, budget] int32 (positions, ascending, then -1),
-    new_lengths [seqs] int32 and new_weights [seqs, new_blocks * 64] fp32.  A row that lies or would go
+    new_lengths [seqs] int32 and new_weights [seqs, new_blocks * 64] fp32; passed in, they are tensors of
+    their own (new_lengths is not lengths, nor new_weights weights: refused).  A row that lies or would go
     outside the cache is not copied and makes the next sync_status() raise SMLA_ERR_INDEX_RANGE.
     """
     num_slots = _cache_rows(kv_cache, kv_format)

@@ -136,6 +136,17 @@ smla_status encode_fn(EncodeTiledFn* fn) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+struct Span {
+    const char* name;
+    const void* at;
+    uint64_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+    const uint64_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x < y + b.bytes && y < x + a.bytes;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // 8 and 16 heads run the warp-MMA kernel (32-row stages); 32 and 64 the tcgen05 kernel.
@@ -1477,6 +1488,21 @@ smla_status sparse_mla_evict(void* kv_cache, const int32_t* block_tables, const 
     if (!aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(weights, 4) || !aligned(new_tables, 4) || !aligned(kept, 4) ||
         !aligned(new_lengths, 4) || !aligned(new_weights, 4))
         return fail(SMLA_ERR_INVALID_ARG, "tables, lengths, weights and kept must be 4-byte aligned");
+    // The selection writes its results while other CTAs still read the inputs: a length that changed under them would
+    // send the CTAs of a cluster different ways past its barriers.
+    const uint64_t n = static_cast<uint64_t>(seqs);
+    const Span spans[] = {{"kept", kept, n * budget * 4},
+                          {"new_lengths", new_lengths, n * 4},
+                          {"new_weights", new_weights, n * new_blocks * smla::kPage * 4},
+                          {"kv_cache", kv_cache, static_cast<uint64_t>(num_slots) * (kv_format == SMLA_KV_FP8 ? smla::kFp8RowBytes : smla::kDQK * 2)},
+                          {"block_tables", block_tables, n * blocks * 4},
+                          {"lengths", lengths, n * 4},
+                          {"weights", weights, n * blocks * smla::kPage * 4},
+                          {"new_tables", new_tables, n * new_blocks * 4}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 8; ++j)
+            if (overlap(spans[i], spans[j]))
+                return fail(SMLA_ERR_INVALID_ARG, "%s must not overlap %s", spans[i].name, spans[j].name);
     int dev = 0;
     DeviceState* ds = nullptr;
     const smla_status st = device_state(&dev, &ds);
