@@ -580,6 +580,14 @@ __device__ __forceinline__ uint2 ld_nc_l1_v2(const void* p) {
     return v;
 }
 
+// A value that another kernel may have written while this one was already running: from L2, never from a line that L1 took
+// before, and not moved ahead of the wait for that kernel.
+__device__ __forceinline__ int ld_gpu_s32(const int* p) {
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float ld_nc_f32(const void* p) {
     float v;
     asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));

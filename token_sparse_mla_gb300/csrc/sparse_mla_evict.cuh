@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kEvCopyThreads, 3) sparse_mla_evict_copy_kerne
                 i = j < p.sinks ? j : p.budget - always + j;
                 pos = n <= p.budget ? (i < n ? i : -1) : j < p.sinks ? i : n - p.budget + i;
             } else {
-                pos = __ldg(p.kept + static_cast<int64_t>(b) * p.budget + i);
+                // written since this kernel began, perhaps beside lengths or tables that the first phase has brought into L1
+                pos = ptx::ld_gpu_s32(p.kept + static_cast<int64_t>(b) * p.budget + i);
             }
             if (pos < 0) return;
             const int old_page = __ldg(p.tables + static_cast<int64_t>(b) * p.nb + pos / kPage);
