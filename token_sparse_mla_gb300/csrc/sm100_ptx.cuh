@@ -93,10 +93,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // The same for a whole warp (converged): every lane looks first, one waits if need be.  The same answer in every
-// lane.
+// lane.  What the phase made visible to the lane that saw it done, the barrier of the warp passes on to the others (a vote
+// orders no memory).
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* err,
                                                unsigned int err_code, uint64_t limit_ns) {
-    if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        __syncwarp();
+        return true;
+    }
     bool ok = true;
     if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort, err, err_code, limit_ns);
     ok = __shfl_sync(0xffffffffu, ok, 0);
