@@ -448,6 +448,19 @@ __device__ __forceinline__ void tmem_wait_ld() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// The same for loads into whole arrays, which are named behind the wait (no instruction): without the names, what computes on
+// them may be moved ahead of the wait, where their registers hold nothing yet.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+template <int... N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&... r)[N]) {
+    tmem_wait_ld();
+    (tmem_loaded(r), ...);
+}
+
 // The same, naming what was loaded: nothing that reads it can be moved before the wait.
 __device__ __forceinline__ void tmem_wait_ld16(uint32_t* r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         SMLA_TMEM_LD16(tmem + lane_base + L::kColS + s * L::kSBuf + 32 * sub + 16 * q, sv + 16 * q);
                         SMLA_TMEM_LD16(tmem + lane_base + L::kColS + s * L::kSBuf + kPfPage + 32 * sub + 16 * q, sw + 16 * q);
                     }
-                    ptx::tmem_wait_ld();
+                    ptx::tmem_wait_ld(sv, sw);
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(s ? s_empty1 : s_empty0);
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                             for (int cc = 0; cc < 8; ++cc) {
                                 uint32_t ov[16];
                                 SMLA_TMEM_LD16(tmem + lane_base + ocol0 + cc * 16, ov);
-                                ptx::tmem_wait_ld();
+                                ptx::tmem_wait_ld(ov);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
                                 SMLA_TMEM_ST16(tmem + lane_base + ocol0 + cc * 16, ov);
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     uint32_t ov[64];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) SMLA_TMEM_LD16(tmem + lane_base + ocol0 + cc * 64 + 16 * q, ov + 16 * q);
-                    ptx::tmem_wait_ld();
+                    ptx::tmem_wait_ld(ov);
                     if (whole) {
                         __nv_bfloat16* dst = p.out + row0 * kDV + 256 * half + 128 * sub + 64 * cc + (lane & 3) * 8;
 #pragma unroll
