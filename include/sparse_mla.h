@@ -465,7 +465,8 @@ smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* 
  * in fp32, and 0 for the positions past the sequence's last drafted token.  A
  * sequence without tokens keeps its decayed weights.  The probabilities are those of
  * that attention (fp8 rows dequantised to bf16); with the lse of a merge they are those of
- * the whole that was merged.  Rows whose lse is -infinity add nothing.
+ * the whole that was merged.  Rows whose lse is -infinity add nothing, whatever their
+ * queries hold.
  *   q, kv_cache, block_tables, lengths, starts, mask   as in sparse_mla_tree
  *   lse        device, [T, h] fp32
  *   weights    device, [seqs, blocks * 64] fp32, or NULL: zeros (decay is then ignored)

@@ -75,3 +75,62 @@ def test_gpu_a_drafted_row_of_nan_alone_in_its_piece_is_not_lost(fmt, n):
     for b in (0, 1):
         o, l = _alone(batch, b)
         assert torch.equal(torch.isnan(o), torch.isnan(out[b:b + 1])) and torch.equal(torch.isnan(l), torch.isnan(lse[b:b + 1]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("seqs,h", [([(300, 5), (64, 0), (129, 1), (0, 7)], 8), ([(900, 3), (40, 30)], 8), ([(300, 9), (64, 40), (700, 2)], 32)])
+def test_gpu_rows_of_lse_minus_infinity_add_nothing(fmt, seqs, h):
+    """Whatever their logits are: NaN or infinite queries (a padded batch's, or tokens that were not accepted) give the same
+    bytes as any others.  Up to 128 rows a sequence, up to 256, and more."""
+    batch = Batch(seqs, h, 43, fmt)
+    _, lse = _tree(batch)
+    g = torch.Generator().manual_seed(5)
+    gone = torch.rand(batch.T, h, generator=g) < 0.3
+    gone[int(batch.starts[1]) - 1] = True  # a token with all its heads
+    lse[gone] = float("-inf")
+    prev = torch.rand(len(seqs), batch.blocks * 64, generator=g)
+
+    def run():
+        out = smla.sparse_mla_weights(**batch.to(DEV), lse=lse.to(DEV), weights=prev.to(DEV), decay=0.5, kv_format=fmt)
+        smla.sync_status()
+        return out.cpu()
+
+    want = run()
+    assert torch.isfinite(want).all()
+    for value in (float("nan"), float("inf"), float("-inf"), 3e38):
+        batch.q[gone] = value
+        assert torch.equal(run(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_gpu_nan_in_a_row_that_counts_is_not_lost(fmt):
+    """Beside rows that add nothing: a NaN query with a finite lse, and an lse of NaN, reach every position that they see;
+    an lse of +infinity makes finite logits nothing and NaN ones NaN."""
+    for many in (3, 40):
+        batch = Batch([(200, many), (70, many)], 8, 44, fmt)
+        _, lse = _tree(batch)
+        lse[many - 1, 2] = float("-inf")
+        lse[0, 1] = float("inf")
+
+        def run():
+            out = smla.sparse_mla_weights(**batch.to(DEV), lse=lse.to(DEV), kv_format=fmt)
+            smla.sync_status()
+            return out.cpu()
+
+        clean = run()
+        assert torch.isfinite(clean).all()
+        keep = batch.q.clone()
+        for hurt in ("query", "query at +inf", "lse"):
+            batch.q = keep.clone()
+            at = lse[0, 3].item()
+            if hurt == "query":
+                batch.q[0, 3, 9] = float("nan")
+            elif hurt == "query at +inf":
+                batch.q[0, 1, 9] = float("nan")
+            else:
+                lse[0, 3] = float("nan")
+            out = run()
+            lse[0, 3] = at
+            assert torch.isnan(out[0, :200]).all() and torch.equal(out[1], clean[1])

@@ -688,14 +688,15 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
         auto warp_wait = [&](int i, uint32_t parity) -> bool {
             return ptx::mbar_wait_warp(bar(i), parity, sAbort, &g_smla_error, kErrTimeout, kWaitLimitNs);
         };
-        // minus the LSE of row tid of row tile i: the table's entry (a row that saw nothing adds nothing: -inf)
+        // minus the LSE of row tid of row tile i: the table's entry.  +inf, of a row that adds nothing, is kept out of the sums
+        // as keys that a token does not see are (a NaN logit would pass through any number).
         auto entry = [&](int i) -> float {
             if (tid >= w.rows(p, i)) return -CUDART_INF_F;
-            const float x = __ldg(p.lse + static_cast<int64_t>(w.s.first) * p.bp.h + static_cast<int64_t>(i) * kWtRows + tid);
-            return x == -CUDART_INF_F ? x : -x;
+            return -__ldg(p.lse + static_cast<int64_t>(w.s.first) * p.bp.h + static_cast<int64_t>(i) * kWtRows + tid);
         };
         bool failed = false;
-        int item = 0, tables = 0;
+        int item = 0;
+        uint32_t tables = 0u;  // bit 0: which of the two tables comes next, bit 1: rows of the last one add nothing
         for (bool more = any; !failed && more; more = w.next(p)) {
             float mine = entry(0);
             for (int k = w.k0; !failed && k < w.k1; ++k) {
@@ -709,13 +710,17 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 for (int i = 0; i < w.row_tiles; ++i, ++item) {
                     if (w.row_tiles > 1 || k == w.k0) {  // the row tile's table, the next one's entry on its way
-                        reinterpret_cast<volatile float*>(smem + L::kOffLse)[(tables & 1) * kWtRows + tid] = mine;
-                        ++tables;
+                        const bool nothing = mine == CUDART_INF_F;
+                        reinterpret_cast<volatile float*>(smem + L::kOffLse)[(tables & 1u) * kWtRows + tid] = mine;
+                        tables = (tables & 1u) ^ 1u;
                         if (w.row_tiles > 1) mine = entry(i + 1 < w.row_tiles ? i + 1 : 0);
-                        failed = ptx::named_bar_red_or(1u, 32u * kWtSumWarps, failed);
+                        if (ptx::named_bar_red_or(1u, 32u * kWtSumWarps, failed || nothing)) {
+                            tables |= 2u;
+                            failed = ptx::named_bar_red_or(1u, 32u * kWtSumWarps, failed);
+                        }
                         if (failed) break;
                     }
-                    const uint32_t table = s_lse + ((tables - 1) & 1) * kWtRows * 4;
+                    const uint32_t table = s_lse + (~tables & 1u) * kWtRows * 4;
                     const int buf = item & 1;
                     const int columns = w.columns(p, i) / 2, c_first = half * columns;
                     const int limit = min(w.rows(p, i) - c_first, columns);  // this half's columns that are rows
@@ -738,10 +743,11 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                             pr[4 * e + 2] = ptx::ex2_approx(y1.x);
                             pr[4 * e + 3] = ptx::ex2_approx(y1.y);
                         }
-                        if (tail || c0 + 16 > limit) {
+                        if (tail || (tables & 2u) || c0 + 16 > limit) {
                             // lane l < 16: which of the warp's 32 keys column c0 + l sees
                             uint32_t seen = 0u;
-                            if (lane < 16 && c0 + lane < limit) seen = seen_bits(p.bp, w.s, (i * kWtRows + c_first + c0 + lane) / p.bp.h, key - lane);
+                            if (lane < 16 && c0 + lane < limit && ptx::ld_shared_f32(table + (c_first + c0 + lane) * 4) != CUDART_INF_F)
+                                seen = seen_bits(p.bp, w.s, (i * kWtRows + c_first + c0 + lane) / p.bp.h, key - lane);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 if (!((__shfl_sync(0xffffffffu, seen, e) >> lane) & 1u)) pr[e] = 0.f;
