@@ -576,24 +576,54 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
+// Global loads.  A kernel here may be on the machine before the one ahead of it has ended (programmatic dependent launch), so
+// that what it reads was written in its own lifetime, if ahead of its grid_dependency_wait.  The read-only path
+// (ld.global.nc, __ldg) is not for that: nothing orders its loads behind the wait, nor keeps them off a line that L1 took
+// before.  So these are ordinary loads; the compiler leaves them behind the wait.
+template <class T>
+__device__ __forceinline__ T ld(const T* p) {
+    return *p;
+}
+
+// The same that the compiler may move and join, for addresses that come out of what was itself read behind the wait, or
+// of a value from `behind`.
+__device__ __forceinline__ uint32_t ld_from(const uint32_t* p) {
+    uint32_t v;
+    asm("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int ld_from(const int* p) { return static_cast<int>(ld_from(reinterpret_cast<const uint32_t*>(p))); }
+__device__ __forceinline__ float ld_from(const float* p) { return __uint_as_float(ld_from(reinterpret_cast<const uint32_t*>(p))); }
+__device__ __forceinline__ float4 ld_from(const float4* p) {
+    float4 v;
+    asm("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
+// x, as known only from here on (no instruction).
+__device__ __forceinline__ int behind(int x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
 }
 
 // the same, kept in L1: for what many warps of an SM read
-__device__ __forceinline__ uint4 ld_nc_l1_v4(const void* p) {
+__device__ __forceinline__ uint4 ld_l1_v4(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 
-__device__ __forceinline__ uint2 ld_nc_l1_v2(const void* p) {
+__device__ __forceinline__ uint2 ld_l1_v2(const void* p) {
     uint2 v;
-    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
 }
 
@@ -605,9 +635,9 @@ __device__ __forceinline__ int ld_gpu_s32(const int* p) {
     return v;
 }
 
-__device__ __forceinline__ float ld_nc_f32(const void* p) {
+__device__ __forceinline__ float ld_f32(const void* p) {
     float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
     return v;
 }
 

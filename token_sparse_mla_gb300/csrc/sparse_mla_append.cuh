@@ -99,23 +99,23 @@ __global__ void __launch_bounds__(kAppendThreads) sparse_mla_append_kernel(const
     const uint4* src16 = reinterpret_cast<const uint4*>(src);
     const int c0 = KVF == 0 ? lane : 2 * lane;       // this lane's 16-byte chunks of the latent
     const int c1 = KVF == 0 ? 32 + lane : 2 * lane + 1;
-    const uint4 v0 = ptx::ld_nc_v4(src16 + c0);
-    const uint4 v1 = ptx::ld_nc_v4(src16 + c1);
-    const uint32_t pair = __float_as_uint(ptx::ld_nc_f32(src + kDV + 2 * lane));
+    const uint4 v0 = ptx::ld_v4(src16 + c0);
+    const uint4 v1 = ptx::ld_v4(src16 + c1);
+    const uint32_t pair = __float_as_uint(ptx::ld_f32(src + kDV + 2 * lane));
     uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
     if (p.norm_w != nullptr) {
-        w0 = ptx::ld_nc_l1_v4(reinterpret_cast<const uint4*>(p.norm_w) + c0);
-        w1 = ptx::ld_nc_l1_v4(reinterpret_cast<const uint4*>(p.norm_w) + c1);
+        w0 = ptx::ld_l1_v4(reinterpret_cast<const uint4*>(p.norm_w) + c0);
+        w1 = ptx::ld_l1_v4(reinterpret_cast<const uint4*>(p.norm_w) + c1);
     }
-    const int slot = __ldg(p.slots + t);
-    const int pos = __ldg(p.positions + t);
+    const int slot = ptx::ld(p.slots + t);
+    const int pos = ptx::ld(p.positions + t);
     if (slot == -1) return;  // an unused place of a padded batch
     if (slot < 0 || static_cast<int64_t>(slot) >= p.num_slots || pos < 0 || pos >= p.max_pos) {
         if (lane == 0) atomicOr(&g_smla_error, kErrRowRange);
         return;  // nothing is written for this token; the next status read says so
     }
     const float* cs = p.cos_sin + static_cast<int64_t>(pos) * 64;
-    const float cosv = __ldg(cs + lane), sinv = __ldg(cs + 32 + lane);
+    const float cosv = ptx::ld(cs + lane), sinv = ptx::ld(cs + 32 + lane);
 
     float x[16];
     unpack_bf16x8(v0, x);

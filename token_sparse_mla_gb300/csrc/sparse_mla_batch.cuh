@@ -23,6 +23,7 @@ struct BatchParams {
 
 // One sequence, its numbers brought into range: whatever the arrays hold, tokens stay inside [0, T) and
 // positions inside the block table.
+// (The loads below may be moved by the compiler, so b is a number from behind the kernel's wait for the one before.)
 struct Seq {
     int first, n;   // tokens [first, first + n)
     int len, keys;  // cached rows, and with the drafted ones
@@ -30,16 +31,16 @@ struct Seq {
 
 __device__ __forceinline__ Seq load_seq(const BatchParams& p, int b) {
     Seq s;
-    s.first = min(max(__ldg(p.starts + b), 0), p.T);
-    s.n = min(max(__ldg(p.starts + b + 1), s.first), p.T) - s.first;
+    s.first = min(max(ptx::ld_from(p.starts + b), 0), p.T);
+    s.n = min(max(ptx::ld_from(p.starts + b + 1), s.first), p.T) - s.first;
     const int most = p.nb * kPage;
-    s.len = min(max(__ldg(p.lengths + b), 0), most);
+    s.len = min(max(ptx::ld_from(p.lengths + b), 0), most);
     s.keys = static_cast<int>(min(static_cast<int64_t>(s.len) + s.n, static_cast<int64_t>(most)));
     return s;
 }
 
 __device__ __forceinline__ int page_of(const BatchParams& p, int b, const Seq& s, int i) {  // -1 past the end
-    return i * kPage < s.keys ? __ldg(p.tables + static_cast<int64_t>(b) * p.nb + i) : -1;
+    return i * kPage < s.keys ? ptx::ld_from(p.tables + static_cast<int64_t>(b) * p.nb + i) : -1;
 }
 
 __device__ __forceinline__ bool page_in_cache(const BatchParams& p, int page) {
@@ -64,9 +65,9 @@ __device__ __forceinline__ uint32_t seen_bits(const BatchParams& p, const Seq& s
         return c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
     }
     const uint32_t* m = p.mask + static_cast<int64_t>(s.first + i) * p.words;
-    if (j < 0) return (__ldg(m) << -j) | ((1u << -j) - 1u);
+    if (j < 0) return (ptx::ld_from(m) << -j) | ((1u << -j) - 1u);
     const int w = j >> 5;
-    const uint32_t lo = w < p.words ? __ldg(m + w) : 0u, hi = w + 1 < p.words ? __ldg(m + w + 1) : 0u;
+    const uint32_t lo = w < p.words ? ptx::ld_from(m + w) : 0u, hi = w + 1 < p.words ? ptx::ld_from(m + w + 1) : 0u;
     return __funnelshift_r(lo, hi, j & 31);
 }
 

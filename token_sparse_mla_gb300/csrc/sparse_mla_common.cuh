@@ -72,7 +72,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // it.  Callers hold raw entries in a ring and check them with valid_slot when they are used.
 __device__ __forceinline__ int fetch_entry(const int32_t* idx_row, int j, int j1, bool pred) {
     int v = -1;
-    if (pred && j < j1) v = __ldg(idx_row + j);
+    if (pred && j < j1) v = ptx::ld(idx_row + j);
     return v;
 }
 
@@ -174,9 +174,9 @@ __device__ __forceinline__ void gather_rows(const FwdParams& p, const int32_t* i
                     scl[i] = 0.f;
                     if (r < kRows && slot >= 0) {
                         const uint8_t* row = kv8 + static_cast<int64_t>(slot) * kFp8RowBytes;
-                        lat[i] = ptx::ld_nc_v4(row + 16 * lane);
-                        scl[i] = ptx::ld_nc_f32(row + 512 + 4 * (lane >> 3));
-                        if (lane < 8) rope[i] = ptx::ld_nc_v4(row + 528 + 16 * lane);
+                        lat[i] = ptx::ld_v4(row + 16 * lane);
+                        scl[i] = ptx::ld_f32(row + 512 + 4 * (lane >> 3));
+                        if (lane < 8) rope[i] = ptx::ld_v4(row + 528 + 16 * lane);
                     }
                 }
                 if (b >= NST) {

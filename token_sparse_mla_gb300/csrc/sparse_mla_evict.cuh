@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kEvThreads) sparse_mla_evict_select_kernel(con
     const float* w = p.weights + static_cast<int64_t>(b) * width;
     int32_t* kept = p.kept + static_cast<int64_t>(b) * p.budget;
     float* new_w = p.new_weights + static_cast<int64_t>(b) * new_width;
-    const int n = min(max(__ldg(p.lengths + b), 0), width);
+    const int n = min(max(ptx::ld(p.lengths + b), 0), width);
     const int k = min(n, p.budget);
     if (rank == 0 && tid == 0) p.new_lengths[b] = k;
     for (int i = k + rank * kEvThreads + tid; i < p.budget; i += cluster * kEvThreads) kept[i] = -1;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kEvThreads) sparse_mla_evict_select_kernel(con
     if (n <= p.budget) {  // uniform across the cluster
         for (int i = rank * kEvThreads + tid; i < n; i += cluster * kEvThreads) {
             kept[i] = i;
-            new_w[i] = __ldg(w + i);
+            new_w[i] = ptx::ld(w + i);
         }
         return;
     }
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kEvThreads) sparse_mla_evict_select_kernel(con
 #pragma unroll
         for (int e = 0; e < kEvPerLane; ++e) {
             const int i = c + kEvPerLane * 32 * warp + 32 * e + lane;
-            x[e] = i < seg1 ? __ldg(w + i) : 0.f;
+            x[e] = i < seg1 ? ptx::ld(w + i) : 0.f;
         }
     };
     float x[kEvPerLane];
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kEvCopyThreads, 3) sparse_mla_evict_copy_kerne
             if (j >= count) return;
             int i = p.sinks + j, pos;
             if (phase == 0) {
-                const int n = min(max(__ldg(p.lengths + b), 0), p.nb * kPage);
+                const int n = min(max(ptx::ld(p.lengths + b), 0), p.nb * kPage);
                 i = j < p.sinks ? j : p.budget - always + j;
                 pos = n <= p.budget ? (i < n ? i : -1) : j < p.sinks ? i : n - p.budget + i;
             } else {
@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(kEvCopyThreads, 3) sparse_mla_evict_copy_kerne
                 pos = ptx::ld_gpu_s32(p.kept + static_cast<int64_t>(b) * p.budget + i);
             }
             if (pos < 0) return;
-            const int old_page = __ldg(p.tables + static_cast<int64_t>(b) * p.nb + pos / kPage);
-            const int new_page = __ldg(p.new_tables + static_cast<int64_t>(b) * p.new_nb + i / kPage);
+            const int old_page = ptx::ld(p.tables + static_cast<int64_t>(b) * p.nb + pos / kPage);
+            const int new_page = ptx::ld(p.new_tables + static_cast<int64_t>(b) * p.new_nb + i / kPage);
             from = static_cast<int64_t>(old_page) * kPage + pos % kPage;
             to = static_cast<int64_t>(new_page) * kPage + i % kPage;
             if (from < 0 || from >= p.num_slots || to < 0 || to >= p.num_slots) {
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kEvCopyThreads, 3) sparse_mla_evict_copy_kerne
             for (int j = 0; j < kLoads; ++j) {
                 const int c = lane + 32 * j, u = c / kChunks;
                 const int64_t f = __shfl_sync(0xffffffffu, from, u & 31), t = __shfl_sync(0xffffffffu, to, u & 31);
-                if (u < kRows && t >= 0) v[j] = ptx::ld_nc_v4(cache + f * (kChunks * 16) + (c - u * kChunks) * 16);
+                if (u < kRows && t >= 0) v[j] = ptx::ld_v4(cache + f * (kChunks * 16) + (c - u * kChunks) * 16);
             }
             const int64_t dst = to;
             places(g + step, from, to);

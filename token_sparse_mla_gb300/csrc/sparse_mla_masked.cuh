@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kScatterThreads)
         __syncthreads();
         const int32_t* row = p.idx + t * p.topk;
         for (int j = threadIdx.x; j < p.topk; j += kScatterThreads) {
-            const int v = __ldg(row + j);
+            const int v = ptx::ld(row + j);
             if (v >= 0 && static_cast<int64_t>(v) < p.S) atomicOr(&words[v >> 5], 1u << (v & 31));
         }
         __syncthreads();
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
                     const int r = warp + i * kWarps;
-                    v[i] = r < nrows ? __ldg(reinterpret_cast<const uint4*>(p.mask + static_cast<int64_t>(t0 + r) * p.W) + cw)
+                    v[i] = r < nrows ? ptx::ld(reinterpret_cast<const uint4*>(p.mask + static_cast<int64_t>(t0 + r) * p.W) + cw)
                                      : make_uint4(0u, 0u, 0u, 0u);
                 }
                 uint4 acc = v[0];
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
                     const int r = warp + i * kWarps;
-                    v[i] = r < nrows ? __ldg(p.mask + static_cast<int64_t>(t0 + r) * p.W + w) : 0u;
+                    v[i] = r < nrows ? ptx::ld(p.mask + static_cast<int64_t>(t0 + r) * p.W + w) : 0u;
                 }
                 uint32_t acc = 0u;
 #pragma unroll
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             uint32_t w = 0u;
             if (live && j < nact) {
                 const int wi = 2 * static_cast<int>(sList[j]) + (kKeys * part) / 32;
-                if (wi < p.W) w = __ldg(mrow + wi) >> ((kKeys * part) % 32);
+                if (wi < p.W) w = ptx::ld(mrow + wi) >> ((kKeys * part) % 32);
             }
             return w;
         };

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kMergeThreads) sparse_mla_merge_kernel(const M
     const int64_t stride = (static_cast<int64_t>(gridDim.x) * kMergeThreads) >> 5;
     constexpr float kLog2e = 1.4426950408889634f;
     for (int64_t row = first; row < mp.rows; row += stride) {
-        const float lp = lane < mp.n ? __ldg(mp.lse_parts + lane * mp.rows + row) : -CUDART_INF_F;
+        const float lp = lane < mp.n ? ptx::ld(mp.lse_parts + lane * mp.rows + row) : -CUDART_INF_F;
         float m = lp;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

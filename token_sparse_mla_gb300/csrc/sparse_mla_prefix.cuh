@@ -128,7 +128,7 @@ struct PfParams {
 };
 
 // Page number of page i of the prefix (-1 past its end).
-__device__ __forceinline__ int pf_page(const PfParams& p, int i) { return i < p.npages ? __ldg(p.pages + i) : -1; }
+__device__ __forceinline__ int pf_page(const PfParams& p, int i) { return i < p.npages ? ptx::ld(p.pages + i) : -1; }
 
 __device__ __forceinline__ bool pf_in_cache(const PfParams& p, int page) {
     return page >= 0 && static_cast<int64_t>(page) * kPfPage < p.num_slots;
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kPfExpandThreads) sparse_mla_prefix_expand_ker
     const int64_t i = ((static_cast<int64_t>(blockIdx.x) * kPfExpandThreads + threadIdx.x) >> 5) * kRows;
     if (i >= static_cast<int64_t>(p.npages) * kPfPage) return;
     const int pg = static_cast<int>(i / kPfPage), in_page = static_cast<int>(i % kPfPage);
-    const int page = __ldg(p.pages + pg);
+    const int page = ptx::ld(p.pages + pg);
     const int valid = pf_valid(p, pg, page);
     const uint8_t* row0 = static_cast<const uint8_t*>(p.kv) + (static_cast<int64_t>(page) * kPfPage + in_page) * kFp8RowBytes;
     // lane l: codes [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8), so that both stores are 512 contiguous bytes
@@ -678,11 +678,11 @@ __global__ void __launch_bounds__(kPfExpandThreads) sparse_mla_prefix_expand_ker
         rope[u] = 0u;
         if (in_page + u < valid) {
             const uint8_t* row = row0 + u * kFp8RowBytes;
-            a[u] = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-            b[u] = __ldg(reinterpret_cast<const uint2*>(row) + 32 + lane);
-            sa[u] = __ldg(reinterpret_cast<const float*>(row + 512) + (lane >> 4));
-            sb[u] = __ldg(reinterpret_cast<const float*>(row + 520) + (lane >> 4));
-            rope[u] = __ldg(reinterpret_cast<const uint32_t*>(row + 528) + lane);
+            a[u] = ptx::ld(reinterpret_cast<const uint2*>(row) + lane);
+            b[u] = ptx::ld(reinterpret_cast<const uint2*>(row) + 32 + lane);
+            sa[u] = ptx::ld(reinterpret_cast<const float*>(row + 512) + (lane >> 4));
+            sb[u] = ptx::ld(reinterpret_cast<const float*>(row + 520) + (lane >> 4));
+            rope[u] = ptx::ld(reinterpret_cast<const uint32_t*>(row + 528) + lane);
         }
     }
 #pragma unroll
@@ -736,9 +736,9 @@ __device__ __forceinline__ void pf_join(const float* slots_o, const float* slots
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             const int64_t g = group_of(min(kk + PARTS * u, k1));
-            mk[u] = __ldg(slots_ml + 64 * g + at);
-            lk[u] = __ldg(slots_ml + 64 * g + 32 + at);
-            v[u] = __ldg(part_o + g * (128 * 32));
+            mk[u] = ptx::ld(slots_ml + 64 * g + at);
+            lk[u] = ptx::ld(slots_ml + 64 * g + 32 + at);
+            v[u] = ptx::ld(part_o + g * (128 * 32));
         }
         float mn = m;
 #pragma unroll

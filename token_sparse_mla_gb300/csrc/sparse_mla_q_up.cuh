@@ -134,13 +134,13 @@ __device__ __forceinline__ void turn_tokens(const QupParams& p, int first, int s
     constexpr int kFlight = 8;
     const int hd = lane >> 3, l8 = lane & 7;
     auto position = [&](int64_t t) -> int {
-        const int pos = t < p.T ? __ldg(p.positions + t) : -1;
+        const int pos = t < p.T ? ptx::ld(p.positions + t) : -1;
         const bool bad = pos != -1 && (pos < 0 || pos >= p.max_pos);
         if (bad && lane == 0) atomicOr(&g_smla_error, kErrRowRange);
         return bad ? -1 : pos;
     };
     auto angles = [&](int pos, int off) -> float4 {
-        const uint4 v = ptx::ld_nc_v4(p.cos_sin + static_cast<int64_t>(max(pos, 0)) * 64 + off + 4 * l8);
+        const uint4 v = ptx::ld_v4(p.cos_sin + static_cast<int64_t>(max(pos, 0)) * 64 + off + 4 * l8);
         return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
     };
     int64_t t = first;
@@ -157,7 +157,7 @@ __device__ __forceinline__ void turn_tokens(const QupParams& p, int first, int s
 #pragma unroll
             for (int e = 0; e < kFlight; ++e) {
                 const int hh = min(h0 + 4 * e + hd, p.h - 1);
-                x[e] = ptx::ld_nc_v4(p.q + (t * p.h + hh) * (DN + 64) + DN + 8 * l8);
+                x[e] = ptx::ld_v4(p.q + (t * p.h + hh) * (DN + 64) + DN + 8 * l8);
             }
 #pragma unroll
             for (int e = 0; e < kFlight; ++e) {

@@ -366,8 +366,8 @@ __device__ __forceinline__ void load_q_frags(const FwdParams& p, int t, int cw, 
         for (int nt = 0; nt < H / 8; ++nt) {
             const unsigned int* qr = reinterpret_cast<const unsigned int*>(
                 qt + (nt * 8 + g) * kDQK + 16 * (kSmKSteps * cw + kk) + 2 * tq);
-            bq[kk][nt][0] = __ldg(qr);
-            bq[kk][nt][1] = __ldg(qr + 4);
+            bq[kk][nt][0] = ptx::ld(qr);
+            bq[kk][nt][1] = ptx::ld(qr + 4);
         }
     }
 }

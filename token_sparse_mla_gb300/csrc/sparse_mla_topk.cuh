@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kTopkThreads, 6) sparse_mla_topk_kernel(const 
     n64 = n64 < 0 ? 0 : (n64 > p.S ? p.S : n64);  // a length outside [0, S] is clamped
     const int n = static_cast<int>(n64);
     const int k = n < p.topk ? n : p.topk;
-    auto slot_of = [&](int i) -> int32_t { return p.block_table ? __ldg(p.block_table + (i >> 6)) * 64 + (i & 63) : i; };
+    auto slot_of = [&](int i) -> int32_t { return p.block_table ? ptx::ld(p.block_table + (i >> 6)) * 64 + (i & 63) : i; };
     if (k == n) {  // the history is no longer than topk: all of it, then the padding
         for (int i = tid; i < p.topk; i += kTopkThreads) orow[i] = i < n ? slot_of(i) : -1;
         return;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kTopkThreads, 6) sparse_mla_topk_kernel(const 
     const bool vec = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
     auto load4 = [&](int q, float* x, auto full) {
         if (vec && (decltype(full)::value || q + 4 <= n)) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(row + q));
+            const float4 v = ptx::ld(reinterpret_cast<const float4*>(row + q));
             x[0] = v.x;
             x[1] = v.y;
             x[2] = v.z;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kTopkThreads, 6) sparse_mla_topk_kernel(const 
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                x[j] = (decltype(full)::value || q + j < n) ? __ldg(row + q + j) : -INFINITY;
+                x[j] = (decltype(full)::value || q + j < n) ? ptx::ld(row + q + j) : -INFINITY;
         }
     };
     // one scan step: thread tid's scores of step c0 are c0 + 1024 g + 4 tid + j (g, j < 4);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kTopkThreads, 6) sparse_mla_topk_kernel(const 
                 const float4* src = row4 + (c0 >> 2) + tid;
                 float4 v[kTopkGroups];
 #pragma unroll
-                for (int g = 0; g < kTopkGroups; ++g) v[g] = __ldg(src + 256 * g);
+                for (int g = 0; g < kTopkGroups; ++g) v[g] = ptx::ld(src + 256 * g);
 #pragma unroll
                 for (int g = 0; g < kTopkGroups; ++g) {
                     atomicAdd(&buf[score_key(v[g].x) >> 20], 1u);
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kTopkThreads, 6) sparse_mla_topk_kernel(const 
                 }
             }
         }
-        for (int i = c0 + tid; i < n; i += kTopkThreads) atomicAdd(&buf[score_key(__ldg(row + i)) >> 20], 1u);
+        for (int i = c0 + tid; i < n; i += kTopkThreads) atomicAdd(&buf[score_key(ptx::ld(row + i)) >> 20], 1u);
     }
     __syncthreads();
     uint32_t krem = static_cast<uint32_t>(k);
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kTopkThreads, 6) sparse_mla_topk_kernel(const 
                 float x[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    x[e] = (decltype(full)::value || q0 + 32 * e < n) ? __ldg(row + q0 + 32 * e) : -INFINITY;
+                    x[e] = (decltype(full)::value || q0 + 32 * e < n) ? ptx::ld(row + q0 + 32 * e) : -INFINITY;
                 uint32_t mine = 0;  // lane e < 16 keeps word e and stores it
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kTopkThreads, 6) sparse_mla_topk_kernel(const 
 #pragma unroll
         for (int e = 0; e < kTopkPerThread; ++e) {
             const int c = 512 * warp + 32 * e + lane;
-            key[e] = c < static_cast<int>(nc) ? score_key(__ldg(row + buf[c])) : 0u;
+            key[e] = c < static_cast<int>(nc) ? score_key(ptx::ld(row + buf[c])) : 0u;
             valid |= static_cast<uint32_t>(c < static_cast<int>(nc)) << e;
         }
         // ---- key bits 19-10, then 9-0, over the candidates in bin
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kTopkThreads, 6) sparse_mla_topk_kernel(const 
         if (vec && i0 + kTopkPerThread <= n) {  // i0 is a multiple of 16: aligned
 #pragma unroll
             for (int e = 0; e < kTopkPerThread / 4; ++e) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(row + i0) + e);
+                const float4 v = ptx::ld(reinterpret_cast<const float4*>(row + i0) + e);
                 xs[4 * e] = v.x;
                 xs[4 * e + 1] = v.y;
                 xs[4 * e + 2] = v.z;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kTopkThreads, 6) sparse_mla_topk_kernel(const 
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < kTopkPerThread; ++e) xs[e] = i0 + e < n ? __ldg(row + i0 + e) : 0.f;
+            for (int e = 0; e < kTopkPerThread; ++e) xs[e] = i0 + e < n ? ptx::ld(row + i0 + e) : 0.f;
         }
         // bit e of gt / eq: score i0 + e is above the threshold / equal to it
         uint32_t gt = 0, eq = 0;

@@ -112,7 +112,7 @@ __device__ __forceinline__ int tree_blocks(const Seq& s) { return (s.keys + kPfK
 // All threads of the CTA: the start of pair `run`'s share, into *start (shared memory).
 __device__ __forceinline__ void tree_plan(const TrParams& p, int run, int threads, int64_t* scratch, TrStart* start) {
     const int per = (p.bp.B + threads - 1) / threads;
-    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.bp.B), b1 = min(b0 + per, p.bp.B);
+    const int b0 = min(ptx::behind(static_cast<int>(threadIdx.x)) * per, p.bp.B), b1 = min(b0 + per, p.bp.B);
     int64_t cost = 0, tiles = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq(p.bp, b);
@@ -209,8 +209,8 @@ struct TrCodes {
 #pragma unroll
             for (int e = 0; e < kParts; ++e) {
 #pragma unroll
-                for (int u = 0; u < kTrExpandRows; ++u) a[e][u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 256 * e);
-                sc[e] = ptx::ld_nc_f32(scales + 2 * e);
+                for (int u = 0; u < kTrExpandRows; ++u) a[e][u] = ptx::ld_l1_v2(src + u * kFp8RowBytes + 256 * e);
+                sc[e] = ptx::ld_f32(scales + 2 * e);
             }
         } else {  // rows that take no part become zeros
 #pragma unroll
@@ -218,9 +218,9 @@ struct TrCodes {
 #pragma unroll
                 for (int u = 0; u < kTrExpandRows; ++u) {
                     a[e][u] = make_uint2(0u, 0u);
-                    if (u < n) a[e][u] = ptx::ld_nc_l1_v2(src + u * kFp8RowBytes + 256 * e);
+                    if (u < n) a[e][u] = ptx::ld_l1_v2(src + u * kFp8RowBytes + 256 * e);
                 }
-                sc[e] = lane % kTrExpandRows < n ? ptx::ld_nc_f32(scales + 2 * e) : 0.f;
+                sc[e] = lane % kTrExpandRows < n ? ptx::ld_f32(scales + 2 * e) : 0.f;
             }
         }
     }
@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kPfMergeThreads) sparse_mla_tree_merge_kernel(
     ptx::grid_launch_dependents();
     const int dg = static_cast<int>(blockIdx.x % kSlices);
     const int group = static_cast<int>(blockIdx.x / kSlices) % p.slot_groups;
-    const int4 job = __ldg(p.job_list + blockIdx.x / kSlices / p.slot_groups);
+    const int4 job = ptx::ld(p.job_list + blockIdx.x / kSlices / p.slot_groups);
     const int live = min(job.y - 32 * group, 32);
     if (live <= 0) return;
     const int64_t row0 = static_cast<int64_t>(job.x) + 32 * group;
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(kTrJoinThreads) sparse_mla_tree_join_kernel(co
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int part = static_cast<int>(blockIdx.x & 1);  // of the dims
     const int group = static_cast<int>(blockIdx.x >> 1) % p.slot_groups;
-    const int4 job = __ldg(p.job_list + static_cast<int>(blockIdx.x >> 1) / p.slot_groups);
+    const int4 job = ptx::ld(p.job_list + static_cast<int>(blockIdx.x >> 1) / p.slot_groups);
     const int live = min(job.y - 32 * group, 32);
     if (live <= 0) return;
     const int at = min(lane, live - 1);  // a lane past the last row repeats it and stores nothing
@@ -864,10 +864,10 @@ __global__ void __launch_bounds__(kTrJoinThreads) sparse_mla_tree_join_kernel(co
         for (int u = 0; u < 2; ++u) {
             const int kk = min(k + u, last);
             const int64_t g = static_cast<int64_t>(kk == first ? job.z : 2 * kk) * p.slot_groups + group;
-            mk[u] = __ldg(p.part_ml + 64 * g + at);
-            lk[u] = __ldg(p.part_ml + 64 * g + 32 + at);
+            mk[u] = ptx::ld(p.part_ml + 64 * g + at);
+            lk[u] = ptx::ld(p.part_ml + 64 * g + 32 + at);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] = __ldg(reinterpret_cast<const float4*>(p.part_o) + (g * 128 + chunk + e) * 32 + at);
+            for (int e = 0; e < 8; ++e) v[u][e] = ptx::ld(reinterpret_cast<const float4*>(p.part_o) + (g * 128 + chunk + e) * 32 + at);
         }
         if (k + 1 > last) {  // no second piece
             mk[1] = -CUDART_INF_F;

@@ -131,7 +131,7 @@ __device__ __forceinline__ int weights_key_tiles(const Seq& s) { return s.n == 0
 // All threads of the CTA: the start of pair `run`'s share, into *start (shared memory).
 __device__ __forceinline__ void weights_plan(const WtParams& p, int run, int threads, int64_t* scratch, WtStart* start) {
     const int per = (p.bp.B + threads - 1) / threads;
-    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.bp.B), b1 = min(b0 + per, p.bp.B);
+    const int b0 = min(ptx::behind(static_cast<int>(threadIdx.x)) * per, p.bp.B), b1 = min(b0 + per, p.bp.B);
     auto cost_of = [&](const Seq& s) -> int64_t {
         return s.n == 0 ? 0 : kWtCostSeq + static_cast<int64_t>(weights_key_tiles(s)) * weights_tile_cost(weights_row_tiles(p, s));
     };
@@ -230,7 +230,7 @@ __device__ __forceinline__ void weights_fill(const WtParams& p, int first, int s
     const int lane = threadIdx.x & 31;
     const int width = p.bp.nb * kPage, chunks = (width + kChunk - 1) / kChunk;
     const int64_t total = static_cast<int64_t>(p.bp.B) * chunks;
-    for (int64_t c0 = first; c0 < total; c0 += 32 * static_cast<int64_t>(stride)) {
+    for (int64_t c0 = ptx::behind(first); c0 < total; c0 += 32 * static_cast<int64_t>(stride)) {
         const int64_t c = c0 + static_cast<int64_t>(lane) * stride;
         int b = 0, from = 0, to = 0, len = 0;
         if (c < total) {
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
                 auto scales = [&](int k, int pg) -> float4 {
                     const int n = page_rows(p.bp, w.s, 4 * k + 2 * rank + row / kPage, pg) - row % kPage, r = lane & (rows - 1);
                     const uint8_t* src = static_cast<const uint8_t*>(p.bp.kv) + (static_cast<int64_t>(pg) * kPage + row % kPage + r) * kFp8RowBytes;
-                    return r < n ? __ldg(reinterpret_cast<const float4*>(src + 512)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    return r < n ? ptx::ld_from(reinterpret_cast<const float4*>(src + 512)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 };
                 const int part = lane & 7, rr = lane >> 3;
                 const bool second = part >= 4;  // of the two panels
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(weights_threads<KVF>(), 1)
         // as keys that a token does not see are (a NaN logit would pass through any number).
         auto entry = [&](int i) -> float {
             if (tid >= w.rows(p, i)) return -CUDART_INF_F;
-            return -__ldg(p.lse + static_cast<int64_t>(w.s.first) * p.bp.h + static_cast<int64_t>(i) * kWtRows + tid);
+            return -ptx::ld_from(p.lse + static_cast<int64_t>(w.s.first) * p.bp.h + static_cast<int64_t>(i) * kWtRows + tid);
         };
         bool failed = false;
         int item = 0;
