@@ -467,6 +467,9 @@ smla_status sparse_mla_tree(const void* q, const void* kv_cache, const int32_t* 
  * that attention (fp8 rows dequantised to bf16); with the lse of a merge they are those of
  * the whole that was merged.  Rows whose lse is -infinity add nothing, whatever their
  * queries hold.
+ * Of drafted tokens only the accepted ones should count, at the places where their rows
+ * stay: append those rows behind the cached ones first, then call this with their q and lse
+ * as a chain.  They see the rows that they saw in the tree, so the lse is still theirs.
  *   q, kv_cache, block_tables, lengths, starts, mask   as in sparse_mla_tree
  *   lse        device, [T, h] fp32
  *   weights    device, [seqs, blocks * 64] fp32, or NULL: zeros (decay is then ignored)

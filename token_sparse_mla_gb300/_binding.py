@@ -726,6 +726,8 @@ def sparse_mla_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: to
     q, kv_cache, block_tables, lengths, starts, scale and mask as in sparse_mla_tree, lse [T, h] fp32 as
     it returned it.  weights [seqs, blocks * 64] fp32 are what earlier calls gathered (None: nothing yet);
     returns out of the same shape, which may be passed in and may be weights itself.
+    Of drafted tokens, gather from the accepted ones, as a chain, when their rows have been appended behind
+    the cached ones.
     """
     dev, T, h, num_slots = _queries(q, kv_cache, kv_format)
     seqs, blocks = _batch(dev, block_tables, lengths)
