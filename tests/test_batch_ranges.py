@@ -92,3 +92,15 @@ def test_the_numbers_brought_into_range():
     assert [s.shape for s in meant.sees] == [(21, 21), (9, 9)]
     out, lse, _, _ = br.tree(meant)
     assert np.isfinite(out[:21]).all() and np.isfinite(lse).sum() >= 21 * 16
+
+
+@pytest.mark.parametrize("seqs", [2 ** 31 - 1, 2 ** 31 - 600, 2 ** 31 - 1024])
+def test_more_sequences_than_the_threads_can_share_are_refused(seqs):
+    """The shares of a CTA's threads are rounded up and have to stay within 31 bits."""
+    import token_sparse_mla_gb300 as smla
+
+    lib, p = smla.library(), 0x1000
+    assert lib.sparse_mla_tree(p, p, p, p, p, p, 4, 8, seqs, 3, 1, 256, 0, 0.04, p, p, p, 1 << 62, None) == 1
+    assert "seqs" in lib.sparse_mla_last_error().decode()
+    assert lib.sparse_mla_weights(p, p, p, p, p, p, p, p, 0.5, 4, 8, seqs, 3, 1, 256, 0, 0.04, p, None) == 1
+    assert "seqs" in lib.sparse_mla_last_error().decode()

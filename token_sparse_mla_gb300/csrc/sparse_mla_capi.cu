@@ -513,6 +513,8 @@ smla_status check_batch_sizes(const uint32_t* mask, int32_t T, int32_t h, int32_
     if (!std::isfinite(scale)) return fail(SMLA_ERR_INVALID_ARG, "scale must be finite");
     if (mask != nullptr && mask_words < 1) return fail(SMLA_ERR_INVALID_ARG, "mask_words must be >= 1 (got %d)", mask_words);
     if (static_cast<int64_t>(T) * h > 0x7f000000LL) return fail(SMLA_ERR_INVALID_ARG, "T * h too large (%d, %d)", T, h);
+    // (a CTA's threads share the sequences, each as many, rounded up)
+    if (seqs > 0x7fffffff - 1024) return fail(SMLA_ERR_INVALID_ARG, "seqs too large (%d)", seqs);
     return SMLA_OK;
 }
 
