@@ -440,7 +440,7 @@ smla_status sparse_mla_prefix(const void* q, const void* kv_cache, const int32_t
  * out, lse and workspace must overlap neither each other nor the inputs.  What rows
  * past a sequence's end hold does not matter, nor what drafted rows hold that a
  * token does not see, infinities and NaN included.  (Of a drafted row with infinities a
- * token that sees it gets NaN, or 0 times it where its logit is -infinity.)
+ * token that sees it gets NaN, or nothing from it where its logit is -infinity.)
  * A token that sees no position gives O = 0 and LSE = -inf.  Lengths, starts and tables
  * are read on the device when the call runs, so that a captured call serves a batch
  * that grows.  Repeated calls with the same arguments give identical bytes.

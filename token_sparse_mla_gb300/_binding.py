@@ -428,7 +428,7 @@ def _call(dev: torch.device, stream, fn, *args) -> None:
 
 
 def _given(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, dev: torch.device) -> torch.Tensor:
-    """A result tensor that the caller passed, checked."""
+    """A tensor that the caller passed, checked."""
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
     if t.device != dev:
@@ -694,20 +694,8 @@ def sparse_mla_tree(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch
     mask_ptr, words = _tokens(dev, T, seqs, starts, mask)
     if scale is None:
         scale = D_QK ** -0.5
-    if out is None:
-        out = _empty((T, h, D_V), _BF16, dev, stream)
-    else:
-        if out.shape != (T, h, D_V) or out.dtype != _BF16 or not out.is_contiguous():
-            raise ValueError("out must be a contiguous [T, h, 512] bf16 tensor")
-        if out.device != dev:
-            _apart(dev, out=out)
-    if lse is None:
-        lse = _empty((T, h), _F32, dev, stream)
-    else:
-        if lse.shape != (T, h) or lse.dtype != _F32 or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous [T, h] fp32 tensor")
-        if lse.device != dev:
-            _apart(dev, lse=lse)
+    out = _empty((T, h, D_V), _BF16, dev, stream) if out is None else _given("out", out, (T, h, D_V), _BF16, dev)
+    lse = _empty((T, h), _F32, dev, stream) if lse is None else _given("lse", lse, (T, h), _F32, dev)
     workspace = _workspace(dev, stream, workspace, _tree_workspace_bytes, T, h, seqs)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     _call(dev, stream, library().sparse_mla_tree, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
@@ -732,26 +720,12 @@ def sparse_mla_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: to
     dev, T, h, num_slots = _queries(q, kv_cache, kv_format)
     seqs, blocks = _batch(dev, block_tables, lengths)
     mask_ptr, words = _tokens(dev, T, seqs, starts, mask)
-    if lse.shape != (T, h) or lse.dtype != _F32 or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous [{T}, {h}] fp32 tensor")
-    if lse.device != dev:
-        _apart(dev, lse=lse)
-    prev = None
-    if weights is not None:
-        if weights.shape != (seqs, blocks * 64) or weights.dtype != _F32 or not weights.is_contiguous():
-            raise ValueError(f"weights must be a contiguous [{seqs}, {blocks * 64}] fp32 tensor")
-        if weights.device != dev:
-            _apart(dev, weights=weights)
-        prev = weights.data_ptr()
+    _given("lse", lse, (T, h), _F32, dev)
+    prev = None if weights is None else _given("weights", weights, (seqs, blocks * 64), _F32, dev).data_ptr()
     if scale is None:
         scale = D_QK ** -0.5
-    if out is None:
-        out = _empty((seqs, blocks * 64), _F32, dev, stream)
-    else:
-        if out.shape != (seqs, blocks * 64) or out.dtype != _F32 or not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous [{seqs}, {blocks * 64}] fp32 tensor")
-        if out.device != dev:
-            _apart(dev, out=out)
+    out = (_empty((seqs, blocks * 64), _F32, dev, stream) if out is None
+           else _given("out", out, (seqs, blocks * 64), _F32, dev))
     _call(dev, stream, library().sparse_mla_weights, q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
           lengths.data_ptr(), starts.data_ptr(), mask_ptr, lse.data_ptr(), prev, float(decay), T, h, seqs, blocks, words,
           num_slots, KV_FORMATS[kv_format], float(scale), out.data_ptr())

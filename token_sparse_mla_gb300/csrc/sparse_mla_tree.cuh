@@ -11,7 +11,8 @@
 //
 // Bound.  A decode batch has few rows per sequence and every sequence its own rows in the cache: at up to
 // 128 rows a block is 147 KB from HBM for one tile.  76 pairs at the tile's pace of 1.65 us a block
-// take 6.8 TB/s, HBM's rate, so rows short of 128 cost nothing that a smaller tile would save.
+// take 6.8 TB/s, HBM's rate: rows short of 128 cost no traffic that a smaller tile would save.  (What one could save is
+// shared memory, for a second stage of K and V, which fp8 rows lack most; not built.)
 //
 // Work.  How many rows and keys there are is known on the device only.  Every CTA sums the cost of all
 // sequences' tiles (blocks, and kTrTileCost for a tile's queries, first block and epilogue) and takes its
@@ -23,7 +24,7 @@
 // that a token does not see has probability 0 there, but 0 times infinity or NaN would still spoil O: in
 // pages that reach past the cached rows the V tile is cleaned in shared memory before it is multiplied (rows
 // past the end zeroed, values that are not finite in the drafted rows zeroed: a token that does see such a
-// row has its NaN from S).
+// row has its NaN from S, but for a logit of -infinity, which counts for nothing).
 //
 // fp8.  Shared memory has no room for a block's codes, so eight more warps take them through registers, eight rows of
 // each page a warp, the next block's in flight as soon as this one's are written: its own page into K, as the MMA
@@ -307,200 +308,200 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
 
     if (warp >= kTrSoftmaxWarps && warp < kTrExpandWarp) {
-    if constexpr (KVF == 1) ptx::regs_down<kTrRegsIssue>();
-    if (warp == kTrTmaWarp) {
-        // ================================================================ TMA producer
-        TrWalk w(p, *start);
+        if constexpr (KVF == 1) ptx::regs_down<kTrRegsIssue>();
+        if (warp == kTrTmaWarp) {
+            // ================================================================ TMA producer
+            TrWalk w(p, *start);
             const bool any = w.next(p);
-        // As in the prefix kernel: the even CTA's thread expects both CTAs' bytes on its barrier, K runs a
-        // block ahead of V, pages are brought into L2 a block ahead.
-        if (p.by_tile && run == 0 && rank == 0)
-            for (int i = start->tiles + lane; i < p.jobs; i += 32) p.job_list[i] = make_int4(0, 0, 0, 0);
-        if (lane == 0) {
-            int4 job = make_int4(0, 0, 0, 0);
-            auto load_v = [&](int x, bool tail0, bool tail1, int row0, int row1) -> bool {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (x > 0 && !wait(kPbVEmpty + i, (x - 1) & 1)) return false;
-                    const uint32_t dst = sbase + L::kOffV + i * kPfVPage;
-                    if (i ? tail1 : tail0) {  // the softmax warps wait for this one themselves and clean it
-                        ptx::mbar_arrive_expect_tx(bar(kTbTail + i), static_cast<uint32_t>(kPfVPage));
-                        ptx::tma_load_3d(dst, &tm_v, 0, i ? row1 : row0, 4 * rank, bar(kTbTail + i));
-                    } else {
-                        if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbVFull + i), 2u * kPfVPage);
-                        ptx::tma_load_3d_pair(dst, &tm_v, 0, i ? row1 : row0, 4 * rank, even_bar(kPbVFull + i));
-                    }
-                }
-                return true;
-            };
-            // a page that is not there loads as zeros, from rows below 0
-            auto first_row = [&](int page) -> int { return page_in_cache(p.bp, page) ? page * kPage : -kPage; };
-            auto prefetch = [&](int i) {
-                if (i >= 2 * w.b1) return;
-                const int pg = page_of(p.bp, w.b, w.s, i);
-                const int n = page_rows(p.bp, w.s, i, pg);
-                if (n > 0)
-                    ptx::bulk_prefetch_l2(static_cast<const char*>(p.bp.kv) + static_cast<int64_t>(pg) * kPage * (KVF ? kFp8RowBytes : kDQK * 2),
-                                          static_cast<uint32_t>(n * (KVF ? kFp8RowBytes : kDQK * 2)));
-            };
-            bool ok = true;
-            int x = 0, piece = 0;
-            bool tail_v0 = false, tail_v1 = false;
-            int row_v0 = 0, row_v1 = 0;
-            for (bool more = any; ok && more; more = w.next(p), ++piece) {
-                if (rank == 0 && w.b0 == 0) {
-                    const int64_t runs = min(start->total, static_cast<int64_t>(p.pairs));
-                    const int64_t tile_end = start->end - w.end + w.nblk + kTrTileCost;
-                    if (!w.whole()) {
-                        const int64_t rows = static_cast<int64_t>(w.s.n) * p.bp.h - w.row0();
-                        job = make_int4(static_cast<int>(static_cast<int64_t>(w.s.first) * p.bp.h + w.row0()),
-                                        static_cast<int>(min(rows, static_cast<int64_t>(kPfRows))), 2 * run + (w.first ? 0 : 1),
-                                        static_cast<int>((tile_end * runs - 1) / start->total));
-                    }
-                    if (p.by_tile && w.tile_index < p.jobs) p.job_list[w.tile_index] = w.whole() ? make_int4(0, 0, 0, 0) : job;
-                }
-                if (piece > 0 && !(ok = wait(kPbQEmpty, (piece - 1) & 1))) break;
-                if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbQFull), 2u * kPfQBytes);
-                ptx::tma_load_3d_pair(sbase + L::kOffQ, &tm_q, 0,
-                                      static_cast<int>(static_cast<int64_t>(w.s.first) * p.bp.h + w.row0() + rank * kPfHalf), 0,
-                                      even_bar(kPbQFull));
-                if constexpr (KVF == 1) {
-                    for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
-                        if (b == w.b0) prefetch(2 * b + 2 + rank);
-                        prefetch(2 * b + 4 + rank);
-                        if (x > 0 && !(ok = wait(kPbKEmpty + 1, (x - 1) & 1))) break;
-                        if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kTbMade), 2u * kPfPanel);
-                        ptx::tma_load_2d_pair(sbase + L::kOffK + 8 * kPfPanel, &tm_k, 528, first_row(page_of(p.bp, w.b, w.s, 2 * b + rank)),
-                                              even_bar(kTbMade));
-                    }
-                    continue;
-                }
-                int pg0 = page_of(p.bp, w.b, w.s, 2 * w.b0), pg1 = page_of(p.bp, w.b, w.s, 2 * w.b0 + 1);
-                for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
-                    const int row0 = first_row(pg0), row1 = first_row(pg1);
-                    const int mine = rank == 0 ? row0 : row1;
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if (x > 0 && !(ok = wait(kPbKEmpty + g, (x - 1) & 1))) break;
-                        const uint32_t bytes = static_cast<uint32_t>((g ? kPfGroupB : kPfGroupA) * kPfPanel);
-                        if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbKFull + g), 2u * bytes);
-                        ptx::tma_load_3d_pair(sbase + L::kOffK + g * kPfGroupA * kPfPanel, g ? &tm_v : &tm_k, 0, mine,
-                                              g * kPfGroupA, even_bar(kPbKFull + g));
-                    }
-                    prefetch(2 * b + 2 + rank);
-                    pg0 = page_of(p.bp, w.b, w.s, 2 * b + 2);
-                    pg1 = page_of(p.bp, w.b, w.s, 2 * b + 3);
-                    if (ok && x > 0) ok = load_v(x - 1, tail_v0, tail_v1, row_v0, row_v1);
-                    row_v0 = row0;
-                    row_v1 = row1;
-                    tail_v0 = tree_tail(w.s, 2 * b);
-                    tail_v1 = tree_tail(w.s, 2 * b + 1);
-                }
-            }
-            if (KVF == 0 && ok && x > 0) ok = load_v(x - 1, tail_v0, tail_v1, row_v0, row_v1);
-            if (rank == 0 && !p.by_tile) p.job_list[run] = job;
-            // every copy has landed and been used, and no release of a stage is still on its way to
-            // this CTA's barriers, before it leaves
-            if (x > 0) {
-                for (int g = 0; ok && g < 2; ++g) ok = wait(kPbKEmpty + g, (x - 1) & 1);
-                // (with fp8 the softmax warps see the last of these; this thread has not followed them)
-                for (int i = 0; KVF == 0 && ok && i < 2; ++i) ok = wait(kPbVEmpty + i, (x - 1) & 1);
-                if (ok) ok = wait(kPbQEmpty, (piece - 1) & 1);
-            }
-            if (!ok) {  // gave up: copies in flight complete on the other CTA's barriers; leave them time to land
-                const uint64_t t0 = ptx::globaltimer_ns();
-                while (ptx::globaltimer_ns() - t0 < 2000000ull) {
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == kTrS1Warp || warp == kTrS2Warp) {
-        // ================================================================ S issuers, as in the prefix kernel
-        TrWalk w(p, *start);
-            const bool any = w.next(p);
-        if (rank == 0 && lane == 0) {
-            constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kPfRows, kPfKeys, 0, 0);
-            const bool ga = warp == kTrS1Warp;
-            const uint32_t off = ga ? 0u : static_cast<uint32_t>(kPfGroupA * kPfPanel);
-            const uint64_t dq = ptx::smem_desc_sw128(sbase + L::kOffQ + off, 16, 1024);
-            const uint64_t dk = ptx::smem_desc_sw128(sbase + L::kOffK + off, 16, 1024);
-            const uint32_t d0 = tmem + PfLayout::kColS + (ga ? 0 : kPfPage);
-            const int g = ga ? 0 : 1;
-            bool ok = true;
-            int x = 0, piece = 0;
-            for (bool more = any; ok && more; more = w.next(p), ++piece) {
-                if (!(ok = wait(kPbQFull, piece & 1))) break;
-                for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
-                    const int s = x & 1;
-                    if (x >= 2 && !(ok = wait(kPbSEmpty + s, ((x >> 1) - 1) & 1))) break;
-                    if (!(ok = wait(KVF == 1 ? kTbMade : kPbKFull + g, x & 1))) break;
-                    ptx::tc_fence_after();
-                    const uint32_t d = d0 + s * PfLayout::kSBuf;
-#pragma unroll
-                    for (int pn = 0; pn < kPfGroupB; ++pn)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            ptx::mma_bf16_ss_pair(d, dq + ((pn * kPfPanel + k * 32) >> 4), dk + ((pn * kPfPanel + k * 32) >> 4),
-                                                  kIdescS, (pn | k) != 0);
-                    if (ga) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            ptx::mma_bf16_ss_pair(d, dq + ((kPfGroupB * kPfPanel + k * 32) >> 4),
-                                                  dk + ((kPfGroupB * kPfPanel + k * 32) >> 4), kIdescS, 1u);
-                    }
-                    ptx::mma_commit_pair(bar(kPbSFull + s));
-                    ptx::mma_commit_pair(bar(kPbKEmpty + g));
-                    if (b + 1 == w.b1) ptx::mma_commit_pair(bar(kPbQEmpty));
-                }
-            }
-            // nothing is in flight when TMEM is freed, also after giving up
-            ptx::mma_commit_pair_local(bar(kTbDrain));
-            ptx::mbar_wait(bar(kTbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
-        }
-        __syncwarp();
-    } else {
-        // ================================================================ PV issuer
-        TrWalk w(p, *start);
-            const bool any = w.next(p);
-        if (rank == 0 && lane == 0) {
-            constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kPfRows, 256, 0, 1);
-            const uint64_t dv = ptx::smem_desc_sw128(sbase + L::kOffV, kPfPanel, 1024);
-            const uint64_t dp = ptx::smem_desc_sw128(sbase + L::kOffP, 16, 1024);
-            uint32_t v_parity = 0u;  // bit i: parity of the loads that came to V page i (tails have their own barriers)
-            bool ok = true;
-            int x = 0;
-            for (bool more = any; ok && more; more = w.next(p)) {
-                for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
+            // As in the prefix kernel: the even CTA's thread expects both CTAs' bytes on its barrier, K runs a
+            // block ahead of V, pages are brought into L2 a block ahead.
+            if (p.by_tile && run == 0 && rank == 0)
+                for (int i = start->tiles + lane; i < p.jobs; i += 32) p.job_list[i] = make_int4(0, 0, 0, 0);
+            if (lane == 0) {
+                int4 job = make_int4(0, 0, 0, 0);
+                auto load_v = [&](int x, bool tail0, bool tail1, int row0, int row1) -> bool {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        if (!(ok = wait(kPbPFull + i, x & 1))) break;
-                        if (KVF == 0 && !tree_tail(w.s, 2 * b + i)) {
-                            if (!(ok = wait(kPbVFull + i, (v_parity >> i) & 1u))) break;
-                            v_parity ^= 1u << i;
+                        if (x > 0 && !wait(kPbVEmpty + i, (x - 1) & 1)) return false;
+                        const uint32_t dst = sbase + L::kOffV + i * kPfVPage;
+                        if (i ? tail1 : tail0) {  // the softmax warps wait for this one themselves and clean it
+                            ptx::mbar_arrive_expect_tx(bar(kTbTail + i), static_cast<uint32_t>(kPfVPage));
+                            ptx::tma_load_3d(dst, &tm_v, 0, i ? row1 : row0, 4 * rank, bar(kTbTail + i));
+                        } else {
+                            if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbVFull + i), 2u * kPfVPage);
+                            ptx::tma_load_3d_pair(dst, &tm_v, 0, i ? row1 : row0, 4 * rank, even_bar(kPbVFull + i));
                         }
-                        ptx::tc_fence_after();
+                    }
+                    return true;
+                };
+                // a page that is not there loads as zeros, from rows below 0
+                auto first_row = [&](int page) -> int { return page_in_cache(p.bp, page) ? page * kPage : -kPage; };
+                auto prefetch = [&](int i) {
+                    if (i >= 2 * w.b1) return;
+                    const int pg = page_of(p.bp, w.b, w.s, i);
+                    const int n = page_rows(p.bp, w.s, i, pg);
+                    if (n > 0)
+                        ptx::bulk_prefetch_l2(static_cast<const char*>(p.bp.kv) + static_cast<int64_t>(pg) * kPage * (KVF ? kFp8RowBytes : kDQK * 2),
+                                              static_cast<uint32_t>(n * (KVF ? kFp8RowBytes : kDQK * 2)));
+                };
+                bool ok = true;
+                int x = 0, piece = 0;
+                bool tail_v0 = false, tail_v1 = false;
+                int row_v0 = 0, row_v1 = 0;
+                for (bool more = any; ok && more; more = w.next(p), ++piece) {
+                    if (rank == 0 && w.b0 == 0) {
+                        const int64_t runs = min(start->total, static_cast<int64_t>(p.pairs));
+                        const int64_t tile_end = start->end - w.end + w.nblk + kTrTileCost;
+                        if (!w.whole()) {
+                            const int64_t rows = static_cast<int64_t>(w.s.n) * p.bp.h - w.row0();
+                            job = make_int4(static_cast<int>(static_cast<int64_t>(w.s.first) * p.bp.h + w.row0()),
+                                            static_cast<int>(min(rows, static_cast<int64_t>(kPfRows))), 2 * run + (w.first ? 0 : 1),
+                                            static_cast<int>((tile_end * runs - 1) / start->total));
+                        }
+                        if (p.by_tile && w.tile_index < p.jobs) p.job_list[w.tile_index] = w.whole() ? make_int4(0, 0, 0, 0) : job;
+                    }
+                    if (piece > 0 && !(ok = wait(kPbQEmpty, (piece - 1) & 1))) break;
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbQFull), 2u * kPfQBytes);
+                    ptx::tma_load_3d_pair(sbase + L::kOffQ, &tm_q, 0,
+                                          static_cast<int>(static_cast<int64_t>(w.s.first) * p.bp.h + w.row0() + rank * kPfHalf), 0,
+                                          even_bar(kPbQFull));
+                    if constexpr (KVF == 1) {
+                        for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
+                            if (b == w.b0) prefetch(2 * b + 2 + rank);
+                            prefetch(2 * b + 4 + rank);
+                            if (x > 0 && !(ok = wait(kPbKEmpty + 1, (x - 1) & 1))) break;
+                            if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kTbMade), 2u * kPfPanel);
+                            ptx::tma_load_2d_pair(sbase + L::kOffK + 8 * kPfPanel, &tm_k, 528, first_row(page_of(p.bp, w.b, w.s, 2 * b + rank)),
+                                                  even_bar(kTbMade));
+                        }
+                        continue;
+                    }
+                    int pg0 = page_of(p.bp, w.b, w.s, 2 * w.b0), pg1 = page_of(p.bp, w.b, w.s, 2 * w.b0 + 1);
+                    for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
+                        const int row0 = first_row(pg0), row1 = first_row(pg1);
+                        const int mine = rank == 0 ? row0 : row1;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int n = 0; n < 2; ++n)
-                                ptx::mma_bf16_ss_pair(tmem + PfLayout::kColO + 128 * n, dp + ((i * kPfPanel + k * 32) >> 4),
-                                                      dv + ((i * kPfVPage + 2 * n * kPfPanel + k * 2048) >> 4), kIdescPV,
-                                                      (b != w.b0 || i > 0 || k > 0) ? 1u : 0u);
-                        ptx::mma_commit_pair(bar(kPbVEmpty + i));
+                        for (int g = 0; g < 2; ++g) {
+                            if (x > 0 && !(ok = wait(kPbKEmpty + g, (x - 1) & 1))) break;
+                            const uint32_t bytes = static_cast<uint32_t>((g ? kPfGroupB : kPfGroupA) * kPfPanel);
+                            if (rank == 0) ptx::mbar_arrive_expect_tx(bar(kPbKFull + g), 2u * bytes);
+                            ptx::tma_load_3d_pair(sbase + L::kOffK + g * kPfGroupA * kPfPanel, g ? &tm_v : &tm_k, 0, mine,
+                                                  g * kPfGroupA, even_bar(kPbKFull + g));
+                        }
+                        prefetch(2 * b + 2 + rank);
+                        pg0 = page_of(p.bp, w.b, w.s, 2 * b + 2);
+                        pg1 = page_of(p.bp, w.b, w.s, 2 * b + 3);
+                        if (ok && x > 0) ok = load_v(x - 1, tail_v0, tail_v1, row_v0, row_v1);
+                        row_v0 = row0;
+                        row_v1 = row1;
+                        tail_v0 = tree_tail(w.s, 2 * b);
+                        tail_v1 = tree_tail(w.s, 2 * b + 1);
+                    }
+                }
+                if (KVF == 0 && ok && x > 0) ok = load_v(x - 1, tail_v0, tail_v1, row_v0, row_v1);
+                if (rank == 0 && !p.by_tile) p.job_list[run] = job;
+                // every copy has landed and been used, and no release of a stage is still on its way to
+                // this CTA's barriers, before it leaves
+                if (x > 0) {
+                    for (int g = 0; ok && g < 2; ++g) ok = wait(kPbKEmpty + g, (x - 1) & 1);
+                    // (with fp8 the softmax warps see the last of these; this thread has not followed them)
+                    for (int i = 0; KVF == 0 && ok && i < 2; ++i) ok = wait(kPbVEmpty + i, (x - 1) & 1);
+                    if (ok) ok = wait(kPbQEmpty, (piece - 1) & 1);
+                }
+                if (!ok) {  // gave up: copies in flight complete on the other CTA's barriers; leave them time to land
+                    const uint64_t t0 = ptx::globaltimer_ns();
+                    while (ptx::globaltimer_ns() - t0 < 2000000ull) {
                     }
                 }
             }
-            // nothing is in flight when TMEM is freed, also after giving up
-            ptx::mma_commit_pair_local(bar(kTbDrain));
-            ptx::mbar_wait(bar(kTbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
+            __syncwarp();
+        } else if (warp == kTrS1Warp || warp == kTrS2Warp) {
+            // ================================================================ S issuers, as in the prefix kernel
+            TrWalk w(p, *start);
+            const bool any = w.next(p);
+            if (rank == 0 && lane == 0) {
+                constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kPfRows, kPfKeys, 0, 0);
+                const bool ga = warp == kTrS1Warp;
+                const uint32_t off = ga ? 0u : static_cast<uint32_t>(kPfGroupA * kPfPanel);
+                const uint64_t dq = ptx::smem_desc_sw128(sbase + L::kOffQ + off, 16, 1024);
+                const uint64_t dk = ptx::smem_desc_sw128(sbase + L::kOffK + off, 16, 1024);
+                const uint32_t d0 = tmem + PfLayout::kColS + (ga ? 0 : kPfPage);
+                const int g = ga ? 0 : 1;
+                bool ok = true;
+                int x = 0, piece = 0;
+                for (bool more = any; ok && more; more = w.next(p), ++piece) {
+                    if (!(ok = wait(kPbQFull, piece & 1))) break;
+                    for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
+                        const int s = x & 1;
+                        if (x >= 2 && !(ok = wait(kPbSEmpty + s, ((x >> 1) - 1) & 1))) break;
+                        if (!(ok = wait(KVF == 1 ? kTbMade : kPbKFull + g, x & 1))) break;
+                        ptx::tc_fence_after();
+                        const uint32_t d = d0 + s * PfLayout::kSBuf;
+#pragma unroll
+                        for (int pn = 0; pn < kPfGroupB; ++pn)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                ptx::mma_bf16_ss_pair(d, dq + ((pn * kPfPanel + k * 32) >> 4), dk + ((pn * kPfPanel + k * 32) >> 4),
+                                                      kIdescS, (pn | k) != 0);
+                        if (ga) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                ptx::mma_bf16_ss_pair(d, dq + ((kPfGroupB * kPfPanel + k * 32) >> 4),
+                                                      dk + ((kPfGroupB * kPfPanel + k * 32) >> 4), kIdescS, 1u);
+                        }
+                        ptx::mma_commit_pair(bar(kPbSFull + s));
+                        ptx::mma_commit_pair(bar(kPbKEmpty + g));
+                        if (b + 1 == w.b1) ptx::mma_commit_pair(bar(kPbQEmpty));
+                    }
+                }
+                // nothing is in flight when TMEM is freed, also after giving up
+                ptx::mma_commit_pair_local(bar(kTbDrain));
+                ptx::mbar_wait(bar(kTbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
+            }
+            __syncwarp();
+        } else {
+            // ================================================================ PV issuer
+            TrWalk w(p, *start);
+            const bool any = w.next(p);
+            if (rank == 0 && lane == 0) {
+                constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kPfRows, 256, 0, 1);
+                const uint64_t dv = ptx::smem_desc_sw128(sbase + L::kOffV, kPfPanel, 1024);
+                const uint64_t dp = ptx::smem_desc_sw128(sbase + L::kOffP, 16, 1024);
+                uint32_t v_parity = 0u;  // bit i: parity of the loads that came to V page i (tails have their own barriers)
+                bool ok = true;
+                int x = 0;
+                for (bool more = any; ok && more; more = w.next(p)) {
+                    for (int b = w.b0; ok && b < w.b1; ++b, ++x) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (!(ok = wait(kPbPFull + i, x & 1))) break;
+                            if (KVF == 0 && !tree_tail(w.s, 2 * b + i)) {
+                                if (!(ok = wait(kPbVFull + i, (v_parity >> i) & 1u))) break;
+                                v_parity ^= 1u << i;
+                            }
+                            ptx::tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int n = 0; n < 2; ++n)
+                                    ptx::mma_bf16_ss_pair(tmem + PfLayout::kColO + 128 * n, dp + ((i * kPfPanel + k * 32) >> 4),
+                                                          dv + ((i * kPfVPage + 2 * n * kPfPanel + k * 2048) >> 4), kIdescPV,
+                                                          (b != w.b0 || i > 0 || k > 0) ? 1u : 0u);
+                            ptx::mma_commit_pair(bar(kPbVEmpty + i));
+                        }
+                    }
+                }
+                // nothing is in flight when TMEM is freed, also after giving up
+                ptx::mma_commit_pair_local(bar(kTbDrain));
+                ptx::mbar_wait(bar(kTbDrain), 0, nullptr, &g_smla_error, 0u, kDrainLimitNs);
+            }
+            __syncwarp();
         }
-        __syncwarp();
-    }
     } else if (warp >= kTrExpandWarp) {
         // ================================================================ expansion of fp8 rows
         if constexpr (KVF == 1) {
             ptx::regs_down<kTrRegsExpand>();
-        TrWalk w(p, *start);
+            TrWalk w(p, *start);
             const bool any = w.next(p);
             const int row = kTrExpandRows * (warp - kTrExpandWarp);
             auto warp_wait = [&](int i, uint32_t parity) -> bool {
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(tree_threads<KVF>(), 1)
         // ================================================================ softmax / output
         if constexpr (KVF == 1) ptx::regs_up<kTrRegsSoftmax>();
         TrWalk w(p, *start);
-            const bool any = w.next(p);
+        const bool any = w.next(p);
         const int quad = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
         const int half = quad >> 1;            // page of the block, dims 256 half .. + 255
