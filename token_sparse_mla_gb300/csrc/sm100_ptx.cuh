@@ -444,24 +444,25 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[4]
                  : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_wait_ld() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// The same for loads into whole arrays, which are named behind the wait (no instruction): without the names, what computes on
+// Waits for loads into the arrays r, which are named behind the wait (no instruction): without the names, what computes on
 // them may be moved ahead of the wait, where their registers hold nothing yet.
 template <int N>
 __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-template <int... N>
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&... r)[N]) {
-    tmem_wait_ld();
+template <int M, int N>
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[M][N]) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) tmem_loaded(r[i]);
+}
+template <class... A>
+__device__ __forceinline__ void tmem_wait_ld(A&... r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     (tmem_loaded(r), ...);
 }
 
-// The same, naming what was loaded: nothing that reads it can be moved before the wait.
+// The same for 16 registers of an array.
 __device__ __forceinline__ void tmem_wait_ld16(uint32_t* r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),

@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(TcRoles<KVF>::kThreads, 1)
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < NG; ++i) ptx::tmem_ld_16x256b(tmem + lane_base + L::kColS + s * HP + 8 * i, sv[i]);
-                ptx::tmem_wait_ld();
+                ptx::tmem_wait_ld(sv);
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(kBarSEmpty + s));
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(TcRoles<KVF>::kThreads, 1)
                                 uint32_t o[16];
                                 const uint32_t ta = tmem + lane_base + blk * HP + cc * 16;
                                 SMLA_TMEM_LD16(ta, o);
-                                ptx::tmem_wait_ld();
+                                ptx::tmem_wait_ld(o);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * a[e]);
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(TcRoles<KVF>::kThreads, 1)
                     uint32_t ov[16];
                     if (have_o) {
                         SMLA_TMEM_LD16(tmem + lane_base + i * HP + cc * 16, ov);
-                        ptx::tmem_wait_ld();
+                        ptx::tmem_wait_ld(ov);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) ov[e] = 0u;
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(TcRoles<KVF>::kThreads, 1)
                     uint32_t ov[16];
                     if (have_o) {
                         SMLA_TMEM_LD16(tmem + lane_base + i * HP + cc * 16, ov);
-                        ptx::tmem_wait_ld();
+                        ptx::tmem_wait_ld(ov);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) ov[e] = 0u;

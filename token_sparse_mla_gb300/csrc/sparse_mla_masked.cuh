@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int q = 0; q < kKeys / 16; ++q) SMLA_TMEM_LD16(tmem + lane_base + L::kColS + kKeys * part + 16 * q, sv + 16 * q);
-                ptx::tmem_wait_ld();
+                ptx::tmem_wait_ld(sv);
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(kMbSEmpty));
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         for (int cc = 0; cc < kOCols / 16; ++cc) {
                             uint32_t o[16];
                             SMLA_TMEM_LD16(tmem + lane_base + L::kColO + ocol0 + cc * 16, o);
-                            ptx::tmem_wait_ld();
+                            ptx::tmem_wait_ld(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                             SMLA_TMEM_ST16(tmem + lane_base + L::kColO + ocol0 + cc * 16, o);
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 #pragma unroll
                     for (int g = 0; g < kBatch; ++g)
                         SMLA_TMEM_LD16(tmem + lane_base + L::kColO + ocol0 + (kBatch * cg + g) * 16, o[g]);
-                    ptx::tmem_wait_ld();
+                    ptx::tmem_wait_ld(o);
                 } else {
 #pragma unroll
                     for (int g = 0; g < kBatch; ++g)

@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kQupThreads, 1)
                         for (int e = 0; e < 2; ++e)
                             SMLA_TMEM_LD16(tmem + lane_base + static_cast<uint32_t>(buf * kQupN + half * 64 + q * 32 + e * 16),
                                            v + 16 * e);
-                        ptx::tmem_wait_ld();
+                        ptx::tmem_wait_ld(v);
                         if (half == 1 && q == 1) {
                             ptx::tc_fence_before();
                             __syncwarp();

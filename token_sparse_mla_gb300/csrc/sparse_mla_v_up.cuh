@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kVupThreads, 1)
             for (int c = 0; c < kVupN / 16; ++c) {
                 uint32_t r[16];
                 SMLA_TMEM_LD16(tmem + lane_base + static_cast<uint32_t>(buf * kVupN + c * 16), r);
-                ptx::tmem_wait_ld();
+                ptx::tmem_wait_ld(r);
                 if (t < p.T) {
                     uint4 v0, v1;
                     v0.x = pack_bf16x2(__uint_as_float(r[0]), __uint_as_float(r[1]));
