@@ -69,10 +69,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 // Raw list entry j of a row (-1 when j is past the CTA's range or pred is false).  The load is
 // not checked here: the check reads the value, and a read right after the load would wait for
-// it.  Callers hold raw entries in a ring and check them with valid_slot when they are used.
+// it.  Callers hold raw entries in a ring and check them with valid_slot when they are used.  (The compiler may move the
+// load, so j is a number from behind the kernel's wait for the one before.)
 __device__ __forceinline__ int fetch_entry(const int32_t* idx_row, int j, int j1, bool pred) {
     int v = -1;
-    if (pred && j < j1) v = ptx::ld(idx_row + j);
+    if (pred && j < j1) v = ptx::ld_from(idx_row + j);
     return v;
 }
 
@@ -108,7 +109,7 @@ __device__ __forceinline__ void gather_rows(const FwdParams& p, const int32_t* i
     // warp pw copies rows pw, pw + NPW, pw + 2 NPW, ... of each block; lane i < kPerWarp
     // holds the slot of the warp's i-th row.
     const char* kv_bytes = reinterpret_cast<const char*>(p.kv);
-    const int my_row = pw + NPW * lane;
+    const int my_row = ptx::behind(pw + NPW * lane);
     const bool row_owner = lane < kPerWarp && my_row < kRows;
     // The entries of this lane's row are loaded kAhead blocks (256 list entries) ahead into a
     // ring indexed by b % kAhead; the block loop is unrolled kAhead times so every ring index is

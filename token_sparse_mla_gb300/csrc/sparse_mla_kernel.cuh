@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(TcRoles<KVF>::kThreads, 1)
         const int quad = warp & 3;  // TMEM lane quadrant this warp may access
         const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
         const int g = lane >> 2, tq = lane & 3;
-        const int r0 = quad * 16 + g, r1 = r0 + 8;
+        const int r0 = ptx::behind(quad * 16 + g), r1 = r0 + 8;
         constexpr int NG = HP / 8;
         const float c = p.sm_scale_log2;
         bool failed = false;

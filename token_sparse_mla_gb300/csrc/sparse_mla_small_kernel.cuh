@@ -203,7 +203,7 @@ __device__ __forceinline__ void small_gather(const FwdParams& p, int64_t x0, int
     // fetch cursor: token ft, first list entry fj of the next block to fetch (blocks x0, x0+1, ...)
     const int kpad = p.nblk * kSmRows;
     int ft = static_cast<int>(x0 / p.nblk);
-    int fj = static_cast<int>(x0 - static_cast<int64_t>(ft) * p.nblk) * kSmRows;
+    int fj = ptx::behind(static_cast<int>(x0 - static_cast<int64_t>(ft) * p.nblk)) * kSmRows;
     auto fetch = [&](bool pred) -> int {
         const int v = fetch_entry(p.indices + static_cast<int64_t>(ft) * p.topk, fj + lane, p.topk, pred);
         fj += kSmRows;
@@ -358,7 +358,7 @@ __device__ __forceinline__ void small_gather(const FwdParams& p, int64_t x0, int
 template <int H>
 __device__ __forceinline__ void load_q_frags(const FwdParams& p, int t, int cw, int lane,
                                              uint32_t (&bq)[kSmKSteps][H / 8][2]) {
-    const int g = lane >> 2, tq = lane & 3;
+    const int g = lane >> 2, tq = ptx::behind(lane & 3);
     const __nv_bfloat16* qt = p.q + static_cast<int64_t>(t) * H * kDQK;
 #pragma unroll
     for (int kk = 0; kk < kSmKSteps; ++kk) {
@@ -366,8 +366,8 @@ __device__ __forceinline__ void load_q_frags(const FwdParams& p, int t, int cw, 
         for (int nt = 0; nt < H / 8; ++nt) {
             const unsigned int* qr = reinterpret_cast<const unsigned int*>(
                 qt + (nt * 8 + g) * kDQK + 16 * (kSmKSteps * cw + kk) + 2 * tq);
-            bq[kk][nt][0] = ptx::ld(qr);
-            bq[kk][nt][1] = ptx::ld(qr + 4);
+            bq[kk][nt][0] = ptx::ld_from(qr);
+            bq[kk][nt][1] = ptx::ld_from(qr + 4);
         }
     }
 }
